@@ -5,16 +5,20 @@ The library is the C ABI in include/dgemm.h (libdgemm.so, built from csrc/ by
 (`gemm_f32_simt`, `gemm_f32_tc`, `gemm_bf16_tc`, ...: raw device pointers,
 status codes) and adds `matmul`, a convenience over torch CUDA tensors that
 only derives pointers, leading dimensions and the stream, allocates C, and
-raises on a non-zero status.  PyTorch is used for device memory and streams;
+raises on a non-zero status; `layer_norm`, `linear`, `gated_ffn` and their
+`_backward` calls (ops.py) do the same for the feed-forward operators.  PyTorch is used for device memory and streams;
 all arithmetic runs in the library's kernels.  There is no fallback: without
 libdgemm.so every call raises.
 """
 from ._lib import (  # noqa: F401  (re-exported C entry points)
+    ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, DTYPE_BF16, DTYPE_F16, DTYPE_F32,
     ERR_ALIAS, ERR_ARCH, ERR_CUDA, ERR_INVALID_POINTER, ERR_INVALID_VALUE, ERR_MISALIGNED,
     ERR_NULL_POINTER, ERR_SCRATCH_LIMIT, ERR_UNSUPPORTED, ERR_WATCHDOG, EXPORTED, F8_E4M3,
     F8_E5M2, LIB_PATH, NOALLOC_SCRATCH_BYTES, OK, OP_N, OP_T, PATH_3XTF32, PATH_BF16,
     PATH_F8_E4M3, PATH_F8_E5M2, PATH_FP16, PATH_SIMT, PATH_TF32, TC_3XTF32, TC_TF32,
-    LibraryMissing, dgemm_gemm_ex, dgemm_kernel_launches, dgemm_last_cuda_error,
+    LibraryMissing, dgemm_gated_ffn, dgemm_gated_ffn_backward, dgemm_gemm_ex,
+    dgemm_kernel_launches, dgemm_last_cuda_error, dgemm_layer_norm, dgemm_layer_norm_backward,
+    dgemm_linear, dgemm_linear_backward,
     dgemm_status_string, dgemm_version, dgemm_watchdog_status, gemm_bf16_tc, gemm_f16_tc,
     gemm_f32_simt, gemm_f32_tc, gemm_f32_tc_noalloc, gemm_f8_tc, load,
 )
@@ -112,3 +116,9 @@ def matmul(A, B, mode="tf32", out=None, stream=None, trans_a=False, trans_b=Fals
                         ldc, stream)
     check(st, f"gemm ({mode})")
     return out
+
+
+from .ops import (  # noqa: E402,F401  (uses DgemmError and check above)
+    ACTIVATIONS, gated_ffn, gated_ffn_backward, layer_norm, layer_norm_backward, linear,
+    linear_backward,
+)

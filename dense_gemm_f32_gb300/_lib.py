@@ -33,10 +33,15 @@ PATH_SIMT, PATH_TF32, PATH_3XTF32, PATH_BF16, PATH_FP16, PATH_F8_E4M3, PATH_F8_E
 F8_E4M3 = 0
 F8_E5M2 = 1
 
+# Element types and activations of the feed-forward operators.
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = range(3)
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+
 EXPORTED = ("gemm_f32_simt", "gemm_f32_tc", "gemm_bf16_tc", "dgemm_status_string",
             "dgemm_last_cuda_error", "dgemm_watchdog_status", "dgemm_version",
             "dgemm_kernel_launches", "gemm_f32_tc_noalloc", "gemm_f16_tc", "dgemm_gemm_ex",
-            "gemm_f8_tc")
+            "gemm_f8_tc", "dgemm_layer_norm", "dgemm_layer_norm_backward", "dgemm_linear",
+            "dgemm_linear_backward", "dgemm_gated_ffn", "dgemm_gated_ffn_backward")
 
 _lib = None
 
@@ -82,6 +87,16 @@ def load():
     lib.dgemm_gemm_ex.restype = i
     lib.gemm_f8_tc.argtypes = [i] + gemm_args
     lib.gemm_f8_tc.restype = i
+    m = [p, i]  # a matrix and its leading dimension
+    lib.dgemm_layer_norm.argtypes = [i, i, i, ctypes.c_float, *m, p, p, *m, p, p, p]
+    lib.dgemm_layer_norm_backward.argtypes = [i, i, i, *m, *m, p, p, p, *m, *m, p, p, p]
+    lib.dgemm_linear.argtypes = [i] * 6 + [*m, *m, p, *m, *m, *m, p]
+    lib.dgemm_linear_backward.argtypes = [i] * 6 + m * 7 + [p, p]
+    lib.dgemm_gated_ffn.argtypes = [i] * 6 + m * 9 + [p]
+    lib.dgemm_gated_ffn_backward.argtypes = [i] * 6 + m * 14 + [p]
+    for name in ("layer_norm", "layer_norm_backward", "linear", "linear_backward", "gated_ffn",
+                 "gated_ffn_backward"):
+        getattr(lib, "dgemm_" + name).restype = i
     _lib = lib
     return lib
 
@@ -114,6 +129,44 @@ def gemm_f8_tc(fmt, M, N, K, A, lda, B, ldb, C, ldc, stream=0):
 
 def dgemm_gemm_ex(path, op_a, op_b, M, N, K, A, lda, B, ldb, C, ldc, stream=0):
     return load().dgemm_gemm_ex(path, op_a, op_b, M, N, K, A, lda, B, ldb, C, ldc, stream)
+
+
+def dgemm_layer_norm(dtype, rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd, stream=0):
+    return load().dgemm_layer_norm(dtype, rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean,
+                                   rstd, stream)
+
+
+def dgemm_layer_norm_backward(dtype, rows, cols, dY, lddy, X, ldx, weight, mean, rstd, dR, lddr,
+                              dX, lddx, dweight, dbias, stream=0):
+    return load().dgemm_layer_norm_backward(dtype, rows, cols, dY, lddy, X, ldx, weight, mean,
+                                            rstd, dR, lddr, dX, lddx, dweight, dbias, stream)
+
+
+def dgemm_linear(dtype, activation, op_w, M, N, K, X, ldx, W, ldw, bias, R, ldr, D, ldd, Z, ldz,
+                 stream=0):
+    return load().dgemm_linear(dtype, activation, op_w, M, N, K, X, ldx, W, ldw, bias, R, ldr, D,
+                               ldd, Z, ldz, stream)
+
+
+def dgemm_linear_backward(dtype, activation, op_w, M, N, K, dD, lddd, X, ldx, W, ldw, Z, ldz, dZ,
+                          lddz, dX, lddx, dW, lddw, dbias, stream=0):
+    return load().dgemm_linear_backward(dtype, activation, op_w, M, N, K, dD, lddd, X, ldx, W, ldw,
+                                        Z, ldz, dZ, lddz, dX, lddx, dW, lddw, dbias, stream)
+
+
+def dgemm_gated_ffn(dtype, activation, op_w, M, D, F, X, ldx, Wg, ldwg, Wu, ldwu, Wd, ldwd, R, ldr,
+                    H, ldh, G, ldg, U, ldu, Y, ldy, stream=0):
+    return load().dgemm_gated_ffn(dtype, activation, op_w, M, D, F, X, ldx, Wg, ldwg, Wu, ldwu, Wd,
+                                  ldwd, R, ldr, H, ldh, G, ldg, U, ldu, Y, ldy, stream)
+
+
+def dgemm_gated_ffn_backward(dtype, activation, op_w, M, D, F, dY, lddy, X, ldx, Wg, ldwg, Wu,
+                             ldwu, Wd, ldwd, G, ldg, U, ldu, H, ldh, dG, lddg, dU, lddu, dX, lddx,
+                             dWg, lddwg, dWu, lddwu, dWd, lddwd, stream=0):
+    return load().dgemm_gated_ffn_backward(dtype, activation, op_w, M, D, F, dY, lddy, X, ldx, Wg,
+                                           ldwg, Wu, ldwu, Wd, ldwd, G, ldg, U, ldu, H, ldh, dG,
+                                           lddg, dU, lddu, dX, lddx, dWg, lddwg, dWu, lddwu, dWd,
+                                           lddwd, stream)
 
 
 def dgemm_status_string(status):

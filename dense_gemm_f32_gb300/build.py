@@ -19,14 +19,17 @@ LIB = os.path.join(PKG, "libdgemm.so")
 HEADER = os.path.join(ROOT, "include", "dgemm.h")
 # (source, object name, defines): simt.cu and tc.cu are compiled once per
 # operand layout so that the four layouts build in parallel.
-UNITS = ([("api.cu", "api", []), ("staging.cu", "staging", [])]
+UNITS = ([("api.cu", "api", []), ("staging.cu", "staging", []), ("ops_api.cu", "ops_api", []),
+          ("norm.cu", "norm", []), ("rowops.cu", "rowops", []),
+          ("fused_simple.cu", "fused_simple", [])]
          + [("simt.cu", f"simt_{u}", [f"-DDGEMM_SIMT_UNIT={u}"]) for u in range(4)]
          + [("tc.cu", f"tc_{u}", [f"-DDGEMM_TC_UNIT={u}"]) for u in range(4)])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 EXPORTS = ["gemm_f32_simt", "gemm_f32_tc", "gemm_bf16_tc", "dgemm_status_string",
            "dgemm_last_cuda_error", "dgemm_watchdog_status", "dgemm_version",
            "dgemm_kernel_launches", "gemm_f32_tc_noalloc", "gemm_f16_tc", "dgemm_gemm_ex",
-           "gemm_f8_tc"]
+           "gemm_f8_tc", "dgemm_layer_norm", "dgemm_layer_norm_backward", "dgemm_linear",
+           "dgemm_linear_backward", "dgemm_gated_ffn", "dgemm_gated_ffn_backward"]
 
 
 def _nvcc():

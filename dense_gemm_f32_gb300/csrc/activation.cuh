@@ -1,0 +1,136 @@
+// activation.cuh -- element types and activation functions of the
+// feed-forward operators (norm.cu, rowops.cu, the fused GEMM epilogues).
+//
+// Every activation and derivative is evaluated in fp32 with CUDA's own math
+// functions; only the store of a result rounds to 16 bits.
+#pragma once
+
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/dgemm.h"
+
+namespace dg {
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) {
+  return __half2float(v);
+}
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+
+// Two neighbouring 16-bit elements packed in a 32-bit word.
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+
+constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+// 1 / (1 + exp(-t)): exp(-t) overflows to infinity for t < -88, giving 0.
+__device__ __forceinline__ float sigmoid_f32(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
+
+// act(z):
+//   relu       max(z, 0)
+//   gelu       z Phi(z), Phi the normal distribution function
+//   gelu_tanh  z sigmoid(2 a (z + b z^3)) = z / 2 (1 + tanh(a (z + b z^3)))
+//   silu       z sigmoid(z)
+template <int ACT>
+__device__ __forceinline__ float act_f32(float z) {
+  if constexpr (ACT == DGEMM_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays a NaN
+  if constexpr (ACT == DGEMM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == DGEMM_ACT_GELU_TANH)
+    return z * sigmoid_f32(2.f * kGeluA * (z + kGeluB * z * z * z));
+  if constexpr (ACT == DGEMM_ACT_SILU) return z * sigmoid_f32(z);
+  return z;
+}
+
+// act(z) and act'(z) together; the derivative of relu at 0 is 0.
+template <int ACT>
+__device__ __forceinline__ void act_grad_f32(float z, float &value, float &slope) {
+  if constexpr (ACT == DGEMM_ACT_RELU) {
+    value = z < 0.f ? 0.f : z;
+    slope = z > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == DGEMM_ACT_GELU) {
+    const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+    value = z * cdf;
+    slope = cdf + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+  } else if constexpr (ACT == DGEMM_ACT_GELU_TANH) {
+    const float s = sigmoid_f32(2.f * kGeluA * (z + kGeluB * z * z * z));
+    value = z * s;
+    slope = s + z * s * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z);
+  } else if constexpr (ACT == DGEMM_ACT_SILU) {
+    const float s = sigmoid_f32(z);
+    value = z * s;
+    slope = s * (1.f + z * (1.f - s));
+  } else {
+    value = z;
+    slope = 1.f;
+  }
+}
+
+// The activation is a run-time argument of the kernels (a warp-uniform
+// branch per group of elements).
+template <class F>
+__device__ __forceinline__ void with_act(int act, F &&f) {
+  switch (act) {
+    case DGEMM_ACT_RELU: f(std::integral_constant<int, DGEMM_ACT_RELU>{}); break;
+    case DGEMM_ACT_GELU: f(std::integral_constant<int, DGEMM_ACT_GELU>{}); break;
+    case DGEMM_ACT_GELU_TANH: f(std::integral_constant<int, DGEMM_ACT_GELU_TANH>{}); break;
+    case DGEMM_ACT_SILU: f(std::integral_constant<int, DGEMM_ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, DGEMM_ACT_NONE>{}); break;
+  }
+}
+
+}  // namespace dg

@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/dgemm.h"
+#include "api_common.h"
 #include "kernels.h"
 
 namespace dg {
@@ -34,19 +35,22 @@ namespace {
 
 thread_local char g_cuda_err[512];
 
-int cuda_fail(cudaError_t e, const char *where) {
-  snprintf(g_cuda_err, sizeof g_cuda_err, "%s: %s (%s)", where, cudaGetErrorString(e),
-           cudaGetErrorName(e));
-  return DGEMM_ERR_CUDA;
-}
-
 // Per-device facts, looked up once.  state: 0 unknown, 1 supported, 2 not CC 10.3.
 struct DeviceInfo {
   std::atomic<int> state{0};
   int num_sms = 0;
 };
-constexpr int kMaxDevices = 64;
-DeviceInfo g_devices[kMaxDevices];
+DeviceInfo g_devices[dg::kMaxDevices];
+
+}  // namespace
+
+namespace dg {
+
+int cuda_fail(cudaError_t e, const char *where) {
+  snprintf(g_cuda_err, sizeof g_cuda_err, "%s: %s (%s)", where, cudaGetErrorString(e),
+           cudaGetErrorName(e));
+  return DGEMM_ERR_CUDA;
+}
 
 int current_device(int *dev, int *num_sms) {
   int d = 0;
@@ -73,7 +77,6 @@ int current_device(int *dev, int *num_sms) {
   return DGEMM_OK;
 }
 
-// A, B and C must be memory that this device's kernels can address directly.
 int check_device_pointer(const void *p, int dev) {
   cudaPointerAttributes at;
   cudaError_t e = cudaPointerGetAttributes(&at, p);
@@ -86,18 +89,19 @@ int check_device_pointer(const void *p, int dev) {
   return DGEMM_ERR_INVALID_POINTER;
 }
 
-inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace dg
 
-// Byte range [lo, hi) spanned by a rows x cols row-major matrix.
-struct Span {
-  uintptr_t lo, hi;
-};
-inline Span span(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t es) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  if (rows <= 0 || cols <= 0) return {lo, lo};
-  return {lo, lo + static_cast<uintptr_t>(((rows - 1) * ld + cols) * es)};
-}
-inline bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+namespace {
+
+using dg::aligned;
+using dg::check_device_pointer;
+using dg::cuda_fail;
+using dg::current_device;
+using dg::kMaxDevices;
+using dg::overlap;
+using dg::Span;
+using dg::span;
+using dg::tma_ok;
 
 // Steps 2-8 of the check list.  *nothing_to_do is set when M or N is zero.
 // a_t / b_t: A is stored K x M (op(A) = A^T) / B is stored N x K.
@@ -193,9 +197,6 @@ int after_launch(cudaError_t e, const char *what) {
   if (e != cudaSuccess) return cuda_fail(e, what);
   return DGEMM_OK;
 }
-
-// TMA needs 16-byte aligned bases and row pitches that are multiples of 16 B.
-inline bool tma_ok(const void *p, int64_t ld, int es) { return aligned(p, 16) && (ld * es) % 16 == 0; }
 
 inline bool is_f8(dg::TcKind k) { return k == dg::TcKind::kE4M3 || k == dg::TcKind::kE5M2; }
 
@@ -511,14 +512,14 @@ int dgemm_gemm_ex(int path, int op_a, int op_b, int M, int N, int K, const void 
 const char *dgemm_status_string(int status) {
   switch (status) {
     case DGEMM_OK: return "success";
-    case DGEMM_ERR_INVALID_VALUE: return "invalid value: negative size or leading dimension too small";
-    case DGEMM_ERR_NULL_POINTER: return "null pointer for A, B or C";
-    case DGEMM_ERR_ALIAS: return "C overlaps A or B";
-    case DGEMM_ERR_UNSUPPORTED: return "unsupported mode";
+    case DGEMM_ERR_INVALID_VALUE: return "invalid value: negative size, leading dimension too small, or eps not finite and >= 0";
+    case DGEMM_ERR_NULL_POINTER: return "null pointer for A, B or C, or for an argument that is not optional";
+    case DGEMM_ERR_ALIAS: return "C (or another output) overlaps another argument";
+    case DGEMM_ERR_UNSUPPORTED: return "unsupported mode, element type, activation or layout";
     case DGEMM_ERR_CUDA: return "CUDA error (see dgemm_last_cuda_error)";
     case DGEMM_ERR_ARCH: return "current device is not compute capability 10.3 (sm_103a)";
     case DGEMM_ERR_MISALIGNED: return "pointer not aligned to its element size";
-    case DGEMM_ERR_INVALID_POINTER: return "A, B or C is not device memory of the current device";
+    case DGEMM_ERR_INVALID_POINTER: return "A, B or C (or another argument) is not device memory of the current device";
     case DGEMM_ERR_WATCHDOG: return "a kernel gave up a bounded wait; its output is incomplete";
     case DGEMM_ERR_SCRATCH_LIMIT:
       return "operands need more re-pitch scratch than gemm_f32_tc_noalloc's fixed 16 MiB; "
@@ -537,7 +538,7 @@ int dgemm_watchdog_status(cudaStream_t stream, int *where) {
   return code ? DGEMM_ERR_WATCHDOG : DGEMM_OK;
 }
 
-int dgemm_version(void) { return 100; }
+int dgemm_version(void) { return 200; }
 
 unsigned long long dgemm_kernel_launches(void) {
   return dg::g_launches.load(std::memory_order_relaxed);

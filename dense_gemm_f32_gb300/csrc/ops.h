@@ -1,0 +1,72 @@
+// ops.h -- internal launchers of the feed-forward operators (not exported).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace dg {
+
+// What a fused product does with its accumulator tile (all in fp32, rounded
+// once per stored element).
+enum class Epi {
+  kLinear,    // z = acc + bias; [Z = z]; D = act(z) + R
+  kGated,     // two accumulators g, u: [G = g, U = u]; H = act(g) u
+  kGatedBwd,  // acc = dh: dG = dh u act'(g), dU = dh act(g), H = act(g) u
+};
+
+// How a second operand pair (A2, B2) of the same shapes and leading
+// dimensions joins the first.
+enum class Dual {
+  kNone,   // out = A B
+  kSum,    // out = A B + A2 B2, one accumulation
+  kPair,   // out0 = A B, out1 = A2 B2
+  kGated,  // g = A B, u = A B2 (Epi::kGated)
+};
+
+// One fused product of 16-bit operands.  a_t: A is stored K x M, else M x K;
+// b_t: B is stored N x K, else K x N; all row-major.  Outputs and the
+// epilogue's inputs are M x N, row-major, of the operands' type.
+struct FusedGemm {
+  Epi epi = Epi::kLinear;
+  Dual dual = Dual::kNone;
+  int dtype = 0;  // dgemm_dtype_t: BF16 or F16
+  int act = 0;    // dgemm_activation_t
+  int M = 0, N = 0, K = 0;
+  bool a_t = false, b_t = false;
+  const void *A = nullptr, *A2 = nullptr, *B = nullptr, *B2 = nullptr;
+  int64_t lda = 0, lda2 = 0, ldb = 0, ldb2 = 0;
+  // kLinear: out0 = D, out1 = Z (or null), in0 = R (or null), bias (or null)
+  //          (Dual::kPair: out0, out1 the two products, no bias, Z or R)
+  // kGated: out0 = H, out1 = G, out2 = U (both or neither)
+  // kGatedBwd: in0 = G, in1 = U; out0 = dG, out1 = dU, out2 = H
+  void *out0 = nullptr, *out1 = nullptr, *out2 = nullptr;
+  int64_t ldo0 = 0, ldo1 = 0, ldo2 = 0;
+  const void *in0 = nullptr, *in1 = nullptr;
+  int64_t ldi0 = 0, ldi1 = 0;
+  const void *bias = nullptr;
+};
+cudaError_t launch_fused(const FusedGemm &p, int num_sms, cudaStream_t stream);
+
+// dZ = dD act'(Z) (act != none; else dZ is not written) and, where dbias is
+// not null, dbias[j] = sum_i dZ[i][j] in fp32, rounded once.  `partial` is
+// fp32 scratch of act_grad_scratch() bytes.
+size_t act_grad_scratch(int M, int N, bool with_bias, int num_sms);
+cudaError_t launch_act_grad(int dtype, int act, int M, int N, const void *dD, int64_t lddd,
+                            const void *Z, int64_t ldz, void *dZ, int64_t lddz, void *dbias,
+                            float *partial, int num_sms, cudaStream_t stream);
+
+// Layer norm over rows of `cols` elements.
+cudaError_t launch_layer_norm(int dtype, int rows, int cols, float eps, const void *X, int64_t ldx,
+                              const void *weight, const void *bias, void *Y, int64_t ldy,
+                              float *mean, float *rstd, int num_sms, cudaStream_t stream);
+// `partial`: fp32 scratch of layer_norm_scratch() bytes (0 when neither
+// dweight nor dbias is asked for).
+size_t layer_norm_scratch(int rows, int cols, bool with_grads, int num_sms);
+cudaError_t launch_layer_norm_backward(int dtype, int rows, int cols, const void *dY, int64_t lddy,
+                                       const void *X, int64_t ldx, const void *weight,
+                                       const float *mean, const float *rstd, const void *dR,
+                                       int64_t lddr, void *dX, int64_t lddx, void *dweight,
+                                       void *dbias, float *partial, int num_sms,
+                                       cudaStream_t stream);
+
+}  // namespace dg

@@ -1,7 +1,9 @@
 /*
  * dgemm.h -- C ABI of the GB300 (sm_103a) dense GEMM library.
  *
- * Every entry point computes the plain row-major matrix product
+ * Every gemm_* entry point and dgemm_gemm_ex computes the plain row-major
+ * matrix product (the feed-forward operators around it are described where
+ * they are declared)
  *
  *     C[i*ldc + j] = sum_{k=0}^{K-1} A[i*lda + k] * B[k*ldb + j],  0 <= i < M, 0 <= j < N
  *
@@ -66,10 +68,10 @@ extern "C" {
  * was enqueued. */
 typedef enum {
     DGEMM_OK = 0,
-    DGEMM_ERR_INVALID_VALUE = 1,   /* negative size, leading dimension too small */
-    DGEMM_ERR_NULL_POINTER = 2,    /* NULL A, B or C with work to do            */
-    DGEMM_ERR_ALIAS = 3,           /* C overlaps A or B                          */
-    DGEMM_ERR_UNSUPPORTED = 4,     /* unknown mode                               */
+    DGEMM_ERR_INVALID_VALUE = 1,   /* negative size, leading dimension too small, bad eps */
+    DGEMM_ERR_NULL_POINTER = 2,    /* NULL A, B or C (or a matrix that is not optional) with work to do */
+    DGEMM_ERR_ALIAS = 3,           /* an output overlaps another argument        */
+    DGEMM_ERR_UNSUPPORTED = 4,     /* unknown mode, element type or activation   */
     DGEMM_ERR_CUDA = 5,            /* CUDA runtime/driver error (see below)      */
     DGEMM_ERR_ARCH = 6,            /* current device is not compute capability 10.3 */
     DGEMM_ERR_MISALIGNED = 7,      /* pointer not aligned to its element size    */
@@ -301,6 +303,131 @@ int dgemm_gemm_ex(int path, int op_a, int op_b, int M, int N, int K,
                   const void *B, int ldb,
                   float *C, int ldc,
                   cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Feed-forward operators: what a transformer layer runs around the product.
+ *
+ * Matrices are row-major with leading dimensions in elements, vectors are
+ * contiguous; pointers, ownership, asynchrony, determinism and status codes
+ * are those of the GEMM entry points.  Every element type below is `dtype`
+ * (dgemm_dtype_t) unless a pointer says float.  Sums, statistics and
+ * activations are computed in fp32; an output element is rounded once, to
+ * nearest even.  Outputs must not overlap any other argument
+ * (DGEMM_ERR_ALIAS) except where an entry point says so.  Matrices marked
+ * "workspace" are outputs whose contents are unspecified afterwards beyond
+ * what is stated.  A sum over nothing (K == 0, no rows) is zero.
+ */
+
+/* Element types of the feed-forward operators. */
+typedef enum {
+    DGEMM_DTYPE_F32 = 0,  /* layer norm only */
+    DGEMM_DTYPE_BF16 = 1,
+    DGEMM_DTYPE_F16 = 2
+} dgemm_dtype_t;
+
+/* Activations act(z). */
+typedef enum {
+    DGEMM_ACT_NONE = 0,       /* z */
+    DGEMM_ACT_RELU = 1,       /* max(z, 0); derivative 0 at 0 */
+    DGEMM_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution function */
+    DGEMM_ACT_GELU_TANH = 3,  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    DGEMM_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} dgemm_activation_t;
+
+/*
+ * dgemm_layer_norm -- y = (x - mu) rstd weight + bias for every row x of X.
+ *
+ * mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps), in two passes over
+ * the row held on the SM (the variance is of the centred values).
+ * X, Y: rows x cols.  weight, bias: cols elements, or NULL (1 and 0).
+ * mean, rstd: rows floats, or NULL when the backward pass is not wanted.
+ * eps >= 0 and finite, else DGEMM_ERR_INVALID_VALUE.
+ */
+int dgemm_layer_norm(int dtype, int rows, int cols, float eps,
+                     const void *X, int ldx,
+                     const void *weight, const void *bias,
+                     void *Y, int ldy, float *mean, float *rstd,
+                     cudaStream_t stream);
+
+/*
+ * dgemm_layer_norm_backward -- with xh = (x - mean) rstd and p = dy weight:
+ * dX = rstd (p - mean(p) - xh mean(p xh)) + dR, dweight = sum over rows of
+ * dy xh, dbias = sum over rows of dy.
+ *
+ * dY, X, dX: rows x cols.  mean, rstd: as the forward pass wrote them.
+ * weight: or NULL (1).  dR: rows x cols, a gradient that joins dX (a skip
+ * connection's), or NULL.  dweight, dbias: cols elements, or NULL.
+ */
+int dgemm_layer_norm_backward(int dtype, int rows, int cols,
+                              const void *dY, int lddy, const void *X, int ldx,
+                              const void *weight, const float *mean, const float *rstd,
+                              const void *dR, int lddr,
+                              void *dX, int lddx, void *dweight, void *dbias,
+                              cudaStream_t stream);
+
+/*
+ * dgemm_linear -- Z = X op(W) + bias, D = act(Z) + R, in one kernel.
+ *
+ * dtype BF16 or F16.  X: M x K.  op_w = DGEMM_OP_N: W is K x N; DGEMM_OP_T: W
+ * is N x K and op(W) = W^T.  bias: N elements, or NULL.  R (residual): M x N,
+ * or NULL; D may be R itself (same address and leading dimension).  D: M x N.
+ * Z: M x N, or NULL when the backward pass does not need it.
+ */
+int dgemm_linear(int dtype, int activation, int op_w, int M, int N, int K,
+                 const void *X, int ldx, const void *W, int ldw,
+                 const void *bias, const void *R, int ldr,
+                 void *D, int ldd, void *Z, int ldz,
+                 cudaStream_t stream);
+
+/*
+ * dgemm_linear_backward -- dZ = dD act'(Z), dX = dZ op(W)^T, dW = X^T dZ
+ * (stored as W is), dbias = sum over rows of dZ.
+ *
+ * Z: as dgemm_linear wrote it; dZ: M x N workspace, holding dZ afterwards;
+ * both are ignored when activation is DGEMM_ACT_NONE (dZ is dD then).  dX, dW,
+ * dbias: NULL for a gradient that is not wanted (X or W may then be NULL).
+ * dZ is rounded to dtype before the two products; dbias sums unrounded values.
+ */
+int dgemm_linear_backward(int dtype, int activation, int op_w, int M, int N, int K,
+                          const void *dD, int lddd, const void *X, int ldx,
+                          const void *W, int ldw, const void *Z, int ldz,
+                          void *dZ, int lddz,
+                          void *dX, int lddx, void *dW, int lddw, void *dbias,
+                          cudaStream_t stream);
+
+/*
+ * dgemm_gated_ffn -- G = X op(Wg), U = X op(Wu), H = act(G) U (one kernel),
+ * Y = H op(Wd) + R (another).
+ *
+ * X, Y: M x D.  op_w = DGEMM_OP_N: Wg, Wu are D x F and Wd is F x D;
+ * DGEMM_OP_T: F x D and D x F.  R: M x D, or NULL; Y may be R itself.  H: M x F
+ * workspace, holding H rounded to dtype afterwards.  G, U: M x F, both or
+ * neither NULL: kept for the backward pass.
+ */
+int dgemm_gated_ffn(int dtype, int activation, int op_w, int M, int D, int F,
+                    const void *X, int ldx, const void *Wg, int ldwg,
+                    const void *Wu, int ldwu, const void *Wd, int ldwd,
+                    const void *R, int ldr, void *H, int ldh,
+                    void *G, int ldg, void *U, int ldu, void *Y, int ldy,
+                    cudaStream_t stream);
+
+/*
+ * dgemm_gated_ffn_backward -- the gradients of dgemm_gated_ffn from G and U.
+ *
+ * dH = dY op(Wd)^T stays in the accumulator of one kernel, which writes
+ * dG = dH U act'(G), dU = dH act(G) and H = act(G) U (M x F workspaces);
+ * dX = dG op(Wg)^T + dU op(Wu)^T, dWg = X^T dG, dWu = X^T dU, dWd = H^T dY
+ * (stored as the weights are).  dX, dWd: or NULL; dWg, dWu: both or neither.
+ */
+int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, int F,
+                             const void *dY, int lddy, const void *X, int ldx,
+                             const void *Wg, int ldwg, const void *Wu, int ldwu,
+                             const void *Wd, int ldwd,
+                             const void *G, int ldg, const void *U, int ldu,
+                             void *H, int ldh, void *dG, int lddg, void *dU, int lddu,
+                             void *dX, int lddx, void *dWg, int lddwg,
+                             void *dWu, int lddwu, void *dWd, int lddwd,
+                             cudaStream_t stream);
 
 /* Static English text for a status code (never NULL). */
 const char *dgemm_status_string(int status);
