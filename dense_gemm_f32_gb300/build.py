@@ -21,7 +21,8 @@ HEADER = os.path.join(ROOT, "include", "dgemm.h")
 # operand layout so that the four layouts build in parallel.
 UNITS = ([("api.cu", "api", []), ("staging.cu", "staging", []), ("ops_api.cu", "ops_api", []),
           ("norm.cu", "norm", []), ("rowops.cu", "rowops", []),
-          ("fused_simple.cu", "fused_simple", [])]
+          ("fused.cu", "fused", [])]
+         + [("fused_pair.cu", f"fused_pair_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(3)]
          + [("simt.cu", f"simt_{u}", [f"-DDGEMM_SIMT_UNIT={u}"]) for u in range(4)]
          + [("tc.cu", f"tc_{u}", [f"-DDGEMM_TC_UNIT={u}"]) for u in range(4)])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

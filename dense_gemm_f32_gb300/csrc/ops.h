@@ -47,6 +47,13 @@ struct FusedGemm {
 };
 cudaError_t launch_fused(const FusedGemm &p, int num_sms, cudaStream_t stream);
 
+// One operand layout each (one translation unit each): 0: A M x K, B K x N;
+// 1: A M x K, B N x K; 2: A K x M, B K x N.  Operands that TMA can read;
+// `watchdog` is the device address of the watchdog word.
+cudaError_t launch_fused_pair_unit_0(const FusedGemm &p, int *watchdog, cudaStream_t stream);
+cudaError_t launch_fused_pair_unit_1(const FusedGemm &p, int *watchdog, cudaStream_t stream);
+cudaError_t launch_fused_pair_unit_2(const FusedGemm &p, int *watchdog, cudaStream_t stream);
+
 // dZ = dD act'(Z) (act != none; else dZ is not written) and, where dbias is
 // not null, dbias[j] = sum_i dZ[i][j] in fp32, rounded once.  `partial` is
 // fp32 scratch of act_grad_scratch() bytes.
