@@ -62,10 +62,15 @@ cudaError_t launch_act_grad(int dtype, int act, int M, int N, const void *dD, in
                             const void *Z, int64_t ldz, void *dZ, int64_t lddz, void *dbias,
                             float *partial, int num_sms, cudaStream_t stream);
 
+// out0[col], out1[col] = sums over parts of partial[part][0][col] and
+// partial[part][1][col]; a null output is skipped.
+cudaError_t launch_column_sums(int dtype, const float *partial, int parts, int cols, void *out0,
+                               void *out1, cudaStream_t stream);
+
 // Layer norm over rows of `cols` elements.
 cudaError_t launch_layer_norm(int dtype, int rows, int cols, float eps, const void *X, int64_t ldx,
                               const void *weight, const void *bias, void *Y, int64_t ldy,
-                              float *mean, float *rstd, int num_sms, cudaStream_t stream);
+                              float *mean, float *rstd, cudaStream_t stream);
 // `partial`: fp32 scratch of layer_norm_scratch() bytes (0 when neither
 // dweight nor dbias is asked for).
 size_t layer_norm_scratch(int rows, int cols, bool with_grads, int num_sms);

@@ -115,7 +115,7 @@ int dgemm_layer_norm(int dtype, int rows, int cols, float eps, const void *X, in
   const int st = check_args(a, 6, -1, -1, &dev, &sms);
   if (st != DGEMM_OK) return st;
   return done(launch_layer_norm(dtype, rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd,
-                                sms, stream),
+                                stream),
               "layer norm launch");
 }
 

@@ -1,5 +1,11 @@
-// rowops.cu -- the element-wise half of a linear layer's backward pass:
-// dZ = dD act'(Z), with the bias gradient's column sums in the same pass.
+// rowops.cu -- the element-wise half of a linear layer's backward pass,
+// dZ = dD act'(Z), with the bias gradient's column sums in the same pass, and
+// the join of column sums that several blocks hold parts of.
+//
+// Bound by memory: two reads and one write of an M x N matrix.  A thread owns
+// eight columns (16 bytes of a row) and walks every eighth row of its block's share, so the column sums stay in registers; the eight
+// row groups of a block are added in shared memory, and each block's sums are
+// joined by a second launch, everything in a fixed order.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -7,55 +13,163 @@
 #include "kernels.h"
 #include "launch.cuh"
 #include "ops.h"
+#include "rowvec.cuh"
 
 namespace dg {
 namespace {
 
-template <class T>
-__global__ void act_grad_kernel(int act, int M, int N, const T *dD, int64_t lddd, const T *Z,
-                                int64_t ldz, T *dZ, int64_t lddz, T *dbias) {
+constexpr int kGroups = 8;  // row groups (warps) of a block
+
+template <class T, bool ALIGNED>
+__global__ void __launch_bounds__(32 * kGroups)
+    act_grad_kernel(int act, int M, int N, const T *dD, int64_t lddd, const T *Z, int64_t ldz,
+                    T *dZ, int64_t lddz, float *partial, T *dbias) {
+  constexpr int V = kVec<T>, TILE = 32 * V;
+  __shared__ float fold[kGroups][TILE];
   pdl_launch_dependents();
   pdl_wait();
-  const int j = blockIdx.x * blockDim.x + threadIdx.x;
-  if (j >= N) return;
-  float sum = 0.f;
-  for (int i = 0; i < M; ++i) {
-    float d = to_f32<T>(dD[(int64_t)i * lddd + j]);
-    with_act(act, [&](auto a) {
-      constexpr int ACT = decltype(a)::value;
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int col = blockIdx.x * TILE + lane * V;
+  float sum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) sum[j] = 0.f;
+  with_act(act, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+#pragma unroll 4
+    for (int64_t i = (int64_t)blockIdx.y * kGroups + group; i < M;
+         i += (int64_t)gridDim.y * kGroups) {
+      float d[V];
+      widen16<T>(load_row16<T, ALIGNED>(dD + i * lddd, col, N), d);
       if constexpr (ACT != DGEMM_ACT_NONE) {
-        float value, slope;
-        act_grad_f32<ACT>(to_f32<T>(Z[(int64_t)i * ldz + j]), value, slope);
-        d *= slope;
-        dZ[(int64_t)i * lddz + j] = from_f32<T>(d);
+        float z[V];
+        widen16<T>(load_row16<T, ALIGNED>(Z + i * ldz, col, N), z);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          float value, slope;
+          act_grad_f32<ACT>(z[j], value, slope);
+          d[j] *= slope;
+        }
+        store_row16<T, ALIGNED>(dZ + i * lddz, col, N, narrow16<T>(d));
       }
-    });
-    sum += d;
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[j] += d[j];
+    }
+  });
+  if (partial == nullptr && dbias == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) fold[group][lane * V + j] = sum[j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < TILE; c += 32 * kGroups) {
+    const int out = blockIdx.x * TILE + c;
+    if (out >= N) break;
+    float v = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) v += fold[g][c];
+    if (partial)
+      partial[(int64_t)blockIdx.y * N + out] = v;
+    else
+      dbias[out] = from_f32<T>(v);
   }
-  if (dbias) dbias[j] = from_f32<T>(sum);
+}
+
+// out[k][col] = sum over parts of partial[part][k][col], k < nvec (gridDim.y).
+// 32 columns per block; 32 groups of threads take every 32nd part.
+template <class T>
+__global__ void __launch_bounds__(1024)
+    column_sums_kernel(const float *partial, int parts, int cols, T *out0, T *out1) {
+  __shared__ float fold[32][33];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5, k = blockIdx.y, nvec = gridDim.y;
+  const int col = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (col < cols)
+#pragma unroll 4
+    for (int i = group; i < parts; i += 32) v += partial[((int64_t)i * nvec + k) * cols + col];
+  fold[group][lane] = v;
+  __syncthreads();
+  v = fold[lane][group];  // part group `lane` of column `group`
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  T *out = k ? out1 : out0;
+  const int c = blockIdx.x * 32 + group;
+  if (lane == 0 && out != nullptr && c < cols) out[c] = from_f32<T>(v);
 }
 
 template <class T>
-cudaError_t act_grad(int act, int M, int N, const void *dD, int64_t lddd, const void *Z,
-                     int64_t ldz, void *dZ, int64_t lddz, void *dbias, cudaStream_t stream) {
+cudaError_t column_sums(const float *partial, int parts, int cols, void *out0, void *out1, int nvec,
+                        cudaStream_t stream) {
   const cudaError_t e = launch_kernel(
-      act_grad_kernel<T>, dim3((unsigned)((N + 127) / 128)), dim3(128), 0, stream, 1u, act, M, N,
-      static_cast<const T *>(dD), lddd, static_cast<const T *>(Z), ldz, static_cast<T *>(dZ), lddz,
-      static_cast<T *>(dbias));
+      column_sums_kernel<T>, dim3((unsigned)((cols + 31) / 32), (unsigned)nvec), dim3(1024), 0,
+      stream, 1u, partial, parts, cols, static_cast<T *>(out0), static_cast<T *>(out1));
   if (e == cudaSuccess) count_launch();
   return e;
 }
 
+cudaError_t column_sums(int dtype, const float *partial, int parts, int cols, void *out0,
+                        void *out1, int nvec, cudaStream_t stream) {
+  switch (dtype) {
+    case DGEMM_DTYPE_BF16:
+      return column_sums<__nv_bfloat16>(partial, parts, cols, out0, out1, nvec, stream);
+    case DGEMM_DTYPE_F16:
+      return column_sums<__half>(partial, parts, cols, out0, out1, nvec, stream);
+    default:
+      return column_sums<float>(partial, parts, cols, out0, out1, nvec, stream);
+  }
+}
+
+// Shares of the rows: four blocks per SM over all column tiles, at least four
+// rows per row group.
+int act_grad_parts(int M, int N, int num_sms) {
+  const int64_t tiles = (N + 255) / 256;
+  int64_t parts = (4 * (int64_t)num_sms + tiles - 1) / tiles;
+  const int64_t most = ((int64_t)M + 4 * kGroups - 1) / (4 * kGroups);
+  parts = parts < most ? parts : most;
+  return (int)(parts < 1 ? 1 : parts);
+}
+
+template <class T, bool ALIGNED>
+cudaError_t act_grad(int act, int M, int N, const void *dD, int64_t lddd, const void *Z,
+                     int64_t ldz, void *dZ, int64_t lddz, void *dbias, float *partial, int parts,
+                     cudaStream_t stream) {
+  const cudaError_t e = launch_kernel(
+      act_grad_kernel<T, ALIGNED>, dim3((unsigned)((N + 255) / 256), (unsigned)parts),
+      dim3(32 * kGroups), 0, stream, 1u, act, M, N, static_cast<const T *>(dD), lddd,
+      static_cast<const T *>(Z), ldz, static_cast<T *>(dZ), lddz,
+      dbias != nullptr && parts > 1 ? partial : nullptr, static_cast<T *>(dbias));
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+inline bool vec_ok(const void *p, int64_t ld) {
+  return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && ld % 8 == 0;
+}
+
 }  // namespace
 
-size_t act_grad_scratch(int, int, bool, int) { return 0; }
+cudaError_t launch_column_sums(int dtype, const float *partial, int parts, int cols, void *out0,
+                               void *out1, cudaStream_t stream) {
+  return column_sums(dtype, partial, parts, cols, out0, out1, 2, stream);
+}
+
+size_t act_grad_scratch(int M, int N, bool with_bias, int num_sms) {
+  if (!with_bias) return 0;
+  return (size_t)act_grad_parts(M, N, num_sms) * N * sizeof(float);
+}
 
 cudaError_t launch_act_grad(int dtype, int act, int M, int N, const void *dD, int64_t lddd,
                             const void *Z, int64_t ldz, void *dZ, int64_t lddz, void *dbias,
-                            float *, int, cudaStream_t stream) {
-  return dtype == DGEMM_DTYPE_BF16
-             ? act_grad<__nv_bfloat16>(act, M, N, dD, lddd, Z, ldz, dZ, lddz, dbias, stream)
-             : act_grad<__half>(act, M, N, dD, lddd, Z, ldz, dZ, lddz, dbias, stream);
+                            float *partial, int num_sms, cudaStream_t stream) {
+  const bool vec = N % 8 == 0 && vec_ok(dD, lddd) &&
+                   (act == DGEMM_ACT_NONE || (vec_ok(Z, ldz) && vec_ok(dZ, lddz)));
+  const int parts = act_grad_parts(M, N, num_sms);
+  auto f = dtype == DGEMM_DTYPE_BF16
+               ? (vec ? act_grad<__nv_bfloat16, true> : act_grad<__nv_bfloat16, false>)
+               : (vec ? act_grad<__half, true> : act_grad<__half, false>);
+  const cudaError_t e =
+      f(act, M, N, dD, lddd, Z, ldz, dZ, lddz, dbias, partial, parts, stream);
+  if (e != cudaSuccess || dbias == nullptr || parts == 1) return e;
+  return column_sums(dtype, partial, parts, N, dbias, nullptr, 1, stream);
 }
 
 }  // namespace dg
