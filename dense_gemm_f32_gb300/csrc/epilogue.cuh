@@ -1,4 +1,4 @@
-// epilogue.cuh -- the arithmetic of the fused products' epilogues, on 32
+// epilogue.cuh -- the arithmetic of the fused products' epilogues, on
 // consecutive columns of one row held by one thread.
 #pragma once
 
@@ -30,19 +30,37 @@ __device__ __forceinline__ void load32(const T *p, int valid, bool vec, uint32_t
   }
 }
 
-// kLinear: z (with the bias added) in a, the residual's words in i0 when
-// has_in0; D in w0, Z in w1.
-// kGated: g in a, u in b; H in w0, G in w1, U in w2.
-// kGatedBwd: dh in a, the words of G and U in i0 and i1; dG, dU, H in w0..w2.
-// Everything is fp32 until the one rounding of each packed result.
-template <Epi EPI, class T>
-__device__ __forceinline__ void epilogue32(int act, bool has_in0, const float (&a)[32],
-                                           const float (&b)[32], const uint32_t (&i0)[16],
-                                           const uint32_t (&i1)[16], uint32_t (&w0)[16],
-                                           uint32_t (&w1)[16], uint32_t (&w2)[16]) {
+// One element.  kLinear: z (with the bias added) in a, the residual in i0 when
+// has_in0; D in o0 (Z is a itself).  kGated: g in a, u in b; H in o0.
+// kGatedBwd: dh in a, G and U in i0 and i1; dG, dU, H in o0, o1, o2.
+template <Epi EPI, int ACT>
+__device__ __forceinline__ void epilogue1(bool has_in0, float a, float b, float i0, float i1,
+                                          float &o0, float &o1, float &o2) {
+  if constexpr (EPI == Epi::kLinear) {
+    o0 = act_f32<ACT>(a);
+    if (has_in0) o0 += i0;
+  } else if constexpr (EPI == Epi::kGated) {
+    o0 = act_f32<ACT>(a) * b;
+  } else {
+    float value, slope;
+    act_grad_f32<ACT>(i0, value, slope);
+    o0 = a * i1 * slope;
+    o1 = a * value;
+    o2 = value * i1;
+  }
+}
+
+// 2 N consecutive elements; packed inputs i0 and i1, packed results w0, w1, w2:
+// kLinear D, Z; kGated H, G, U; kGatedBwd dG, dU, H.  Everything is fp32 until
+// the one rounding of each packed result.
+template <Epi EPI, class T, int N>
+__device__ __forceinline__ void epilogue_row(int act, bool has_in0, const float (&a)[2 * N],
+                                             const float (&b)[2 * N], const uint32_t (&i0)[N],
+                                             const uint32_t (&i1)[N], uint32_t (&w0)[N],
+                                             uint32_t (&w1)[N], uint32_t (&w2)[N]) {
   if constexpr (EPI != Epi::kGatedBwd) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < N; ++j) {
       w1[j] = pack2<T>(a[2 * j], a[2 * j + 1]);
       if constexpr (EPI == Epi::kGated) w2[j] = pack2<T>(b[2 * j], b[2 * j + 1]);
     }
@@ -50,25 +68,17 @@ __device__ __forceinline__ void epilogue32(int act, bool has_in0, const float (&
   with_act(act, [&](auto c) {
     constexpr int ACT = decltype(c)::value;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if constexpr (EPI == Epi::kLinear) {
-        float lo = act_f32<ACT>(a[2 * j]), hi = act_f32<ACT>(a[2 * j + 1]);
-        if (has_in0) {
-          const float2 r = unpack2<T>(i0[j]);
-          lo += r.x, hi += r.y;
-        }
-        w0[j] = pack2<T>(lo, hi);
-      } else if constexpr (EPI == Epi::kGated) {
-        w0[j] = pack2<T>(act_f32<ACT>(a[2 * j]) * b[2 * j],
-                         act_f32<ACT>(a[2 * j + 1]) * b[2 * j + 1]);
-      } else {
-        const float2 g = unpack2<T>(i0[j]), u = unpack2<T>(i1[j]);
-        float v0, s0, v1, s1;
-        act_grad_f32<ACT>(g.x, v0, s0);
-        act_grad_f32<ACT>(g.y, v1, s1);
-        w0[j] = pack2<T>(a[2 * j] * u.x * s0, a[2 * j + 1] * u.y * s1);
-        w1[j] = pack2<T>(a[2 * j] * v0, a[2 * j + 1] * v1);
-        w2[j] = pack2<T>(v0 * u.x, v1 * u.y);
+    for (int j = 0; j < N; ++j) {
+      float2 x = make_float2(0.f, 0.f), y = x;
+      float lo[3], hi[3];
+      if (EPI == Epi::kGatedBwd || (EPI == Epi::kLinear && has_in0)) x = unpack2<T>(i0[j]);
+      if constexpr (EPI == Epi::kGatedBwd) y = unpack2<T>(i1[j]);
+      epilogue1<EPI, ACT>(has_in0, a[2 * j], b[2 * j], x.x, y.x, lo[0], lo[1], lo[2]);
+      epilogue1<EPI, ACT>(has_in0, a[2 * j + 1], b[2 * j + 1], x.y, y.y, hi[0], hi[1], hi[2]);
+      w0[j] = pack2<T>(lo[0], hi[0]);
+      if constexpr (EPI == Epi::kGatedBwd) {
+        w1[j] = pack2<T>(lo[1], hi[1]);
+        w2[j] = pack2<T>(lo[2], hi[2]);
       }
     }
   });

@@ -1,6 +1,7 @@
 // fused.cu -- the fused products of the feed-forward operators: operands that
 // TMA cannot read are staged first, then one kernel runs.
 #include <cstdint>
+#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "api_common.h"
@@ -61,6 +62,52 @@ struct Staging {
   static int64_t pitch(int cols) { return (cols + 7) / 8 * 8; }
 };
 
+// DGEMM_FUSED_*: an environment variable's value in lo .. hi, or -1 (read at
+// every launch, for tests and tuning).
+int knob(const char *name, int lo, int hi) {
+  const char *e = getenv(name);
+  if (e == nullptr || e[0] < '0' || e[0] > '9') return -1;
+  const int v = atoi(e);
+  return v >= lo && v <= hi ? v : -1;
+}
+
+// Whether a product runs on CTA pairs: once its 256-row tiles occupy a quarter
+// of the SMs and more than one 256-column tile of tokens is there to fill
+// them.  DGEMM_FUSED_PAIR=0 / =1 forces the choice.
+bool use_pair(const FusedGemm &p, int num_sms) {
+  const int force = knob("DGEMM_FUSED_PAIR", 0, 1);
+  if (force >= 0) return force == 1;
+  if (p.M <= 256) return false;
+  const int tn = p.epi == Epi::kGated ? 128 : 256;
+  const int64_t tiles = (int64_t)((p.M + 255) / 256) * ((p.N + tn - 1) / tn) *
+                        (p.dual == Dual::kPair ? 2 : 1);
+  return tiles * 4 >= num_sms;
+}
+
+// DGEMM_FUSED_NT / _KD / _SPLITS override the parts of the plan.
+SmallPlan small_plan(const FusedGemm &p, int num_sms) {
+  SmallPlan plan;
+  const int step = p.a_t ? 64 : 16;
+  plan.nt = p.M <= 256 ? (p.M + step - 1) / step * step : 128;
+  const int nt = knob("DGEMM_FUSED_NT", 16, 256);
+  if (nt >= 0) plan.nt = (nt + step - 1) / step * step;
+  const int tf = p.epi == Epi::kGated ? 64 : 128;
+  const int64_t tiles = (int64_t)((p.M + plan.nt - 1) / plan.nt) * ((p.N + tf - 1) / tf) *
+                        (p.dual == Dual::kPair ? 2 : 1);
+  plan.kd = plan.nt <= 32 && p.K > 64 ? 2 : 1;
+  const int kd = knob("DGEMM_FUSED_KD", 1, 2);
+  if (kd >= 0 && (kd == 1 || plan.nt <= 64)) plan.kd = kd;
+  const int kblocks = (p.K + 64 * plan.kd - 1) / (64 * plan.kd) * (p.dual == Dual::kSum ? 2 : 1);
+  const int64_t slots = (plan.nt <= 128 ? 2 : 1) * (int64_t)num_sms;
+  int64_t s = slots / (tiles > 0 ? tiles : 1);
+  s = s < 8 ? s : 8;
+  s = s < kblocks / 2 ? s : kblocks / 2;
+  plan.splits = s < 1 ? 1 : (int)s;
+  const int splits = knob("DGEMM_FUSED_SPLITS", 1, 8);
+  if (splits >= 0) plan.splits = splits;
+  return plan;
+}
+
 }  // namespace
 
 cudaError_t launch_fused(const FusedGemm &p0, int num_sms, cudaStream_t stream) {
@@ -77,10 +124,19 @@ cudaError_t launch_fused(const FusedGemm &p0, int num_sms, cudaStream_t stream) 
   void *scratch = nullptr;
   cudaError_t e = st.run(&scratch, num_sms, stream);
   if (e == cudaSuccess) {
-    if (p.a_t)
-      e = p.b_t ? cudaErrorInvalidValue : launch_fused_pair_unit_2(p, wd, stream);
-    else
-      e = p.b_t ? launch_fused_pair_unit_1(p, wd, stream) : launch_fused_pair_unit_0(p, wd, stream);
+    const int unit = p.a_t ? 2 : p.b_t ? 1 : 0;
+    if (p.a_t && p.b_t) {
+      e = cudaErrorInvalidValue;
+    } else if (use_pair(p, num_sms)) {
+      e = unit == 0   ? launch_fused_pair_unit_0(p, wd, stream)
+          : unit == 1 ? launch_fused_pair_unit_1(p, wd, stream)
+                      : launch_fused_pair_unit_2(p, wd, stream);
+    } else {
+      const SmallPlan plan = small_plan(p, num_sms);
+      e = unit == 0   ? launch_fused_small_unit_0(p, plan, wd, stream)
+          : unit == 1 ? launch_fused_small_unit_1(p, plan, wd, stream)
+                      : launch_fused_small_unit_2(p, plan, wd, stream);
+    }
   }
   if (scratch != nullptr) {
     const cudaError_t e2 = scratch_free(scratch, stream);

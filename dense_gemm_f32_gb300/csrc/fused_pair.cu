@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
           }
         }
         uint32_t w[3][16];
-        epilogue32<EPI, T>(p.act, has_in0, a, b, i0, i1, w[0], w[1], w[2]);
+        epilogue_row<EPI, T, 16>(p.act, has_in0, a, b, i0, i1, w[0], w[1], w[2]);
         constexpr int kOuts = EPI == Epi::kLinear ? 2 : 3;
 #pragma unroll
         for (int o = 0; o < kOuts; ++o) {

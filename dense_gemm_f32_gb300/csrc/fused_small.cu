@@ -1,0 +1,493 @@
+// fused_small.cu -- the fused products of the feed-forward operators for few
+// rows or few tiles: single tokens, serving batches, small layers.
+//
+// Such a product is bound by reading its weights once, so the roles of the
+// operands are swapped with respect to a large product: the weights' output
+// features are the 128 rows of the MMA and the tokens its columns (16 to 256,
+// a multiple of 16), D^T = op(W)^T X^T, and one token costs little more than
+// the weights' traffic.  A tile is 128 features x NT tokens; with few tiles its
+// K range is split over a thread-block cluster of up to 8 CTAs, so that enough
+// SMs pull weights at once.
+//  * Warp 0 loads by TMA (weights and tokens of 64 or 128 k per stage), warp 1
+//    issues tcgen05.mma, one accumulator of NT columns in tensor memory; two
+//    CTAs fit on an SM while NT <= 128.
+//  * Every CTA parks its fp32 partial tile in its own shared memory, token by
+//    token, and the cluster's CTAs add the partials through distributed shared
+//    memory in part order, each finishing a share of the tile's elements: the
+//    epilogue (epilogue.cuh) runs once per element, on 8 neighbouring features
+//    of a token per thread with 16-byte accesses, or one feature per thread
+//    where a row is not 16-byte aligned.
+//  * kGated: the tile's 128 rows are 64 features of Wg and the same 64 of Wu,
+//    so one MMA stream gives both projections of a hidden unit in one tile.
+//  * Every wait is bounded (ptx.cuh).
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "epilogue.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+#include "tc_tile.cuh"
+#include "tmap.cuh"
+
+// Compiled once per operand layout (DGEMM_FUSED_UNIT, as in fused_pair.cu).
+#ifndef DGEMM_FUSED_UNIT
+#define DGEMM_FUSED_UNIT 0
+#endif
+#define DG_CAT2(a, b) a##b
+#define DG_CAT(a, b) DG_CAT2(a, b)
+#define DG_UNIT_LAUNCHER DG_CAT(launch_fused_small_unit_, DGEMM_FUSED_UNIT)
+
+namespace dg {
+namespace {
+
+constexpr bool kXT = DGEMM_FUSED_UNIT == 2;  // tokens stored K x M: read MN-major
+constexpr bool kWT = DGEMM_FUSED_UNIT == 1;  // weights stored N x K: read K-major
+
+struct SmallCfg {
+  static constexpr int ES = 2, UMMA_K = 16, BOX = 64;
+  static constexpr int TF = 128;              // features (MMA rows) of a tile
+  static constexpr int W_CHUNK = TF * 128;    // weights of 64 k
+  static constexpr int MAX_STAGES = 8, MAX_SPLITS = 8, MAX_NT = 256;
+  static constexpr int THREADS = 192;         // producer, MMA, four drain warps
+  static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
+  // bars (full[8], empty[8], accf), TMEM slot, abort flag; 1024 for alignment
+  static constexpr int TAIL_BYTES = (2 * MAX_STAGES + 1) * 8 + 16 + 1024;
+  static constexpr int BUDGET2 = 113 * 1024 - TAIL_BYTES;  // two CTAs per SM
+  static constexpr int BUDGET1 = 226 * 1024 - TAIL_BYTES;  // one
+};
+
+// Site codes of the bounded waits.
+enum : int {
+  kSite4ProducerEmpty = 0x91,
+  kSite4ProducerDrain = 0x92,
+  kSite4MmaFull = 0x93,
+  kSite4MmaDrain = 0x94,
+  kSite4DrainAccFull = 0x95,
+};
+
+struct SmallMaps {
+  CUtensorMap w, x, w2, x2;
+};
+
+struct SmallArgs {
+  int M, N, K;
+  int dual, act;
+  int nt, kd, stages, splits;
+  uint32_t idesc;
+  uint32_t tmem_cols;
+  int vec;  // 8 features per thread: every row of every output and input is aligned
+  const void *in0, *in1, *bias;
+  int64_t ldi0, ldi1;
+  void *out[3];
+  int64_t ldo[3];
+  int *watchdog;
+};
+
+template <class T, Epi EPI>
+__global__ void __launch_bounds__(SmallCfg::THREADS, 2)
+    fused_small_kernel(const __grid_constant__ SmallMaps maps,
+                       const __grid_constant__ SmallArgs p) {
+  using G = SmallCfg;
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw_base);
+  const int bk = p.kd * G::BOX;
+  const uint32_t w_bytes = (uint32_t)(G::W_CHUNK * p.kd), x_bytes = (uint32_t)(p.nt * 128 * p.kd);
+  const uint32_t stage_bytes = w_bytes + x_bytes;
+  const uint32_t bars = base + (uint32_t)p.stages * stage_bytes;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (G::MAX_STAGES + s); };
+  const uint32_t accf_bar = bars + 8u * (2 * G::MAX_STAGES);
+  uint8_t *tail = smem + (bars - base) + 8 * (2 * G::MAX_STAGES + 1);
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
+  auto w_tile = [&](int s) { return base + (uint32_t)s * stage_bytes; };
+  auto x_tile = [&](int s) { return base + (uint32_t)s * stage_bytes + w_bytes; };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int TF = EPI == Epi::kGated ? G::TF / 2 : G::TF;  // output features of a tile
+  const int tiles_t = (p.M + p.nt - 1) / p.nt, tiles_f = (p.N + TF - 1) / TF;
+  const int tiles1 = tiles_t * tiles_f;
+  const int unit = blockIdx.x / p.splits, part = blockIdx.x % p.splits;
+  const bool second = unit >= tiles1;  // kPair: a tile of the second product
+  const int tile = second ? unit - tiles1 : unit;
+  const int f0 = (tile / tiles_t) * TF, t0 = (tile % tiles_t) * p.nt;
+  const bool sum = EPI == Epi::kLinear && p.dual == (int)Dual::kSum;
+  const int kb1 = (p.K + bk - 1) / bk;
+  const int kblocks = sum ? 2 * kb1 : kb1;
+  const int per = (kblocks + p.splits - 1) / p.splits;
+  const int kb_begin = min(kblocks, part * per), kb_end = min(kblocks, part * per + per);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(accf_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0 && p.K > 0) {
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.x);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // set-up done; the previous kernel on the stream has completed
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_try_wait(empty_bar(stage), phase ^ 1u) &&
+            (*abort_flag || !mbar_wait(empty_bar(stage), phase ^ 1u))) {
+          if (!*abort_flag) watchdog_trip(p.watchdog, kSite4ProducerEmpty, abort_flag);
+          ok = false;
+          break;
+        }
+        const bool set2 = second || kb >= kb1;
+        const int k0 = (kb >= kb1 ? kb - kb1 : kb) * bk;
+        const CUtensorMap *mw = set2 ? &maps.w2 : &maps.w, *mx = set2 ? &maps.x2 : &maps.x;
+        const uint32_t fb = full_bar(stage);
+        if constexpr (kWT) {  // K-major: 64 k x features per box
+          for (int c = 0; c < p.kd; ++c) {
+            const uint32_t dst = w_tile(stage) + (uint32_t)(c * G::W_CHUNK);
+            tma_load_2d(dst, mw, fb, k0 + c * G::BOX, f0);
+            if constexpr (EPI == Epi::kGated)
+              tma_load_2d(dst + G::W_CHUNK / 2, &maps.w2, fb, k0 + c * G::BOX, f0);
+          }
+        } else {  // MN-major: 64 features x bk k per box
+          tma_load_2d(w_tile(stage), mw, fb, f0, k0);
+          if constexpr (EPI == Epi::kGated)
+            tma_load_2d(w_tile(stage) + w_bytes / 2, &maps.w2, fb, f0, k0);
+          else
+            tma_load_2d(w_tile(stage) + w_bytes / 2, mw, fb, f0 + G::BOX, k0);
+        }
+        if constexpr (kXT) {
+          for (int c = 0; c < p.nt / G::BOX; ++c)
+            tma_load_2d(x_tile(stage) + (uint32_t)(c * bk * 128), mx, fb, t0 + c * G::BOX, k0);
+        } else {
+          for (int c = 0; c < p.kd; ++c)
+            tma_load_2d(x_tile(stage) + (uint32_t)(c * p.nt * 128), mx, fb, k0 + c * G::BOX, t0);
+        }
+        mbar_arrive_expect_tx(fb, stage_bytes);  // announced after the copies are issued
+        ++issued;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {  // no TMA write lands after this CTA has left
+        int s = stage;
+        uint32_t ph = phase;
+        const int n = issued < p.stages ? issued : p.stages;
+        for (int i = 0; i < n; ++i) {
+          if (--s < 0) {
+            s = p.stages - 1;
+            ph ^= 1u;
+          }
+          if (!mbar_wait(full_bar(s), ph)) atomicCAS(p.watchdog, 0, kSite4ProducerDrain);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const uint32_t w_box = kWT ? (uint32_t)G::W_CHUNK : w_bytes / 2;
+      const uint32_t x_box = kXT ? (uint32_t)(bk * 128) : (uint32_t)(p.nt * 128);
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_try_wait(full_bar(stage), phase) &&
+            (*abort_flag || !mbar_wait(full_bar(stage), phase))) {
+          if (!*abort_flag) watchdog_trip(p.watchdog, kSite4MmaFull, abort_flag);
+          break;
+        }
+        tc_fence_after();
+        for (int h = 0; h < p.kd; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int k = 4 * h + q;
+            umma_f16(tmem_base, operand_desc<G, !kWT>(w_tile(stage), k, w_box),
+                     operand_desc<G, kXT>(x_tile(stage), k, x_box), p.idesc,
+                     (kb > kb_begin || k > 0) ? 1u : 0u);
+          }
+        umma_commit(empty_bar(stage));
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      umma_commit(accf_bar);  // every MMA issued above has completed
+      if (!mbar_wait(accf_bar, 0)) atomicCAS(p.watchdog, 0, kSite4MmaDrain);
+    }
+  } else {
+    // ------------------------------- drain: partial tile to shared memory
+    const int quarter = warp & 3;
+    const bool ok = !*abort_flag && mbar_wait(accf_bar, 0);
+    if (!ok && lane == 0 && !*abort_flag) watchdog_trip(p.watchdog, kSite4DrainAccFull, abort_flag);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      // Every MMA has completed, so the stage area is idle: partial[t][f]
+      float *col = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
+      const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16);
+      const int live = min(p.nt, p.M - t0);
+      for (int c0 = 0; c0 < live; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(t_row + (uint32_t)c0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          col[(c0 + j) * G::TF] = kb_end > kb_begin ? __uint_as_float(r[j]) : 0.f;
+      }
+      tc_fence_before();
+    }
+  }
+
+  // ------------------------------------------ join the parts, finish, store
+  // Every thread of every CTA of the cluster gets here, also after a bounded
+  // wait gave up.
+  __syncthreads();
+  if (p.splits > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
+  bool aborted = false;
+  for (int s = 0; s < p.splits; ++s)
+    aborted |= ld_cluster_s32(mapa_shared(smem_u32(const_cast<int *>(abort_flag)), (uint32_t)s)) != 0;
+  if (!aborted) {
+    const int live = min(p.nt, p.M - t0);
+    const int feats = min(TF, p.N - f0);
+    uint32_t at[G::MAX_SPLITS];
+#pragma unroll
+    for (int s = 0; s < G::MAX_SPLITS; ++s)
+      at[s] = s < p.splits ? mapa_shared(base, (uint32_t)s) : 0u;
+    auto sum4 = [&](uint32_t off) {  // parts added in K order
+      float4 v[G::MAX_SPLITS];
+#pragma unroll
+      for (int s = 0; s < G::MAX_SPLITS; ++s)
+        if (s < p.splits) v[s] = ld_cluster_f4(at[s] + off);
+      float4 r = v[0];
+#pragma unroll
+      for (int s = 1; s < G::MAX_SPLITS; ++s)
+        if (s < p.splits) r.x += v[s].x, r.y += v[s].y, r.z += v[s].z, r.w += v[s].w;
+      return r;
+    };
+    constexpr int kOuts = EPI == Epi::kLinear ? 2 : 3;
+    const bool pair_out = EPI == Epi::kLinear && p.dual == (int)Dual::kPair;
+    auto output = [&](int o, int *slot) {  // which output array result o goes to; false: none
+      *slot = pair_out ? (second ? 1 : 0) : o;
+      return !(pair_out && o) && p.out[*slot] != nullptr;
+    };
+    const T *in0 = static_cast<const T *>(p.in0), *in1 = static_cast<const T *>(p.in1);
+    const T *bias = static_cast<const T *>(p.bias);
+    const bool has_in0 = in0 != nullptr;
+    if (p.vec) {
+      constexpr int Q = TF / 8;  // threads per token
+      const int n = live * Q;
+      for (int e = part * G::THREADS + threadIdx.x; e < n; e += p.splits * G::THREADS) {
+        const int t = e / Q, f = 8 * (e % Q);
+        if (f >= feats) continue;
+        const int64_t row = t0 + t;
+        float a[8], b[8];
+        uint32_t i0[4], i1[4], w[3][4];
+        auto get = [&](const T *m, int64_t off, uint32_t (&v)[4]) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(m + off);
+          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        };
+        if (EPI != Epi::kGated && has_in0) get(in0, row * p.ldi0 + f0 + f, i0);
+        if (EPI == Epi::kGatedBwd) get(in1, row * p.ldi1 + f0 + f, i1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 v = sum4((uint32_t)((t * G::TF + f + 4 * h) * 4));
+          a[4 * h] = v.x, a[4 * h + 1] = v.y, a[4 * h + 2] = v.z, a[4 * h + 3] = v.w;
+          if constexpr (EPI == Epi::kGated) {
+            const float4 u = sum4((uint32_t)((t * G::TF + TF + f + 4 * h) * 4));
+            b[4 * h] = u.x, b[4 * h + 1] = u.y, b[4 * h + 2] = u.z, b[4 * h + 3] = u.w;
+          }
+        }
+        if (EPI == Epi::kLinear && bias != nullptr) {
+          uint32_t v[4];
+          get(bias, f0 + f, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 c = unpack2<T>(v[j]);
+            a[2 * j] += c.x, a[2 * j + 1] += c.y;
+          }
+        }
+        epilogue_row<EPI, T, 4>(p.act, has_in0, a, b, i0, i1, w[0], w[1], w[2]);
+#pragma unroll
+        for (int o = 0; o < kOuts; ++o) {
+          int slot;
+          if (output(o, &slot))
+            *reinterpret_cast<uint4 *>(static_cast<T *>(p.out[slot]) + row * p.ldo[slot] + f0 + f) =
+                make_uint4(w[o][0], w[o][1], w[o][2], w[o][3]);
+        }
+      }
+    } else {
+      const int n = live * TF;
+      for (int e = part * G::THREADS + threadIdx.x; e < n; e += p.splits * G::THREADS) {
+        const int t = e / TF, f = e % TF;
+        if (f >= feats) continue;
+        const int64_t row = t0 + t;
+        auto sum1 = [&](int ff) {
+          float r = 0.f;
+          for (int s = 0; s < p.splits; ++s) {
+            const float v = ld_cluster_f32(at[s] + (uint32_t)((t * G::TF + ff) * 4));
+            r = s ? r + v : v;
+          }
+          return r;
+        };
+        float a = sum1(f), b = 0.f, x = 0.f, y = 0.f, o[3];
+        if constexpr (EPI == Epi::kGated) b = sum1(TF + f);
+        if (EPI == Epi::kLinear && bias != nullptr) a += to_f32<T>(bias[f0 + f]);
+        if (EPI != Epi::kGated && has_in0) x = to_f32<T>(in0[row * p.ldi0 + f0 + f]);
+        if (EPI == Epi::kGatedBwd) y = to_f32<T>(in1[row * p.ldi1 + f0 + f]);
+        with_act(p.act, [&](auto c) {
+          epilogue1<EPI, decltype(c)::value>(has_in0, a, b, x, y, o[0], o[1], o[2]);
+        });
+        if constexpr (EPI != Epi::kGatedBwd) o[1] = a;
+        if constexpr (EPI == Epi::kGated) o[2] = b;
+#pragma unroll
+        for (int i = 0; i < kOuts; ++i) {
+          int slot;
+          if (output(i, &slot))
+            static_cast<T *>(p.out[slot])[row * p.ldo[slot] + f0 + f] = from_f32<T>(o[i]);
+        }
+      }
+    }
+  }
+  if (p.splits > 1) {
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while a peer may still read its partial
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------- host side
+inline bool rows_aligned(const void *p, int64_t ld) {
+  return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && ld % 8 == 0;
+}
+
+// Maps of the weights (boxes of 64 k x `w_rows` features, or 64 features x bk
+// k) and the tokens.
+bool small_maps(CUtensorMap *tw, CUtensorMap *tx, CUtensorMapDataType dt, const FusedGemm &p,
+                const void *X, int64_t ldx, const void *W, int64_t ldw, int nt, int bk, int w_rows) {
+  const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
+  const bool w = kWT ? make_map(tw, W, dt, 2, p.N, p.K, ldw, 64, w_rows, swz)
+                     : make_map(tw, W, dt, 2, p.K, p.N, ldw, 64, bk, swz);
+  const bool x = kXT ? make_map(tx, X, dt, 2, p.K, p.M, ldx, 64, bk, swz)
+                     : make_map(tx, X, dt, 2, p.M, p.K, ldx, 64, nt, swz);
+  return w && x;
+}
+
+template <class T, Epi EPI>
+cudaError_t launch_small(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+                         cudaStream_t stream) {
+  using G = SmallCfg;
+  SmallMaps maps;
+  memset(&maps, 0, sizeof maps);
+  SmallArgs a;
+  memset(&a, 0, sizeof a);
+  const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  a.nt = plan.nt, a.kd = plan.kd, a.splits = plan.splits;
+  const int bk = 64 * plan.kd;
+  if (p.K > 0) {
+    const int w_rows = EPI == Epi::kGated ? G::TF / 2 : G::TF;
+    if (!small_maps(&maps.w, &maps.x, dt, p, p.A, p.lda, p.B, p.ldb, plan.nt, bk, w_rows))
+      return cudaErrorInvalidValue;
+    if (p.dual != Dual::kNone) {
+      const bool gated = p.dual == Dual::kGated;
+      if (!small_maps(&maps.w2, &maps.x2, dt, p, gated ? p.A : p.A2, gated ? p.lda : p.lda2, p.B2,
+                      p.ldb2, plan.nt, bk, w_rows))
+        return cudaErrorInvalidValue;
+    }
+  }
+  const int stage_bytes = (G::W_CHUNK + plan.nt * 128) * plan.kd;
+  const int budget = plan.nt <= 128 ? G::BUDGET2 : G::BUDGET1;
+  a.stages = budget / stage_bytes;
+  if (a.stages > G::MAX_STAGES) a.stages = G::MAX_STAGES;
+  // the parked partial tile takes the stages' place
+  if (a.stages < 2 || a.stages * stage_bytes < plan.nt * G::TF * 4) return cudaErrorInvalidValue;
+  const int smem = a.stages * stage_bytes + G::TAIL_BYTES;
+  const uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
+  a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kWT ? 0u : 1u) << 15) |
+            ((kXT ? 1u : 0u) << 16) | ((uint32_t)(plan.nt >> 3) << 17) |
+            ((uint32_t)(G::TF >> 4) << 24);
+  a.tmem_cols = 32;
+  while ((int)a.tmem_cols < plan.nt) a.tmem_cols *= 2;
+  a.M = p.M, a.N = p.N, a.K = p.K;
+  a.dual = (int)p.dual, a.act = p.act;
+  a.in0 = p.in0, a.in1 = p.in1, a.bias = p.bias;
+  a.ldi0 = p.ldi0, a.ldi1 = p.ldi1;
+  a.out[0] = p.out0, a.out[1] = p.out1, a.out[2] = p.out2;
+  a.ldo[0] = p.ldo0, a.ldo[1] = p.ldo1, a.ldo[2] = p.ldo2;
+  a.vec = p.N % 8 == 0 && rows_aligned(p.in0, p.in0 ? p.ldi0 : 0) &&
+          rows_aligned(p.in1, p.in1 ? p.ldi1 : 0) && rows_aligned(p.bias, 0);
+  for (int i = 0; i < 3; ++i) a.vec = a.vec && rows_aligned(a.out[i], a.out[i] ? a.ldo[i] : 0);
+  a.watchdog = watchdog;
+  auto kern = fused_small_kernel<T, EPI>;
+  static std::atomic<bool> attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             G::BUDGET1 + G::TAIL_BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  const int tf = EPI == Epi::kGated ? G::TF / 2 : G::TF;
+  const int64_t tiles = (int64_t)((p.M + plan.nt - 1) / plan.nt) * ((p.N + tf - 1) / tf) *
+                        (p.dual == Dual::kPair ? 2 : 1);
+  if (tiles * plan.splits > 0x3fffffff) return cudaErrorInvalidValue;
+  e = launch_kernel(kern, dim3((unsigned)(tiles * plan.splits)), dim3(G::THREADS), (size_t)smem,
+                    stream, (unsigned)plan.splits, maps, a);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+template <class T>
+cudaError_t launch_epi(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+                       cudaStream_t stream) {
+  if (p.epi == Epi::kLinear) return launch_small<T, Epi::kLinear>(p, plan, watchdog, stream);
+  if constexpr (!kXT) {  // the gated epilogues' tokens are activations, M x K
+    if (p.epi == Epi::kGated) return launch_small<T, Epi::kGated>(p, plan, watchdog, stream);
+    return launch_small<T, Epi::kGatedBwd>(p, plan, watchdog, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t DG_UNIT_LAUNCHER(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+                             cudaStream_t stream) {
+  return p.dtype == DGEMM_DTYPE_BF16 ? launch_epi<__nv_bfloat16>(p, plan, watchdog, stream)
+                                     : launch_epi<__half>(p, plan, watchdog, stream);
+}
+
+}  // namespace dg

@@ -54,6 +54,19 @@ cudaError_t launch_fused_pair_unit_0(const FusedGemm &p, int *watchdog, cudaStre
 cudaError_t launch_fused_pair_unit_1(const FusedGemm &p, int *watchdog, cudaStream_t stream);
 cudaError_t launch_fused_pair_unit_2(const FusedGemm &p, int *watchdog, cudaStream_t stream);
 
+// How fused_small.cu cuts a product: token columns of a tile (a multiple of
+// 16, of 64 when A is stored K x M; at most 256), 64-element rows of K per
+// stage (1 or 2), CTAs that share a tile's K range (1 to 8).
+struct SmallPlan {
+  int nt, kd, splits;
+};
+cudaError_t launch_fused_small_unit_0(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+                                      cudaStream_t stream);
+cudaError_t launch_fused_small_unit_1(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+                                      cudaStream_t stream);
+cudaError_t launch_fused_small_unit_2(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+                                      cudaStream_t stream);
+
 // dZ = dD act'(Z) (act != none; else dZ is not written) and, where dbias is
 // not null, dbias[j] = sum_i dZ[i][j] in fp32, rounded once.  `partial` is
 // fp32 scratch of act_grad_scratch() bytes.
