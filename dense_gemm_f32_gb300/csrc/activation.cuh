@@ -1,8 +1,12 @@
 // activation.cuh -- element types and activation functions of the
 // feed-forward operators (norm.cu, rowops.cu, the fused GEMM epilogues).
 //
-// Every activation and derivative is evaluated in fp32 with CUDA's own math
-// functions; only the store of a result rounds to 16 bits.
+// Every activation and derivative is evaluated in fp32 (errors of a few 2^-23,
+// far below the 2^-8 or 2^-11 that the store of a result rounds away); only
+// that store rounds to 16 bits.  The special-function unit's 2^x and 1/x
+// without subnormals are 4 instructions per sigmoid against 14 with CUDA's
+// subnormal-safe forms, which made the epilogue of a 16384 x 14336 x 4096
+// gelu_tanh layer as long as its main loop.
 #pragma once
 
 #include <cstdint>
@@ -75,11 +79,26 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return w;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// 1 / (1 + exp(-t)): exp(-t) overflows to infinity for t < -88, giving 0.
-__device__ __forceinline__ float sigmoid_f32(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
+// 2^x and 1/x by the special-function unit (about 2 units in the last place,
+// subnormals to zero).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 1 / (1 + 2^-t), the sigmoid of t / log2(e): 2^-t overflows to infinity for
+// t < -128, giving 0.
+__device__ __forceinline__ float sigmoid2(float t) { return rcp_approx(1.f + exp2_approx(-t)); }
 
 // act(z):
 //   relu       max(z, 0)
@@ -91,8 +110,8 @@ __device__ __forceinline__ float act_f32(float z) {
   if constexpr (ACT == DGEMM_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays a NaN
   if constexpr (ACT == DGEMM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
   if constexpr (ACT == DGEMM_ACT_GELU_TANH)
-    return z * sigmoid_f32(2.f * kGeluA * (z + kGeluB * z * z * z));
-  if constexpr (ACT == DGEMM_ACT_SILU) return z * sigmoid_f32(z);
+    return z * sigmoid2(z * fmaf(2.f * kGeluA * kGeluB * kLog2e, z * z, 2.f * kGeluA * kLog2e));
+  if constexpr (ACT == DGEMM_ACT_SILU) return z * sigmoid2(kLog2e * z);
   return z;
 }
 
@@ -105,15 +124,16 @@ __device__ __forceinline__ void act_grad_f32(float z, float &value, float &slope
   } else if constexpr (ACT == DGEMM_ACT_GELU) {
     const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
     value = z * cdf;
-    slope = cdf + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    slope = cdf + z * 0.3989422804014327f * exp2_approx(-0.5f * kLog2e * z * z);
   } else if constexpr (ACT == DGEMM_ACT_GELU_TANH) {
-    const float s = sigmoid_f32(2.f * kGeluA * (z + kGeluB * z * z * z));
+    const float z2 = z * z;
+    const float s = sigmoid2(z * fmaf(2.f * kGeluA * kGeluB * kLog2e, z2, 2.f * kGeluA * kLog2e));
     value = z * s;
-    slope = s + z * s * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z);
+    slope = fmaf(value * (1.f - s), fmaf(6.f * kGeluA * kGeluB, z2, 2.f * kGeluA), s);
   } else if constexpr (ACT == DGEMM_ACT_SILU) {
-    const float s = sigmoid_f32(z);
+    const float s = sigmoid2(kLog2e * z);
     value = z * s;
-    slope = s * (1.f + z * (1.f - s));
+    slope = fmaf(value, 1.f - s, s);
   } else {
     value = z;
     slope = 1.f;

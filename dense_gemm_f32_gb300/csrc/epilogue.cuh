@@ -53,12 +53,14 @@ __device__ __forceinline__ void epilogue1(bool has_in0, float a, float b, float 
 // 2 N consecutive elements; packed inputs i0 and i1, packed results w0, w1, w2:
 // kLinear D, Z; kGated H, G, U; kGatedBwd dG, dU, H.  Everything is fp32 until
 // the one rounding of each packed result.
+// kept: whether Z (G and U) are wanted at all.
 template <Epi EPI, class T, int N>
-__device__ __forceinline__ void epilogue_row(int act, bool has_in0, const float (&a)[2 * N],
+__device__ __forceinline__ void epilogue_row(int act, bool has_in0, bool kept,
+                                             const float (&a)[2 * N],
                                              const float (&b)[2 * N], const uint32_t (&i0)[N],
                                              const uint32_t (&i1)[N], uint32_t (&w0)[N],
                                              uint32_t (&w1)[N], uint32_t (&w2)[N]) {
-  if constexpr (EPI != Epi::kGatedBwd) {
+  if (EPI != Epi::kGatedBwd && kept) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       w1[j] = pack2<T>(a[2 * j], a[2 * j + 1]);

@@ -11,57 +11,6 @@
 namespace dg {
 namespace {
 
-// Re-pitched copies of operands whose rows do not start on 16-byte
-// boundaries, in stream-ordered scratch that lives until the product has run.
-// An operand given twice is staged once.
-struct Staging {
-  struct Item {
-    const void **p;
-    int64_t *ld;
-    int rows, cols;
-  };
-  Item items[4];
-  int n = 0;
-
-  void want(const void *&p, int64_t &ld, int rows, int cols) {
-    if (p == nullptr || rows == 0 || cols == 0 || tma_ok(p, ld, 2)) return;
-    items[n++] = {&p, &ld, rows, cols};
-  }
-
-  cudaError_t run(void **scratch, int num_sms, cudaStream_t stream) {
-    *scratch = nullptr;
-    if (n == 0) return cudaSuccess;
-    int owner[4];
-    size_t at[4], total = 0;
-    for (int i = 0; i < n; ++i) {
-      owner[i] = i;
-      for (int j = 0; j < i; ++j)
-        if (*items[j].p == *items[i].p && *items[j].ld == *items[i].ld) owner[i] = j;
-      at[i] = total;
-      if (owner[i] == i)
-        total += (size_t)((int64_t)items[i].rows * pitch(items[i].cols) * 2 + 255) / 256 * 256;
-    }
-    cudaError_t e = scratch_alloc(scratch, total, stream);
-    if (e != cudaSuccess) return e;
-    char *s = static_cast<char *>(*scratch);
-    StageJob jobs[4];
-    int njobs = 0;
-    for (int i = 0; i < n; ++i)
-      if (owner[i] == i)
-        jobs[njobs++] = {*items[i].p, *items[i].ld, s + at[i], pitch(items[i].cols),
-                         items[i].rows, items[i].cols, false};
-    for (int j = 0; j < njobs && e == cudaSuccess; j += 2)
-      e = launch_stage(jobs + j, njobs - j < 2 ? njobs - j : 2, 2, num_sms, stream);
-    for (int i = 0; i < n; ++i) {
-      *items[i].p = s + at[owner[i]];
-      *items[i].ld = pitch(items[i].cols);
-    }
-    return e;
-  }
-
-  static int64_t pitch(int cols) { return (cols + 7) / 8 * 8; }
-};
-
 // DGEMM_FUSED_*: an environment variable's value in lo .. hi, or -1 (read at
 // every launch, for tests and tuning).
 int knob(const char *name, int lo, int hi) {
@@ -75,6 +24,7 @@ int knob(const char *name, int lo, int hi) {
 // of the SMs and more than one 256-column tile of tokens is there to fill
 // them.  DGEMM_FUSED_PAIR=0 / =1 forces the choice.
 bool use_pair(const FusedGemm &p, int num_sms) {
+  if (p.K == 0) return false;  // the small kernel takes an empty sum
   const int force = knob("DGEMM_FUSED_PAIR", 0, 1);
   if (force >= 0) return force == 1;
   if (p.M <= 256) return false;
@@ -114,15 +64,14 @@ cudaError_t launch_fused(const FusedGemm &p0, int num_sms, cudaStream_t stream) 
   FusedGemm p = p0;
   int *wd = watchdog_address();
   if (wd == nullptr) return cudaErrorInvalidSymbol;
-  Staging st;
+  Stager st(num_sms, stream);
   const int ar = p.a_t ? p.K : p.M, ac = p.a_t ? p.M : p.K;
   const int br = p.b_t ? p.N : p.K, bc = p.b_t ? p.K : p.N;
-  st.want(p.A, p.lda, ar, ac);
-  st.want(p.B, p.ldb, br, bc);
-  if (p.dual == Dual::kSum || p.dual == Dual::kPair) st.want(p.A2, p.lda2, ar, ac);
-  if (p.dual != Dual::kNone) st.want(p.B2, p.ldb2, br, bc);
-  void *scratch = nullptr;
-  cudaError_t e = st.run(&scratch, num_sms, stream);
+  st.add(p.A, p.lda, ar, ac);
+  st.add(p.B, p.ldb, br, bc);
+  if (p.dual == Dual::kSum || p.dual == Dual::kPair) st.add(p.A2, p.lda2, ar, ac);
+  if (p.dual != Dual::kNone) st.add(p.B2, p.ldb2, br, bc);
+  cudaError_t e = st.run();
   if (e == cudaSuccess) {
     const int unit = p.a_t ? 2 : p.b_t ? 1 : 0;
     if (p.a_t && p.b_t) {
@@ -138,11 +87,54 @@ cudaError_t launch_fused(const FusedGemm &p0, int num_sms, cudaStream_t stream) 
                       : launch_fused_small_unit_2(p, plan, wd, stream);
     }
   }
-  if (scratch != nullptr) {
-    const cudaError_t e2 = scratch_free(scratch, stream);
-    if (e == cudaSuccess) e = e2;
+  const cudaError_t e2 = st.release();
+  return e == cudaSuccess ? e2 : e;
+}
+
+// ------------------------------------------------------------------ Stager
+void Stager::add(const void *&p, int64_t &ld, int64_t rows, int64_t cols) {
+  if (p == nullptr || rows == 0 || cols == 0 || tma_ok(p, ld, 2) || n_ == kMax) return;
+  items_[n_++] = {&p, &ld, rows, cols};
+}
+
+cudaError_t Stager::run() {
+  if (n_ == 0) return cudaSuccess;
+  const int n = n_;
+  n_ = 0;
+  RepitchJob jobs[kMax];
+  int njobs = 0, job_of[kMax];
+  size_t at[kMax], total = 0;
+  for (int i = 0; i < n; ++i) {
+    const Item &x = items_[i];
+    int j = 0;
+    while (j < njobs && !(jobs[j].src == *x.p && jobs[j].lds == *x.ld && jobs[j].rows == x.rows &&
+                          jobs[j].cols == x.cols))
+      ++j;
+    job_of[i] = j;
+    if (j < njobs) continue;  // given twice, staged once
+    const int64_t pitch = (x.cols + 7) / 8 * 8;
+    jobs[njobs++] = {*x.p, *x.ld, nullptr, pitch, x.rows, x.cols};
+    at[j] = total;
+    total += (size_t)(x.rows * pitch * 2 + 255) / 256 * 256;
   }
-  return e;
+  cudaError_t e = scratch_alloc(&scratch_, total, stream_);
+  if (e != cudaSuccess) {
+    scratch_ = nullptr;
+    return e;
+  }
+  for (int j = 0; j < njobs; ++j) jobs[j].dst = static_cast<char *>(scratch_) + at[j];
+  for (int i = 0; i < n; ++i) {
+    *items_[i].p = jobs[job_of[i]].dst;
+    *items_[i].ld = jobs[job_of[i]].ldd;
+  }
+  return launch_repitch(jobs, njobs, num_sms_, stream_);
+}
+
+cudaError_t Stager::release() {
+  if (scratch_ == nullptr) return cudaSuccess;
+  void *s = scratch_;
+  scratch_ = nullptr;
+  return scratch_free(s, stream_);
 }
 
 }  // namespace dg

@@ -1,5 +1,6 @@
 // fused_pair.cu -- the fused products of the feed-forward operators on CTA
-// pairs (tcgen05.mma.cta_group::2), for outputs of many 256 x 256 tiles.
+// pairs (tcgen05.mma.cta_group::2), for outputs of many 256 x 256 tiles and
+// K > 0.
 //
 // The main loop is that of tc.cu's pair kernel: a cluster of two CTAs
 // accumulates 256 x 256 in the two SMs' tensor memory, CTA r holding rows
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0 && p.K > 0) {
+  if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b);
   }
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
     const uint32_t slots = epi_base + (uint32_t)((warp - 2) * 2 * G::PIECE_BYTES);
     const uint32_t acce_leader0 = mapa_shared(acce_bar(0), 0);
     const uint32_t acce_leader1 = mapa_shared(acce_bar(1), 0);
+    const bool kept = !pair_out && p.out[1] != nullptr;
     int stores = 0;  // pieces staged by this warp
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -334,16 +336,14 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
         }
         float a[32], b[32];
         {
-          uint32_t r[32];
+          uint32_t r[32], q[32];
           tmem_ld_32x32b_x32(t_row + (uint32_t)c0, r);
+          if constexpr (EPI == Epi::kGated) tmem_ld_32x32b_x32(t_row + (uint32_t)(G::HN + c0), q);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) a[j] = kblocks ? __uint_as_float(r[j]) : 0.f;
-          if constexpr (EPI == Epi::kGated) {
-            tmem_ld_32x32b_x32(t_row + (uint32_t)(G::HN + c0), r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) b[j] = kblocks ? __uint_as_float(r[j]) : 0.f;
+          for (int j = 0; j < 32; ++j) {
+            a[j] = __uint_as_float(r[j]);
+            if constexpr (EPI == Epi::kGated) b[j] = __uint_as_float(q[j]);
           }
         }
         if (EPI == Epi::kLinear && p.bias != nullptr) {
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
           }
         }
         uint32_t w[3][16];
-        epilogue_row<EPI, T, 16>(p.act, has_in0, a, b, i0, i1, w[0], w[1], w[2]);
+        epilogue_row<EPI, T, 16>(p.act, has_in0, kept, a, b, i0, i1, w[0], w[1], w[2]);
         constexpr int kOuts = EPI == Epi::kLinear ? 2 : 3;
 #pragma unroll
         for (int o = 0; o < kOuts; ++o) {
@@ -468,17 +468,15 @@ cudaError_t launch_pair(const FusedGemm &p, int *watchdog, cudaStream_t stream) 
   memset(&maps, 0, sizeof maps);
   PairArgs a;
   memset(&a, 0, sizeof a);
-  if (p.K > 0) {
-    if (!pair_operand_maps<T>(&maps.a, &maps.b, p, p.A, p.lda, p.B, p.ldb, &a.mn3d))
+  if (!pair_operand_maps<T>(&maps.a, &maps.b, p, p.A, p.lda, p.B, p.ldb, &a.mn3d))
+    return cudaErrorInvalidValue;
+  if (p.dual != Dual::kNone) {
+    int mn3d2 = 0;
+    const bool gated = p.dual == Dual::kGated;
+    if (!pair_operand_maps<T>(&maps.a2, &maps.b2, p, gated ? p.A : p.A2, gated ? p.lda : p.lda2,
+                              p.B2, p.ldb2, &mn3d2) ||
+        mn3d2 != a.mn3d)
       return cudaErrorInvalidValue;
-    if (p.dual != Dual::kNone) {
-      int mn3d2 = 0;
-      const bool gated = p.dual == Dual::kGated;
-      if (!pair_operand_maps<T>(&maps.a2, &maps.b2, p, gated ? p.A : p.A2, gated ? p.lda : p.lda2,
-                                p.B2, p.ldb2, &mn3d2) ||
-          mn3d2 != a.mn3d)
-        return cudaErrorInvalidValue;
-    }
   }
   a.M = p.M, a.N = p.N, a.K = p.K;
   a.dual = (int)p.dual, a.act = p.act;

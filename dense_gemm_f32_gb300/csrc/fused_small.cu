@@ -15,8 +15,8 @@
 //    token, and the cluster's CTAs add the partials through distributed shared
 //    memory in part order, each finishing a share of the tile's elements: the
 //    epilogue (epilogue.cuh) runs once per element, on 8 neighbouring features
-//    of a token per thread with 16-byte accesses, or one feature per thread
-//    where a row is not 16-byte aligned.
+//    of a token per thread, 16 bytes per access also where rows are not
+//    aligned (rowvec.cuh).
 //  * kGated: the tile's 128 rows are 64 features of Wg and the same 64 of Wu,
 //    so one MMA stream gives both projections of a hidden unit in one tile.
 //  * Every wait is bounded (ptx.cuh).
@@ -31,6 +31,7 @@
 #include "launch.cuh"
 #include "ops.h"
 #include "ptx.cuh"
+#include "rowvec.cuh"
 #include "tc_tile.cuh"
 #include "tmap.cuh"
 
@@ -297,81 +298,59 @@ __global__ void __launch_bounds__(SmallCfg::THREADS, 2)
     };
     const T *in0 = static_cast<const T *>(p.in0), *in1 = static_cast<const T *>(p.in1);
     const T *bias = static_cast<const T *>(p.bias);
-    const bool has_in0 = in0 != nullptr;
-    if (p.vec) {
-      constexpr int Q = TF / 8;  // threads per token
-      const int n = live * Q;
-      for (int e = part * G::THREADS + threadIdx.x; e < n; e += p.splits * G::THREADS) {
-        const int t = e / Q, f = 8 * (e % Q);
-        if (f >= feats) continue;
+    const bool has_in0 = in0 != nullptr, kept = !pair_out && p.out[1] != nullptr;
+    constexpr int Q = TF / 8;  // threads per token
+    auto finish = [&](auto aligned) {
+      constexpr bool AL = decltype(aligned)::value;
+      const int n = live * Q, end = f0 + feats;
+      // whole warps go round together: their stores put blocks together
+      for (int e = part * G::THREADS + threadIdx.x; e - lane < n; e += p.splits * G::THREADS) {
+        const int t = e / Q, f = 8 * (e % Q), col = f0 + f;
+        const bool in = t < live && f < feats;
         const int64_t row = t0 + t;
         float a[8], b[8];
         uint32_t i0[4], i1[4], w[3][4];
-        auto get = [&](const T *m, int64_t off, uint32_t (&v)[4]) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(m + off);
+        auto get = [&](const T *m, uint32_t (&v)[4]) {
+          const uint4 x = load_row16<T, AL>(m, col, end);
           v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
         };
-        if (EPI != Epi::kGated && has_in0) get(in0, row * p.ldi0 + f0 + f, i0);
-        if (EPI == Epi::kGatedBwd) get(in1, row * p.ldi1 + f0 + f, i1);
+        if (in) {
+          if (EPI != Epi::kGated && has_in0) get(in0 + row * p.ldi0, i0);
+          if (EPI == Epi::kGatedBwd) get(in1 + row * p.ldi1, i1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 v = sum4((uint32_t)((t * G::TF + f + 4 * h) * 4));
-          a[4 * h] = v.x, a[4 * h + 1] = v.y, a[4 * h + 2] = v.z, a[4 * h + 3] = v.w;
-          if constexpr (EPI == Epi::kGated) {
-            const float4 u = sum4((uint32_t)((t * G::TF + TF + f + 4 * h) * 4));
-            b[4 * h] = u.x, b[4 * h + 1] = u.y, b[4 * h + 2] = u.z, b[4 * h + 3] = u.w;
+          for (int h = 0; h < 2; ++h) {
+            const float4 v = sum4((uint32_t)((t * G::TF + f + 4 * h) * 4));
+            a[4 * h] = v.x, a[4 * h + 1] = v.y, a[4 * h + 2] = v.z, a[4 * h + 3] = v.w;
+            if constexpr (EPI == Epi::kGated) {
+              const float4 u = sum4((uint32_t)((t * G::TF + TF + f + 4 * h) * 4));
+              b[4 * h] = u.x, b[4 * h + 1] = u.y, b[4 * h + 2] = u.z, b[4 * h + 3] = u.w;
+            }
           }
-        }
-        if (EPI == Epi::kLinear && bias != nullptr) {
-          uint32_t v[4];
-          get(bias, f0 + f, v);
+          if (EPI == Epi::kLinear && bias != nullptr) {
+            uint32_t v[4];
+            get(bias, v);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 c = unpack2<T>(v[j]);
-            a[2 * j] += c.x, a[2 * j + 1] += c.y;
+            for (int j = 0; j < 4; ++j) {
+              const float2 c = unpack2<T>(v[j]);
+              a[2 * j] += c.x, a[2 * j + 1] += c.y;
+            }
           }
+          epilogue_row<EPI, T, 4>(p.act, has_in0, kept, a, b, i0, i1, w[0], w[1], w[2]);
         }
-        epilogue_row<EPI, T, 4>(p.act, has_in0, a, b, i0, i1, w[0], w[1], w[2]);
 #pragma unroll
         for (int o = 0; o < kOuts; ++o) {
           int slot;
           if (output(o, &slot))
-            *reinterpret_cast<uint4 *>(static_cast<T *>(p.out[slot]) + row * p.ldo[slot] + f0 + f) =
-                make_uint4(w[o][0], w[o][1], w[o][2], w[o][3]);
+            store_row16<T, AL, Q>(static_cast<T *>(p.out[slot]) + row * p.ldo[slot],
+                                  in ? col : end, end,
+                                  make_uint4(w[o][0], w[o][1], w[o][2], w[o][3]));
         }
       }
-    } else {
-      const int n = live * TF;
-      for (int e = part * G::THREADS + threadIdx.x; e < n; e += p.splits * G::THREADS) {
-        const int t = e / TF, f = e % TF;
-        if (f >= feats) continue;
-        const int64_t row = t0 + t;
-        auto sum1 = [&](int ff) {
-          float r = 0.f;
-          for (int s = 0; s < p.splits; ++s) {
-            const float v = ld_cluster_f32(at[s] + (uint32_t)((t * G::TF + ff) * 4));
-            r = s ? r + v : v;
-          }
-          return r;
-        };
-        float a = sum1(f), b = 0.f, x = 0.f, y = 0.f, o[3];
-        if constexpr (EPI == Epi::kGated) b = sum1(TF + f);
-        if (EPI == Epi::kLinear && bias != nullptr) a += to_f32<T>(bias[f0 + f]);
-        if (EPI != Epi::kGated && has_in0) x = to_f32<T>(in0[row * p.ldi0 + f0 + f]);
-        if (EPI == Epi::kGatedBwd) y = to_f32<T>(in1[row * p.ldi1 + f0 + f]);
-        with_act(p.act, [&](auto c) {
-          epilogue1<EPI, decltype(c)::value>(has_in0, a, b, x, y, o[0], o[1], o[2]);
-        });
-        if constexpr (EPI != Epi::kGatedBwd) o[1] = a;
-        if constexpr (EPI == Epi::kGated) o[2] = b;
-#pragma unroll
-        for (int i = 0; i < kOuts; ++i) {
-          int slot;
-          if (output(i, &slot))
-            static_cast<T *>(p.out[slot])[row * p.ldo[slot] + f0 + f] = from_f32<T>(o[i]);
-        }
-      }
-    }
+    };
+    if (p.vec)
+      finish(std::true_type{});
+    else
+      finish(std::false_type{});
   }
   if (p.splits > 1) {
     __syncwarp();

@@ -47,6 +47,41 @@ struct FusedGemm {
 };
 cudaError_t launch_fused(const FusedGemm &p, int num_sms, cudaStream_t stream);
 
+// A 16-bit rows x cols matrix copied to a 16-byte aligned pitch (ldd >= cols, a
+// multiple of 8), the padding zeroed.  Up to eight in one launch.
+struct RepitchJob {
+  const void *src;
+  int64_t lds;
+  void *dst;
+  int64_t ldd;
+  int64_t rows, cols;
+};
+cudaError_t launch_repitch(const RepitchJob *jobs, int njobs, int num_sms, cudaStream_t stream);
+
+// Copies of operands that TMA cannot read (rows that do not start on 16-byte
+// boundaries): add() them, run() re-pitches all of them in one launch into
+// stream-ordered scratch and points the operands there; release() after the
+// last launch that reads them.
+class Stager {
+ public:
+  Stager(int num_sms, cudaStream_t stream) : num_sms_(num_sms), stream_(stream) {}
+  void add(const void *&p, int64_t &ld, int64_t rows, int64_t cols);
+  cudaError_t run();
+  cudaError_t release();
+
+ private:
+  static constexpr int kMax = 8;
+  struct Item {
+    const void **p;
+    int64_t *ld;
+    int64_t rows, cols;
+  };
+  Item items_[kMax];
+  int n_ = 0, num_sms_;
+  cudaStream_t stream_;
+  void *scratch_ = nullptr;
+};
+
 // One operand layout each (one translation unit each): 0: A M x K, B K x N;
 // 1: A M x K, B N x K; 2: A K x M, B K x N.  Operands that TMA can read;
 // `watchdog` is the device address of the watchdog word.

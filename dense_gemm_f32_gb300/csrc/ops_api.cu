@@ -97,6 +97,12 @@ int with_scratch(size_t bytes, cudaStream_t stream, const char *what, F &&f) {
   return st;
 }
 
+// The end of a call that staged operands.
+int release(Stager &stage, int st) {
+  const cudaError_t e = stage.release();
+  return st == DGEMM_OK ? done(e, "scratch release") : st;
+}
+
 }  // namespace
 
 extern "C" {
@@ -202,27 +208,34 @@ int dgemm_linear_backward(int dtype, int activation, int op_w, int M, int N, int
                       });
     if (st != DGEMM_OK) return st;
   }
-  const void *dz = act ? dZ : dD;
-  const int lddz_use = act ? lddz : lddd;
+  // operands that TMA cannot read, all in one launch (dZ by its own product
+  // when a caller's workspace is not aligned)
+  const void *dz = act ? dZ : dD, *x = X, *w = W;
+  int64_t ldz_use = act ? lddz : lddd, ldx_use = ldx, ldw_use = ldw;
+  Stager stage(sms, stream);
+  if (!act && (want_dx || want_dw)) stage.add(dz, ldz_use, M, N);
+  if (want_dw) stage.add(x, ldx_use, M, K);
+  if (want_dx) stage.add(w, ldw_use, wr, wc);
+  if ((st = done(stage.run(), "operand staging")) != DGEMM_OK) return release(stage, st);
   if (want_dx) {  // dX (M x K) = dZ op(W)^T
     FusedGemm p;
     p.dtype = dtype;
     p.M = M, p.N = K, p.K = N;
-    p.A = dz, p.lda = lddz_use, p.B = W, p.ldb = ldw, p.b_t = !t;
+    p.A = dz, p.lda = ldz_use, p.B = w, p.ldb = ldw_use, p.b_t = !t;
     p.out0 = dX, p.ldo0 = lddx;
-    if ((st = done(launch_fused(p, sms, stream), "input gradient launch")) != DGEMM_OK) return st;
+    st = done(launch_fused(p, sms, stream), "input gradient launch");
   }
-  if (want_dw) {  // dW as W is stored: X^T dZ, or its transpose dZ^T X
+  if (st == DGEMM_OK && want_dw) {  // dW as W is stored: X^T dZ, or its transpose dZ^T X
     FusedGemm p;
     p.dtype = dtype;
     p.M = wr, p.N = wc, p.K = M;
     p.a_t = true;
-    p.A = t ? dz : X, p.lda = t ? lddz_use : ldx;
-    p.B = t ? X : dz, p.ldb = t ? ldx : lddz_use;
+    p.A = t ? dz : x, p.lda = t ? ldz_use : ldx_use;
+    p.B = t ? x : dz, p.ldb = t ? ldx_use : ldz_use;
     p.out0 = dW, p.ldo0 = lddw;
-    if ((st = done(launch_fused(p, sms, stream), "weight gradient launch")) != DGEMM_OK) return st;
+    st = done(launch_fused(p, sms, stream), "weight gradient launch");
   }
-  return DGEMM_OK;
+  return release(stage, st);
 }
 
 int dgemm_gated_ffn(int dtype, int activation, int op_w, int M, int D, int F, const void *X,
@@ -242,25 +255,35 @@ int dgemm_gated_ffn(int dtype, int activation, int op_w, int M, int D, int F, co
   int dev = 0, sms = 0;
   int st = check_args(a, 9, 8, 4, &dev, &sms);  // Y may be R itself
   if (st != DGEMM_OK) return st;
+  const void *x = X, *wg = Wg, *wu = Wu, *wd = Wd;
+  int64_t lx = ldx, lg = ldwg, lu = ldwu, ld = ldwd;
+  Stager stage(sms, stream);  // operands that TMA cannot read, in one launch
+  if (F > 0) {
+    stage.add(x, lx, M, D);
+    stage.add(wg, lg, ur, uc);
+    stage.add(wu, lu, ur, uc);
+    if (D > 0) stage.add(wd, ld, uc, ur);
+  }
+  if ((st = done(stage.run(), "operand staging")) != DGEMM_OK) return release(stage, st);
   if (F > 0) {
     FusedGemm p;
     p.epi = Epi::kGated, p.dual = Dual::kGated;
     p.dtype = dtype, p.act = activation;
     p.M = M, p.N = F, p.K = D;
-    p.A = X, p.lda = ldx, p.b_t = t;
-    p.B = Wg, p.ldb = ldwg, p.B2 = Wu, p.ldb2 = ldwu;
+    p.A = x, p.lda = lx, p.b_t = t;
+    p.B = wg, p.ldb = lg, p.B2 = wu, p.ldb2 = lu;
     p.out0 = H, p.ldo0 = ldh, p.out1 = G, p.ldo1 = ldg, p.out2 = U, p.ldo2 = ldu;
-    if ((st = done(launch_fused(p, sms, stream), "gated product launch")) != DGEMM_OK) return st;
+    st = done(launch_fused(p, sms, stream), "gated product launch");
   }
-  if (D > 0) {
+  if (st == DGEMM_OK && D > 0) {
     FusedGemm p;
     p.dtype = dtype;
     p.M = M, p.N = D, p.K = F;
-    p.A = H, p.lda = ldh, p.B = Wd, p.ldb = ldwd, p.b_t = t;
+    p.A = H, p.lda = ldh, p.B = wd, p.ldb = ld, p.b_t = t;
     p.in0 = R, p.ldi0 = ldr, p.out0 = Y, p.ldo0 = ldy;
-    return done(launch_fused(p, sms, stream), "down product launch");
+    st = done(launch_fused(p, sms, stream), "down product launch");
   }
-  return DGEMM_OK;
+  return release(stage, st);
 }
 
 int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, int F,
@@ -287,47 +310,60 @@ int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, 
   int dev = 0, sms = 0;
   int st = check_args(a, 14, -1, -1, &dev, &sms);
   if (st != DGEMM_OK) return st;
+  const void *dy = dY, *x = X, *wg = Wg, *wu = Wu, *wd = Wd;
+  int64_t ly = lddy, lx = ldx, lg = ldwg, lu = ldwu, ld = ldwd;
+  Stager stage(sms, stream);  // operands that TMA cannot read, in one launch
+  if (M > 0 && F > 0) {
+    stage.add(dy, ly, M, D);
+    stage.add(wd, ld, uc, ur);
+    if (want_up) stage.add(x, lx, M, D);
+    if (want_dx) {
+      stage.add(wg, lg, ur, uc);
+      stage.add(wu, lu, ur, uc);
+    }
+  }
+  if ((st = done(stage.run(), "operand staging")) != DGEMM_OK) return release(stage, st);
   if (M > 0 && F > 0) {  // dh = dY op(Wd)^T in the accumulator -> dG, dU, H
     FusedGemm p;
     p.epi = Epi::kGatedBwd;
     p.dtype = dtype, p.act = activation;
     p.M = M, p.N = F, p.K = D;
-    p.A = dY, p.lda = lddy, p.B = Wd, p.ldb = ldwd, p.b_t = !t;
+    p.A = dy, p.lda = ly, p.B = wd, p.ldb = ld, p.b_t = !t;
     p.in0 = G, p.ldi0 = ldg, p.in1 = U, p.ldi1 = ldu;
     p.out0 = dG, p.ldo0 = lddg, p.out1 = dU, p.ldo1 = lddu, p.out2 = H, p.ldo2 = ldh;
-    if ((st = done(launch_fused(p, sms, stream), "gate gradient launch")) != DGEMM_OK) return st;
+    st = done(launch_fused(p, sms, stream), "gate gradient launch");
   }
-  if (want_dx) {  // dX = dG op(Wg)^T + dU op(Wu)^T
+  if (st == DGEMM_OK && want_dx) {  // dX = dG op(Wg)^T + dU op(Wu)^T
     FusedGemm p;
     p.dual = Dual::kSum;
     p.dtype = dtype;
     p.M = M, p.N = D, p.K = F;
     p.A = dG, p.lda = lddg, p.A2 = dU, p.lda2 = lddu, p.b_t = !t;
-    p.B = Wg, p.ldb = ldwg, p.B2 = Wu, p.ldb2 = ldwu;
+    p.B = wg, p.ldb = lg, p.B2 = wu, p.ldb2 = lu;
     p.out0 = dX, p.ldo0 = lddx;
-    if ((st = done(launch_fused(p, sms, stream), "input gradient launch")) != DGEMM_OK) return st;
+    st = done(launch_fused(p, sms, stream), "input gradient launch");
   }
-  if (want_up) {  // dWg, dWu as stored: X^T dG and X^T dU, or their transposes
+  if (st == DGEMM_OK && want_up) {  // dWg, dWu as stored: X^T dG, X^T dU, or transposed
     FusedGemm p;
     p.dual = Dual::kPair;
     p.dtype = dtype;
     p.M = ur, p.N = uc, p.K = M;
     p.a_t = true;
-    p.A = t ? dG : X, p.lda = t ? lddg : ldx, p.A2 = t ? dU : X, p.lda2 = t ? lddu : ldx;
-    p.B = t ? X : dG, p.ldb = t ? ldx : lddg, p.B2 = t ? X : dU, p.ldb2 = t ? ldx : lddu;
+    p.A = t ? dG : x, p.lda = t ? lddg : lx, p.A2 = t ? dU : x, p.lda2 = t ? lddu : lx;
+    p.B = t ? x : dG, p.ldb = t ? lx : lddg, p.B2 = t ? x : dU, p.ldb2 = t ? lx : lddu;
     p.out0 = dWg, p.ldo0 = lddwg, p.out1 = dWu, p.ldo1 = lddwu;
-    if ((st = done(launch_fused(p, sms, stream), "weight gradient launch")) != DGEMM_OK) return st;
+    st = done(launch_fused(p, sms, stream), "weight gradient launch");
   }
-  if (want_down) {  // dWd as stored: H^T dY, or its transpose
+  if (st == DGEMM_OK && want_down) {  // dWd as stored: H^T dY, or its transpose
     FusedGemm p;
     p.dtype = dtype;
     p.M = uc, p.N = ur, p.K = M;
     p.a_t = true;
-    p.A = t ? dY : H, p.lda = t ? lddy : ldh, p.B = t ? H : dY, p.ldb = t ? ldh : lddy;
+    p.A = t ? dy : H, p.lda = t ? ly : ldh, p.B = t ? H : dy, p.ldb = t ? ldh : ly;
     p.out0 = dWd, p.ldo0 = lddwd;
-    if ((st = done(launch_fused(p, sms, stream), "weight gradient launch")) != DGEMM_OK) return st;
+    st = done(launch_fused(p, sms, stream), "weight gradient launch");
   }
-  return DGEMM_OK;
+  return release(stage, st);
 }
 
 }  // extern "C"

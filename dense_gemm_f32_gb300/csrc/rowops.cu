@@ -1,8 +1,9 @@
 // rowops.cu -- the element-wise half of a linear layer's backward pass,
-// dZ = dD act'(Z), with the bias gradient's column sums in the same pass, and
-// the join of column sums that several blocks hold parts of.
+// dZ = dD act'(Z), with the bias gradient's column sums in the same pass, the
+// join of column sums that several blocks hold parts of, and the re-pitching
+// of 16-bit operands.
 //
-// Bound by memory: two reads and one write of an M x N matrix.  A thread owns
+// Bound by memory: dZ is two reads and one write of an M x N matrix.  A thread owns
 // eight columns (16 bytes of a row) and walks every eighth row of its block's share, so the column sums stay in registers; the eight
 // row groups of a block are added in shared memory, and each block's sums are
 // joined by a second launch, everything in a fixed order.
@@ -96,6 +97,45 @@ __global__ void __launch_bounds__(1024)
   if (lane == 0 && out != nullptr && c < cols) out[c] = from_f32<T>(v);
 }
 
+struct RepitchJobs {
+  RepitchJob job[8];
+  int64_t first[9];  // units (256 columns of a row) before each job
+  int n;
+};
+
+// A warp per 256 columns of a row, four of them at a time: 16-byte loads
+// shifted to the aligned pitch, 16-byte stores.
+__global__ void __launch_bounds__(256) repitch_kernel(const __grid_constant__ RepitchJobs jobs) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t total = jobs.first[jobs.n];
+  for (int64_t u0 = 4 * ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)); u0 < total;
+       u0 += 32 * (int64_t)gridDim.x) {
+    uint4 v[4];
+    __half *dst[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t u = u0 + k;
+      dst[k] = nullptr;
+      if (u >= total) continue;
+      int j = 0;
+      while (u >= jobs.first[j + 1]) ++j;
+      const RepitchJob &job = jobs.job[j];
+      const int64_t per_row = (job.ldd + 255) / 256, i = u - jobs.first[j];
+      const int64_t row = i / per_row;
+      const int col = (int)(i - row * per_row) * 256 + lane * 8;
+      if (col >= job.ldd) continue;
+      v[k] = load_row16<__half, false>(static_cast<const __half *>(job.src) + row * job.lds, col,
+                                       (int)job.cols);
+      dst[k] = static_cast<__half *>(job.dst) + row * job.ldd + col;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (dst[k] != nullptr) *reinterpret_cast<uint4 *>(dst[k]) = v[k];
+  }
+}
+
 template <class T>
 cudaError_t column_sums(const float *partial, int parts, int cols, void *out0, void *out1, int nvec,
                         cudaStream_t stream) {
@@ -170,6 +210,22 @@ cudaError_t launch_act_grad(int dtype, int act, int M, int N, const void *dD, in
       f(act, M, N, dD, lddd, Z, ldz, dZ, lddz, dbias, partial, parts, stream);
   if (e != cudaSuccess || dbias == nullptr || parts == 1) return e;
   return column_sums(dtype, partial, parts, N, dbias, nullptr, 1, stream);
+}
+
+cudaError_t launch_repitch(const RepitchJob *jobs, int njobs, int num_sms, cudaStream_t stream) {
+  RepitchJobs a;
+  if (njobs < 1 || njobs > 8) return cudaErrorInvalidValue;
+  a.n = njobs;
+  a.first[0] = 0;
+  for (int j = 0; j < njobs; ++j) {
+    a.job[j] = jobs[j];
+    a.first[j + 1] = a.first[j] + jobs[j].rows * ((jobs[j].ldd + 255) / 256);
+  }
+  const int64_t blocks = (a.first[njobs] + 31) / 32, most = 8 * (int64_t)num_sms;
+  const cudaError_t e = launch_kernel(repitch_kernel, dim3((unsigned)(blocks < most ? blocks : most)),
+                                      dim3(256), 0, stream, 1u, a);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 }  // namespace dg

@@ -24,18 +24,20 @@ constexpr int kVec = 16 / (int)sizeof(T);
 // sizeof(T), below 16.
 template <class T>
 __device__ __forceinline__ uint4 shift16(uint4 a, uint4 b, int off) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  const int s = off >> 2;
-  uint32_t r[5];
-#pragma unroll
-  for (int j = 0; j < 5; ++j)
-    r[j] = s == 0 ? w[j] : s == 1 ? w[j + 1] : s == 2 ? w[j + 2] : j + 3 < 8 ? w[j + 3] : 0u;
+  // `off` is the same in every lane that shares a row: branches, not selects
+  uint32_t r0, r1, r2, r3, r4;
+  switch (off >> 2) {
+    case 0: r0 = a.x, r1 = a.y, r2 = a.z, r3 = a.w, r4 = b.x; break;
+    case 1: r0 = a.y, r1 = a.z, r2 = a.w, r3 = b.x, r4 = b.y; break;
+    case 2: r0 = a.z, r1 = a.w, r2 = b.x, r3 = b.y, r4 = b.z; break;
+    default: r0 = a.w, r1 = b.x, r2 = b.y, r3 = b.z, r4 = b.w; break;
+  }
   if constexpr (sizeof(T) == 4) {
-    return make_uint4(r[0], r[1], r[2], r[3]);
+    return make_uint4(r0, r1, r2, r3);
   } else {
     const int sh = 8 * (off & 3);
-    return make_uint4(__funnelshift_r(r[0], r[1], sh), __funnelshift_r(r[1], r[2], sh),
-                      __funnelshift_r(r[2], r[3], sh), __funnelshift_r(r[3], r[4], sh));
+    return make_uint4(__funnelshift_r(r0, r1, sh), __funnelshift_r(r1, r2, sh),
+                      __funnelshift_r(r2, r3, sh), __funnelshift_r(r3, r4, sh));
   }
 }
 
@@ -71,17 +73,18 @@ __device__ __forceinline__ uint4 load_row16(const T *row, int col, int cols) {
   }
 }
 
-// Store v at `col` of `row`.  The whole warp calls it, lane i with the vector
-// of column col0 + i * V of the same row (lanes past `cols` store nothing).
-template <class T, bool ALIGNED>
+// Store v at `col` of `row`.  The whole warp calls it; each group of LANES
+// lanes holds neighbouring vectors of one row, lane i of the group that of
+// column col0 + i * V (lanes past `cols` store nothing).
+template <class T, bool ALIGNED, int LANES = 32>
 __device__ __forceinline__ void store_row16(T *row, int col, int cols, uint4 v) {
   constexpr int V = kVec<T>;
   if constexpr (ALIGNED) {
     if (col < cols) *reinterpret_cast<uint4 *>(row + col) = v;
   } else {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & (LANES - 1);
     const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
-    const int off = (int)(at & 15);  // the same in every lane
+    const int off = (int)(at & 15);  // the same in every lane of the group
     uint4 prev;
     prev.x = __shfl_up_sync(0xffffffffu, v.x, 1);
     prev.y = __shfl_up_sync(0xffffffffu, v.y, 1);
@@ -93,7 +96,7 @@ __device__ __forceinline__ void store_row16(T *row, int col, int cols, uint4 v) 
     if (block)
       *reinterpret_cast<uint4 *>(at - off) = off == 0 ? v : shift16<T>(prev, v, 16 - off);
     // elements that no lane's block holds
-    const bool tail = off != 0 && (lane == 31 || !whole(col + V));
+    const bool tail = off != 0 && (lane == LANES - 1 || !whole(col + V));
     if ((!block || tail) && col < cols) {
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
