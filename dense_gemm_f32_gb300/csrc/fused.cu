@@ -20,42 +20,80 @@ int knob(const char *name, int lo, int hi) {
   return v >= lo && v <= hi ? v : -1;
 }
 
-// Whether a product runs on CTA pairs: once its 256-row tiles occupy a quarter
-// of the SMs and more than one 256-column tile of tokens is there to fill
-// them.  DGEMM_FUSED_PAIR=0 / =1 forces the choice.
-bool use_pair(const FusedGemm &p, int num_sms) {
-  if (p.K == 0) return false;  // the small kernel takes an empty sum
-  const int force = knob("DGEMM_FUSED_PAIR", 0, 1);
-  if (force >= 0) return force == 1;
-  if (p.M <= 256) return false;
+// Time models (microseconds) of the two kernels, fitted to 45 shapes of one to
+// 16384 tokens with every cut of the small kernel on GB300, in a graph with
+// operands rotating through more than L2.  Choosing by them is within 7% of
+// the best cut on average (1.32 times at worst); 256-row tiles once they fill a
+// quarter of the SMs, and 128-token tiles below that, were 30% off on average.
+//
+// Pair kernel: a wave of 256 x 256 tiles takes 0.318 us per 64 k, or as long as
+// writing its outputs.
+double pair_time(const FusedGemm &p, int num_sms) {
   const int tn = p.epi == Epi::kGated ? 128 : 256;
-  const int64_t tiles = (int64_t)((p.M + 255) / 256) * ((p.N + tn - 1) / tn) *
-                        (p.dual == Dual::kPair ? 2 : 1);
-  return tiles * 4 >= num_sms;
+  const int64_t products = p.dual == Dual::kPair ? 2 : 1;
+  const int64_t tiles = (int64_t)((p.M + 255) / 256) * ((p.N + tn - 1) / tn) * products;
+  const int64_t waves = (tiles + num_sms / 2 - 1) / (num_sms / 2);
+  const int kblocks = (p.K + 63) / 64 * (p.dual == Dual::kSum ? 2 : 1);
+  const int outs = p.dual == Dual::kPair ? 1 : (p.out0 != nullptr) + (p.out1 != nullptr) + (p.out2 != nullptr);
+  const double written = 2.0 * (double)p.M * p.N * outs * products;
+  const double main = waves * (kblocks * 0.318), out = written / 2.4e6;
+  return 5.95 + (main > out ? main : out);
 }
 
-// DGEMM_FUSED_NT / _KD / _SPLITS override the parts of the plan.
-SmallPlan small_plan(const FusedGemm &p, int num_sms) {
+// Small kernel: a CTA takes 0.167 us + its bytes at 139 GB/s per stage, or its
+// share of the SM's 266 GB/s when two run there; all together at most 15.2 TB/s
+// from L2; a tile's drain and epilogue grow with its tokens, and joining the
+// parts of a K split costs 2.3 us.
+double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int num_sms) {
+  const double nt = plan.nt, stage = (128 + nt) * 128 * plan.kd;
+  const int64_t parts = (kblocks + plan.splits - 1) / plan.splits, ctas = tiles * plan.splits;
+  const int per_sm = plan.nt <= 128 ? 2 : 1;
+  const int64_t waves = (ctas + (int64_t)per_sm * num_sms - 1) / ((int64_t)per_sm * num_sms);
+  const double share = per_sm == 2 && ctas > num_sms ? 2 : 1;
+  const double alone = 0.167 + stage / 139e3, shared = stage * share / 266e3;
+  const double loads = waves * (parts * (alone > shared ? alone : shared));
+  const double l2 = parts * stage * ctas / 15.2e6;
+  const double tail = 0.0286 * nt + 0.0093 * nt / plan.splits + (plan.splits > 1 ? 2.3 : 0.0);
+  return 3.13 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
+}
+
+// The kernel and its cut for a product.  DGEMM_FUSED_PAIR=0 / =1 forces the
+// kernel, DGEMM_FUSED_NT / _KD / _SPLITS parts of the small kernel's cut.
+struct Choice {
+  bool pair;
   SmallPlan plan;
-  const int step = p.a_t ? 64 : 16;
-  plan.nt = p.M <= 256 ? (p.M + step - 1) / step * step : 128;
-  const int nt = knob("DGEMM_FUSED_NT", 16, 256);
-  if (nt >= 0) plan.nt = (nt + step - 1) / step * step;
-  const int tf = p.epi == Epi::kGated ? 64 : 128;
-  const int64_t tiles = (int64_t)((p.M + plan.nt - 1) / plan.nt) * ((p.N + tf - 1) / tf) *
-                        (p.dual == Dual::kPair ? 2 : 1);
-  plan.kd = plan.nt <= 32 && p.K > 64 ? 2 : 1;
-  const int kd = knob("DGEMM_FUSED_KD", 1, 2);
-  if (kd >= 0 && (kd == 1 || plan.nt <= 64)) plan.kd = kd;
-  const int kblocks = (p.K + 64 * plan.kd - 1) / (64 * plan.kd) * (p.dual == Dual::kSum ? 2 : 1);
-  const int64_t slots = (plan.nt <= 128 ? 2 : 1) * (int64_t)num_sms;
-  int64_t s = slots / (tiles > 0 ? tiles : 1);
-  s = s < 8 ? s : 8;
-  s = s < kblocks / 2 ? s : kblocks / 2;
-  plan.splits = s < 1 ? 1 : (int)s;
-  const int splits = knob("DGEMM_FUSED_SPLITS", 1, 8);
-  if (splits >= 0) plan.splits = splits;
-  return plan;
+};
+Choice choose(const FusedGemm &p, int num_sms) {
+  const int force = p.K == 0 ? 0 : knob("DGEMM_FUSED_PAIR", 0, 1);  // an empty sum is the small one's
+  Choice c = {force == 1, {}};
+  if (c.pair) return c;
+  const int f_nt = knob("DGEMM_FUSED_NT", 16, 256), f_kd = knob("DGEMM_FUSED_KD", 1, 2);
+  const int f_splits = knob("DGEMM_FUSED_SPLITS", 1, 8);
+  const int step = p.a_t ? 64 : 16, tf = p.epi == Epi::kGated ? 64 : 128;
+  const int64_t tiles_f = (int64_t)((p.N + tf - 1) / tf) * (p.dual == Dual::kPair ? 2 : 1);
+  double best = 0;
+  for (int nt : {16, 32, 48, 64, 96, 128, 192, 256}) {
+    if (f_nt >= 0) nt = f_nt;
+    nt = (nt + step - 1) / step * step;
+    const int64_t tiles = tiles_f * ((p.M + nt - 1) / nt);
+    // stages of 128 k where two of them fit beside another CTA's
+    const int kd = f_kd == 1 || nt > 64 || (f_kd < 0 && p.K <= 64) ? 1 : 2;
+    const int64_t kblocks = (int64_t)((p.K + 64 * kd - 1) / (64 * kd)) * (p.dual == Dual::kSum ? 2 : 1);
+    for (int s : {1, 2, 3, 4, 6, 8}) {
+      if (f_splits >= 0) s = f_splits;
+      else if (s > 1 && s > kblocks) break;
+      const SmallPlan plan = {nt, kd, s};
+      const double t = small_time(tiles, kblocks, plan, num_sms);
+      if (best == 0 || t < best) {
+        best = t;
+        c.plan = plan;
+      }
+      if (f_splits >= 0) break;
+    }
+    if (f_nt >= 0 || nt >= p.M) break;
+  }
+  if (force < 0) c.pair = pair_time(p, num_sms) < best;
+  return c;
 }
 
 }  // namespace
@@ -76,15 +114,16 @@ cudaError_t launch_fused(const FusedGemm &p0, int num_sms, cudaStream_t stream) 
     const int unit = p.a_t ? 2 : p.b_t ? 1 : 0;
     if (p.a_t && p.b_t) {
       e = cudaErrorInvalidValue;
-    } else if (use_pair(p, num_sms)) {
-      e = unit == 0   ? launch_fused_pair_unit_0(p, wd, stream)
-          : unit == 1 ? launch_fused_pair_unit_1(p, wd, stream)
-                      : launch_fused_pair_unit_2(p, wd, stream);
     } else {
-      const SmallPlan plan = small_plan(p, num_sms);
-      e = unit == 0   ? launch_fused_small_unit_0(p, plan, wd, stream)
-          : unit == 1 ? launch_fused_small_unit_1(p, plan, wd, stream)
-                      : launch_fused_small_unit_2(p, plan, wd, stream);
+      const Choice c = choose(p, num_sms);
+      if (c.pair)
+        e = unit == 0   ? launch_fused_pair_unit_0(p, wd, stream)
+            : unit == 1 ? launch_fused_pair_unit_1(p, wd, stream)
+                        : launch_fused_pair_unit_2(p, wd, stream);
+      else
+        e = unit == 0   ? launch_fused_small_unit_0(p, c.plan, wd, stream)
+            : unit == 1 ? launch_fused_small_unit_1(p, c.plan, wd, stream)
+                        : launch_fused_small_unit_2(p, c.plan, wd, stream);
     }
   }
   const cudaError_t e2 = st.release();

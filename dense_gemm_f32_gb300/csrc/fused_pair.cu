@@ -79,13 +79,13 @@ struct PairCfg {
 
 // Site codes of the bounded waits.
 enum : int {
-  kSite3ProducerEmpty = 0x81,
-  kSite3ProducerTail = 0x82,
-  kSite3MmaFull = 0x83,
-  kSite3MmaAccEmpty = 0x84,
-  kSite3MmaDrain = 0x85,
-  kSite3MmaTail = 0x86,
-  kSite3EpiAccFull = 0x87,
+  kSite3ProducerEmpty = 0xa1,
+  kSite3ProducerTail = 0xa2,
+  kSite3MmaFull = 0xa3,
+  kSite3MmaAccEmpty = 0xa4,
+  kSite3MmaDrain = 0xa5,
+  kSite3MmaTail = 0xa6,
+  kSite3EpiAccFull = 0xa7,
 };
 
 struct PairMaps {

@@ -64,11 +64,11 @@ struct SmallCfg {
 
 // Site codes of the bounded waits.
 enum : int {
-  kSite4ProducerEmpty = 0x91,
-  kSite4ProducerDrain = 0x92,
-  kSite4MmaFull = 0x93,
-  kSite4MmaDrain = 0x94,
-  kSite4DrainAccFull = 0x95,
+  kSite4ProducerEmpty = 0xb1,
+  kSite4ProducerDrain = 0xb2,
+  kSite4MmaFull = 0xb3,
+  kSite4MmaDrain = 0xb4,
+  kSite4DrainAccFull = 0xb5,
 };
 
 struct SmallMaps {

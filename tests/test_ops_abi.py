@@ -1,6 +1,9 @@
 """Refusals of the feed-forward operators, none of which needs a GPU: the C
 entry points check on the host before any CUDA call, in the documented order,
 and the tensor calls check shapes and types first."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -208,3 +211,13 @@ def test_tensor_calls_refuse_other_types(call):
 def test_tensor_calls_refuse_other_shapes(call):
     with pytest.raises(ValueError):
         call()
+
+
+def test_watchdog_site_codes_are_distinct():
+    """Every bounded wait of every kernel has its own site code, across files."""
+    root = os.path.join(os.path.dirname(os.path.abspath(dg.__file__)), "csrc")
+    codes = []
+    for f in sorted(os.listdir(root)):
+        text = open(os.path.join(root, f), encoding="utf-8").read()
+        codes += re.findall(r"kSite\w+ = (0x[0-9a-f]+)", text)
+    assert len(codes) == len(set(codes)) >= 20
