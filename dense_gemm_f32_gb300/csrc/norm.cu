@@ -9,13 +9,17 @@
 // Bound by memory: forward one read and one write of the matrix, backward two
 // (three) reads and one write.  A row is held in registers by the threads that
 // share it, so it is read once and the variance is that of the centred values
-// (two passes over registers).  Short rows take a warp each (no block
-// barrier), longer ones a block of 256 to 1024 threads, at most 16 (32 for a
-// warp) elements per thread; rows beyond 16384 elements are read again for
-// each pass (from L2).  The backward kernel is persistent: a thread keeps the
-// same columns for every row its block takes, so the column sums of dw and db
-// stay in its registers and each block writes one partial sum, which a second
-// launch adds up in a fixed order.
+// (two passes over registers).  What the SMs issue is the other bound: a row
+// costs a thread about 190 instructions besides the 9 to 12 per element, so a
+// thread takes 32 elements (16 in the backward pass, which has to hold column
+// sums too) and a row as few threads as that leaves: a warp up to 1024
+// elements, without a block barrier, then 64 to 512 threads.  Rows beyond
+// 16384 elements (backward: 32 KB) are read again for each pass, from L2.  The
+// backward kernel is persistent: a ring of rows per block is filled ahead by
+// bulk copies, and a thread keeps the same columns for every row, so the
+// column sums of dw and db stay in its registers and each block writes one
+// partial sum, which a second launch adds up in a fixed order.
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -23,6 +27,7 @@
 #include "kernels.h"
 #include "launch.cuh"
 #include "ops.h"
+#include "ptx.cuh"
 #include "rowvec.cuh"
 
 namespace dg {
@@ -39,7 +44,17 @@ struct Shape {
   static constexpr int V = kVec<T_>, CH = CH_, GROUP = GROUP_;
   static constexpr int BLOCK = GROUP == 32 ? 128 : GROUP, ROWS = BLOCK / GROUP;
   static constexpr int CAPACITY = GROUP * CH * V;
+  // backward: a row's values stay in registers between its two passes, else
+  // they are read again from the ring
+  static constexpr bool KEEP = CH * V <= 16;
+  // backward: blocks per SM, 128 registers a thread
+  static constexpr int BWD_BLOCKS = 512 / BLOCK;
 };
+
+constexpr int kMaxStages = 8;
+
+// Site code of the bounded wait for a row's copy.
+enum : int { kSiteNormRow = 0xc1 };
 
 // Sums of N values over the threads of a row; every thread gets them.  `red`
 // alternates between two buffers, so one barrier per sum is enough.
@@ -69,7 +84,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[32]) {
 
 template <class S>
 __global__ void __launch_bounds__(S::BLOCK)
-    ln_fwd_kernel(int rows, int cols, float eps, const typename S::T *X, int64_t ldx,
+    ln_fwd_kernel(int rows, int cols, float inv, float eps, const typename S::T *X, int64_t ldx,
                   const typename S::T *w, const typename S::T *b, typename S::T *Y, int64_t ldy,
                   float *mean, float *rstd) {
   using T = typename S::T;
@@ -91,7 +106,7 @@ __global__ void __launch_bounds__(S::BLOCK)
 #pragma unroll
     for (int j = 0; j < V; ++j) s[0] += v[c][j];
   row_sum<S>(s, red[0]);
-  const float mu = s[0] / cols;
+  const float mu = s[0] * inv;
   s[0] = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -101,7 +116,7 @@ __global__ void __launch_bounds__(S::BLOCK)
       if ((c * GROUP + t) * V + (S::ALIGNED ? 0 : j) < cols) s[0] += v[c][j] * v[c][j];
     }
   row_sum<S>(s, red[1]);
-  const float r = rsqrtf(s[0] / cols + eps);
+  const float r = rsqrtf(s[0] * inv + eps);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int col = (c * GROUP + t) * V;
@@ -120,109 +135,201 @@ __global__ void __launch_bounds__(S::BLOCK)
   }
 }
 
+// A ring of rows in shared memory, filled ahead by bulk copies: one per group
+// of threads that shares rows.  A stage holds NIN matrices' rows, each copied
+// as the whole 16-byte blocks it lies in; a row starts `offset` bytes into its
+// place.  Every wait is bounded; a group whose wait gave up records it, stops
+// waiting and finishes with incomplete results.
+template <class S, int NIN>
+struct Ring {
+  using T = typename S::T;
+  const T *src[NIN];
+  int64_t ld[NIN];
+  uint32_t data, bars;   // shared-memory addresses
+  uint8_t *base;         // data, as a pointer
+  int place, stages, cols;
+  bool leader, dead;
+  int *watchdog;
+
+  // Bytes of one matrix's row in a stage.
+  static __host__ __device__ int place_bytes(int cols) {
+    return (cols * (int)sizeof(T) + (S::ALIGNED ? 15 : 29)) / 16 * 16;
+  }
+  static __host__ __device__ size_t group_bytes(int cols, int stages) {
+    return (size_t)stages * NIN * place_bytes(cols);
+  }
+
+  __device__ void init(uint8_t *smem, uint64_t *bar, int group, bool lead, int st, int c, int *wd) {
+    cols = c, stages = st, place = place_bytes(c), leader = lead, dead = false, watchdog = wd;
+    base = smem + (size_t)group * stages * NIN * place;
+    data = smem_u32(base);
+    bars = smem_u32(bar) + 8u * (uint32_t)(group * stages);
+    if (leader) {
+      for (int s = 0; s < stages; ++s) mbar_init(bars + 8u * s, 1);
+      fence_mbar_init();
+    }
+  }
+  // Leader: start the copies of `row` into `stage`.
+  __device__ void fill(int stage, int64_t row) {
+    const uint32_t bar = bars + 8u * (uint32_t)stage;
+    uint32_t bytes[NIN], total = 0;
+    const uint8_t *from[NIN];
+#pragma unroll
+    for (int i = 0; i < NIN; ++i) {
+      bytes[i] = 0;
+      if (src[i] == nullptr) continue;
+      const uintptr_t p = reinterpret_cast<uintptr_t>(src[i] + row * ld[i]);
+      from[i] = reinterpret_cast<const uint8_t *>(p & ~(uintptr_t)15);
+      bytes[i] = ((uint32_t)(p & 15) + (uint32_t)cols * (uint32_t)sizeof(T) + 15u) & ~15u;
+      total += bytes[i];
+    }
+    mbar_arrive_expect_tx(bar, total);
+#pragma unroll
+    for (int i = 0; i < NIN; ++i)
+      if (bytes[i]) bulk_load(data + (uint32_t)((stage * NIN + i) * place), from[i], bytes[i], bar);
+  }
+  __device__ void wait(int stage, uint32_t parity) {
+    if (!dead && !mbar_wait(bars + 8u * (uint32_t)stage, parity)) {
+      dead = true;
+      if (leader) atomicCAS(watchdog, 0, kSiteNormRow);
+    }
+  }
+  // Matrix i's copy of `row` in `stage`.
+  __device__ const T *row_at(int stage, int i, int64_t row) const {
+    const uintptr_t off = reinterpret_cast<uintptr_t>(src[i] + row * ld[i]) & 15;
+    return reinterpret_cast<const T *>(base + (stage * NIN + i) * place + (S::ALIGNED ? 0 : off));
+  }
+};
+
 // dX, and this block's partial sums of dw and db: partial[block][0][col] and
-// partial[block][1][col] (or dw and db themselves when there is one block).
+// partial[block][1][col] (or dw and db themselves when there is one block).  A
+// stage of the ring is refilled one row later, when the next row's sums have
+// shown that nobody reads it any more.
 template <class S>
-__global__ void __launch_bounds__(S::BLOCK, S::BLOCK <= 256 ? 2 : 1)
-    ln_bwd_kernel(int rows, int cols, const typename S::T *dY, int64_t lddy,
+__global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
+    ln_bwd_kernel(int rows, int cols, float inv, const typename S::T *dY, int64_t lddy,
                   const typename S::T *X, int64_t ldx, const typename S::T *w, const float *mean,
                   const float *rstd, const typename S::T *dR, int64_t lddr, typename S::T *dX,
-                  int64_t lddx, float *partial, typename S::T *dw, typename S::T *db) {
+                  int64_t lddx, float *partial, typename S::T *dw, typename S::T *db, int stages,
+                  int *watchdog) {
   using T = typename S::T;
   constexpr int V = S::V, CH = S::CH, GROUP = S::GROUP;
   __shared__ float red[2][2][32];
-  __shared__ float fold[S::ROWS > 1 ? S::ROWS : 1][S::ROWS > 1 ? S::CAPACITY : 1];
+  __shared__ uint64_t bars[S::ROWS * kMaxStages];
+  extern __shared__ __align__(16) uint8_t rows_smem[];
   pdl_launch_dependents();
-  pdl_wait();
   const int t = threadIdx.x % GROUP, sub = threadIdx.x / GROUP;
+  Ring<S, 3> ring;
+  ring.src[0] = dY, ring.ld[0] = lddy;
+  ring.src[1] = X, ring.ld[1] = ldx;
+  ring.src[2] = dR, ring.ld[2] = lddr;
+  ring.init(rows_smem, bars, sub, t == 0, stages, cols, watchdog);
+  __syncthreads();
+  pdl_wait();
   const bool grads = partial != nullptr || dw != nullptr || db != nullptr;
-  float sw[CH][V], sb[CH][V], g[CH][V];
+  const int64_t step = (int64_t)gridDim.x * S::ROWS;
+  int64_t row = (int64_t)blockIdx.x * S::ROWS + sub;
+  if (t == 0)
+    for (int s = 0; s < stages && row + s * step < rows; ++s) ring.fill(s, row + s * step);
+  float sw[CH][V], sb[CH][V];
+  uint4 wr[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) sw[c][j] = sb[c][j] = 0.f, g[c][j] = 1.f;
-    if (w) widen16<T>(load_row16<T, S::ALIGNED>(w, (c * GROUP + t) * V, cols), g[c]);
+    for (int j = 0; j < V; ++j) sw[c][j] = sb[c][j] = 0.f;
+    wr[c] = load_row16<T, S::ALIGNED>(w, (c * GROUP + t) * V, w ? cols : 0);
   }
-  const float inv = 1.f / cols;
-  const int64_t step = (int64_t)gridDim.x * S::ROWS;
-  int64_t row = (int64_t)blockIdx.x * S::ROWS + sub;
-  // the next row's loads are in flight while a row is reduced
-  uint4 rd[CH], rx[CH], rr[CH];
-  float mu = 0.f, r = 0.f;
-  auto fetch = [&](int64_t i) {
-    mu = mean[i], r = rstd[i];
+  auto weights = [&](int c, float(&g)[V]) {
+    if (w) {
+      widen16<T>(wr[c], g);
+    } else {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (c * GROUP + t) * V;
-      rd[c] = load_row16<T, S::ALIGNED>(dY + i * lddy, col, cols);
-      rx[c] = load_row16<T, S::ALIGNED>(X + i * ldx, col, cols);
+      for (int j = 0; j < V; ++j) g[j] = 1.f;
     }
   };
-  auto fetch_skip = [&](int64_t i) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      rr[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (dR != nullptr)
-        rr[c] = load_row16<T, S::ALIGNED>(dR + i * lddr, (c * GROUP + t) * V, cols);
-    }
-  };
-  if (row < rows) {
-    fetch(row);
-    fetch_skip(row);
-  }
-  int buf = 0;
+  float mu_next = 0.f, r_next = 0.f;
+  if (row < rows) mu_next = mean[row], r_next = rstd[row];
+  int buf = 0, stage = 0, last = -1;
+  uint32_t phase = 0;
   for (; row < rows; row += step) {
-    float d[CH][V], xh[CH][V], s[2] = {0.f, 0.f};
-    const float r_now = r;
+    const float mu = mu_next, r = r_next;
+    if (row + step < rows) mu_next = mean[row + step], r_next = rstd[row + step];
+    ring.wait(stage, phase);
+    const T *dy = ring.row_at(stage, 0, row), *x = ring.row_at(stage, 1, row);
+    float p[S::KEEP ? CH : 1][V], xh[S::KEEP ? CH : 1][V], s[2] = {0.f, 0.f};
+    // p = dy w and xh of vector c
+    auto read = [&](int c, float(&d)[V], float(&pc)[V], float(&hc)[V]) {
+      float g[V];
+      widen16<T>(load_row16<T, S::ALIGNED>(dy, (c * GROUP + t) * V, cols), d);
+      widen16<T>(load_row16<T, S::ALIGNED>(x, (c * GROUP + t) * V, cols), hc);
+      weights(c, g);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        hc[j] = (hc[j] - mu) * r;
+        pc[j] = d[j] * g[j];
+      }
+    };
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      widen16<T>(rd[c], d[c]);
-      widen16<T>(rx[c], xh[c]);
+      float d[V];
+      float(&pc)[V] = p[S::KEEP ? c : 0], (&hc)[V] = xh[S::KEEP ? c : 0];
+      read(c, d, pc, hc);
 #pragma unroll
       for (int j = 0; j < V; ++j) {  // past the row's end d is 0, and with it every term
-        xh[c][j] = (xh[c][j] - mu) * r;
-        const float p = d[c][j] * g[c][j];
-        s[0] += p;
-        s[1] += p * xh[c][j];
-        sw[c][j] += d[c][j] * xh[c][j];
-        sb[c][j] += d[c][j];
+        s[0] += pc[j];
+        s[1] += pc[j] * hc[j];
+        sw[c][j] += d[j] * hc[j];
+        sb[c][j] += d[j];
       }
     }
-    if (row + step < rows) fetch(row + step);
     row_sum<S>(s, red[buf]);
     buf ^= 1;
+    if (GROUP == 32) __syncwarp();
+    if (t == 0 && last >= 0 && row + (stages - 1) * step < rows)
+      ring.fill(last, row + (stages - 1) * step);
+    last = stage;
     const float m1 = s[0] * inv, m2 = s[1] * inv;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * GROUP + t) * V;
-      float e[V];
-      widen16<T>(rr[c], e);
+      float e[V], d[V];
+      float(&pc)[V] = p[S::KEEP ? c : 0], (&hc)[V] = xh[S::KEEP ? c : 0];
+      if constexpr (!S::KEEP) read(c, d, pc, hc);
+      if (dR) {
+        widen16<T>(load_row16<T, S::ALIGNED>(ring.row_at(stage, 2, row), (c * GROUP + t) * V, cols), e);
 #pragma unroll
-      for (int j = 0; j < V; ++j) e[j] += r_now * (d[c][j] * g[c][j] - m1 - xh[c][j] * m2);
-      store_row16<T, S::ALIGNED>(dX + row * lddx, col, cols, narrow16<T>(e));
+        for (int j = 0; j < V; ++j) e[j] += r * (pc[j] - m1 - hc[j] * m2);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) e[j] = r * (pc[j] - m1 - hc[j] * m2);
+      }
+      store_row16<T, S::ALIGNED>(dX + row * lddx, (c * GROUP + t) * V, cols, narrow16<T>(e));
     }
-    if (row + step < rows) fetch_skip(row + step);
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
   }
+  if (ring.dead && t == 0)  // no copy lands after the block has left
+    for (int s = 0; s < stages; ++s) mbar_wait(ring.bars + 8u * s, phase ^ (s < stage ? 1u : 0u));
   if (!grads) return;
-  // the block's rows side by side, added in their order
+  // the block's rows side by side, added in their order (the ring is idle now)
+  float *fold = reinterpret_cast<float *>(rows_smem);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float(&sum)[CH][V] = k ? sb : sw;
+    T *out = k ? db : dw;
+    float *part = partial ? partial + ((int64_t)blockIdx.x * 2 + k) * cols : nullptr;
     if constexpr (S::ROWS > 1) {
       __syncthreads();
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int j = 0; j < V; ++j) fold[sub][(c * GROUP + t) * V + j] = sum[c][j];
+        for (int j = 0; j < V; ++j) fold[sub * S::CAPACITY + (c * GROUP + t) * V + j] = sum[c][j];
       __syncthreads();
-    }
-    T *out = k ? db : dw;
-    float *part = partial ? partial + ((int64_t)blockIdx.x * 2 + k) * cols : nullptr;
-    if constexpr (S::ROWS > 1) {
       for (int col = threadIdx.x; col < cols; col += S::BLOCK) {
         float v = 0.f;
 #pragma unroll
-        for (int i = 0; i < S::ROWS; ++i) v += fold[i][col];
+        for (int i = 0; i < S::ROWS; ++i) v += fold[i * S::CAPACITY + col];
         if (part)
           part[col] = v;
         else if (out)
@@ -326,29 +433,63 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------- host side
 constexpr int kMaxRegisterCols = 16384;
+constexpr int kMaxRingBytes = 32768;  // of a row in the backward ring: two stages of three rows fit
+constexpr int kLongParts = 16;        // row shares of the column sums of longer rows
 
-// f(shape) for the shape a row of `cols` elements is held in: the smallest
-// group that holds it in at most 16 elements per thread (32 for a warp), since
-// more rows per SM then have their loads in flight.
-template <class T, bool ALIGNED, class F>
+// f(shape) for the shape a row of `cols` elements is held in: at most 32
+// elements per thread forward, 16 (for rows beyond 8192, 32) backward.
+// Measured at 16384 x 4096 bf16, forward: 128 threads to a row 45.3 us (5.93
+// TB/s), 256 threads 54.8 us; 65536 x 1024: a warp 44.3 us.  Backward with dR:
+// 92.2 us (5.82 TB/s); one row ahead in registers instead of the ring 115 us.
+template <class T, bool ALIGNED, bool BWD, class F>
 cudaError_t with_shape(int cols, F &&f) {
   constexpr int K = 8 / kVec<T>;  // vectors in 8 elements
+  constexpr int W = BWD ? 2 : 1;  // threads, relative to forward
   if (cols <= 256) return f(Shape<T, ALIGNED, K, 32>{});
   if (cols <= 512) return f(Shape<T, ALIGNED, 2 * K, 32>{});
-  if (cols <= 1024) return f(Shape<T, ALIGNED, 4 * K, 32>{});
-  if (cols <= 2048) return f(Shape<T, ALIGNED, K, 256>{});
-  if (cols <= 4096) return f(Shape<T, ALIGNED, 2 * K, 256>{});
-  if (cols <= 8192) return f(Shape<T, ALIGNED, 2 * K, 512>{});
-  return f(Shape<T, ALIGNED, 2 * K, 1024>{});
+  if (cols <= 1024) return f(Shape<T, ALIGNED, 4 * K / W, 32 * W>{});
+  if (cols <= 2048) return f(Shape<T, ALIGNED, 4 * K / W, 64 * W>{});
+  if (cols <= 4096) return f(Shape<T, ALIGNED, 4 * K / W, 128 * W>{});
+  if (cols <= 8192) return f(Shape<T, ALIGNED, 4 * K / W, 256 * W>{});
+  return f(Shape<T, ALIGNED, 4 * K, 512>{});
 }
-template <class T, class F>
+template <class T, bool BWD, class F>
 cudaError_t with_shape(int cols, bool aligned, F &&f) {
-  return aligned ? with_shape<T, true>(cols, f) : with_shape<T, false>(cols, f);
+  return aligned ? with_shape<T, true, BWD>(cols, f) : with_shape<T, false, BWD>(cols, f);
 }
 
 template <class T>
 bool vec_ok(const void *p, int64_t ld) {
   return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
+}
+
+// Stages of a persistent kernel's rings and its dynamic shared memory: what
+// `blocks` blocks per SM leave room for, and the fold of the column sums.
+template <class S, int NIN>
+int ring_stages(int cols, int blocks, bool fold, size_t *smem) {
+  const size_t one = Ring<S, NIN>::group_bytes(cols, 1) * S::ROWS;
+  const size_t budget = 216 * 1024 / blocks - 4096;  // static shared memory and the system's share
+  int stages = (int)(budget / one);
+  stages = stages < 2 ? 2 : stages > kMaxStages ? kMaxStages : stages;
+  *smem = one * stages;
+  const size_t sums = fold && S::ROWS > 1 ? (size_t)S::ROWS * S::CAPACITY * sizeof(float) : 0;
+  if (*smem < sums) *smem = sums;
+  return stages;
+}
+
+// Opt in to `smem` bytes of dynamic shared memory, once per kernel and device
+// (the largest any call needs: 220 KB).
+template <auto KERNEL>
+cudaError_t allow_smem() {
+  static std::atomic<bool> set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+  if (e == cudaSuccess) set[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 template <class T>
@@ -365,22 +506,21 @@ cudaError_t fwd(int rows, int cols, float eps, const void *X, int64_t ldx, const
   } else {
     const bool vec = vec_ok<T>(X, ldx) && vec_ok<T>(Y, ldy) && vec_ok<T>(w, 0) &&
                      vec_ok<T>(b, 0) && (cols * (int)sizeof(T)) % 16 == 0;
-    e = with_shape<T>(cols, vec, [&](auto shape) {
+    e = with_shape<T, false>(cols, vec, [&](auto shape) {
       using S = decltype(shape);
-      return launch_kernel(ln_fwd_kernel<S>, dim3((unsigned)((rows + S::ROWS - 1) / S::ROWS)),
-                           dim3(S::BLOCK), 0, stream, 1u, rows, cols, eps, x, ldx, w, b, y, ldy,
-                           mean, rstd);
+      const int64_t blocks = ((int64_t)rows + S::ROWS - 1) / S::ROWS;
+      return launch_kernel(ln_fwd_kernel<S>, dim3((unsigned)blocks), dim3(S::BLOCK), 0, stream, 1u,
+                           rows, cols, 1.f / cols, eps, x, ldx, w, b, y, ldy, mean, rstd);
     });
   }
   if (e == cudaSuccess) count_launch();
   return e;
 }
 
-// Blocks of the backward kernel, each one partial sum: two per SM.
-int bwd_parts(int rows, int rows_per_block, int num_sms) {
+// Blocks of the backward kernel, each one partial sum.
+int bwd_parts(int rows, int rows_per_block, int64_t resident) {
   const int64_t need = ((int64_t)rows + rows_per_block - 1) / rows_per_block;
-  const int64_t most = 2 * (int64_t)num_sms;
-  return (int)(need < 1 ? 1 : need < most ? need : most);
+  return (int)(need < 1 ? 1 : need < resident ? need : resident);
 }
 
 template <class T>
@@ -394,7 +534,7 @@ cudaError_t bwd(int dtype, int rows, int cols, const void *dY, int64_t lddy, con
   const bool grads = dw != nullptr || db != nullptr;
   cudaError_t e = cudaSuccess;
   int parts = 1;
-  if (cols > kMaxRegisterCols) {
+  if (cols > kMaxRingBytes / (int)sizeof(T)) {
     if (rows > 0) {
       e = launch_kernel(ln_dx_long_kernel<T>, dim3((unsigned)rows), dim3(1024), 0, stream, 1u, cols,
                         dy, lddy, x, ldx, w, mean, rstd, dr, lddr, dx, lddx);
@@ -403,22 +543,28 @@ cudaError_t bwd(int dtype, int rows, int cols, const void *dY, int64_t lddy, con
     }
     if (!grads) return e;
     const unsigned gx = (unsigned)((cols + 255) / 256);
-    parts = rows < 16 ? (rows < 1 ? 1 : rows) : 16;
+    parts = rows < kLongParts ? (rows < 1 ? 1 : rows) : kLongParts;
     e = launch_kernel(ln_dw_long_kernel<T>, dim3(gx, (unsigned)parts), dim3(256), 0, stream, 1u,
                       rows, cols, dy, lddy, x, ldx, mean, rstd, partial);
     if (e != cudaSuccess) return e;
     count_launch();
     return launch_column_sums(dtype, partial, parts, cols, dw, db, stream);
   }
+  int *wd = watchdog_address();
+  if (wd == nullptr) return cudaErrorInvalidSymbol;
   const bool vec = vec_ok<T>(dY, lddy) && vec_ok<T>(X, ldx) && vec_ok<T>(w, 0) &&
                    vec_ok<T>(dr, dr ? lddr : 0) && vec_ok<T>(dX, lddx) &&
                    (cols * (int)sizeof(T)) % 16 == 0;
-  e = with_shape<T>(cols, vec, [&](auto shape) {
+  e = with_shape<T, true>(cols, vec, [&](auto shape) {
     using S = decltype(shape);
-    parts = bwd_parts(rows, S::ROWS, num_sms);
-    return launch_kernel(ln_bwd_kernel<S>, dim3((unsigned)parts), dim3(S::BLOCK), 0, stream, 1u,
-                         rows, cols, dy, lddy, x, ldx, w, mean, rstd, dr, lddr, dx, lddx,
-                         grads && parts > 1 ? partial : nullptr, dw, db);
+    parts = bwd_parts(rows, S::ROWS, (int64_t)S::BWD_BLOCKS * num_sms);
+    size_t smem = 0;
+    const int stages = ring_stages<S, 3>(cols, S::BWD_BLOCKS, grads, &smem);
+    const cudaError_t ea = allow_smem<ln_bwd_kernel<S>>();
+    if (ea != cudaSuccess) return ea;
+    return launch_kernel(ln_bwd_kernel<S>, dim3((unsigned)parts), dim3(S::BLOCK), smem, stream, 1u,
+                         rows, cols, 1.f / cols, dy, lddy, x, ldx, w, mean, rstd, dr, lddr, dx,
+                         lddx, grads && parts > 1 ? partial : nullptr, dw, db, stages, wd);
   });
   if (e != cudaSuccess) return e;
   count_launch();
@@ -442,7 +588,13 @@ cudaError_t launch_layer_norm(int dtype, int rows, int cols, float eps, const vo
 
 size_t layer_norm_scratch(int rows, int cols, bool with_grads, int num_sms) {
   if (!with_grads) return 0;
-  const int parts = cols > kMaxRegisterCols ? 16 : bwd_parts(rows, 1, num_sms);
+  int parts = kLongParts;
+  with_shape<__half, true>(cols, true, [&](auto shape) {  // the groups do not depend on the type
+    using S = decltype(shape);
+    const int ring = bwd_parts(rows, S::ROWS, (int64_t)S::BWD_BLOCKS * num_sms);
+    parts = ring > parts ? ring : parts;
+    return cudaSuccess;
+  });
   return (size_t)parts * 2 * cols * sizeof(float);
 }
 

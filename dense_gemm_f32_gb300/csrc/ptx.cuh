@@ -94,6 +94,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// `bytes` consecutive bytes from global memory into shared memory at dst; both
+// addresses 16-byte aligned, bytes a multiple of 16.  Completion is signalled
+// on `bar` as tx bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // 2-D tiled store of the box at (x, y) from shared memory at src; the parts of
 // the box outside the tensor are not written.  Tracked by bulk async-groups.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int32_t x,

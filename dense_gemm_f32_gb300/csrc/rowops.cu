@@ -20,6 +20,7 @@ namespace dg {
 namespace {
 
 constexpr int kGroups = 8;  // row groups (warps) of a block
+constexpr int kAhead = 4;   // rows of a thread in flight
 
 template <class T, bool ALIGNED>
 __global__ void __launch_bounds__(32 * kGroups)
@@ -36,24 +37,36 @@ __global__ void __launch_bounds__(32 * kGroups)
   for (int j = 0; j < V; ++j) sum[j] = 0.f;
   with_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-#pragma unroll 4
-    for (int64_t i = (int64_t)blockIdx.y * kGroups + group; i < M;
-         i += (int64_t)gridDim.y * kGroups) {
-      float d[V];
-      widen16<T>(load_row16<T, ALIGNED>(dD + i * lddd, col, N), d);
-      if constexpr (ACT != DGEMM_ACT_NONE) {
-        float z[V];
-        widen16<T>(load_row16<T, ALIGNED>(Z + i * ldz, col, N), z);
+    const int64_t step = (int64_t)gridDim.y * kGroups;
+    for (int64_t i0 = (int64_t)blockIdx.y * kGroups + group; i0 < M; i0 += kAhead * step) {
+      uint4 dr[kAhead], zr[kAhead];  // all of them in flight before the first is used
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float value, slope;
-          act_grad_f32<ACT>(z[j], value, slope);
-          d[j] *= slope;
-        }
-        store_row16<T, ALIGNED>(dZ + i * lddz, col, N, narrow16<T>(d));
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t i = i0 + k * step;
+        const int n = i < M ? N : 0;
+        dr[k] = load_row16<T, ALIGNED>(dD + i * lddd, col, n);
+        if (ACT != DGEMM_ACT_NONE) zr[k] = load_row16<T, ALIGNED>(Z + i * ldz, col, n);
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) sum[j] += d[j];
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t i = i0 + k * step;
+        if (i >= M) break;
+        float d[V];
+        widen16<T>(dr[k], d);
+        if constexpr (ACT != DGEMM_ACT_NONE) {
+          float z[V];
+          widen16<T>(zr[k], z);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            float value, slope;
+            act_grad_f32<ACT>(z[j], value, slope);
+            d[j] *= slope;
+          }
+          store_row16<T, ALIGNED>(dZ + i * lddz, col, N, narrow16<T>(d));
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] += d[j];
+      }
     }
   });
   if (partial == nullptr && dbias == nullptr) return;
