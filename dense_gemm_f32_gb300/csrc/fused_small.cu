@@ -340,10 +340,11 @@ __global__ void __launch_bounds__(SmallCfg::THREADS, 2)
 #pragma unroll
         for (int o = 0; o < kOuts; ++o) {
           int slot;
-          if (output(o, &slot))
-            store_row16<T, AL, Q>(static_cast<T *>(p.out[slot]) + row * p.ldo[slot],
-                                  in ? col : end, end,
-                                  make_uint4(w[o][0], w[o][1], w[o][2], w[o][3]));
+          if (output(o, &slot)) {
+            const uint4 v[1] = {make_uint4(w[o][0], w[o][1], w[o][2], w[o][3])};
+            store_row16<T, AL, 1, Q>(static_cast<T *>(p.out[slot]) + row * p.ldo[slot],
+                                     in ? col : end, end, v);
+          }
         }
       }
     };

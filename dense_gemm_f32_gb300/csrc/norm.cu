@@ -33,9 +33,9 @@
 namespace dg {
 namespace {
 
-// A row's share of a thread: CH vectors, vector c at column (c * GROUP + index
-// in the group) * V.  GROUP threads share a row; a block holds BLOCK / GROUP
-// rows.  The share does not depend on the rows' alignment, so neither do the
+// A row's share of a thread: CH vectors.  GROUP threads share a row, each warp
+// of them CH * 32 neighbouring vectors, 32 at a time; a block holds BLOCK /
+// GROUP rows.  The share does not depend on the rows' alignment, so neither do the
 // sums.
 template <class T_, bool ALIGNED_, int CH_, int GROUP_>
 struct Shape {
@@ -44,6 +44,10 @@ struct Shape {
   static constexpr int V = kVec<T_>, CH = CH_, GROUP = GROUP_;
   static constexpr int BLOCK = GROUP == 32 ? 128 : GROUP, ROWS = BLOCK / GROUP;
   static constexpr int CAPACITY = GROUP * CH * V;
+  // column of vector c of thread t of the group
+  static __device__ __forceinline__ int col(int c, int t) {
+    return ((t / 32 * CH + c) * 32 + t % 32) * V;
+  }
   // backward: a row's values stay in registers between its two passes, else
   // they are read again from the ring
   static constexpr bool KEEP = CH * V <= 16;
@@ -99,7 +103,7 @@ __global__ void __launch_bounds__(S::BLOCK)
   float v[CH][V], s[1] = {0.f};
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    widen16<T>(load_row16<T, S::ALIGNED>(x, (c * GROUP + t) * V, cols), v[c]);
+    widen16<T>(load_row16<T, S::ALIGNED>(x, S::col(c, t), cols), v[c]);
   }
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -113,13 +117,14 @@ __global__ void __launch_bounds__(S::BLOCK)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       v[c][j] -= mu;
-      if ((c * GROUP + t) * V + (S::ALIGNED ? 0 : j) < cols) s[0] += v[c][j] * v[c][j];
+      if (S::col(c, t) + (S::ALIGNED ? 0 : j) < cols) s[0] += v[c][j] * v[c][j];
     }
   row_sum<S>(s, red[1]);
   const float r = rsqrtf(s[0] * inv + eps);
+  uint4 out[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int col = (c * GROUP + t) * V;
+    const int col = S::col(c, t);
     float g[V], h[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) g[j] = 1.f, h[j] = 0.f;
@@ -127,8 +132,9 @@ __global__ void __launch_bounds__(S::BLOCK)
     if (b) widen16<T>(load_row16<T, S::ALIGNED>(b, col, cols), h);
 #pragma unroll
     for (int j = 0; j < V; ++j) v[c][j] = v[c][j] * r * g[j] + h[j];
-    store_row16<T, S::ALIGNED>(Y + row * ldy, col, cols, narrow16<T>(v[c]));
+    out[c] = narrow16<T>(v[c]);
   }
+  store_row16<T, S::ALIGNED, CH>(Y + row * ldy, S::col(0, t), cols, out);
   if (t == 0) {
     if (mean) mean[row] = mu;
     if (rstd) rstd[row] = r;
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
     for (int j = 0; j < V; ++j) sw[c][j] = sb[c][j] = 0.f;
-    wr[c] = load_row16<T, S::ALIGNED>(w, (c * GROUP + t) * V, w ? cols : 0);
+    wr[c] = load_row16<T, S::ALIGNED>(w, S::col(c, t), w ? cols : 0);
   }
   auto weights = [&](int c, float(&g)[V]) {
     if (w) {
@@ -260,8 +266,8 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
     // p = dy w and xh of vector c
     auto read = [&](int c, float(&d)[V], float(&pc)[V], float(&hc)[V]) {
       float g[V];
-      widen16<T>(load_row16<T, S::ALIGNED>(dy, (c * GROUP + t) * V, cols), d);
-      widen16<T>(load_row16<T, S::ALIGNED>(x, (c * GROUP + t) * V, cols), hc);
+      widen16<T>(load_row16<T, S::ALIGNED>(dy, S::col(c, t), cols), d);
+      widen16<T>(load_row16<T, S::ALIGNED>(x, S::col(c, t), cols), hc);
       weights(c, g);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -289,21 +295,23 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
       ring.fill(last, row + (stages - 1) * step);
     last = stage;
     const float m1 = s[0] * inv, m2 = s[1] * inv;
+    uint4 out[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float e[V], d[V];
       float(&pc)[V] = p[S::KEEP ? c : 0], (&hc)[V] = xh[S::KEEP ? c : 0];
       if constexpr (!S::KEEP) read(c, d, pc, hc);
       if (dR) {
-        widen16<T>(load_row16<T, S::ALIGNED>(ring.row_at(stage, 2, row), (c * GROUP + t) * V, cols), e);
+        widen16<T>(load_row16<T, S::ALIGNED>(ring.row_at(stage, 2, row), S::col(c, t), cols), e);
 #pragma unroll
         for (int j = 0; j < V; ++j) e[j] += r * (pc[j] - m1 - hc[j] * m2);
       } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) e[j] = r * (pc[j] - m1 - hc[j] * m2);
       }
-      store_row16<T, S::ALIGNED>(dX + row * lddx, (c * GROUP + t) * V, cols, narrow16<T>(e));
+      out[c] = narrow16<T>(e);
     }
+    store_row16<T, S::ALIGNED, CH>(dX + row * lddx, S::col(0, t), cols, out);
     if (++stage == stages) {
       stage = 0;
       phase ^= 1u;
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int j = 0; j < V; ++j) fold[sub * S::CAPACITY + (c * GROUP + t) * V + j] = sum[c][j];
+        for (int j = 0; j < V; ++j) fold[sub * S::CAPACITY + S::col(c, t) + j] = sum[c][j];
       __syncthreads();
       for (int col = threadIdx.x; col < cols; col += S::BLOCK) {
         float v = 0.f;
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int col = (c * GROUP + t) * V + j;
+          const int col = S::col(c, t) + j;
           if (col >= cols) continue;
           if (part)
             part[col] = sum[c][j];

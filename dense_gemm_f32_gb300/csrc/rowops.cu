@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(32 * kGroups)
             act_grad_f32<ACT>(z[j], value, slope);
             d[j] *= slope;
           }
-          store_row16<T, ALIGNED>(dZ + i * lddz, col, N, narrow16<T>(d));
+          const uint4 out[1] = {narrow16<T>(d)};
+          store_row16<T, ALIGNED>(dZ + i * lddz, col, N, out);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] += d[j];

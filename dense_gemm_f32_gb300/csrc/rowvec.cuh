@@ -24,17 +24,16 @@ constexpr int kVec = 16 / (int)sizeof(T);
 // sizeof(T), below 16.
 template <class T>
 __device__ __forceinline__ uint4 shift16(uint4 a, uint4 b, int off) {
-  // `off` is the same in every lane that shares a row: branches, not selects
-  uint32_t r0, r1, r2, r3, r4;
-  switch (off >> 2) {
-    case 0: r0 = a.x, r1 = a.y, r2 = a.z, r3 = a.w, r4 = b.x; break;
-    case 1: r0 = a.y, r1 = a.z, r2 = a.w, r3 = b.x, r4 = b.y; break;
-    case 2: r0 = a.z, r1 = a.w, r2 = b.x, r3 = b.y, r4 = b.z; break;
-    default: r0 = a.w, r1 = b.x, r2 = b.y, r3 = b.z, r4 = b.w; break;
-  }
+  // two selects per word and a funnel shift; `off` belongs to the row, so what
+  // depends on it alone is computed once per row
+  const bool two = (off & 8) != 0, one = (off & 4) != 0;
+  const uint32_t b0 = two ? a.z : a.x, b1 = two ? a.w : a.y, b2 = two ? b.x : a.z;
+  const uint32_t b3 = two ? b.y : a.w, b4 = two ? b.z : b.x, b5 = two ? b.w : b.y;
+  const uint32_t r0 = one ? b1 : b0, r1 = one ? b2 : b1, r2 = one ? b3 : b2, r3 = one ? b4 : b3;
   if constexpr (sizeof(T) == 4) {
     return make_uint4(r0, r1, r2, r3);
   } else {
+    const uint32_t r4 = one ? b5 : b4;
     const int sh = 8 * (off & 3);
     return make_uint4(__funnelshift_r(r0, r1, sh), __funnelshift_r(r1, r2, sh),
                       __funnelshift_r(r2, r3, sh), __funnelshift_r(r3, r4, sh));
@@ -50,9 +49,9 @@ __device__ __forceinline__ uint4 load_row16(const T *row, int col, int cols) {
   if constexpr (ALIGNED) {
     return *reinterpret_cast<const uint4 *>(row + col);
   } else {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
-    const int off = (int)(at & 15);
-    const uint4 *block = reinterpret_cast<const uint4 *>(at - off);
+    const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);  // col is whole vectors
+    const uint4 *block = reinterpret_cast<const uint4 *>(
+        reinterpret_cast<const uint8_t *>(row) - off + col * (int)sizeof(T));
     v = block[0];
     uint4 next = make_uint4(0u, 0u, 0u, 0u);
     if (off != 0 && col + V - off / (int)sizeof(T) < cols) next = block[1];
@@ -73,39 +72,50 @@ __device__ __forceinline__ uint4 load_row16(const T *row, int col, int cols) {
   }
 }
 
-// Store v at `col` of `row`.  The whole warp calls it; each group of LANES
-// lanes holds neighbouring vectors of one row, lane i of the group that of
-// column col0 + i * V (lanes past `cols` store nothing).
-template <class T, bool ALIGNED, int LANES = 32>
-__device__ __forceinline__ void store_row16(T *row, int col, int cols, uint4 v) {
+// Store N vectors of `row`, vector k at column col + k * LANES * V.  The whole
+// warp calls it; each group of LANES lanes shares a row, lane i of the group
+// holding column col0 + i * V (vectors past `cols` are not stored), so the
+// group's N * LANES vectors are neighbours and only its first and last element
+// blocks are put together from single elements.
+template <class T, bool ALIGNED, int N = 1, int LANES = 32>
+__device__ __forceinline__ void store_row16(T *row, int col, int cols, const uint4 (&v)[N]) {
   constexpr int V = kVec<T>;
   if constexpr (ALIGNED) {
-    if (col < cols) *reinterpret_cast<uint4 *>(row + col) = v;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (col + k * LANES * V < cols) *reinterpret_cast<uint4 *>(row + col + k * LANES * V) = v[k];
   } else {
     const int lane = threadIdx.x & (LANES - 1);
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
-    const int off = (int)(at & 15);  // the same in every lane of the group
-    uint4 prev;
-    prev.x = __shfl_up_sync(0xffffffffu, v.x, 1);
-    prev.y = __shfl_up_sync(0xffffffffu, v.y, 1);
-    prev.z = __shfl_up_sync(0xffffffffu, v.z, 1);
-    prev.w = __shfl_up_sync(0xffffffffu, v.w, 1);
-    const int head = V - off / (int)sizeof(T);  // own elements in the block at `at - off`
-    auto whole = [&](int c) { return c + head <= cols; };  // a lane at column c stores its block
-    const bool block = (off == 0 || lane > 0) && whole(col);
-    if (block)
-      *reinterpret_cast<uint4 *>(at - off) = off == 0 ? v : shift16<T>(prev, v, 16 - off);
-    // elements that no lane's block holds
-    const bool tail = off != 0 && (lane == LANES - 1 || !whole(col + V));
-    if ((!block || tail) && col < cols) {
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);  // col is whole vectors
+    const int head = V - off / (int)sizeof(T);  // elements of a vector in the block it begins in
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (col + j < cols && (j < head ? !block : tail)) {
-          if constexpr (sizeof(T) == 4)
-            reinterpret_cast<uint32_t *>(row + col)[j] = w[j];
-          else
-            reinterpret_cast<uint16_t *>(row + col)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    for (int k = 0; k < N; ++k) {
+      const int c = col + k * LANES * V;
+      uint8_t *dst = reinterpret_cast<uint8_t *>(row) - off + c * (int)sizeof(T);
+      // the vector before: the lane before's, and for the first lane the last
+      // lane's of the round before
+      const uint4 send = k > 0 && lane == LANES - 1 ? v[k > 0 ? k - 1 : 0] : v[k];
+      const int from = (threadIdx.x & 31 & ~(LANES - 1)) | ((lane + LANES - 1) & (LANES - 1));
+      uint4 prev;
+      prev.x = __shfl_sync(0xffffffffu, send.x, from);
+      prev.y = __shfl_sync(0xffffffffu, send.y, from);
+      prev.z = __shfl_sync(0xffffffffu, send.z, from);
+      prev.w = __shfl_sync(0xffffffffu, send.w, from);
+      auto whole = [&](int x) { return x + head <= cols; };  // column x's lane stores its block
+      const bool block = (off == 0 || lane > 0 || k > 0) && whole(c);
+      if (block) *reinterpret_cast<uint4 *>(dst) = off == 0 ? v[k] : shift16<T>(prev, v[k], 16 - off);
+      // elements that no block holds
+      const bool tail = off != 0 && ((lane == LANES - 1 && k == N - 1) || !whole(c + V));
+      if ((!block || tail) && c < cols) {
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (c + j < cols && (j < head ? !block : tail)) {
+            if constexpr (sizeof(T) == 4)
+              reinterpret_cast<uint32_t *>(row + c)[j] = w[j];
+            else
+              reinterpret_cast<uint16_t *>(row + c)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+          }
         }
       }
     }
