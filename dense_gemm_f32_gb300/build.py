@@ -1,4 +1,6 @@
-"""Build libdgemm.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libdgemm.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+beside it _torch_binding.so (the operators' tensor calls) with the host
+compiler against the installed PyTorch.
 
 The translation units compile in parallel; the link keeps only the symbols
 declared in include/dgemm.h visible.  ptxas resource usage (-Xptxas -v:
@@ -6,16 +8,19 @@ registers, spills, shared memory per kernel) is written to
 _build/ptxas_<unit>.log next to the objects.
 """
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdgemm.so")
+BINDING = os.path.join(PKG, "_torch_binding.so")
 HEADER = os.path.join(ROOT, "include", "dgemm.h")
 # (source, object name, defines): simt.cu and tc.cu are compiled once per
 # operand layout so that the four layouts build in parallel.
@@ -47,10 +52,30 @@ def _sources():
 
 
 def _stale():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(s) > t for s in _sources())
+
+
+def _compile_binding(nvcc):
+    """The tensor calls' object file, and the directory of PyTorch's libraries."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("PyTorch is required to build the operators' tensor calls")
+    torch = os.path.dirname(spec.origin)
+    obj = os.path.join(BUILD, "torch_binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    include = os.path.join(torch, "include")
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+           "-isystem", include,
+           "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+           "-c", os.path.join(CSRC, "torch_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on torch_binding.cpp:\n{r.stderr[-6000:]}")
+    return obj, os.path.join(torch, "lib")
 
 
 def _compile(nvcc, unit):
@@ -73,17 +98,28 @@ def build(force=False, verbose=False):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding, nvcc)
         objs = list(ex.map(lambda u: _compile(nvcc, u), UNITS))
+        binding_obj, torch_lib = binding.result()
     vs = os.path.join(BUILD, "exports.map")
     with open(vs, "w") as f:
         f.write("{\n  global:\n" + "".join(f"    {s};\n" for s in EXPORTS) + "  local: *;\n};\n")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", f"--version-script={vs}", *objs, "-o", tmp]
+    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libdgemm.so", "-Xlinker",
+           f"--version-script={vs}", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-6000:]}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", binding_obj, "-o", tmp, LIB, "-L", torch_lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the tensor calls failed:\n{r.stderr[-6000:]}")
+    os.replace(tmp, BINDING)
     if verbose:
         for _, name, _ in UNITS:
             with open(os.path.join(BUILD, f"ptxas_{name}.log")) as f:
