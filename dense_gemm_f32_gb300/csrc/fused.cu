@@ -20,13 +20,13 @@ int knob(const char *name, int lo, int hi) {
   return v >= lo && v <= hi ? v : -1;
 }
 
-// Time models (microseconds) of the two kernels, fitted to 45 shapes of one to
+// Time models (microseconds) of the two kernels, fitted to 50 shapes of one to
 // 16384 tokens with every cut of the small kernel on GB300, in a graph with
-// operands rotating through more than L2.  Choosing by them is within 7% of
-// the best cut on average (1.32 times at worst); 256-row tiles once they fill a
+// operands rotating through more than L2.  Choosing by them is within 4% of
+// the best cut on average (1.17 times at worst); 256-row tiles once they fill a
 // quarter of the SMs, and 128-token tiles below that, were 30% off on average.
 //
-// Pair kernel: a wave of 256 x 256 tiles takes 0.318 us per 64 k, or as long as
+// Pair kernel: a wave of 256 x 256 tiles takes 0.331 us per 64 k, or as long as
 // writing its outputs.
 double pair_time(const FusedGemm &p, int num_sms) {
   const int tn = p.epi == Epi::kGated ? 128 : 256;
@@ -36,25 +36,26 @@ double pair_time(const FusedGemm &p, int num_sms) {
   const int kblocks = (p.K + 63) / 64 * (p.dual == Dual::kSum ? 2 : 1);
   const int outs = p.dual == Dual::kPair ? 1 : (p.out0 != nullptr) + (p.out1 != nullptr) + (p.out2 != nullptr);
   const double written = 2.0 * (double)p.M * p.N * outs * products;
-  const double main = waves * (kblocks * 0.318), out = written / 2.4e6;
-  return 5.95 + (main > out ? main : out);
+  const double main = waves * (kblocks * 0.331), out = written / 2.4e6;
+  return 6.04 + (main > out ? main : out);
 }
 
-// Small kernel: a CTA takes 0.167 us + its bytes at 139 GB/s per stage, or its
-// share of the SM's 266 GB/s when two run there; all together at most 15.2 TB/s
-// from L2; a tile's drain and epilogue grow with its tokens, and joining the
-// parts of a K split costs 2.3 us.
-double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int num_sms) {
-  const double nt = plan.nt, stage = (128 + nt) * 128 * plan.kd;
-  const int64_t parts = (kblocks + plan.splits - 1) / plan.splits, ctas = tiles * plan.splits;
-  const int per_sm = plan.nt <= 128 ? 2 : 1;
-  const int64_t waves = (ctas + (int64_t)per_sm * num_sms - 1) / ((int64_t)per_sm * num_sms);
-  const double share = per_sm == 2 && ctas > num_sms ? 2 : 1;
-  const double alone = 0.167 + stage / 139e3, shared = stage * share / 266e3;
-  const double loads = waves * (parts * (alone > shared ? alone : shared));
-  const double l2 = parts * stage * ctas / 15.2e6;
-  const double tail = 0.0286 * nt + 0.0093 * nt / plan.splits + (plan.splits > 1 ? 2.3 : 0.0);
-  return 3.13 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
+// Small kernel: a stage costs a CTA its wait (0.255 us, and 0.546 us shared by
+// the stages in flight), its bytes at 96 GB/s, or its share of the SM's 127
+// GB/s when two run there; all together at most 16.9 TB/s from L2; a tile's
+// drain and epilogue grow with its tokens, and joining the parts of a K split
+// costs 1 us.
+double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int64_t resident) {
+  const double nt = plan.nt, share = plan.per_sm, stage = (128 + nt) * 128 * plan.kd;
+  const int64_t parts = (kblocks + plan.splits - 1) / plan.splits;
+  const int64_t waves = (tiles + resident - 1) / resident;
+  double per = 0.546 / small_stages(plan) + 0.255;
+  if (per < stage / 96.5e3) per = stage / 96.5e3;
+  if (per < stage * share / 126.7e3) per = stage * share / 126.7e3;
+  const double loads = waves * (3.0 + parts * per);
+  const double l2 = parts * stage * tiles * plan.splits / 16.9e6;
+  const double tail = 0.029 * nt + (plan.splits > 1 ? 0.97 : 0.0);
+  return 1.24 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
 }
 
 // The kernel and its cut for a product.  DGEMM_FUSED_PAIR=0 / =1 forces the
@@ -82,8 +83,15 @@ Choice choose(const FusedGemm &p, int num_sms) {
     for (int s : {1, 2, 3, 4, 6, 8}) {
       if (f_splits >= 0) s = f_splits;
       else if (s > 1 && s > kblocks) break;
-      const SmallPlan plan = {nt, kd, s};
-      const double t = small_time(tiles, kblocks, plan, num_sms);
+      // all of an SM's shared memory for one CTA's stages where that holds every
+      // tile at once
+      SmallPlan plan = {nt, kd, s, 1};
+      int64_t resident = small_resident(plan, num_sms);
+      if (tiles > resident && nt <= 128) {
+        plan.per_sm = 2;
+        resident = small_resident(plan, num_sms);
+      }
+      const double t = small_time(tiles, kblocks, plan, resident);
       if (best == 0 || t < best) {
         best = t;
         c.plan = plan;

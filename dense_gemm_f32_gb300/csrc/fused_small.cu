@@ -9,8 +9,9 @@
 // K range is split over a thread-block cluster of up to 8 CTAs, so that enough
 // SMs pull weights at once.
 //  * Warp 0 loads by TMA (weights and tokens of 64 or 128 k per stage), warp 1
-//    issues tcgen05.mma, one accumulator of NT columns in tensor memory; two
-//    CTAs fit on an SM while NT <= 128.
+//    issues tcgen05.mma, one accumulator of NT columns in tensor memory.  A
+//    grid that fits one CTA per SM takes all of the shared memory for its
+//    stages; a larger one half of it, two CTAs per SM, while NT <= 128.
 //  * Every CTA parks its fp32 partial tile in its own shared memory, token by
 //    token, and the cluster's CTAs add the partials through distributed shared
 //    memory in part order, each finishing a share of the tile's elements: the
@@ -407,9 +408,7 @@ cudaError_t launch_small(const FusedGemm &p, const SmallPlan &plan, int *watchdo
     }
   }
   const int stage_bytes = (G::W_CHUNK + plan.nt * 128) * plan.kd;
-  const int budget = plan.nt <= 128 ? G::BUDGET2 : G::BUDGET1;
-  a.stages = budget / stage_bytes;
-  if (a.stages > G::MAX_STAGES) a.stages = G::MAX_STAGES;
+  a.stages = small_stages(plan);
   // the parked partial tile takes the stages' place
   if (a.stages < 2 || a.stages * stage_bytes < plan.nt * G::TF * 4) return cudaErrorInvalidValue;
   const int smem = a.stages * stage_bytes + G::TAIL_BYTES;
@@ -469,5 +468,48 @@ cudaError_t DG_UNIT_LAUNCHER(const FusedGemm &p, const SmallPlan &plan, int *wat
   return p.dtype == DGEMM_DTYPE_BF16 ? launch_epi<__nv_bfloat16>(p, plan, watchdog, stream)
                                      : launch_epi<__half>(p, plan, watchdog, stream);
 }
+
+#if DGEMM_FUSED_UNIT == 0
+int small_stages(const SmallPlan &plan) {
+  using G = SmallCfg;
+  const int n = (plan.per_sm == 2 ? G::BUDGET2 : G::BUDGET1) / ((G::W_CHUNK + plan.nt * 128) * plan.kd);
+  return n < G::MAX_STAGES ? n : G::MAX_STAGES;
+}
+
+// By the occupancy query, once per device, cluster size and share of an SM
+// (every instance of the kernel has the same block and bounds; a cluster has
+// to fit in one GPC, which holds a few SMs more than a multiple of its size).
+int64_t small_resident(const SmallPlan &plan, int num_sms) {
+  using G = SmallCfg;
+  if (plan.splits == 1) return (int64_t)plan.per_sm * num_sms;
+  static std::atomic<int> cache[64][3][G::MAX_SPLITS + 1] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / plan.splits;
+  std::atomic<int> &slot = cache[dev][plan.per_sm][plan.splits];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n == 0) {
+    auto kern = fused_small_kernel<__half, Epi::kLinear>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)plan.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)plan.splits);
+    cfg.blockDim = dim3(G::THREADS);
+    cfg.dynamicSmemBytes = (size_t)((plan.per_sm == 2 ? G::BUDGET2 : G::BUDGET1) + G::TAIL_BYTES);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             G::BUDGET1 + G::TAIL_BYTES) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();  // not sticky; an estimate will do
+      n = plan.per_sm * num_sms / plan.splits;
+    }
+    slot.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+#endif
 
 }  // namespace dg

@@ -91,10 +91,15 @@ cudaError_t launch_fused_pair_unit_2(const FusedGemm &p, int *watchdog, cudaStre
 
 // How fused_small.cu cuts a product: token columns of a tile (a multiple of
 // 16, of 64 when A is stored K x M; at most 256), 64-element rows of K per
-// stage (1 or 2), CTAs that share a tile's K range (1 to 8).
+// stage (1 or 2), CTAs that share a tile's K range (1 to 8), CTAs per SM whose
+// stages have to fit (1 or 2; 2 only up to 128 tokens).
 struct SmallPlan {
-  int nt, kd, splits;
+  int nt, kd, splits, per_sm;
 };
+// Stages of a plan's operand ring, and how many of its tiles (clusters of
+// `splits` CTAs) the device holds at once.
+int small_stages(const SmallPlan &plan);
+int64_t small_resident(const SmallPlan &plan, int num_sms);
 cudaError_t launch_fused_small_unit_0(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
                                       cudaStream_t stream);
 cudaError_t launch_fused_small_unit_1(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
