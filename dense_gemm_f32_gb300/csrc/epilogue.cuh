@@ -9,6 +9,19 @@
 
 namespace dg {
 
+// The first `valid` of 32 columns of a row, element by element; the rest zero.
+// Not inlined: the loop around it runs from the instruction cache only while
+// it is short.
+template <class T>
+__device__ __noinline__ void load32_single(const T *p, int valid, uint32_t (&w)[16]) {
+  const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t lo = 2 * j < valid ? h[2 * j] : 0u, hi = 2 * j + 1 < valid ? h[2 * j + 1] : 0u;
+    w[j] = lo | (hi << 16);
+  }
+}
+
 // 32 columns of one row of a 16-bit matrix, packed in pairs; columns from
 // `valid` on read as zero.  vec: the row is 16-byte aligned here.  Plain
 // loads: the row may be overwritten by this call's own output later on.
@@ -21,12 +34,10 @@ __device__ __forceinline__ void load32(const T *p, int valid, bool vec, uint32_t
       w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
     }
   } else {
-    const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+    uint32_t x[16];
+    load32_single<T>(p, valid, x);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t lo = 2 * j < valid ? h[2 * j] : 0u, hi = 2 * j + 1 < valid ? h[2 * j + 1] : 0u;
-      w[j] = lo | (hi << 16);
-    }
+    for (int j = 0; j < 16; ++j) w[j] = x[j];
   }
 }
 

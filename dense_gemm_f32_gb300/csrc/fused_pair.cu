@@ -105,6 +105,19 @@ struct PairArgs {
   int *watchdog;
 };
 
+// A staged 32 x 32 piece written element by element, a row per instruction:
+// pieces that TMA may not write.  Not inlined, to keep the epilogue's loop
+// short (it runs from the instruction cache: 16 x 14336 x 4096 weight gradient
+// NI_BEFORE us with this inlined, NI_AFTER us).
+__device__ __noinline__ void store_piece(const uint16_t *wb, uint16_t *out, int64_t ld, int rows,
+                                         int valid, int lane) {
+#pragma unroll 4
+  for (int rr = 0; rr < 32; ++rr) {
+    const uint16_t v = wb[rr * 32 + (((lane >> 3) ^ ((rr >> 1) & 3)) << 3) + (lane & 7)];
+    if (rr < rows && lane < valid) out[(int64_t)rr * ld + lane] = v;
+  }
+}
+
 template <class T, Epi EPI>
 __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
     fused_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairArgs p) {
@@ -387,15 +400,10 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
           if (tma) {
             if (lane == 0) tma_store_2d(&maps.o[slot_out], buf, col, row0);
           } else {
-            const uint16_t *wb = reinterpret_cast<const uint16_t *>(smem + (buf - base));
-            uint16_t *out = static_cast<uint16_t *>(p.out[slot_out]);
-            const int64_t ld = p.ldo[slot_out];
-#pragma unroll 8
-            for (int rr = 0; rr < 32; ++rr) {
-              const uint16_t v =
-                  wb[rr * 32 + (((lane >> 3) ^ ((rr >> 1) & 3)) << 3) + (lane & 7)];
-              if (row0 + rr < p.M && lane < valid) out[(int64_t)(row0 + rr) * ld + col + lane] = v;
-            }
+            store_piece(reinterpret_cast<const uint16_t *>(smem + (buf - base)),
+                        static_cast<uint16_t *>(p.out[slot_out]) +
+                            (int64_t)row0 * p.ldo[slot_out] + col,
+                        p.ldo[slot_out], p.M - row0, valid, lane);
           }
           if (lane == 0) bulk_commit_group();  // one (possibly empty) group per piece
           __syncwarp();
