@@ -6,36 +6,52 @@
 
 #include "activation.cuh"
 #include "ops.h"
+#include "rowvec.cuh"
 
 namespace dg {
 
-// The first `valid` of 32 columns of a row, element by element; the rest zero.
+// Columns col .. col + 31 (col a multiple of 32) of a row on any alignment,
+// from the at most five 16-byte blocks they lie in; from column `cols` on zero.
 // Not inlined: the loop around it runs from the instruction cache only while
 // it is short.
 template <class T>
-__device__ __noinline__ void load32_single(const T *p, int valid, uint32_t (&w)[16]) {
-  const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+__device__ __noinline__ void load32_unaligned(const T *row, int col, int cols, uint32_t (&w)[16]) {
+  const int valid = min(32, cols - col);
+  const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+  const uint4 *block = reinterpret_cast<const uint4 *>(
+      reinterpret_cast<const uint8_t *>(row) - off + col * (int)sizeof(T));
+  const int blocks = valid > 0 ? (off + 2 * valid + 15) / 16 : 0;
+  uint4 b[5];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t lo = 2 * j < valid ? h[2 * j] : 0u, hi = 2 * j + 1 < valid ? h[2 * j + 1] : 0u;
-    w[j] = lo | (hi << 16);
+  for (int k = 0; k < 5; ++k) b[k] = k < blocks ? block[k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 v = shift16<T>(b[q], b[q + 1], off);
+    w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+  }
+  if (valid < 32) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      w[j] = 2 * j + 1 < valid ? w[j] : 2 * j < valid ? w[j] & 0xFFFFu : 0u;
   }
 }
 
 // 32 columns of one row of a 16-bit matrix, packed in pairs; columns from
-// `valid` on read as zero.  vec: the row is 16-byte aligned here.  Plain
-// loads: the row may be overwritten by this call's own output later on.
+// `cols` on read as zero (cols = 0: none are read).  vec: the row is 16-byte
+// aligned.  Plain loads: the row may be overwritten by this call's own output
+// later on.
 template <class T>
-__device__ __forceinline__ void load32(const T *p, int valid, bool vec, uint32_t (&w)[16]) {
-  if (vec && valid >= 32) {
+__device__ __forceinline__ void load32(const T *row, int col, int cols, bool vec,
+                                       uint32_t (&w)[16]) {
+  if (vec && col + 32 <= cols) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(p + 8 * q);
+      const uint4 v = *reinterpret_cast<const uint4 *>(row + col + 8 * q);
       w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
     }
   } else {
     uint32_t x[16];
-    load32_single<T>(p, valid, x);
+    load32_unaligned<T>(row, col, cols, x);
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = x[j];
   }

@@ -101,10 +101,12 @@ __global__ void __launch_bounds__(S::BLOCK)
   if (GROUP == 32 && row >= rows) return;
   const T *x = X + row * ldx;
   float v[CH][V], s[1] = {0.f};
+  RowBlocks raw[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    widen16<T>(load_row16<T, S::ALIGNED>(x, S::col(c, t), cols), v[c]);
-  }
+  for (int c = 0; c < CH; ++c) raw[c] = fetch_row16<T, S::ALIGNED>(x, S::col(c, t), cols);
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+    widen16<T>(take_row16<T, S::ALIGNED>(raw[c], x, S::col(c, t), cols), v[c]);
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll

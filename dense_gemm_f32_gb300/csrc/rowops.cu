@@ -39,23 +39,23 @@ __global__ void __launch_bounds__(32 * kGroups)
     constexpr int ACT = decltype(a)::value;
     const int64_t step = (int64_t)gridDim.y * kGroups;
     for (int64_t i0 = (int64_t)blockIdx.y * kGroups + group; i0 < M; i0 += kAhead * step) {
-      uint4 dr[kAhead], zr[kAhead];  // all of them in flight before the first is used
+      RowBlocks dr[kAhead], zr[kAhead];  // all of them in flight before the first is used
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int64_t i = i0 + k * step;
         const int n = i < M ? N : 0;
-        dr[k] = load_row16<T, ALIGNED>(dD + i * lddd, col, n);
-        if (ACT != DGEMM_ACT_NONE) zr[k] = load_row16<T, ALIGNED>(Z + i * ldz, col, n);
+        dr[k] = fetch_row16<T, ALIGNED>(dD + i * lddd, col, n);
+        if (ACT != DGEMM_ACT_NONE) zr[k] = fetch_row16<T, ALIGNED>(Z + i * ldz, col, n);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int64_t i = i0 + k * step;
         if (i >= M) break;
         float d[V];
-        widen16<T>(dr[k], d);
+        widen16<T>(take_row16<T, ALIGNED>(dr[k], dD + i * lddd, col, N), d);
         if constexpr (ACT != DGEMM_ACT_NONE) {
           float z[V];
-          widen16<T>(zr[k], z);
+          widen16<T>(take_row16<T, ALIGNED>(zr[k], Z + i * ldz, col, N), z);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             float value, slope;
@@ -117,36 +117,52 @@ struct RepitchJobs {
   int n;
 };
 
-// A warp per 256 columns of a row, four of them at a time: 16-byte loads
-// shifted to the aligned pitch, 16-byte stores.
+// A warp takes kUnits neighbouring units (256 columns of a row each), all of
+// their loads in flight at once: 16-byte blocks shifted to the aligned pitch,
+// 16-byte stores.  One division per warp and round, the units after the first
+// follow by counting, and every load of a round is issued before the first is
+// used (GB300: staging 33 MB of weights for 15 rows takes 12 us; one vector at a
+// time took 18).
+constexpr int kUnits = 4;
 __global__ void __launch_bounds__(256) repitch_kernel(const __grid_constant__ RepitchJobs jobs) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t total = jobs.first[jobs.n];
-  for (int64_t u0 = 4 * ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)); u0 < total;
-       u0 += 32 * (int64_t)gridDim.x) {
-    uint4 v[4];
-    __half *dst[4];
+  for (int64_t u0 = kUnits * ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)); u0 < total;
+       u0 += 8 * kUnits * (int64_t)gridDim.x) {
+    int j = 0;
+    while (u0 >= jobs.first[j + 1]) ++j;
+    int per_row = (int)((jobs.job[j].ldd + 255) / 256);
+    int64_t row = (u0 - jobs.first[j]) / per_row;
+    int unit = (int)(u0 - jobs.first[j] - row * per_row);
+    RowBlocks v[kUnits];
+    const __half *src[kUnits];
+    __half *dst[kUnits];
+    int cols[kUnits], at[kUnits];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t u = u0 + k;
+    for (int k = 0; k < kUnits; ++k) {
       dst[k] = nullptr;
-      if (u >= total) continue;
-      int j = 0;
-      while (u >= jobs.first[j + 1]) ++j;
+      if (u0 + k >= total) continue;
       const RepitchJob &job = jobs.job[j];
-      const int64_t per_row = (job.ldd + 255) / 256, i = u - jobs.first[j];
-      const int64_t row = i / per_row;
-      const int col = (int)(i - row * per_row) * 256 + lane * 8;
-      if (col >= job.ldd) continue;
-      v[k] = load_row16<__half, false>(static_cast<const __half *>(job.src) + row * job.lds, col,
-                                       (int)job.cols);
-      dst[k] = static_cast<__half *>(job.dst) + row * job.ldd + col;
+      const int col = unit * 256 + lane * 8;
+      src[k] = static_cast<const __half *>(job.src) + row * job.lds;
+      at[k] = col, cols[k] = (int)job.cols;
+      v[k] = fetch_row16<__half, false>(src[k], col, cols[k]);
+      if (col < job.ldd) dst[k] = static_cast<__half *>(job.dst) + row * job.ldd + col;
+      if (++unit == per_row) {
+        unit = 0;
+        if (++row == job.rows && j + 1 < jobs.n) {
+          row = 0;
+          ++j;
+          per_row = (int)((jobs.job[j].ldd + 255) / 256);
+        }
+      }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (dst[k] != nullptr) *reinterpret_cast<uint4 *>(dst[k]) = v[k];
+    for (int k = 0; k < kUnits; ++k)
+      if (dst[k] != nullptr)
+        *reinterpret_cast<uint4 *>(dst[k]) = take_row16<__half, false>(v[k], src[k], at[k], cols[k]);
   }
 }
 
@@ -235,7 +251,7 @@ cudaError_t launch_repitch(const RepitchJob *jobs, int njobs, int num_sms, cudaS
     a.job[j] = jobs[j];
     a.first[j + 1] = a.first[j] + jobs[j].rows * ((jobs[j].ldd + 255) / 256);
   }
-  const int64_t blocks = (a.first[njobs] + 31) / 32, most = 8 * (int64_t)num_sms;
+  const int64_t blocks = (a.first[njobs] + 8 * kUnits - 1) / (8 * kUnits), most = 8 * (int64_t)num_sms;
   const cudaError_t e = launch_kernel(repitch_kernel, dim3((unsigned)(blocks < most ? blocks : most)),
                                       dim3(256), 0, stream, 1u, a);
   if (e == cudaSuccess) count_launch();

@@ -40,22 +40,34 @@ __device__ __forceinline__ uint4 shift16(uint4 a, uint4 b, int off) {
   }
 }
 
-// The vector of `row` at `col`; elements from `cols` on are zero.
+// A vector as loaded: the one or two blocks it lies in.  fetch_row16 of several
+// vectors before take_row16 of the first keeps all their loads in flight.
+struct RowBlocks {
+  uint4 a, b;
+};
 template <class T, bool ALIGNED>
-__device__ __forceinline__ uint4 load_row16(const T *row, int col, int cols) {
+__device__ __forceinline__ RowBlocks fetch_row16(const T *row, int col, int cols) {
   constexpr int V = kVec<T>;
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (col >= cols) return v;
+  RowBlocks r;
+  r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
+  const int off = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(row) & 15);  // col: whole vectors
+  const uint4 *block = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(row) - off +
+                                                       (int64_t)col * (int)sizeof(T));
+  if (col < cols) r.a = block[0];
+  if constexpr (!ALIGNED) {
+    if (off != 0 && col + V - off / (int)sizeof(T) < cols) r.b = block[1];
+  }
+  return r;
+}
+
+// The elements of a fetched vector; those from `cols` on are zero.
+template <class T, bool ALIGNED>
+__device__ __forceinline__ uint4 take_row16(const RowBlocks &r, const T *row, int col, int cols) {
+  constexpr int V = kVec<T>;
   if constexpr (ALIGNED) {
-    return *reinterpret_cast<const uint4 *>(row + col);
+    return r.a;
   } else {
-    const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);  // col is whole vectors
-    const uint4 *block = reinterpret_cast<const uint4 *>(
-        reinterpret_cast<const uint8_t *>(row) - off + col * (int)sizeof(T));
-    v = block[0];
-    uint4 next = make_uint4(0u, 0u, 0u, 0u);
-    if (off != 0 && col + V - off / (int)sizeof(T) < cols) next = block[1];
-    v = shift16<T>(v, next, off);
+    uint4 v = shift16<T>(r.a, r.b, (int)(reinterpret_cast<uintptr_t>(row) & 15));
     const int valid = cols - col;  // the row's last vector may be short
     if (valid < V) {
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -70,6 +82,12 @@ __device__ __forceinline__ uint4 load_row16(const T *row, int col, int cols) {
     }
     return v;
   }
+}
+
+// The vector of `row` at `col`; elements from `cols` on are zero.
+template <class T, bool ALIGNED>
+__device__ __forceinline__ uint4 load_row16(const T *row, int col, int cols) {
+  return take_row16<T, ALIGNED>(fetch_row16<T, ALIGNED>(row, col, cols), row, col, cols);
 }
 
 // Store N vectors of `row`, vector k at column col + k * LANES * V.  The whole
