@@ -51,17 +51,20 @@ constexpr bool kXT = DGEMM_FUSED_UNIT == 2;  // tokens stored K x M: read MN-maj
 constexpr bool kWT = DGEMM_FUSED_UNIT == 1;  // weights stored N x K: read K-major
 
 struct SmallCfg {
-  static constexpr int ES = 2, UMMA_K = 16, BOX = 64;
+  static constexpr int UMMA_K = 16, BOX = 64;
   static constexpr int TF = 128;              // features (MMA rows) of a tile
   static constexpr int W_CHUNK = TF * 128;    // weights of 64 k
-  static constexpr int MAX_STAGES = 8, MAX_SPLITS = 8, MAX_NT = 256;
-  static constexpr int THREADS = 192;         // producer, MMA, four drain warps
+  static constexpr int MAX_STAGES = 8, MAX_SPLITS = 8;
   static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
   // bars (full[8], empty[8], accf), TMEM slot, abort flag; 1024 for alignment
   static constexpr int TAIL_BYTES = (2 * MAX_STAGES + 1) * 8 + 16 + 1024;
   static constexpr int BUDGET2 = 113 * 1024 - TAIL_BYTES;  // two CTAs per SM
   static constexpr int BUDGET1 = 226 * 1024 - TAIL_BYTES;  // one
 };
+
+// producer, MMA, four drain warps; without a K split two more for the epilogue
+template <bool SPLIT>
+constexpr int kThreads = SPLIT ? 192 : 256;
 
 // Site codes of the bounded waits.
 enum : int {
@@ -82,7 +85,6 @@ struct SmallArgs {
   int nt, kd, stages, splits;
   uint32_t idesc;
   uint32_t tmem_cols;
-  int vec;  // 8 features per thread: every row of every output and input is aligned
   const void *in0, *in1, *bias;
   int64_t ldi0, ldi1;
   void *out[3];
@@ -90,11 +92,17 @@ struct SmallArgs {
   int *watchdog;
 };
 
-template <class T, Epi EPI>
-__global__ void __launch_bounds__(SmallCfg::THREADS, 2)
+// SPLIT: a tile's K range is shared by a cluster.  AL: every row of every
+// output and input of the epilogue is 16-byte aligned.  (Template arguments
+// because a short kernel's time is partly that of fetching its instructions:
+// one kernel for all four took 0.3 us longer for 1 x 1024 x 1024.)
+template <class T, Epi EPI, bool SPLIT, bool AL>
+__global__ void __launch_bounds__(kThreads<SPLIT>, 2)
     fused_small_kernel(const __grid_constant__ SmallMaps maps,
                        const __grid_constant__ SmallArgs p) {
   using G = SmallCfg;
+  constexpr int THREADS = kThreads<SPLIT>;
+  const int splits = SPLIT ? p.splits : 1;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -117,14 +125,14 @@ __global__ void __launch_bounds__(SmallCfg::THREADS, 2)
   constexpr int TF = EPI == Epi::kGated ? G::TF / 2 : G::TF;  // output features of a tile
   const int tiles_t = (p.M + p.nt - 1) / p.nt, tiles_f = (p.N + TF - 1) / TF;
   const int tiles1 = tiles_t * tiles_f;
-  const int unit = blockIdx.x / p.splits, part = blockIdx.x % p.splits;
+  const int unit = SPLIT ? blockIdx.x / splits : blockIdx.x, part = SPLIT ? blockIdx.x % splits : 0;
   const bool second = unit >= tiles1;  // kPair: a tile of the second product
   const int tile = second ? unit - tiles1 : unit;
   const int f0 = (tile / tiles_t) * TF, t0 = (tile % tiles_t) * p.nt;
   const bool sum = EPI == Epi::kLinear && p.dual == (int)Dual::kSum;
   const int kb1 = (p.K + bk - 1) / bk;
   const int kblocks = sum ? 2 * kb1 : kb1;
-  const int per = (kblocks + p.splits - 1) / p.splits;
+  const int per = (kblocks + splits - 1) / splits;
   const int kb_begin = min(kblocks, part * per), kb_end = min(kblocks, part * per + per);
 
   if (threadIdx.x == 0) {
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(SmallCfg::THREADS, 2)
       umma_commit(accf_bar);  // every MMA issued above has completed
       if (!mbar_wait(accf_bar, 0)) atomicCAS(p.watchdog, 0, kSite4MmaDrain);
     }
-  } else {
+  } else if (warp < 6) {
     // ------------------------------- drain: partial tile to shared memory
     const int quarter = warp & 3;
     const bool ok = !*abort_flag && mbar_wait(accf_bar, 0);
@@ -266,30 +274,40 @@ __global__ void __launch_bounds__(SmallCfg::THREADS, 2)
   // Every thread of every CTA of the cluster gets here, also after a bounded
   // wait gave up.
   __syncthreads();
-  if (p.splits > 1) {
+  bool aborted = false;
+  uint32_t at[G::MAX_SPLITS];
+  if constexpr (SPLIT) {
     __syncwarp();
     cluster_sync();
-  }
-  bool aborted = false;
-  for (int s = 0; s < p.splits; ++s)
-    aborted |= ld_cluster_s32(mapa_shared(smem_u32(const_cast<int *>(abort_flag)), (uint32_t)s)) != 0;
-  if (!aborted) {
-    const int live = min(p.nt, p.M - t0);
-    const int feats = min(TF, p.N - f0);
-    uint32_t at[G::MAX_SPLITS];
 #pragma unroll
     for (int s = 0; s < G::MAX_SPLITS; ++s)
-      at[s] = s < p.splits ? mapa_shared(base, (uint32_t)s) : 0u;
+      at[s] = s < splits ? mapa_shared(base, (uint32_t)s) : 0u;
+    // looked at before anything is stored, so that these loads and those of the
+    // partials are in flight together
+    const uint32_t flag = smem_u32(const_cast<int *>(abort_flag)) - base;
+#pragma unroll
+    for (int s = 0; s < G::MAX_SPLITS; ++s)
+      if (s < splits) aborted |= ld_cluster_s32(at[s] + flag) != 0;
+  } else {
+    aborted = *abort_flag != 0;
+  }
+  {
+    const int live = min(p.nt, p.M - t0);
+    const int feats = min(TF, p.N - f0);
     auto sum4 = [&](uint32_t off) {  // parts added in K order
-      float4 v[G::MAX_SPLITS];
+      if constexpr (SPLIT) {
+        float4 v[G::MAX_SPLITS];
 #pragma unroll
-      for (int s = 0; s < G::MAX_SPLITS; ++s)
-        if (s < p.splits) v[s] = ld_cluster_f4(at[s] + off);
-      float4 r = v[0];
+        for (int s = 0; s < G::MAX_SPLITS; ++s)
+          if (s < splits) v[s] = ld_cluster_f4(at[s] + off);
+        float4 r = v[0];
 #pragma unroll
-      for (int s = 1; s < G::MAX_SPLITS; ++s)
-        if (s < p.splits) r.x += v[s].x, r.y += v[s].y, r.z += v[s].z, r.w += v[s].w;
-      return r;
+        for (int s = 1; s < G::MAX_SPLITS; ++s)
+          if (s < splits) r.x += v[s].x, r.y += v[s].y, r.z += v[s].z, r.w += v[s].w;
+        return r;
+      } else {
+        return *reinterpret_cast<const float4 *>(smem + off);
+      }
     };
     constexpr int kOuts = EPI == Epi::kLinear ? 2 : 3;
     const bool pair_out = EPI == Epi::kLinear && p.dual == (int)Dual::kPair;
@@ -301,60 +319,55 @@ __global__ void __launch_bounds__(SmallCfg::THREADS, 2)
     const T *bias = static_cast<const T *>(p.bias);
     const bool has_in0 = in0 != nullptr, kept = !pair_out && p.out[1] != nullptr;
     constexpr int Q = TF / 8;  // threads per token
-    auto finish = [&](auto aligned) {
-      constexpr bool AL = decltype(aligned)::value;
-      const int n = live * Q, end = f0 + feats;
-      // whole warps go round together: their stores put blocks together
-      for (int e = part * G::THREADS + threadIdx.x; e - lane < n; e += p.splits * G::THREADS) {
-        const int t = e / Q, f = 8 * (e % Q), col = f0 + f;
-        const bool in = t < live && f < feats;
-        const int64_t row = t0 + t;
-        float a[8], b[8];
-        uint32_t i0[4], i1[4], w[3][4];
-        auto get = [&](const T *m, uint32_t (&v)[4]) {
-          const uint4 x = load_row16<T, AL>(m, col, end);
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        };
-        if (in) {
-          if (EPI != Epi::kGated && has_in0) get(in0 + row * p.ldi0, i0);
-          if (EPI == Epi::kGatedBwd) get(in1 + row * p.ldi1, i1);
+    const int n = live * Q, end = f0 + feats;
+    // whole warps go round together: their stores put blocks together
+#pragma unroll 1
+    for (int e = part * THREADS + threadIdx.x; e - lane < n; e += splits * THREADS) {
+      const int t = e / Q, f = 8 * (e % Q), col = f0 + f;
+      const bool in = t < live && f < feats;
+      const int64_t row = t0 + t;
+      float a[8], b[8];
+      uint32_t i0[4], i1[4], w[3][4];
+      auto get = [&](const T *m, uint32_t (&v)[4]) {
+        const uint4 x = load_row16<T, AL>(m, col, end);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      };
+      if (in) {
+        if (EPI != Epi::kGated && has_in0) get(in0 + row * p.ldi0, i0);
+        if (EPI == Epi::kGatedBwd) get(in1 + row * p.ldi1, i1);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 v = sum4((uint32_t)((t * G::TF + f + 4 * h) * 4));
-            a[4 * h] = v.x, a[4 * h + 1] = v.y, a[4 * h + 2] = v.z, a[4 * h + 3] = v.w;
-            if constexpr (EPI == Epi::kGated) {
-              const float4 u = sum4((uint32_t)((t * G::TF + TF + f + 4 * h) * 4));
-              b[4 * h] = u.x, b[4 * h + 1] = u.y, b[4 * h + 2] = u.z, b[4 * h + 3] = u.w;
-            }
+        for (int h = 0; h < 2; ++h) {
+          const float4 v = sum4((uint32_t)((t * G::TF + f + 4 * h) * 4));
+          a[4 * h] = v.x, a[4 * h + 1] = v.y, a[4 * h + 2] = v.z, a[4 * h + 3] = v.w;
+          if constexpr (EPI == Epi::kGated) {
+            const float4 u = sum4((uint32_t)((t * G::TF + TF + f + 4 * h) * 4));
+            b[4 * h] = u.x, b[4 * h + 1] = u.y, b[4 * h + 2] = u.z, b[4 * h + 3] = u.w;
           }
-          if (EPI == Epi::kLinear && bias != nullptr) {
-            uint32_t v[4];
-            get(bias, v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 c = unpack2<T>(v[j]);
-              a[2 * j] += c.x, a[2 * j + 1] += c.y;
-            }
-          }
-          epilogue_row<EPI, T, 4>(p.act, has_in0, kept, a, b, i0, i1, w[0], w[1], w[2]);
         }
+        if (EPI == Epi::kLinear && bias != nullptr) {
+          uint32_t v[4];
+          get(bias, v);
 #pragma unroll
-        for (int o = 0; o < kOuts; ++o) {
-          int slot;
-          if (output(o, &slot)) {
-            const uint4 v[1] = {make_uint4(w[o][0], w[o][1], w[o][2], w[o][3])};
-            store_row16<T, AL, 1, Q>(static_cast<T *>(p.out[slot]) + row * p.ldo[slot],
-                                     in ? col : end, end, v);
+          for (int j = 0; j < 4; ++j) {
+            const float2 c = unpack2<T>(v[j]);
+            a[2 * j] += c.x, a[2 * j + 1] += c.y;
           }
+        }
+        epilogue_row<EPI, T, 4>(p.act, has_in0, kept, a, b, i0, i1, w[0], w[1], w[2]);
+      }
+      if (aborted) break;  // the same for the whole cluster
+#pragma unroll
+      for (int o = 0; o < kOuts; ++o) {
+        int slot;
+        if (output(o, &slot)) {
+          const uint4 v[1] = {make_uint4(w[o][0], w[o][1], w[o][2], w[o][3])};
+          store_row16<T, AL, 1, Q>(static_cast<T *>(p.out[slot]) + row * p.ldo[slot],
+                                   in ? col : end, end, v);
         }
       }
-    };
-    if (p.vec)
-      finish(std::true_type{});
-    else
-      finish(std::false_type{});
+    }
   }
-  if (p.splits > 1) {
+  if constexpr (SPLIT) {
     __syncwarp();
     cluster_sync();  // no CTA leaves while a peer may still read its partial
   }
@@ -382,6 +395,28 @@ bool small_maps(CUtensorMap *tw, CUtensorMap *tx, CUtensorMapDataType dt, const 
   const bool x = kXT ? make_map(tx, X, dt, 2, p.K, p.M, ldx, 64, bk, swz)
                      : make_map(tx, X, dt, 2, p.M, p.K, ldx, 64, nt, swz);
   return w && x;
+}
+
+// Launch one instance, opted in to all of the shared memory once per device.
+template <auto KERNEL>
+cudaError_t launch_one(unsigned grid, bool split, int smem, cudaStream_t stream, unsigned cluster,
+                       const SmallMaps &maps, const SmallArgs &args) {
+  using G = SmallCfg;
+  static std::atomic<bool> attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             G::BUDGET1 + G::TAIL_BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  e = launch_kernel(KERNEL, dim3(grid), dim3(split ? kThreads<true> : kThreads<false>), (size_t)smem, stream, cluster, maps,
+                    args);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 template <class T, Epi EPI>
@@ -424,30 +459,20 @@ cudaError_t launch_small(const FusedGemm &p, const SmallPlan &plan, int *watchdo
   a.ldi0 = p.ldi0, a.ldi1 = p.ldi1;
   a.out[0] = p.out0, a.out[1] = p.out1, a.out[2] = p.out2;
   a.ldo[0] = p.ldo0, a.ldo[1] = p.ldo1, a.ldo[2] = p.ldo2;
-  a.vec = p.N % 8 == 0 && rows_aligned(p.in0, p.in0 ? p.ldi0 : 0) &&
-          rows_aligned(p.in1, p.in1 ? p.ldi1 : 0) && rows_aligned(p.bias, 0);
-  for (int i = 0; i < 3; ++i) a.vec = a.vec && rows_aligned(a.out[i], a.out[i] ? a.ldo[i] : 0);
+  bool vec = p.N % 8 == 0 && rows_aligned(p.in0, p.in0 ? p.ldi0 : 0) &&
+             rows_aligned(p.in1, p.in1 ? p.ldi1 : 0) && rows_aligned(p.bias, 0);
+  for (int i = 0; i < 3; ++i) vec = vec && rows_aligned(a.out[i], a.out[i] ? a.ldo[i] : 0);
   a.watchdog = watchdog;
-  auto kern = fused_small_kernel<T, EPI>;
-  static std::atomic<bool> attr_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             G::BUDGET1 + G::TAIL_BYTES);
-    if (e != cudaSuccess) return e;
-    attr_set[dev].store(true, std::memory_order_release);
-  }
   const int tf = EPI == Epi::kGated ? G::TF / 2 : G::TF;
   const int64_t tiles = (int64_t)((p.M + plan.nt - 1) / plan.nt) * ((p.N + tf - 1) / tf) *
                         (p.dual == Dual::kPair ? 2 : 1);
   if (tiles * plan.splits > 0x3fffffff) return cudaErrorInvalidValue;
-  e = launch_kernel(kern, dim3((unsigned)(tiles * plan.splits)), dim3(G::THREADS), (size_t)smem,
-                    stream, (unsigned)plan.splits, maps, a);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  const unsigned grid = (unsigned)(tiles * plan.splits), cluster = (unsigned)plan.splits;
+  if (plan.splits > 1)
+    return vec ? launch_one<fused_small_kernel<T, EPI, true, true>>(grid, true, smem, stream, cluster, maps, a)
+               : launch_one<fused_small_kernel<T, EPI, true, false>>(grid, true, smem, stream, cluster, maps, a);
+  return vec ? launch_one<fused_small_kernel<T, EPI, false, true>>(grid, false, smem, stream, 1u, maps, a)
+             : launch_one<fused_small_kernel<T, EPI, false, false>>(grid, false, smem, stream, 1u, maps, a);
 }
 
 template <class T>
@@ -488,7 +513,7 @@ int64_t small_resident(const SmallPlan &plan, int num_sms) {
   std::atomic<int> &slot = cache[dev][plan.per_sm][plan.splits];
   int n = slot.load(std::memory_order_relaxed);
   if (n == 0) {
-    auto kern = fused_small_kernel<__half, Epi::kLinear>;
+    auto kern = fused_small_kernel<__half, Epi::kLinear, true, true>;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)plan.splits;
@@ -496,7 +521,7 @@ int64_t small_resident(const SmallPlan &plan, int num_sms) {
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)plan.splits);
-    cfg.blockDim = dim3(G::THREADS);
+    cfg.blockDim = dim3(kThreads<true>);
     cfg.dynamicSmemBytes = (size_t)((plan.per_sm == 2 ? G::BUDGET2 : G::BUDGET1) + G::TAIL_BYTES);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
