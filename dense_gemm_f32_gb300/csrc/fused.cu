@@ -22,11 +22,11 @@ int knob(const char *name, int lo, int hi) {
 
 // Time models (microseconds) of the two kernels, fitted to 50 shapes of one to
 // 16384 tokens with every cut of the small kernel on GB300, in a graph with
-// operands rotating through more than L2.  Choosing by them is within 4% of
-// the best cut on average (1.17 times at worst); 256-row tiles once they fill a
+// operands rotating through more than L2.  Choosing by them is within 2% of
+// the best cut on average (1.13 times at worst); 256-row tiles once they fill a
 // quarter of the SMs, and 128-token tiles below that, were 30% off on average.
 //
-// Pair kernel: a wave of 256 x 256 tiles takes 0.331 us per 64 k, or as long as
+// Pair kernel: a wave of 256 x 256 tiles takes 0.31 us per 64 k, or as long as
 // writing its outputs.
 double pair_time(const FusedGemm &p, int num_sms) {
   const int tn = p.epi == Epi::kGated ? 128 : 256;
@@ -36,26 +36,26 @@ double pair_time(const FusedGemm &p, int num_sms) {
   const int kblocks = (p.K + 63) / 64 * (p.dual == Dual::kSum ? 2 : 1);
   const int outs = p.dual == Dual::kPair ? 1 : (p.out0 != nullptr) + (p.out1 != nullptr) + (p.out2 != nullptr);
   const double written = 2.0 * (double)p.M * p.N * outs * products;
-  const double main = waves * (kblocks * 0.331), out = written / 2.4e6;
-  return 6.04 + (main > out ? main : out);
+  const double main = waves * (kblocks * 0.31), out = written / 2.4e6;
+  return 6.1 + (main > out ? main : out);
 }
 
-// Small kernel: a stage costs a CTA its wait (0.255 us, and 0.546 us shared by
-// the stages in flight), its bytes at 96 GB/s, or its share of the SM's 127
-// GB/s when two run there; all together at most 16.9 TB/s from L2; a tile's
+// Small kernel: a stage costs a CTA its wait (0.197 us, and 0.959 us shared by
+// the stages in flight), its bytes at 96 GB/s, or its share of the SM's 312
+// GB/s when two run there; all together at most 17.8 TB/s from L2; a tile's
 // drain and epilogue grow with its tokens, and joining the parts of a K split
-// costs 1 us.
+// costs 1.6 us.
 double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int64_t resident) {
   const double nt = plan.nt, share = plan.per_sm, stage = (128 + nt) * 128 * plan.kd;
   const int64_t parts = (kblocks + plan.splits - 1) / plan.splits;
   const int64_t waves = (tiles + resident - 1) / resident;
-  double per = 0.546 / small_stages(plan) + 0.255;
-  if (per < stage / 96.5e3) per = stage / 96.5e3;
-  if (per < stage * share / 126.7e3) per = stage * share / 126.7e3;
-  const double loads = waves * (3.0 + parts * per);
-  const double l2 = parts * stage * tiles * plan.splits / 16.9e6;
-  const double tail = 0.029 * nt + (plan.splits > 1 ? 0.97 : 0.0);
-  return 1.24 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
+  double per = 0.959 / small_stages(plan) + 0.197;
+  if (per < stage / 96.2e3) per = stage / 96.2e3;
+  if (per < stage * share / 312e3) per = stage * share / 312e3;
+  const double loads = waves * (2.18 + parts * per);
+  const double l2 = parts * stage * tiles * plan.splits / 17.8e6;
+  const double tail = plan.splits > 1 ? 0.0283 * nt + 1.61 : 0.0124 * nt;
+  return 1.27 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
 }
 
 // The kernel and its cut for a product.  DGEMM_FUSED_PAIR=0 / =1 forces the
