@@ -66,6 +66,11 @@ struct SmallCfg {
 template <bool SPLIT>
 constexpr int kThreads = SPLIT ? 192 : 256;
 
+// Stages of weights that a CTA sends for before the kernel ahead of it on the
+// stream is done: 1 x 4096 x 14336 22.1 -> 21.7 us, gated block 64 x 1024 x 4096
+// 16.3 -> 15.4; from 8 on slower than none (23.3 us with 16).
+constexpr int kAheadStages = 3;
+
 // Site codes of the bounded waits.
 enum : int {
   kSite4ProducerEmpty = 0xb1,
@@ -147,6 +152,26 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
   if (warp == 0 && lane == 0 && p.K > 0) {
     tma_prefetch_desc(&maps.w);
     tma_prefetch_desc(&maps.x);
+    // The first weights towards L2 while the kernel before this one on the
+    // stream is still at work.
+    const int ahead = min(kb_end, kb_begin + kAheadStages);
+    for (int kb = kb_begin; kb < ahead; ++kb) {
+      const bool set2 = second || kb >= kb1;
+      const int k0 = (kb >= kb1 ? kb - kb1 : kb) * bk;
+      const CUtensorMap *mw = set2 ? &maps.w2 : &maps.w;
+      if constexpr (kWT) {
+        for (int c = 0; c < p.kd; ++c) {
+          tma_prefetch_2d(mw, k0 + c * G::BOX, f0);
+          if constexpr (EPI == Epi::kGated) tma_prefetch_2d(&maps.w2, k0 + c * G::BOX, f0);
+        }
+      } else {
+        tma_prefetch_2d(mw, f0, k0);
+        if constexpr (EPI == Epi::kGated)
+          tma_prefetch_2d(&maps.w2, f0, k0);
+        else
+          tma_prefetch_2d(mw, f0 + G::BOX, k0);
+      }
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), p.tmem_cols);

@@ -83,6 +83,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// Bring the box at (x, y) into L2 only.  L2 is where all writers and readers of
+// global memory meet, so this is sound before griddepcontrol.wait: a line that
+// an earlier kernel still writes is written there.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x),
+               "r"(y)
+               : "memory");
+}
+
 // 3-D tiled load of the box at (x, y, z); same completion rule as the 2-D
 // load.  The box lands in shared memory with x fastest, then y, then z.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
