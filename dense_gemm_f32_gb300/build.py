@@ -28,7 +28,7 @@ UNITS = ([("api.cu", "api", []), ("staging.cu", "staging", []), ("ops_api.cu", "
           ("norm.cu", "norm", []), ("rowops.cu", "rowops", []),
           ("fused.cu", "fused", [])]
          + [("fused_pair.cu", f"fused_pair_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(3)]
-         + [("fused_small.cu", f"fused_small_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(3)]
+         + [("fused_small.cu", f"fused_small_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(4)]
          + [("simt.cu", f"simt_{u}", [f"-DDGEMM_SIMT_UNIT={u}"]) for u in range(4)]
          + [("tc.cu", f"tc_{u}", [f"-DDGEMM_TC_UNIT={u}"]) for u in range(4)])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,9 +1,12 @@
 // fused.cu -- the fused products of the feed-forward operators: operands that
 // TMA cannot read are staged first, then one kernel runs.
+#include <atomic>
 #include <cstdint>
 #include <cstdlib>
+#include <new>
 #include <cuda_runtime.h>
 
+#include "../../include/dgemm.h"
 #include "api_common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -45,97 +48,180 @@ double pair_time(const FusedGemm &p, int num_sms) {
 // GB/s when two run there; all together at most 17.8 TB/s from L2; a tile's
 // drain and epilogue grow with its tokens, and joining the parts of a K split
 // costs 1.6 us.
-double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int64_t resident) {
+// `tiles` of this product among `all` of the launch.
+double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int64_t resident,
+                  int64_t all) {
   const double nt = plan.nt, share = plan.per_sm, stage = (128 + nt) * 128 * plan.kd;
   const int64_t parts = (kblocks + plan.splits - 1) / plan.splits;
-  const int64_t waves = (tiles + resident - 1) / resident;
+  const int64_t waves = (all + resident - 1) / resident;
   double per = 0.959 / small_stages(plan) + 0.197;
   if (per < stage / 96.2e3) per = stage / 96.2e3;
   if (per < stage * share / 312e3) per = stage * share / 312e3;
   const double loads = waves * (2.18 + parts * per);
-  const double l2 = parts * stage * tiles * plan.splits / 17.8e6;
+  const double l2 = parts * stage * (all > tiles ? all : tiles) * plan.splits / 17.8e6;
   const double tail = plan.splits > 1 ? 0.0283 * nt + 1.61 : 0.0124 * nt;
   return 1.27 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
 }
 
-// The kernel and its cut for a product.  DGEMM_FUSED_PAIR=0 / =1 forces the
-// kernel, DGEMM_FUSED_NT / _KD / _SPLITS parts of the small kernel's cut.
-struct Choice {
-  bool pair;
-  SmallPlan plan;
+int64_t tiles_of(const FusedGemm &p, int nt) {
+  const int tf = p.epi == Epi::kGated ? 64 : 128;
+  return (int64_t)((p.N + tf - 1) / tf) * ((p.M + nt - 1) / nt) * (p.dual == Dual::kPair ? 2 : 1);
+}
+int64_t kblocks_of(const FusedGemm &p, int kd) {
+  return (int64_t)((p.K + 64 * kd - 1) / (64 * kd)) * (p.dual == Dual::kSum ? 2 : 1);
+}
+
+// Tiles of the small kernel resident at once, by CTAs per SM and K split.
+struct Residency {
+  int64_t tiles[3][9];
+  explicit Residency(int num_sms) {
+    for (int per_sm = 1; per_sm <= 2; ++per_sm)
+      for (int s = 1; s <= 8; ++s) tiles[per_sm][s] = small_resident({16, 1, s, per_sm}, num_sms);
+  }
 };
-Choice choose(const FusedGemm &p, int num_sms) {
-  const int force = p.K == 0 ? 0 : knob("DGEMM_FUSED_PAIR", 0, 1);  // an empty sum is the small one's
-  Choice c = {force == 1, {}};
-  if (c.pair) return c;
+// The current device's, made once.
+const Residency *residency(int num_sms) {
+  static std::atomic<const Residency *> made[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  const Residency *r = made[dev].load(std::memory_order_acquire);
+  if (r == nullptr) {
+    const Residency *mine = new (std::nothrow) Residency(num_sms);
+    if (mine == nullptr) return nullptr;
+    if (made[dev].compare_exchange_strong(r, mine, std::memory_order_acq_rel))
+      r = mine;
+    else
+      delete mine;
+  }
+  return r;
+}
+
+// The best cut of `n` products as one launch of the small kernel, and its time.
+// Token counts tried are the same for all, each product's cut down to its own;
+// stages hold 128 k where two of them fit beside another CTA's.
+// DGEMM_FUSED_NT / _KD / _SPLITS force parts of the cut.
+double small_plan(const FusedGemm *ps, int n, const Residency &res, SmallPlan *best_plans) {
   const int f_nt = knob("DGEMM_FUSED_NT", 16, 256), f_kd = knob("DGEMM_FUSED_KD", 1, 2);
   const int f_splits = knob("DGEMM_FUSED_SPLITS", 1, 8);
-  const int step = p.a_t ? 64 : 16, tf = p.epi == Epi::kGated ? 64 : 128;
-  const int64_t tiles_f = (int64_t)((p.N + tf - 1) / tf) * (p.dual == Dual::kPair ? 2 : 1);
   double best = 0;
-  for (int nt : {16, 32, 48, 64, 96, 128, 192, 256}) {
-    if (f_nt >= 0) nt = f_nt;
-    nt = (nt + step - 1) / step * step;
-    const int64_t tiles = tiles_f * ((p.M + nt - 1) / nt);
-    // stages of 128 k where two of them fit beside another CTA's
-    const int kd = f_kd == 1 || nt > 64 || (f_kd < 0 && p.K <= 64) ? 1 : 2;
-    const int64_t kblocks = (int64_t)((p.K + 64 * kd - 1) / (64 * kd)) * (p.dual == Dual::kSum ? 2 : 1);
+  for (int cap : {16, 32, 48, 64, 96, 128, 192, 256}) {
+    SmallPlan plans[kMaxBatch];
+    int64_t tiles = 0, kmax = 0;
+    int widest = 0;
+    bool last = true;
+    for (int j = 0; j < n; ++j) {
+      const int step = ps[j].a_t ? 64 : 16, all = (ps[j].M + step - 1) / step * step;
+      int nt = ((f_nt >= 0 ? f_nt : cap) + step - 1) / step * step;
+      if (f_nt < 0 && nt > all) nt = all;
+      last = last && nt >= all;
+      const int kd = f_kd == 1 || nt > 64 || (f_kd < 0 && ps[j].K <= 64) ? 1 : 2;
+      plans[j] = {nt, kd, 1, 1};
+      tiles += tiles_of(ps[j], nt);
+      const int64_t kb = kblocks_of(ps[j], kd);
+      kmax = kmax > kb ? kmax : kb;
+      widest = widest > nt ? widest : nt;
+    }
     for (int s : {1, 2, 3, 4, 6, 8}) {
       if (f_splits >= 0) s = f_splits;
-      else if (s > 1 && s > kblocks) break;
+      else if (s > 1 && s > kmax) break;
       // all of an SM's shared memory for one CTA's stages where that holds every
       // tile at once
-      SmallPlan plan = {nt, kd, s, 1};
-      int64_t resident = small_resident(plan, num_sms);
-      if (tiles > resident && nt <= 128) {
-        plan.per_sm = 2;
-        resident = small_resident(plan, num_sms);
+      for (int j = 0; j < n; ++j) plans[j].splits = s, plans[j].per_sm = 1;
+      int64_t resident = res.tiles[1][s];
+      if (tiles > resident && widest <= 128) {
+        for (int j = 0; j < n; ++j) plans[j].per_sm = 2;
+        resident = res.tiles[2][s];
       }
-      const double t = small_time(tiles, kblocks, plan, resident);
+      double t = 0;
+      for (int j = 0; j < n; ++j) {
+        const double tj = small_time(tiles_of(ps[j], plans[j].nt), kblocks_of(ps[j], plans[j].kd),
+                                     plans[j], resident, tiles);
+        t = t > tj ? t : tj;
+      }
       if (best == 0 || t < best) {
         best = t;
-        c.plan = plan;
+        for (int j = 0; j < n; ++j) best_plans[j] = plans[j];
       }
       if (f_splits >= 0) break;
     }
-    if (f_nt >= 0 || nt >= p.M) break;
+    if (f_nt >= 0 || last) break;
   }
-  if (force < 0) c.pair = pair_time(p, num_sms) < best;
-  return c;
+  return best;
 }
 
-}  // namespace
+cudaError_t run_pair(const FusedGemm &p, int *wd, cudaStream_t stream) {
+  if (p.a_t) return p.b_t ? cudaErrorInvalidValue : launch_fused_pair_unit_2(p, wd, stream);
+  return p.b_t ? launch_fused_pair_unit_1(p, wd, stream) : launch_fused_pair_unit_0(p, wd, stream);
+}
 
-cudaError_t launch_fused(const FusedGemm &p0, int num_sms, cudaStream_t stream) {
-  FusedGemm p = p0;
-  int *wd = watchdog_address();
-  if (wd == nullptr) return cudaErrorInvalidSymbol;
-  Stager st(num_sms, stream);
+cudaError_t run_small(const FusedGemm *p, const SmallPlan *plans, int n, int *wd,
+                      cudaStream_t stream) {
+  const bool half = p->dtype == DGEMM_DTYPE_F16, linear = p->epi == Epi::kLinear;
+  return linear ? (half ? launch_fused_small_unit_1(p, plans, n, wd, stream)
+                        : launch_fused_small_unit_0(p, plans, n, wd, stream))
+                : (half ? launch_fused_small_unit_3(p, plans, n, wd, stream)
+                        : launch_fused_small_unit_2(p, plans, n, wd, stream));
+}
+
+// DGEMM_FUSED_PAIR=0 / =1 forces the kernel; an empty sum is the small one's.
+int forced_kernel(const FusedGemm &p) {
+  return p.K == 0 ? 0 : knob("DGEMM_FUSED_PAIR", 0, 1);
+}
+
+void stage_operands(Stager &st, FusedGemm &p) {
   const int ar = p.a_t ? p.K : p.M, ac = p.a_t ? p.M : p.K;
   const int br = p.b_t ? p.N : p.K, bc = p.b_t ? p.K : p.N;
   st.add(p.A, p.lda, ar, ac);
   st.add(p.B, p.ldb, br, bc);
   if (p.dual == Dual::kSum || p.dual == Dual::kPair) st.add(p.A2, p.lda2, ar, ac);
   if (p.dual != Dual::kNone) st.add(p.B2, p.ldb2, br, bc);
+}
+
+}  // namespace
+
+cudaError_t launch_fused_batch(const FusedGemm *ps, int n, int num_sms, cudaStream_t stream) {
+  if (n < 1 || n > kMaxBatch) return n == 0 ? cudaSuccess : cudaErrorInvalidValue;
+  int *wd = watchdog_address();
+  if (wd == nullptr) return cudaErrorInvalidSymbol;
+  const Residency *table = residency(num_sms);
+  if (table == nullptr) return cudaErrorInvalidDevice;
+  const Residency &res = *table;
+  FusedGemm p[kMaxBatch];
+  Stager st(num_sms, stream);
+  for (int j = 0; j < n; ++j) {
+    p[j] = ps[j];
+    stage_operands(st, p[j]);
+  }
   cudaError_t e = st.run();
   if (e == cudaSuccess) {
-    const int unit = p.a_t ? 2 : p.b_t ? 1 : 0;
-    if (p.a_t && p.b_t) {
-      e = cudaErrorInvalidValue;
+    // each by itself, on the kernel that is quicker for it
+    SmallPlan alone[kMaxBatch], together[kMaxBatch];
+    bool pair[kMaxBatch];
+    double sum = 0;
+    for (int j = 0; j < n; ++j) {
+      const int force = forced_kernel(p[j]);
+      const double small = small_plan(&p[j], 1, res, &alone[j]);
+      const double big = pair_time(p[j], num_sms);
+      pair[j] = force >= 0 ? force == 1 : big < small;
+      sum += pair[j] ? big : small;
+    }
+    // DGEMM_FUSED_BATCH=0 / =1 forces the choice
+    const int force = knob("DGEMM_FUSED_BATCH", 0, 1);
+    const bool batch = n > 1 && force != 0 &&
+                       (small_plan(p, n, res, together) < sum || force == 1);
+    if (batch) {
+      e = run_small(p, together, n, wd, stream);
     } else {
-      const Choice c = choose(p, num_sms);
-      if (c.pair)
-        e = unit == 0   ? launch_fused_pair_unit_0(p, wd, stream)
-            : unit == 1 ? launch_fused_pair_unit_1(p, wd, stream)
-                        : launch_fused_pair_unit_2(p, wd, stream);
-      else
-        e = unit == 0   ? launch_fused_small_unit_0(p, c.plan, wd, stream)
-            : unit == 1 ? launch_fused_small_unit_1(p, c.plan, wd, stream)
-                        : launch_fused_small_unit_2(p, c.plan, wd, stream);
+      for (int j = 0; j < n && e == cudaSuccess; ++j)
+        e = pair[j] ? run_pair(p[j], wd, stream) : run_small(&p[j], &alone[j], 1, wd, stream);
     }
   }
   const cudaError_t e2 = st.release();
   return e == cudaSuccess ? e2 : e;
+}
+
+cudaError_t launch_fused(const FusedGemm &p, int num_sms, cudaStream_t stream) {
+  return launch_fused_batch(&p, 1, num_sms, stream);
 }
 
 // ------------------------------------------------------------------ Stager

@@ -20,6 +20,8 @@
 //    aligned (rowvec.cuh).
 //  * kGated: the tile's 128 rows are 64 features of Wg and the same 64 of Wu,
 //    so one MMA stream gives both projections of a hidden unit in one tile.
+//  * Up to three independent products (a backward pass's) go out as one launch,
+//    their tiles one after the other in one grid.
 //  * Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>
@@ -36,7 +38,8 @@
 #include "tc_tile.cuh"
 #include "tmap.cuh"
 
-// Compiled once per operand layout (DGEMM_FUSED_UNIT, as in fused_pair.cu).
+// Compiled once per type and kind of epilogue (DGEMM_FUSED_UNIT): 0: bf16
+// linear, 1: fp16 linear, 2: bf16 gated, 3: fp16 gated.
 #ifndef DGEMM_FUSED_UNIT
 #define DGEMM_FUSED_UNIT 0
 #endif
@@ -47,15 +50,17 @@
 namespace dg {
 namespace {
 
-constexpr bool kXT = DGEMM_FUSED_UNIT == 2;  // tokens stored K x M: read MN-major
-constexpr bool kWT = DGEMM_FUSED_UNIT == 1;  // weights stored N x K: read K-major
+#if DGEMM_FUSED_UNIT & 1
+using Elem = __half;
+#else
+using Elem = __nv_bfloat16;
+#endif
 
 struct SmallCfg {
-  static constexpr int UMMA_K = 16, BOX = 64;
+  static constexpr int BOX = 64;              // elements in a 128-byte swizzle row
   static constexpr int TF = 128;              // features (MMA rows) of a tile
   static constexpr int W_CHUNK = TF * 128;    // weights of 64 k
   static constexpr int MAX_STAGES = 8, MAX_SPLITS = 8;
-  static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
   // bars (full[8], empty[8], accf), TMEM slot, abort flag; 1024 for alignment
   static constexpr int TAIL_BYTES = (2 * MAX_STAGES + 1) * 8 + 16 + 1024;
   static constexpr int BUDGET2 = 113 * 1024 - TAIL_BYTES;  // two CTAs per SM
@@ -87,7 +92,8 @@ struct SmallMaps {
 struct SmallArgs {
   int M, N, K;
   int dual, act;
-  int nt, kd, stages, splits;
+  int wt, xt;  // weights stored N x K (read K-major); tokens stored K x M (MN-major)
+  int nt, kd, stages;
   uint32_t idesc;
   uint32_t tmem_cols;
   const void *in0, *in1, *bias;
@@ -97,18 +103,48 @@ struct SmallArgs {
   int *watchdog;
 };
 
+// NP products of one launch: their maps and arguments, the first tile of each.
+template <int NP>
+struct SmallBatch {
+  SmallMaps maps[NP];
+  SmallArgs p[NP];
+  int first[NP + 1];
+  int splits;
+};
+
+// Descriptor of the k-th 16-element K slice of an operand tile (tc_tile.cuh's
+// operand_desc with the layout as an argument): MN-major tiles advance two
+// groups of 8 K rows, K-major ones 32 bytes within a 128-byte row; box is the
+// distance between 128-byte blocks of M or N, or between 64-element blocks of K.
+__device__ __forceinline__ uint64_t slice_desc(uint32_t tile, int k, uint32_t box, bool mn) {
+  return smem_desc(tile + (mn ? (uint32_t)k * 2048u : (uint32_t)(k >> 2) * box + (uint32_t)(k & 3) * 32u),
+                   mn ? box : 16u, 1024u);
+}
+
 // SPLIT: a tile's K range is shared by a cluster.  AL: every row of every
 // output and input of the epilogue is 16-byte aligned.  (Template arguments
 // because a short kernel's time is partly that of fetching its instructions:
 // one kernel for all four took 0.3 us longer for 1 x 1024 x 1024.)
-template <class T, Epi EPI, bool SPLIT, bool AL>
+// LAYOUT: 0: tokens M x K, weights K x N; 1: weights N x K; 2: tokens K x M,
+// weights K x N; 3: as the arguments say (for several products; the descriptors
+// cost the MMA thread instructions then, 0.3 us at 64 x 4096 x 1024).
+template <class T, Epi EPI, bool SPLIT, bool AL, int NP, int LAYOUT>
 __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
-    fused_small_kernel(const __grid_constant__ SmallMaps maps,
-                       const __grid_constant__ SmallArgs p) {
+    fused_small_kernel(const __grid_constant__ SmallBatch<NP> batch) {
   using G = SmallCfg;
   constexpr int THREADS = kThreads<SPLIT>;
-  const int splits = SPLIT ? p.splits : 1;
+  const int splits = SPLIT ? batch.splits : 1;
   pdl_launch_dependents();
+  const int part = SPLIT ? blockIdx.x % splits : 0;
+  int unit = SPLIT ? blockIdx.x / splits : blockIdx.x;
+  int job = 0;
+#pragma unroll
+  for (int j = 1; j < NP; ++j)
+    if (unit >= batch.first[j]) job = j;
+  const SmallArgs &p = batch.p[job];
+  const SmallMaps &maps = batch.maps[job];
+  unit -= batch.first[job];
+  const bool wt = LAYOUT == 3 ? p.wt != 0 : LAYOUT == 1, xt = LAYOUT == 3 ? p.xt != 0 : LAYOUT == 2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -130,7 +166,6 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
   constexpr int TF = EPI == Epi::kGated ? G::TF / 2 : G::TF;  // output features of a tile
   const int tiles_t = (p.M + p.nt - 1) / p.nt, tiles_f = (p.N + TF - 1) / TF;
   const int tiles1 = tiles_t * tiles_f;
-  const int unit = SPLIT ? blockIdx.x / splits : blockIdx.x, part = SPLIT ? blockIdx.x % splits : 0;
   const bool second = unit >= tiles1;  // kPair: a tile of the second product
   const int tile = second ? unit - tiles1 : unit;
   const int f0 = (tile / tiles_t) * TF, t0 = (tile % tiles_t) * p.nt;
@@ -159,7 +194,7 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
       const bool set2 = second || kb >= kb1;
       const int k0 = (kb >= kb1 ? kb - kb1 : kb) * bk;
       const CUtensorMap *mw = set2 ? &maps.w2 : &maps.w;
-      if constexpr (kWT) {
+      if (wt) {
         for (int c = 0; c < p.kd; ++c) {
           tma_prefetch_2d(mw, k0 + c * G::BOX, f0);
           if constexpr (EPI == Epi::kGated) tma_prefetch_2d(&maps.w2, k0 + c * G::BOX, f0);
@@ -200,7 +235,7 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
         const int k0 = (kb >= kb1 ? kb - kb1 : kb) * bk;
         const CUtensorMap *mw = set2 ? &maps.w2 : &maps.w, *mx = set2 ? &maps.x2 : &maps.x;
         const uint32_t fb = full_bar(stage);
-        if constexpr (kWT) {  // K-major: 64 k x features per box
+        if (wt) {  // K-major: 64 k x features per box
           for (int c = 0; c < p.kd; ++c) {
             const uint32_t dst = w_tile(stage) + (uint32_t)(c * G::W_CHUNK);
             tma_load_2d(dst, mw, fb, k0 + c * G::BOX, f0);
@@ -214,7 +249,7 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
           else
             tma_load_2d(w_tile(stage) + w_bytes / 2, mw, fb, f0 + G::BOX, k0);
         }
-        if constexpr (kXT) {
+        if (xt) {
           for (int c = 0; c < p.nt / G::BOX; ++c)
             tma_load_2d(x_tile(stage) + (uint32_t)(c * bk * 128), mx, fb, t0 + c * G::BOX, k0);
         } else {
@@ -246,8 +281,8 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      const uint32_t w_box = kWT ? (uint32_t)G::W_CHUNK : w_bytes / 2;
-      const uint32_t x_box = kXT ? (uint32_t)(bk * 128) : (uint32_t)(p.nt * 128);
+      const uint32_t w_box = wt ? (uint32_t)G::W_CHUNK : w_bytes / 2;
+      const uint32_t x_box = xt ? (uint32_t)(bk * 128) : (uint32_t)(p.nt * 128);
       for (int kb = kb_begin; kb < kb_end; ++kb) {
         if (!mbar_try_wait(full_bar(stage), phase) &&
             (*abort_flag || !mbar_wait(full_bar(stage), phase))) {
@@ -259,8 +294,8 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int k = 4 * h + q;
-            umma_f16(tmem_base, operand_desc<G, !kWT>(w_tile(stage), k, w_box),
-                     operand_desc<G, kXT>(x_tile(stage), k, x_box), p.idesc,
+            umma_f16(tmem_base, slice_desc(w_tile(stage), k, w_box, !wt),
+                     slice_desc(x_tile(stage), k, x_box, xt), p.idesc,
                      (kb > kb_begin || k > 0) ? 1u : 0u);
           }
         umma_commit(empty_bar(stage));
@@ -415,17 +450,17 @@ inline bool rows_aligned(const void *p, int64_t ld) {
 bool small_maps(CUtensorMap *tw, CUtensorMap *tx, CUtensorMapDataType dt, const FusedGemm &p,
                 const void *X, int64_t ldx, const void *W, int64_t ldw, int nt, int bk, int w_rows) {
   const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
-  const bool w = kWT ? make_map(tw, W, dt, 2, p.N, p.K, ldw, 64, w_rows, swz)
-                     : make_map(tw, W, dt, 2, p.K, p.N, ldw, 64, bk, swz);
-  const bool x = kXT ? make_map(tx, X, dt, 2, p.K, p.M, ldx, 64, bk, swz)
-                     : make_map(tx, X, dt, 2, p.M, p.K, ldx, 64, nt, swz);
+  const bool w = p.b_t ? make_map(tw, W, dt, 2, p.N, p.K, ldw, 64, w_rows, swz)
+                       : make_map(tw, W, dt, 2, p.K, p.N, ldw, 64, bk, swz);
+  const bool x = p.a_t ? make_map(tx, X, dt, 2, p.K, p.M, ldx, 64, bk, swz)
+                       : make_map(tx, X, dt, 2, p.M, p.K, ldx, 64, nt, swz);
   return w && x;
 }
 
 // Launch one instance, opted in to all of the shared memory once per device.
-template <auto KERNEL>
+template <auto KERNEL, class B>
 cudaError_t launch_one(unsigned grid, bool split, int smem, cudaStream_t stream, unsigned cluster,
-                       const SmallMaps &maps, const SmallArgs &args) {
+                       const B &batch) {
   using G = SmallCfg;
   static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
@@ -438,85 +473,103 @@ cudaError_t launch_one(unsigned grid, bool split, int smem, cudaStream_t stream,
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  e = launch_kernel(KERNEL, dim3(grid), dim3(split ? kThreads<true> : kThreads<false>), (size_t)smem, stream, cluster, maps,
-                    args);
+  e = launch_kernel(KERNEL, dim3(grid), dim3(split ? kThreads<true> : kThreads<false>),
+                    (size_t)smem, stream, cluster, batch);
   if (e == cudaSuccess) count_launch();
   return e;
 }
 
-template <class T, Epi EPI>
-cudaError_t launch_small(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+// `n` products (n <= NP) in one launch; their plans agree in splits and per_sm.
+template <Epi EPI, int NP, int LAYOUT>
+cudaError_t launch_small(const FusedGemm *ps, const SmallPlan *plans, int n, int *watchdog,
                          cudaStream_t stream) {
   using G = SmallCfg;
-  SmallMaps maps;
-  memset(&maps, 0, sizeof maps);
-  SmallArgs a;
-  memset(&a, 0, sizeof a);
+  using T = Elem;
+  SmallBatch<NP> batch;
+  memset(&batch, 0, sizeof batch);
   const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  a.nt = plan.nt, a.kd = plan.kd, a.splits = plan.splits;
-  const int bk = 64 * plan.kd;
-  if (p.K > 0) {
-    const int w_rows = EPI == Epi::kGated ? G::TF / 2 : G::TF;
-    if (!small_maps(&maps.w, &maps.x, dt, p, p.A, p.lda, p.B, p.ldb, plan.nt, bk, w_rows))
-      return cudaErrorInvalidValue;
-    if (p.dual != Dual::kNone) {
-      const bool gated = p.dual == Dual::kGated;
-      if (!small_maps(&maps.w2, &maps.x2, dt, p, gated ? p.A : p.A2, gated ? p.lda : p.lda2, p.B2,
-                      p.ldb2, plan.nt, bk, w_rows))
-        return cudaErrorInvalidValue;
-    }
-  }
-  const int stage_bytes = (G::W_CHUNK + plan.nt * 128) * plan.kd;
-  a.stages = small_stages(plan);
-  // the parked partial tile takes the stages' place
-  if (a.stages < 2 || a.stages * stage_bytes < plan.nt * G::TF * 4) return cudaErrorInvalidValue;
-  const int smem = a.stages * stage_bytes + G::TAIL_BYTES;
   const uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
-  a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kWT ? 0u : 1u) << 15) |
-            ((kXT ? 1u : 0u) << 16) | ((uint32_t)(plan.nt >> 3) << 17) |
-            ((uint32_t)(G::TF >> 4) << 24);
-  a.tmem_cols = 32;
-  while ((int)a.tmem_cols < plan.nt) a.tmem_cols *= 2;
-  a.M = p.M, a.N = p.N, a.K = p.K;
-  a.dual = (int)p.dual, a.act = p.act;
-  a.in0 = p.in0, a.in1 = p.in1, a.bias = p.bias;
-  a.ldi0 = p.ldi0, a.ldi1 = p.ldi1;
-  a.out[0] = p.out0, a.out[1] = p.out1, a.out[2] = p.out2;
-  a.ldo[0] = p.ldo0, a.ldo[1] = p.ldo1, a.ldo[2] = p.ldo2;
-  bool vec = p.N % 8 == 0 && rows_aligned(p.in0, p.in0 ? p.ldi0 : 0) &&
-             rows_aligned(p.in1, p.in1 ? p.ldi1 : 0) && rows_aligned(p.bias, 0);
-  for (int i = 0; i < 3; ++i) vec = vec && rows_aligned(a.out[i], a.out[i] ? a.ldo[i] : 0);
-  a.watchdog = watchdog;
-  const int tf = EPI == Epi::kGated ? G::TF / 2 : G::TF;
-  const int64_t tiles = (int64_t)((p.M + plan.nt - 1) / plan.nt) * ((p.N + tf - 1) / tf) *
-                        (p.dual == Dual::kPair ? 2 : 1);
-  if (tiles * plan.splits > 0x3fffffff) return cudaErrorInvalidValue;
-  const unsigned grid = (unsigned)(tiles * plan.splits), cluster = (unsigned)plan.splits;
-  if (plan.splits > 1)
-    return vec ? launch_one<fused_small_kernel<T, EPI, true, true>>(grid, true, smem, stream, cluster, maps, a)
-               : launch_one<fused_small_kernel<T, EPI, true, false>>(grid, true, smem, stream, cluster, maps, a);
-  return vec ? launch_one<fused_small_kernel<T, EPI, false, true>>(grid, false, smem, stream, 1u, maps, a)
-             : launch_one<fused_small_kernel<T, EPI, false, false>>(grid, false, smem, stream, 1u, maps, a);
-}
-
-template <class T>
-cudaError_t launch_epi(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
-                       cudaStream_t stream) {
-  if (p.epi == Epi::kLinear) return launch_small<T, Epi::kLinear>(p, plan, watchdog, stream);
-  if constexpr (!kXT) {  // the gated epilogues' tokens are activations, M x K
-    if (p.epi == Epi::kGated) return launch_small<T, Epi::kGated>(p, plan, watchdog, stream);
-    return launch_small<T, Epi::kGatedBwd>(p, plan, watchdog, stream);
+  constexpr int tf = EPI == Epi::kGated ? G::TF / 2 : G::TF;
+  const int splits = plans[0].splits;
+  int smem = 0;
+  int64_t tiles = 0;
+  bool vec = true;
+  for (int j = 0; j < n; ++j) {
+    const FusedGemm &p = ps[j];
+    const SmallPlan &plan = plans[j];
+    SmallMaps &maps = batch.maps[j];
+    SmallArgs &a = batch.p[j];
+    if (plan.splits != splits || plan.per_sm != plans[0].per_sm) return cudaErrorInvalidValue;
+    a.nt = plan.nt, a.kd = plan.kd;
+    a.wt = p.b_t, a.xt = p.a_t;
+    const int bk = 64 * plan.kd;
+    if (p.K > 0) {
+      if (!small_maps(&maps.w, &maps.x, dt, p, p.A, p.lda, p.B, p.ldb, plan.nt, bk, tf))
+        return cudaErrorInvalidValue;
+      if (p.dual != Dual::kNone) {
+        const bool gated = p.dual == Dual::kGated;
+        if (!small_maps(&maps.w2, &maps.x2, dt, p, gated ? p.A : p.A2, gated ? p.lda : p.lda2, p.B2,
+                        p.ldb2, plan.nt, bk, tf))
+          return cudaErrorInvalidValue;
+      }
+    }
+    const int stage_bytes = (G::W_CHUNK + plan.nt * 128) * plan.kd;
+    a.stages = small_stages(plan);
+    // the parked partial tile takes the stages' place
+    if (a.stages < 2 || a.stages * stage_bytes < plan.nt * G::TF * 4) return cudaErrorInvalidValue;
+    const int bytes = a.stages * stage_bytes + G::TAIL_BYTES;
+    smem = smem > bytes ? smem : bytes;
+    a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((p.b_t ? 0u : 1u) << 15) |
+              ((p.a_t ? 1u : 0u) << 16) | ((uint32_t)(plan.nt >> 3) << 17) |
+              ((uint32_t)(G::TF >> 4) << 24);
+    a.tmem_cols = 32;
+    while ((int)a.tmem_cols < plan.nt) a.tmem_cols *= 2;
+    a.M = p.M, a.N = p.N, a.K = p.K;
+    a.dual = (int)p.dual, a.act = p.act;
+    a.in0 = p.in0, a.in1 = p.in1, a.bias = p.bias;
+    a.ldi0 = p.ldi0, a.ldi1 = p.ldi1;
+    a.out[0] = p.out0, a.out[1] = p.out1, a.out[2] = p.out2;
+    a.ldo[0] = p.ldo0, a.ldo[1] = p.ldo1, a.ldo[2] = p.ldo2;
+    vec = vec && p.N % 8 == 0 && rows_aligned(p.in0, p.in0 ? p.ldi0 : 0) &&
+          rows_aligned(p.in1, p.in1 ? p.ldi1 : 0) && rows_aligned(p.bias, 0);
+    for (int i = 0; i < 3; ++i) vec = vec && rows_aligned(a.out[i], a.out[i] ? a.ldo[i] : 0);
+    a.watchdog = watchdog;
+    batch.first[j] = (int)tiles;
+    tiles += (int64_t)((p.M + plan.nt - 1) / plan.nt) * ((p.N + tf - 1) / tf) *
+             (p.dual == Dual::kPair ? 2 : 1);
+    if (tiles * splits > 0x3fffffff) return cudaErrorInvalidValue;
   }
-  return cudaErrorInvalidValue;
+  for (int j = n; j <= NP; ++j) batch.first[j] = (int)tiles;
+  batch.splits = splits;
+  const unsigned grid = (unsigned)(tiles * splits), cluster = (unsigned)splits;
+  if (splits > 1)
+    return vec ? launch_one<fused_small_kernel<T, EPI, true, true, NP, LAYOUT>>(grid, true, smem, stream,
+                                                                        cluster, batch)
+               : launch_one<fused_small_kernel<T, EPI, true, false, NP, LAYOUT>>(grid, true, smem, stream,
+                                                                         cluster, batch);
+  return vec ? launch_one<fused_small_kernel<T, EPI, false, true, NP, LAYOUT>>(grid, false, smem, stream,
+                                                                       1u, batch)
+             : launch_one<fused_small_kernel<T, EPI, false, false, NP, LAYOUT>>(grid, false, smem, stream,
+                                                                        1u, batch);
 }
 
 }  // namespace
 
-cudaError_t DG_UNIT_LAUNCHER(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
+cudaError_t DG_UNIT_LAUNCHER(const FusedGemm *p, const SmallPlan *plan, int n, int *watchdog,
                              cudaStream_t stream) {
-  return p.dtype == DGEMM_DTYPE_BF16 ? launch_epi<__nv_bfloat16>(p, plan, watchdog, stream)
-                                     : launch_epi<__half>(p, plan, watchdog, stream);
+#if DGEMM_FUSED_UNIT < 2
+  if (n > 1) return launch_small<Epi::kLinear, kMaxBatch, 3>(p, plan, n, watchdog, stream);
+  if (p->a_t) return launch_small<Epi::kLinear, 1, 2>(p, plan, n, watchdog, stream);
+  return p->b_t ? launch_small<Epi::kLinear, 1, 1>(p, plan, n, watchdog, stream)
+                : launch_small<Epi::kLinear, 1, 0>(p, plan, n, watchdog, stream);
+#else  // the gated epilogues' tokens are activations, M x K
+  if (p->epi == Epi::kGated)
+    return p->b_t ? launch_small<Epi::kGated, 1, 1>(p, plan, n, watchdog, stream)
+                  : launch_small<Epi::kGated, 1, 0>(p, plan, n, watchdog, stream);
+  return p->b_t ? launch_small<Epi::kGatedBwd, 1, 1>(p, plan, n, watchdog, stream)
+                : launch_small<Epi::kGatedBwd, 1, 0>(p, plan, n, watchdog, stream);
+#endif
 }
 
 #if DGEMM_FUSED_UNIT == 0
@@ -538,7 +591,7 @@ int64_t small_resident(const SmallPlan &plan, int num_sms) {
   std::atomic<int> &slot = cache[dev][plan.per_sm][plan.splits];
   int n = slot.load(std::memory_order_relaxed);
   if (n == 0) {
-    auto kern = fused_small_kernel<__half, Epi::kLinear, true, true>;
+    auto kern = fused_small_kernel<Elem, Epi::kLinear, true, true, 1, 0>;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)plan.splits;

@@ -51,8 +51,10 @@ struct Shape {
   // backward: a row's values stay in registers between its two passes, else
   // they are read again from the ring
   static constexpr bool KEEP = CH * V <= 16;
-  // backward: blocks per SM, 128 registers a thread
-  static constexpr int BWD_BLOCKS = 512 / BLOCK;
+  // backward: one block of 512 threads per SM, so that there are few partial
+  // column sums to write and join (1000 x 1013 bf16: 22 us with blocks of 64
+  // threads and eight per SM, 10.5 us)
+  static constexpr int BWD_BLOCK = 512, BWD_ROWS = BWD_BLOCK / GROUP;
 };
 
 constexpr int kMaxStages = 8;
@@ -61,20 +63,21 @@ constexpr int kMaxStages = 8;
 enum : int { kSiteNormRow = 0xc1 };
 
 // Sums of N values over the threads of a row; every thread gets them.  `red`
-// alternates between two buffers, so one barrier per sum is enough.
+// alternates between two buffers, so one barrier per sum is enough (barrier 1 +
+// sub, which only the row's threads use).
 template <class S, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[32]) {
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[32], int sub = 0) {
 #pragma unroll
   for (int o = 16; o; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if constexpr (S::GROUP > 32) {
     constexpr int W = S::GROUP / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x % S::GROUP >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) red[i][warp] = v[i];
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(S::GROUP) : "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float s = lane < W ? red[i][lane] : 0.f;
@@ -214,16 +217,16 @@ struct Ring {
 // stage of the ring is refilled one row later, when the next row's sums have
 // shown that nobody reads it any more.
 template <class S>
-__global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
+__global__ void __launch_bounds__(S::BWD_BLOCK, 1)
     ln_bwd_kernel(int rows, int cols, float inv, const typename S::T *dY, int64_t lddy,
                   const typename S::T *X, int64_t ldx, const typename S::T *w, const float *mean,
                   const float *rstd, const typename S::T *dR, int64_t lddr, typename S::T *dX,
                   int64_t lddx, float *partial, typename S::T *dw, typename S::T *db, int stages,
                   int *watchdog) {
   using T = typename S::T;
-  constexpr int V = S::V, CH = S::CH, GROUP = S::GROUP;
-  __shared__ float red[2][2][32];
-  __shared__ uint64_t bars[S::ROWS * kMaxStages];
+  constexpr int V = S::V, CH = S::CH, GROUP = S::GROUP, ROWS = S::BWD_ROWS;
+  __shared__ float red[GROUP > 32 ? ROWS : 1][2][2][32];
+  __shared__ uint64_t bars[ROWS * kMaxStages];
   extern __shared__ __align__(16) uint8_t rows_smem[];
   pdl_launch_dependents();
   const int t = threadIdx.x % GROUP, sub = threadIdx.x / GROUP;
@@ -235,8 +238,8 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
   __syncthreads();
   pdl_wait();
   const bool grads = partial != nullptr || dw != nullptr || db != nullptr;
-  const int64_t step = (int64_t)gridDim.x * S::ROWS;
-  int64_t row = (int64_t)blockIdx.x * S::ROWS + sub;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row = (int64_t)blockIdx.x * ROWS + sub;
   if (t == 0)
     for (int s = 0; s < stages && row + s * step < rows; ++s) ring.fill(s, row + s * step);
   float sw[CH][V], sb[CH][V];
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
         sb[c][j] += d[j];
       }
     }
-    row_sum<S>(s, red[buf]);
+    row_sum<S>(s, red[GROUP > 32 ? sub : 0][buf], sub);
     buf ^= 1;
     if (GROUP == 32) __syncwarp();
     if (t == 0 && last >= 0 && row + (stages - 1) * step < rows)
@@ -329,17 +332,17 @@ __global__ void __launch_bounds__(S::BLOCK, S::BWD_BLOCKS)
     float(&sum)[CH][V] = k ? sb : sw;
     T *out = k ? db : dw;
     float *part = partial ? partial + ((int64_t)blockIdx.x * 2 + k) * cols : nullptr;
-    if constexpr (S::ROWS > 1) {
+    if constexpr (ROWS > 1) {
       __syncthreads();
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < V; ++j) fold[sub * S::CAPACITY + S::col(c, t) + j] = sum[c][j];
       __syncthreads();
-      for (int col = threadIdx.x; col < cols; col += S::BLOCK) {
+      for (int col = threadIdx.x; col < cols; col += S::BWD_BLOCK) {
         float v = 0.f;
 #pragma unroll
-        for (int i = 0; i < S::ROWS; ++i) v += fold[i * S::CAPACITY + col];
+        for (int i = 0; i < ROWS; ++i) v += fold[i * S::CAPACITY + col];
         if (part)
           part[col] = v;
         else if (out)
@@ -450,7 +453,7 @@ constexpr int kLongParts = 16;        // row shares of the column sums of longer
 // elements per thread forward, 16 (for rows beyond 8192, 32) backward.
 // Measured at 16384 x 4096 bf16, forward: 128 threads to a row 45.3 us (5.93
 // TB/s), 256 threads 54.8 us; 65536 x 1024: a warp 44.3 us.  Backward with dR:
-// 92.2 us (5.82 TB/s); one row ahead in registers instead of the ring 115 us.
+// 86.3 us (6.22 TB/s); one row ahead in registers instead of the ring 115 us.
 template <class T, bool ALIGNED, bool BWD, class F>
 cudaError_t with_shape(int cols, F &&f) {
   constexpr int K = 8 / kVec<T>;  // vectors in 8 elements
@@ -473,16 +476,16 @@ bool vec_ok(const void *p, int64_t ld) {
   return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
 }
 
-// Stages of a persistent kernel's rings and its dynamic shared memory: what
-// `blocks` blocks per SM leave room for, and the fold of the column sums.
+// Stages of the backward kernel's rings, and its dynamic shared memory: the
+// rings, and the fold of the column sums in their place.
 template <class S, int NIN>
-int ring_stages(int cols, int blocks, bool fold, size_t *smem) {
-  const size_t one = Ring<S, NIN>::group_bytes(cols, 1) * S::ROWS;
-  const size_t budget = 216 * 1024 / blocks - 4096;  // static shared memory and the system's share
+int ring_stages(int cols, bool fold, size_t *smem) {
+  const size_t one = Ring<S, NIN>::group_bytes(cols, 1) * S::BWD_ROWS;
+  const size_t budget = 212 * 1024;  // static shared memory and the system's share aside
   int stages = (int)(budget / one);
   stages = stages < 2 ? 2 : stages > kMaxStages ? kMaxStages : stages;
   *smem = one * stages;
-  const size_t sums = fold && S::ROWS > 1 ? (size_t)S::ROWS * S::CAPACITY * sizeof(float) : 0;
+  const size_t sums = fold && S::BWD_ROWS > 1 ? (size_t)S::BWD_ROWS * S::CAPACITY * sizeof(float) : 0;
   if (*smem < sums) *smem = sums;
   return stages;
 }
@@ -528,9 +531,9 @@ cudaError_t fwd(int rows, int cols, float eps, const void *X, int64_t ldx, const
 }
 
 // Blocks of the backward kernel, each one partial sum.
-int bwd_parts(int rows, int rows_per_block, int64_t resident) {
+int bwd_parts(int rows, int rows_per_block, int num_sms) {
   const int64_t need = ((int64_t)rows + rows_per_block - 1) / rows_per_block;
-  return (int)(need < 1 ? 1 : need < resident ? need : resident);
+  return (int)(need < 1 ? 1 : need < num_sms ? need : num_sms);
 }
 
 template <class T>
@@ -567,12 +570,12 @@ cudaError_t bwd(int dtype, int rows, int cols, const void *dY, int64_t lddy, con
                    (cols * (int)sizeof(T)) % 16 == 0;
   e = with_shape<T, true>(cols, vec, [&](auto shape) {
     using S = decltype(shape);
-    parts = bwd_parts(rows, S::ROWS, (int64_t)S::BWD_BLOCKS * num_sms);
+    parts = bwd_parts(rows, S::BWD_ROWS, num_sms);
     size_t smem = 0;
-    const int stages = ring_stages<S, 3>(cols, S::BWD_BLOCKS, grads, &smem);
+    const int stages = ring_stages<S, 3>(cols, grads, &smem);
     const cudaError_t ea = allow_smem<ln_bwd_kernel<S>>();
     if (ea != cudaSuccess) return ea;
-    return launch_kernel(ln_bwd_kernel<S>, dim3((unsigned)parts), dim3(S::BLOCK), smem, stream, 1u,
+    return launch_kernel(ln_bwd_kernel<S>, dim3((unsigned)parts), dim3(S::BWD_BLOCK), smem, stream, 1u,
                          rows, cols, 1.f / cols, dy, lddy, x, ldx, w, mean, rstd, dr, lddr, dx,
                          lddx, grads && parts > 1 ? partial : nullptr, dw, db, stages, wd);
   });
@@ -598,13 +601,8 @@ cudaError_t launch_layer_norm(int dtype, int rows, int cols, float eps, const vo
 
 size_t layer_norm_scratch(int rows, int cols, bool with_grads, int num_sms) {
   if (!with_grads) return 0;
-  int parts = kLongParts;
-  with_shape<__half, true>(cols, true, [&](auto shape) {  // the groups do not depend on the type
-    using S = decltype(shape);
-    const int ring = bwd_parts(rows, S::ROWS, (int64_t)S::BWD_BLOCKS * num_sms);
-    parts = ring > parts ? ring : parts;
-    return cudaSuccess;
-  });
+  const int ring = bwd_parts(rows, 1, num_sms);
+  const int parts = ring > kLongParts ? ring : kLongParts;
   return (size_t)parts * 2 * cols * sizeof(float);
 }
 

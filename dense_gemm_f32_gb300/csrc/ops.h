@@ -47,8 +47,14 @@ struct FusedGemm {
 };
 cudaError_t launch_fused(const FusedGemm &p, int num_sms, cudaStream_t stream);
 
+// Up to kMaxBatch independent Epi::kLinear products of one type: in one launch
+// of the small kernel where that is the quicker way, else one after the other.
+cudaError_t launch_fused_batch(const FusedGemm *p, int n, int num_sms, cudaStream_t stream);
+
+constexpr int kMaxRepitch = 12;  // jobs in one launch
+
 // A 16-bit rows x cols matrix copied to a 16-byte aligned pitch (ldd >= cols, a
-// multiple of 8), the padding zeroed.  Up to eight in one launch.
+// multiple of 8), the padding zeroed.
 struct RepitchJob {
   const void *src;
   int64_t lds;
@@ -70,7 +76,7 @@ class Stager {
   cudaError_t release();
 
  private:
-  static constexpr int kMax = 8;
+  static constexpr int kMax = kMaxRepitch;
   struct Item {
     const void **p;
     int64_t *ld;
@@ -100,12 +106,18 @@ struct SmallPlan {
 // `splits` CTAs) the device holds at once.
 int small_stages(const SmallPlan &plan);
 int64_t small_resident(const SmallPlan &plan, int num_sms);
-cudaError_t launch_fused_small_unit_0(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
-                                      cudaStream_t stream);
-cudaError_t launch_fused_small_unit_1(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
-                                      cudaStream_t stream);
-cudaError_t launch_fused_small_unit_2(const FusedGemm &p, const SmallPlan &plan, int *watchdog,
-                                      cudaStream_t stream);
+// `n` products in one launch (three at most for Epi::kLinear, one otherwise;
+// their plans agree in splits and per_sm).  0: bf16 linear, 1: fp16 linear, 2:
+// bf16 gated, 3: fp16 gated.
+constexpr int kMaxBatch = 3;
+#define DG_DECLARE_SMALL_UNIT(u)                                                               \
+  cudaError_t launch_fused_small_unit_##u(const FusedGemm *p, const SmallPlan *plan, int n,    \
+                                          int *watchdog, cudaStream_t stream);
+DG_DECLARE_SMALL_UNIT(0)
+DG_DECLARE_SMALL_UNIT(1)
+DG_DECLARE_SMALL_UNIT(2)
+DG_DECLARE_SMALL_UNIT(3)
+#undef DG_DECLARE_SMALL_UNIT
 
 // dZ = dD act'(Z) (act != none; else dZ is not written) and, where dbias is
 // not null, dbias[j] = sum_i dZ[i][j] in fp32, rounded once.  `partial` is

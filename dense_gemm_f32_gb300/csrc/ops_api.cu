@@ -217,25 +217,25 @@ int dgemm_linear_backward(int dtype, int activation, int op_w, int M, int N, int
   if (want_dw) stage.add(x, ldx_use, M, K);
   if (want_dx) stage.add(w, ldw_use, wr, wc);
   if ((st = done(stage.run(), "operand staging")) != DGEMM_OK) return release(stage, st);
+  FusedGemm ps[2];
+  int n = 0;
   if (want_dx) {  // dX (M x K) = dZ op(W)^T
-    FusedGemm p;
+    FusedGemm &p = ps[n++];
     p.dtype = dtype;
     p.M = M, p.N = K, p.K = N;
     p.A = dz, p.lda = ldz_use, p.B = w, p.ldb = ldw_use, p.b_t = !t;
     p.out0 = dX, p.ldo0 = lddx;
-    st = done(launch_fused(p, sms, stream), "input gradient launch");
   }
-  if (st == DGEMM_OK && want_dw) {  // dW as W is stored: X^T dZ, or its transpose dZ^T X
-    FusedGemm p;
+  if (want_dw) {  // dW as W is stored: X^T dZ, or its transpose dZ^T X
+    FusedGemm &p = ps[n++];
     p.dtype = dtype;
     p.M = wr, p.N = wc, p.K = M;
     p.a_t = true;
     p.A = t ? dz : x, p.lda = t ? ldz_use : ldx_use;
     p.B = t ? x : dz, p.ldb = t ? ldx_use : ldz_use;
     p.out0 = dW, p.ldo0 = lddw;
-    st = done(launch_fused(p, sms, stream), "weight gradient launch");
   }
-  return release(stage, st);
+  return release(stage, done(launch_fused_batch(ps, n, sms, stream), "gradient launch"));
 }
 
 int dgemm_gated_ffn(int dtype, int activation, int op_w, int M, int D, int F, const void *X,
@@ -333,18 +333,20 @@ int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, 
     p.out0 = dG, p.ldo0 = lddg, p.out1 = dU, p.ldo1 = lddu, p.out2 = H, p.ldo2 = ldh;
     st = done(launch_fused(p, sms, stream), "gate gradient launch");
   }
-  if (st == DGEMM_OK && want_dx) {  // dX = dG op(Wg)^T + dU op(Wu)^T
-    FusedGemm p;
+  if (st != DGEMM_OK) return release(stage, st);
+  FusedGemm ps[3];
+  int n = 0;
+  if (want_dx) {  // dX = dG op(Wg)^T + dU op(Wu)^T
+    FusedGemm &p = ps[n++];
     p.dual = Dual::kSum;
     p.dtype = dtype;
     p.M = M, p.N = D, p.K = F;
     p.A = dG, p.lda = lddg, p.A2 = dU, p.lda2 = lddu, p.b_t = !t;
     p.B = wg, p.ldb = lg, p.B2 = wu, p.ldb2 = lu;
     p.out0 = dX, p.ldo0 = lddx;
-    st = done(launch_fused(p, sms, stream), "input gradient launch");
   }
-  if (st == DGEMM_OK && want_up) {  // dWg, dWu as stored: X^T dG, X^T dU, or transposed
-    FusedGemm p;
+  if (want_up) {  // dWg, dWu as stored: X^T dG, X^T dU, or transposed
+    FusedGemm &p = ps[n++];
     p.dual = Dual::kPair;
     p.dtype = dtype;
     p.M = ur, p.N = uc, p.K = M;
@@ -352,18 +354,16 @@ int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, 
     p.A = t ? dG : x, p.lda = t ? lddg : lx, p.A2 = t ? dU : x, p.lda2 = t ? lddu : lx;
     p.B = t ? x : dG, p.ldb = t ? lx : lddg, p.B2 = t ? x : dU, p.ldb2 = t ? lx : lddu;
     p.out0 = dWg, p.ldo0 = lddwg, p.out1 = dWu, p.ldo1 = lddwu;
-    st = done(launch_fused(p, sms, stream), "weight gradient launch");
   }
-  if (st == DGEMM_OK && want_down) {  // dWd as stored: H^T dY, or its transpose
-    FusedGemm p;
+  if (want_down) {  // dWd as stored: H^T dY, or its transpose
+    FusedGemm &p = ps[n++];
     p.dtype = dtype;
     p.M = uc, p.N = ur, p.K = M;
     p.a_t = true;
     p.A = t ? dy : H, p.lda = t ? ly : ldh, p.B = t ? H : dy, p.ldb = t ? ldh : ly;
     p.out0 = dWd, p.ldo0 = lddwd;
-    st = done(launch_fused(p, sms, stream), "weight gradient launch");
   }
-  return release(stage, st);
+  return release(stage, done(launch_fused_batch(ps, n, sms, stream), "gradient launch"));
 }
 
 }  // extern "C"

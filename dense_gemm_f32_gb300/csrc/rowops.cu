@@ -88,32 +88,32 @@ __global__ void __launch_bounds__(32 * kGroups)
 }
 
 // out[k][col] = sum over parts of partial[part][k][col], k < nvec (gridDim.y).
-// 32 columns per block; 32 groups of threads take every 32nd part.
+// 32 columns per block; eight warps take every eighth part, eight in flight.
 template <class T>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(256)
     column_sums_kernel(const float *partial, int parts, int cols, T *out0, T *out1) {
-  __shared__ float fold[32][33];
+  __shared__ float fold[8][32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 5, k = blockIdx.y, nvec = gridDim.y;
   const int col = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (col < cols)
-#pragma unroll 4
-    for (int i = group; i < parts; i += 32) v += partial[((int64_t)i * nvec + k) * cols + col];
+#pragma unroll 8
+    for (int i = group; i < parts; i += 8) v += partial[((int64_t)i * nvec + k) * cols + col];
   fold[group][lane] = v;
   __syncthreads();
-  v = fold[lane][group];  // part group `lane` of column `group`
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   T *out = k ? out1 : out0;
-  const int c = blockIdx.x * 32 + group;
-  if (lane == 0 && out != nullptr && c < cols) out[c] = from_f32<T>(v);
+  if (group != 0 || col >= cols || out == nullptr) return;
+  v = 0.f;
+#pragma unroll
+  for (int g = 0; g < 8; ++g) v += fold[g][lane];
+  out[col] = from_f32<T>(v);
 }
 
 struct RepitchJobs {
-  RepitchJob job[8];
-  int64_t first[9];  // units (256 columns of a row) before each job
+  RepitchJob job[kMaxRepitch];
+  int64_t first[kMaxRepitch + 1];  // units (256 columns of a row) before each job
   int n;
 };
 
@@ -170,8 +170,8 @@ template <class T>
 cudaError_t column_sums(const float *partial, int parts, int cols, void *out0, void *out1, int nvec,
                         cudaStream_t stream) {
   const cudaError_t e = launch_kernel(
-      column_sums_kernel<T>, dim3((unsigned)((cols + 31) / 32), (unsigned)nvec), dim3(1024), 0,
-      stream, 1u, partial, parts, cols, static_cast<T *>(out0), static_cast<T *>(out1));
+      column_sums_kernel<T>, dim3((unsigned)((cols + 31) / 32), (unsigned)nvec), dim3(256), 0, stream,
+      1u, partial, parts, cols, static_cast<T *>(out0), static_cast<T *>(out1));
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -189,10 +189,11 @@ cudaError_t column_sums(int dtype, const float *partial, int parts, int cols, vo
 }
 
 // Shares of the rows: four blocks per SM over all column tiles, at least four
-// rows per row group.
+// rows per row group; up to 128 rows one share, which needs no second launch.
 int act_grad_parts(int M, int N, int num_sms) {
   const int64_t tiles = (N + 255) / 256;
   int64_t parts = (4 * (int64_t)num_sms + tiles - 1) / tiles;
+  if (M <= 16 * kGroups) return 1;
   const int64_t most = ((int64_t)M + 4 * kGroups - 1) / (4 * kGroups);
   parts = parts < most ? parts : most;
   return (int)(parts < 1 ? 1 : parts);
@@ -244,7 +245,7 @@ cudaError_t launch_act_grad(int dtype, int act, int M, int N, const void *dD, in
 
 cudaError_t launch_repitch(const RepitchJob *jobs, int njobs, int num_sms, cudaStream_t stream) {
   RepitchJobs a;
-  if (njobs < 1 || njobs > 8) return cudaErrorInvalidValue;
+  if (njobs < 1 || njobs > kMaxRepitch) return cudaErrorInvalidValue;
   a.n = njobs;
   a.first[0] = 0;
   for (int j = 0; j < njobs; ++j) {

@@ -70,3 +70,28 @@ def test_gated(M, D, F, trans_w, plan, monkeypatch):
     for i, (v, w_, what) in enumerate(zip(got, want, ("dx", "dwg", "dwu", "dwd"))):
         ref.check(v.t() if trans_w and i else v, w_, what)
     gu.check_watchdog()
+
+
+@pytest.mark.parametrize("batch", [0, 1])
+@pytest.mark.parametrize("plan", [{}] + PLANS[1::3], ids=str)
+@pytest.mark.parametrize("M, D, F", [(1, 200, 136), (97, 130, 264), (300, 77, 333)])
+def test_gradients_together_and_apart(M, D, F, plan, batch, monkeypatch):
+    """The independent products of a backward pass as one launch, or one each."""
+    _force(monkeypatch, dict(plan, BATCH=batch))
+    n = ref.make(M + D)
+    dtype = torch.float16
+    x, dy, g, u = n((M, D), dtype), n((M, D), dtype, 0.2), n((M, F), dtype), n((M, F), dtype)
+    ws = [n((D, F), dtype, D ** -0.5), n((D, F), dtype, D ** -0.5), n((F, D), dtype, F ** -0.5)]
+    got = dg.gated_ffn_backward(dy, x, *ws, g, u, "silu")
+    want = ref.gated_backward(_d(dy), _d(x), *map(_d, ws), _d(g), _d(u), "silu", dtype)
+    for v, w_, what in zip(got, want, ("dx", "dwg", "dwu", "dwd")):
+        ref.check(v, w_, what)
+    n0 = dg.dgemm_kernel_launches()
+    got = dg.linear_backward(g, x, ws[0], "none", with_bias=False)
+    launched = dg.dgemm_kernel_launches() - n0
+    want = ref.linear_backward(_d(g), _d(x), _d(ws[0]), "none", None, dtype)
+    for v, w_, what in zip(got, want, ("dx", "dw")):
+        ref.check(v, w_, what)
+    if D % 8 == 0 and F % 8 == 0:  # nothing to stage
+        assert launched == (1 if batch else 2)
+    gu.check_watchdog()
