@@ -65,7 +65,7 @@ struct PairCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int kEpiWarps = 8, kProdBWarp = 2 + kEpiWarps;
   static constexpr int THREADS = 32 * (3 + kEpiWarps);
-  static constexpr int NUM_BARS = 2 * STAGES + 5;  // full, empty, accf[2], acce[2], drain
+  static constexpr int NUM_BARS = 2 * STAGES + 6;  // full, empty, accf[2], acce[2], drain, stall
   static constexpr int PIECE_BYTES = 32 * 64;      // 32 rows x 32 columns of 2 bytes
   static constexpr int EPI_BYTES = kEpiWarps * 2 * PIECE_BYTES;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + NUM_BARS * 8 + 16 + 1024;
@@ -86,6 +86,7 @@ enum : int {
   kSite3MmaDrain = 0xa5,
   kSite3MmaTail = 0xa6,
   kSite3EpiAccFull = 0xa7,
+  kSite3TestStall = 0xa8,  // DGEMM_TC_TEST_STALL: the MMA thread's test wait ran out
 };
 
 struct PairMaps {
@@ -95,7 +96,7 @@ struct PairMaps {
 
 struct PairArgs {
   int M, N, K;
-  int dual, act, group_m, mn3d;
+  int dual, act, group_m, mn3d, stall;
   int o_tma;       // bit i: output i may be written by TMA
   int i_vec;       // bit i: rows of input i are 16-byte aligned; bit 2: the bias is
   const void *in0, *in1, *bias;
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
   auto accf_bar = [&](int b) { return bars + 8u * (2 * G::STAGES + b); };
   auto acce_bar = [&](int b) { return bars + 8u * (2 * G::STAGES + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * G::STAGES + 4);
+  const uint32_t stall_bar = bars + 8u * (2 * G::STAGES + 5);  // nothing ever arrives here
   uint8_t *tail = smem + G::STAGES * G::STAGE_BYTES + G::EPI_BYTES + G::NUM_BARS * 8;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
@@ -173,6 +175,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
       mbar_init(acce_bar(b), 2 * G::kEpiWarps);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(stall_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -267,6 +270,10 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
+      if (p.stall && cluster == 0) {  // test hook: a wait that runs out
+        if (!mbar_wait(stall_bar, 0)) watchdog_trip(p.watchdog, kSite3TestStall, abort_flag);
+        ok = false;
+      }
       for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
         if (*abort_flag || !mbar_wait(acce_bar(acc), acc_phase ^ 1u)) {
           if (!*abort_flag) watchdog_trip(p.watchdog, kSite3MmaAccEmpty, abort_flag);
@@ -499,6 +506,7 @@ cudaError_t launch_pair(const FusedGemm &p, int *watchdog, cudaStream_t stream) 
   a.M = p.M, a.N = p.N, a.K = p.K;
   a.dual = (int)p.dual, a.act = p.act;
   a.group_m = 16;
+  a.stall = test_stall();
   a.in0 = p.in0, a.in1 = p.in1, a.bias = p.bias;
   a.ldi0 = p.ldi0, a.ldi1 = p.ldi1;
   a.i_vec = (rows_aligned(p.in0, p.ldi0) ? 1 : 0) | (rows_aligned(p.in1, p.ldi1) ? 2 : 0) |

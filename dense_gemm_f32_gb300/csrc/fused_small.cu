@@ -61,8 +61,8 @@ struct SmallCfg {
   static constexpr int TF = 128;              // features (MMA rows) of a tile
   static constexpr int W_CHUNK = TF * 128;    // weights of 64 k
   static constexpr int MAX_STAGES = 8, MAX_SPLITS = 8;
-  // bars (full[8], empty[8], accf), TMEM slot, abort flag; 1024 for alignment
-  static constexpr int TAIL_BYTES = (2 * MAX_STAGES + 1) * 8 + 16 + 1024;
+  // bars (full[8], empty[8], accf, stall), TMEM slot, abort flag; 1024 for alignment
+  static constexpr int TAIL_BYTES = (2 * MAX_STAGES + 2) * 8 + 16 + 1024;
   static constexpr int BUDGET2 = 113 * 1024 - TAIL_BYTES;  // two CTAs per SM
   static constexpr int BUDGET1 = 226 * 1024 - TAIL_BYTES;  // one
 };
@@ -83,6 +83,7 @@ enum : int {
   kSite4MmaFull = 0xb3,
   kSite4MmaDrain = 0xb4,
   kSite4DrainAccFull = 0xb5,
+  kSite4TestStall = 0xb6,  // DGEMM_TC_TEST_STALL: the MMA thread's test wait ran out
 };
 
 struct SmallMaps {
@@ -109,7 +110,7 @@ struct SmallBatch {
   SmallMaps maps[NP];
   SmallArgs p[NP];
   int first[NP + 1];
-  int splits;
+  int splits, stall;
 };
 
 // Descriptor of the k-th 16-element K slice of an operand tile (tc_tile.cuh's
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (G::MAX_STAGES + s); };
   const uint32_t accf_bar = bars + 8u * (2 * G::MAX_STAGES);
-  uint8_t *tail = smem + (bars - base) + 8 * (2 * G::MAX_STAGES + 1);
+  const uint32_t stall_bar = bars + 8u * (2 * G::MAX_STAGES + 1);  // nothing ever arrives here
+  uint8_t *tail = smem + (bars - base) + 8 * (2 * G::MAX_STAGES + 2);
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
   auto w_tile = [&](int s) { return base + (uint32_t)s * stage_bytes; };
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(accf_bar, 1);
+    mbar_init(stall_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -283,7 +286,12 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
       uint32_t phase = 0;
       const uint32_t w_box = wt ? (uint32_t)G::W_CHUNK : w_bytes / 2;
       const uint32_t x_box = xt ? (uint32_t)(bk * 128) : (uint32_t)(p.nt * 128);
-      for (int kb = kb_begin; kb < kb_end; ++kb) {
+      bool ok = true;
+      if (batch.stall && blockIdx.x == 0) {  // test hook: a wait that runs out
+        if (!mbar_wait(stall_bar, 0)) watchdog_trip(p.watchdog, kSite4TestStall, abort_flag);
+        ok = false;
+      }
+      for (int kb = kb_begin; kb < kb_end && ok; ++kb) {
         if (!mbar_try_wait(full_bar(stage), phase) &&
             (*abort_flag || !mbar_wait(full_bar(stage), phase))) {
           if (!*abort_flag) watchdog_trip(p.watchdog, kSite4MmaFull, abort_flag);
@@ -542,6 +550,7 @@ cudaError_t launch_small(const FusedGemm *ps, const SmallPlan *plans, int n, int
   }
   for (int j = n; j <= NP; ++j) batch.first[j] = (int)tiles;
   batch.splits = splits;
+  batch.stall = test_stall();
   const unsigned grid = (unsigned)(tiles * splits), cluster = (unsigned)splits;
   if (splits > 1)
     return vec ? launch_one<fused_small_kernel<T, EPI, true, true, NP, LAYOUT>>(grid, true, smem, stream,

@@ -25,6 +25,16 @@ inline bool pdl_enabled() {
   return on;
 }
 
+// DGEMM_TC_TEST_STALL=1 makes one thread of the first CTA (pair) of a kernel
+// wait on a barrier that nothing arrives at: its bounded wait runs out after
+// ~2 s and the kernel takes its abort path (watchdog site code, drained
+// copies, freed tensor memory, incomplete results).  For the failure-detection
+// tests only; read at every launch.
+inline int test_stall() {
+  const char *e = std::getenv("DGEMM_TC_TEST_STALL");
+  return (e && e[0] == '1') ? 1 : 0;
+}
+
 // Launch `kern` with grid x block threads, `smem` bytes of dynamic shared
 // memory, on `stream`, in clusters of `cluster` CTAs along x (1 = none).
 template <class... KArgs, class... Args>

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
                   const typename S::T *X, int64_t ldx, const typename S::T *w, const float *mean,
                   const float *rstd, const typename S::T *dR, int64_t lddr, typename S::T *dX,
                   int64_t lddx, float *partial, typename S::T *dw, typename S::T *db, int stages,
-                  int *watchdog) {
+                  int stall, int *watchdog) {
   using T = typename S::T;
   constexpr int V = S::V, CH = S::CH, GROUP = S::GROUP, ROWS = S::BWD_ROWS;
   __shared__ float red[GROUP > 32 ? ROWS : 1][2][2][32];
@@ -241,7 +241,9 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + sub;
   if (t == 0)
-    for (int s = 0; s < stages && row + s * step < rows; ++s) ring.fill(s, row + s * step);
+    for (int s = stall && blockIdx.x == 0 && sub == 0 ? 1 : 0;  // test hook: a copy never begun
+         s < stages && row + s * step < rows; ++s)
+      ring.fill(s, row + s * step);
   float sw[CH][V], sb[CH][V];
   uint4 wr[CH];
 #pragma unroll
@@ -322,8 +324,9 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
       phase ^= 1u;
     }
   }
-  if (ring.dead && t == 0)  // no copy lands after the block has left
-    for (int s = 0; s < stages; ++s) mbar_wait(ring.bars + 8u * s, phase ^ (s < stage ? 1u : 0u));
+  if (ring.dead && t == 0)  // no copy lands after the block has left (2 s have passed by now)
+    for (int s = 0; s < stages; ++s)
+      if (!mbar_wait(ring.bars + 8u * s, phase ^ (s < stage ? 1u : 0u))) break;
   if (!grads) return;
   // the block's rows side by side, added in their order (the ring is idle now)
   float *fold = reinterpret_cast<float *>(rows_smem);
@@ -577,7 +580,8 @@ cudaError_t bwd(int dtype, int rows, int cols, const void *dY, int64_t lddy, con
     if (ea != cudaSuccess) return ea;
     return launch_kernel(ln_bwd_kernel<S>, dim3((unsigned)parts), dim3(S::BWD_BLOCK), smem, stream, 1u,
                          rows, cols, 1.f / cols, dy, lddy, x, ldx, w, mean, rstd, dr, lddr, dx,
-                         lddx, grads && parts > 1 ? partial : nullptr, dw, db, stages, wd);
+                         lddx, grads && parts > 1 ? partial : nullptr, dw, db, stages,
+                         test_stall(), wd);
   });
   if (e != cudaSuccess) return e;
   count_launch();

@@ -88,11 +88,12 @@ __global__ void __launch_bounds__(32 * kGroups)
 }
 
 // out[k][col] = sum over parts of partial[part][k][col], k < nvec (gridDim.y).
-// 32 columns per block; eight warps take every eighth part, eight in flight.
+// 32 columns per block; 16 warps take every 16th part, eight in flight.
+constexpr int kSumWarps = 16;
 template <class T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kSumWarps)
     column_sums_kernel(const float *partial, int parts, int cols, T *out0, T *out1) {
-  __shared__ float fold[8][32];
+  __shared__ float fold[kSumWarps][32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 5, k = blockIdx.y, nvec = gridDim.y;
@@ -100,14 +101,15 @@ __global__ void __launch_bounds__(256)
   float v = 0.f;
   if (col < cols)
 #pragma unroll 8
-    for (int i = group; i < parts; i += 8) v += partial[((int64_t)i * nvec + k) * cols + col];
+    for (int i = group; i < parts; i += kSumWarps)
+      v += partial[((int64_t)i * nvec + k) * cols + col];
   fold[group][lane] = v;
   __syncthreads();
   T *out = k ? out1 : out0;
   if (group != 0 || col >= cols || out == nullptr) return;
   v = 0.f;
 #pragma unroll
-  for (int g = 0; g < 8; ++g) v += fold[g][lane];
+  for (int g = 0; g < kSumWarps; ++g) v += fold[g][lane];
   out[col] = from_f32<T>(v);
 }
 
@@ -170,8 +172,8 @@ template <class T>
 cudaError_t column_sums(const float *partial, int parts, int cols, void *out0, void *out1, int nvec,
                         cudaStream_t stream) {
   const cudaError_t e = launch_kernel(
-      column_sums_kernel<T>, dim3((unsigned)((cols + 31) / 32), (unsigned)nvec), dim3(256), 0, stream,
-      1u, partial, parts, cols, static_cast<T *>(out0), static_cast<T *>(out1));
+      column_sums_kernel<T>, dim3((unsigned)((cols + 31) / 32), (unsigned)nvec),
+      dim3(32 * kSumWarps), 0, stream, 1u, partial, parts, cols, static_cast<T *>(out0), static_cast<T *>(out1));
   if (e == cudaSuccess) count_launch();
   return e;
 }

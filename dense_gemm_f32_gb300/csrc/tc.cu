@@ -1306,16 +1306,6 @@ Tile single_tile(TcKind kind, int M, int N, int K, int num_sms) {
   return deepen(best);
 }
 
-// DGEMM_TC_TEST_STALL=1 makes the MMA thread of the first CTA (pair) wait on
-// a barrier that nothing arrives at: its bounded wait runs out after ~2 s and
-// the kernel takes its abort path (watchdog site code, drained copies, freed
-// tensor memory, incomplete C).  For the failure-detection test only; read
-// at every launch.
-int test_stall() {
-  const char *e = getenv("DGEMM_TC_TEST_STALL");
-  return (e && e[0] == '1') ? 1 : 0;
-}
-
 template <TcKind KIND>
 constexpr CUtensorMapDataType tma_type() {
   return KIND == TcKind::kBF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
