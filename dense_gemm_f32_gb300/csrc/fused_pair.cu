@@ -5,7 +5,7 @@
 // The main loop is that of tc.cu's pair kernel: a cluster of two CTAs
 // accumulates 256 x 256 in the two SMs' tensor memory, CTA r holding rows
 // [128 r, 128 r + 128) of the accumulator and loading half of each operand
-// tile by TMA (6 stages of 32 KB, one producer thread per operand), two
+// tile by TMA (5 or 6 stages of 32 KB, one producer thread per operand), two
 // accumulators so that the epilogue of one tile overlaps the next tile's
 // main loop.  What is different:
 //  * A second operand pair.  kSum walks the k-blocks of A B, then those of
@@ -17,12 +17,17 @@
 //    gives each thread of the epilogue both projections of its row.
 //  * The epilogue (epilogue.cuh): eight warps, two per quarter of the TMEM
 //    lanes taking alternate 32-column pieces.  A thread holds 32 columns of
-//    one row; it reads the residual (or g and u) of that row segment straight
-//    from global memory, whole sectors at a time, computes in fp32, and packs
-//    16-bit results into a 64-byte-swizzled 32 x 32 piece of shared memory
-//    that goes out as one TMA store per output (pieces that TMA may not write
-//    go out element by element).  Each warp owns two 2 KB pieces and runs on
-//    its own, with no barrier among the epilogue warps.
+//    one row; it reads the residual of that row segment from global memory (g
+//    and u have come by TMA while the piece before was finished), computes in
+//    fp32, and packs 16-bit results into a 64-byte-swizzled 32 x 32 piece of
+//    shared memory that goes out as one TMA store per output (pieces that TMA
+//    may not write go out element by element).  Each warp owns two 2 KB pieces
+//    and runs on its own, with no barrier among the epilogue warps.
+// Bound by the tensor pipe under the power limit: 16384 x 14336 x 4096 bf16
+// with bias, gelu_tanh and both outputs 1.19 ms, 1620 TFLOP/s, where cuBLAS
+// sustains 1736 without an epilogue; 256 x 256 x 64 per pair and 0.31 us.  With
+// little K (1024 and less) the epilogue bounds it: a warp's chain through one
+// piece takes about 900 cycles.
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>
@@ -52,7 +57,7 @@ namespace {
 
 constexpr bool kAT = DGEMM_FUSED_UNIT == 2, kBT = DGEMM_FUSED_UNIT == 1;
 
-template <class T>
+template <class T, Epi EPI>
 struct PairCfg {
   static constexpr int BM = 256, BN = 256, HM = 128, HN = 128;  // pair tile, per-CTA halves
   static constexpr int ES = 2, BK = 64, UMMA_K = 16, KSTEPS = BK / UMMA_K;
@@ -61,13 +66,21 @@ struct PairCfg {
   static constexpr int A_BOXES = kAT ? HM / BOX : 1, B_BOXES = kBT ? 1 : HN / BOX;
   static constexpr int A_BOX_BYTES = kAT ? BK * 128 : A_BYTES;
   static constexpr int B_BOX_BYTES = kBT ? B_BYTES : BK * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, STAGES = 6;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  // Inputs of the epilogue that come by TMA, in one stage's place: G and U
+  // (4096 x 1024 x 8192: 101 us with 16-byte loads of a row per thread, 87).  A
+  // residual is read by the threads: the sixth stage is worth more (8192 x 4096
+  // x 14336: 565 us with six, 579 with five and the residual by TMA).
+  static constexpr int INS = EPI == Epi::kGatedBwd ? 2 : 0;
+  static constexpr int STAGES = INS ? 5 : 6;
   static constexpr int TMEM_COLS = 512;
   static constexpr int kEpiWarps = 8, kProdBWarp = 2 + kEpiWarps;
   static constexpr int THREADS = 32 * (3 + kEpiWarps);
-  static constexpr int NUM_BARS = 2 * STAGES + 6;  // full, empty, accf[2], acce[2], drain, stall
+  // full, empty, accf[2], acce[2], drain, stall, one per epilogue warp
+  static constexpr int NUM_BARS = 2 * STAGES + 6 + kEpiWarps;
   static constexpr int PIECE_BYTES = 32 * 64;      // 32 rows x 32 columns of 2 bytes
-  static constexpr int EPI_BYTES = kEpiWarps * 2 * PIECE_BYTES;
+  static constexpr int OUT_BYTES = kEpiWarps * 2 * PIECE_BYTES;
+  static constexpr int EPI_BYTES = OUT_BYTES + kEpiWarps * INS * PIECE_BYTES;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + NUM_BARS * 8 + 16 + 1024;
   static_assert(SMEM_BYTES <= 232448, "fits the 227 KB opt-in shared memory of a CTA");
   static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
@@ -86,12 +99,14 @@ enum : int {
   kSite3MmaDrain = 0xa5,
   kSite3MmaTail = 0xa6,
   kSite3EpiAccFull = 0xa7,
+  kSite3EpiInput = 0xa9,
   kSite3TestStall = 0xa8,  // DGEMM_TC_TEST_STALL: the MMA thread's test wait ran out
 };
 
 struct PairMaps {
   CUtensorMap a, b, a2, b2;  // operands
   CUtensorMap o[3];          // outputs, 32 x 32 boxes
+  CUtensorMap i[2];          // the epilogue's inputs, likewise
 };
 
 struct PairArgs {
@@ -105,6 +120,16 @@ struct PairArgs {
   int64_t ldo[3];
   int *watchdog;
 };
+
+// Row `lane` of a 32 x 32 piece that TMA loaded (64-byte swizzle).
+__device__ __forceinline__ void take_piece(const uint8_t *piece, int lane, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 v =
+        *reinterpret_cast<const uint4 *>(piece + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+    w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+  }
+}
 
 // A staged 32 x 32 piece written element by element, a row per instruction:
 // pieces that TMA may not write.  Not inlined, to keep the epilogue's loop
@@ -130,9 +155,9 @@ __device__ __noinline__ void store_piece(const uint16_t *wb, uint16_t *out, int6
 }
 
 template <class T, Epi EPI>
-__global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
+__global__ void __launch_bounds__(PairCfg<T, EPI>::THREADS, 1)
     fused_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairArgs p) {
-  using G = PairCfg<T>;
+  using G = PairCfg<T, EPI>;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -146,6 +171,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
   auto acce_bar = [&](int b) { return bars + 8u * (2 * G::STAGES + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * G::STAGES + 4);
   const uint32_t stall_bar = bars + 8u * (2 * G::STAGES + 5);  // nothing ever arrives here
+  auto in_bar = [&](int w) { return bars + 8u * (2 * G::STAGES + 6 + w); };
   uint8_t *tail = smem + G::STAGES * G::STAGE_BYTES + G::EPI_BYTES + G::NUM_BARS * 8;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
@@ -176,6 +202,7 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     mbar_init(stall_bar, 1);
+    for (int w = 0; w < G::kEpiWarps; ++w) mbar_init(in_bar(w), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -332,6 +359,31 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
     const uint32_t acce_leader1 = mapa_shared(acce_bar(1), 0);
     const bool kept = !pair_out && p.out[1] != nullptr;
     int stores = 0;  // pieces staged by this warp
+    // G and U come by TMA where their rows are aligned, a piece ahead: the first
+    // from (tile, c0) on that has elements inside the output.
+    const bool in_tma = G::INS > 0 && (p.i_vec & 3) == 3;
+    const uint32_t in_buf =
+        epi_base + (uint32_t)(G::OUT_BYTES + (warp - 2) * G::INS * G::PIECE_BYTES);
+    const uint32_t my_bar = in_bar(warp - 2);
+    uint32_t in_phase = 0;
+    bool in_flight = false;
+    auto send_for_inputs = [&](int tile, int c0) {
+      for (; tile < num_tiles; tile += clusters, c0 = 32 * half) {
+        int tm, tn;
+        tile_coords(tile, tiles_m, tiles_n, p.group_m, tm, tn);
+        const int r0 = tm * G::BM + (int)rank * G::HM + quarter * 32, col = tn * TN + c0;
+        if (c0 >= TN || col >= p.N || r0 >= p.M) continue;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(my_bar, (uint32_t)(G::INS * G::PIECE_BYTES));
+          for (int i = 0; i < G::INS; ++i)
+            tma_load_2d(in_buf + (uint32_t)(i * G::PIECE_BYTES), &maps.i[i], my_bar, col, r0);
+        }
+        in_flight = true;
+        return;
+      }
+      in_flight = false;
+    };
+    if (in_tma) send_for_inputs(cluster, 32 * half);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = cluster; tile < num_tiles; tile += clusters) {
@@ -352,17 +404,21 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
         const int valid = min(32, p.N - col);  // columns of the piece inside the output
         if (valid <= 0 || row0 >= p.M) break;  // the same for the whole warp
         uint32_t i0[16], i1[16];
-        bool has_in0 = false;
-        if constexpr (EPI == Epi::kLinear) {
-          has_in0 = p.in0 != nullptr;
-          if (has_in0)
-            load32<T>(static_cast<const T *>(p.in0) + (int64_t)row * p.ldi0, col,
-                      row < p.M ? p.N : 0, p.i_vec & 1, i0);
-        } else if constexpr (EPI == Epi::kGatedBwd) {
+        const bool has_in0 = EPI == Epi::kGatedBwd || (EPI == Epi::kLinear && p.in0 != nullptr);
+        if (G::INS > 0 && in_tma) {
+          const bool got = !*abort_flag && mbar_wait(my_bar, in_phase);
+          if (!got && lane == 0 && !*abort_flag) watchdog_trip(p.watchdog, kSite3EpiInput, abort_flag);
+          in_phase ^= 1u;
+          take_piece(smem + (in_buf - base), lane, i0);
+          take_piece(smem + (in_buf - base) + G::PIECE_BYTES, lane, i1);
+          __syncwarp();
+          send_for_inputs(tile, c0 + 64);
+        } else if (has_in0) {
           load32<T>(static_cast<const T *>(p.in0) + (int64_t)row * p.ldi0, col,
                     row < p.M ? p.N : 0, p.i_vec & 1, i0);
-          load32<T>(static_cast<const T *>(p.in1) + (int64_t)row * p.ldi1, col,
-                    row < p.M ? p.N : 0, p.i_vec & 2, i1);
+          if constexpr (EPI == Epi::kGatedBwd)
+            load32<T>(static_cast<const T *>(p.in1) + (int64_t)row * p.ldi1, col,
+                      row < p.M ? p.N : 0, p.i_vec & 2, i1);
         }
         float a[32], b[32];
         {
@@ -435,7 +491,10 @@ __global__ void __launch_bounds__(PairCfg<T>::THREADS, 1)
         acc_phase ^= 1u;
       }
     }
-    if (lane == 0) bulk_wait_group<0>();  // every TMA store of this warp complete
+    if (lane == 0) {
+      bulk_wait_group<0>();  // every TMA store of this warp complete
+      if (in_flight) mbar_wait(my_bar, in_phase);  // after an abort: its input has landed
+    }
     __syncwarp();
   }
 
@@ -457,10 +516,10 @@ constexpr CUtensorMapDataType map_type() {
 }
 
 // Maps of one operand pair; mn3d gets which of them are 3-D.
-template <class T>
+template <class T, Epi EPI>
 bool pair_operand_maps(CUtensorMap *ta, CUtensorMap *tb, const FusedGemm &p, const void *A,
                        int64_t lda, const void *B, int64_t ldb, int *mn3d) {
-  using G = PairCfg<T>;
+  using G = PairCfg<T, EPI>;
   const CUtensorMapDataType dt = map_type<T>();
   const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
   *mn3d = 0;
@@ -488,17 +547,17 @@ inline bool rows_aligned(const void *p, int64_t ld) {
 
 template <class T, Epi EPI>
 cudaError_t launch_pair(const FusedGemm &p, int *watchdog, cudaStream_t stream) {
-  using G = PairCfg<T>;
+  using G = PairCfg<T, EPI>;
   PairMaps maps;
   memset(&maps, 0, sizeof maps);
   PairArgs a;
   memset(&a, 0, sizeof a);
-  if (!pair_operand_maps<T>(&maps.a, &maps.b, p, p.A, p.lda, p.B, p.ldb, &a.mn3d))
+  if (!pair_operand_maps<T, EPI>(&maps.a, &maps.b, p, p.A, p.lda, p.B, p.ldb, &a.mn3d))
     return cudaErrorInvalidValue;
   if (p.dual != Dual::kNone) {
     int mn3d2 = 0;
     const bool gated = p.dual == Dual::kGated;
-    if (!pair_operand_maps<T>(&maps.a2, &maps.b2, p, gated ? p.A : p.A2, gated ? p.lda : p.lda2,
+    if (!pair_operand_maps<T, EPI>(&maps.a2, &maps.b2, p, gated ? p.A : p.A2, gated ? p.lda : p.lda2,
                               p.B2, p.ldb2, &mn3d2) ||
         mn3d2 != a.mn3d)
       return cudaErrorInvalidValue;
@@ -521,6 +580,13 @@ cudaError_t launch_pair(const FusedGemm &p, int *watchdog, cudaStream_t stream) 
                  CU_TENSOR_MAP_SWIZZLE_64B))
       a.o_tma |= 1 << i;
   }
+  const void *ins[2] = {p.in0, p.in1};
+  const int64_t ldi[2] = {p.ldi0, p.ldi1};
+  for (int i = 0; i < 2; ++i)
+    if (i < G::INS && ((a.i_vec >> i) & 1) &&
+        !make_map(&maps.i[i], ins[i], map_type<T>(), G::ES, p.M, p.N, ldi[i], 32, 32,
+                  CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
   a.watchdog = watchdog;
   auto kern = fused_pair_kernel<T, EPI>;
   static std::atomic<int> max_clusters[64] = {};
