@@ -24,10 +24,9 @@
 //    may not write go out element by element).  Each warp owns two 2 KB pieces
 //    and runs on its own, with no barrier among the epilogue warps.
 // Bound by the tensor pipe under the power limit: 16384 x 14336 x 4096 bf16
-// with bias, gelu_tanh and both outputs 1.19 ms, 1620 TFLOP/s, where cuBLAS
-// sustains 1736 without an epilogue; 256 x 256 x 64 per pair and 0.31 us.  With
-// little K (1024 and less) the epilogue bounds it: a warp's chain through one
-// piece takes about 900 cycles.
+// with bias, gelu_tanh and both outputs 1.19 ms, 1615 TFLOP/s, where a cuBLAS
+// product without an epilogue sustains 1736.  With little K (1024 and less) the
+// epilogue bounds it: a warp's chain through one piece takes about 900 cycles.
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>

@@ -3,10 +3,11 @@
 // join of column sums that several blocks hold parts of, and the re-pitching
 // of 16-bit operands.
 //
-// Bound by memory: dZ is two reads and one write of an M x N matrix.  A thread owns
-// eight columns (16 bytes of a row) and walks every eighth row of its block's share, so the column sums stay in registers; the eight
-// row groups of a block are added in shared memory, and each block's sums are
-// joined by a second launch, everything in a fixed order.
+// Bound by memory: dZ is two reads and one write of an M x N matrix.  A thread
+// owns eight columns (16 bytes of a row) and walks every eighth row of its
+// block's share, so the column sums stay in registers; the eight row groups of
+// a block are added in shared memory, and each block's sums are joined by a
+// second launch, everything in a fixed order.
 #include <cstdint>
 #include <cuda_runtime.h>
 
