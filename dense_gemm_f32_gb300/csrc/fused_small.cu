@@ -79,6 +79,11 @@ constexpr int kThreads = SPLIT ? 192 : 256;
 // 16.3 -> 15.4; from 8 on slower than none (23.3 us with 16).
 constexpr int kAheadStages = 3;
 
+// Rounds of the epilogue whose inputs are in flight: 256 x 4096 x 4096 with a
+// residual 21.6 -> 20.6 us, 1 x 4096 x 14336 21.8 -> 21.4, gated backward 5136 x
+// 784 x 3408 218 -> 210 (one round ahead 20.9, 21.4 and 212).
+constexpr int kInputsAhead = 2;
+
 // Site codes of the bounded waits.
 enum : int {
   kSite4ProducerEmpty = 0xb1,
@@ -224,6 +229,33 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();  // set-up done; the previous kernel on the stream has completed
 
+  // The epilogue's inputs (residual; G and U) are read kInputsAhead rounds
+  // ahead, the first of them during the main loop.
+  constexpr int Q = TF / 8;  // threads per token
+  const int live = min(p.nt, p.M - t0), feats = min(TF, p.N - f0);
+  const int n = live * Q, end = f0 + feats, round = splits * THREADS;
+  const int e0 = part * THREADS + threadIdx.x;
+  const int f = 8 * (e0 % Q), col = f0 + f;  // the same in every round
+  const T *in0 = static_cast<const T *>(p.in0), *in1 = static_cast<const T *>(p.in1);
+  const bool has_in0 = EPI != Epi::kGated && in0 != nullptr;
+  struct Inputs {
+    RowBlocks x0, x1;
+  } ahead[kInputsAhead];
+  auto fetch = [&](int e) {
+    const int t = e / Q;
+    const int cols = t < live && f < feats ? end : 0;
+    const int64_t row = t0 + t;
+    Inputs r = {};
+    if (has_in0) r.x0 = fetch_row16<T, AL>(in0 + row * p.ldi0, col, cols);
+    if (EPI == Epi::kGatedBwd) r.x1 = fetch_row16<T, AL>(in1 + row * p.ldi1, col, cols);
+    return r;
+  };
+  auto fetch_first = [&] {
+#pragma unroll
+    for (int k = 0; k < kInputsAhead; ++k) ahead[k] = fetch(e0 + k * round);
+  };
+  if (warp != 0) fetch_first();
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -328,7 +360,6 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
       // Every MMA has completed, so the stage area is idle: partial[t][f]
       float *col = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
       const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16);
-      const int live = min(p.nt, p.M - t0);
       for (int c0 = 0; c0 < live; c0 += 16) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(t_row + (uint32_t)c0, r);
@@ -341,6 +372,10 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
     }
   }
 
+  if (warp == 0) {
+    __syncwarp();
+    fetch_first();
+  }
   // ------------------------------------------ join the parts, finish, store
   // Every thread of every CTA of the cluster gets here, also after a bounded
   // wait gave up.
@@ -363,8 +398,6 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
     aborted = *abort_flag != 0;
   }
   {
-    const int live = min(p.nt, p.M - t0);
-    const int feats = min(TF, p.N - f0);
     auto sum4 = [&](uint32_t off) {  // parts added in K order
       if constexpr (SPLIT) {
         float4 v[G::MAX_SPLITS];
@@ -386,26 +419,25 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
       *slot = pair_out ? (second ? 1 : 0) : o;
       return !(pair_out && o) && p.out[*slot] != nullptr;
     };
-    const T *in0 = static_cast<const T *>(p.in0), *in1 = static_cast<const T *>(p.in1);
     const T *bias = static_cast<const T *>(p.bias);
-    const bool has_in0 = in0 != nullptr, kept = !pair_out && p.out[1] != nullptr;
-    constexpr int Q = TF / 8;  // threads per token
-    const int n = live * Q, end = f0 + feats;
+    const bool kept = !pair_out && p.out[1] != nullptr;
     // whole warps go round together: their stores put blocks together
 #pragma unroll 1
-    for (int e = part * THREADS + threadIdx.x; e - lane < n; e += splits * THREADS) {
-      const int t = e / Q, f = 8 * (e % Q), col = f0 + f;
+    for (int e = e0; e - lane < n; e += round) {
+      const int t = e / Q;
       const bool in = t < live && f < feats;
       const int64_t row = t0 + t;
       float a[8], b[8];
       uint32_t i0[4], i1[4], w[3][4];
-      auto get = [&](const T *m, uint32_t (&v)[4]) {
-        const uint4 x = load_row16<T, AL>(m, col, end);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      };
+      auto unpack = [&](uint4 x, uint32_t (&v)[4]) { v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w; };
+      const Inputs now = ahead[0];
+#pragma unroll
+      for (int k = 0; k + 1 < kInputsAhead; ++k) ahead[k] = ahead[k + 1];
+      ahead[kInputsAhead - 1] = fetch(e + kInputsAhead * round);
       if (in) {
-        if (EPI != Epi::kGated && has_in0) get(in0 + row * p.ldi0, i0);
-        if (EPI == Epi::kGatedBwd) get(in1 + row * p.ldi1, i1);
+        if (has_in0) unpack(take_row16<T, AL>(now.x0, in0 + row * p.ldi0, col, end), i0);
+        if (EPI == Epi::kGatedBwd)
+          unpack(take_row16<T, AL>(now.x1, in1 + row * p.ldi1, col, end), i1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float4 v = sum4((uint32_t)((t * G::TF + f + 4 * h) * 4));
@@ -417,7 +449,7 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
         }
         if (EPI == Epi::kLinear && bias != nullptr) {
           uint32_t v[4];
-          get(bias, v);
+          unpack(load_row16<T, AL>(bias, col, end), v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 c = unpack2<T>(v[j]);
