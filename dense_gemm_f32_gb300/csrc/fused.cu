@@ -30,7 +30,8 @@ int knob(const char *name, int lo, int hi) {
 // quarter of the SMs, and 128-token tiles below that, were 30% off on average.
 //
 // Pair kernel: a wave of 256 x 256 tiles takes 0.31 us per 64 k, or as long as
-// writing its outputs.
+// writing its outputs; the gate gradient's last epilogue shows, and inputs that
+// do not come by TMA cost it 15%.
 double pair_time(const FusedGemm &p, int num_sms) {
   const int tn = p.epi == Epi::kGated ? 128 : 256;
   const int64_t products = p.dual == Dual::kPair ? 2 : 1;
@@ -40,17 +41,21 @@ double pair_time(const FusedGemm &p, int num_sms) {
   const int outs = p.dual == Dual::kPair ? 1 : (p.out0 != nullptr) + (p.out1 != nullptr) + (p.out2 != nullptr);
   const double written = 2.0 * (double)p.M * p.N * outs * products;
   const double main = waves * (kblocks * 0.31), out = written / 2.4e6;
-  return 6.1 + (main > out ? main : out);
+  if (p.epi != Epi::kGatedBwd) return 6.1 + (main > out ? main : out);
+  const bool in_tma = tma_ok(p.in0, p.ldi0, 2) && tma_ok(p.in1, p.ldi1, 2);
+  return (13 + (main > out ? main : out)) * (in_tma ? 1.0 : 1.15);
 }
 
 // Small kernel: a stage costs a CTA its wait (0.197 us, and 0.959 us shared by
 // the stages in flight), its bytes at 96 GB/s, or its share of the SM's 312
 // GB/s when two run there; all together at most 17.8 TB/s from L2; a tile's
 // drain and epilogue grow with its tokens, and joining the parts of a K split
-// costs 1.6 us.
+// costs 1.6 us.  The gate gradient's epilogue, shared by the parts, is three
+// times a linear layer's (5136 x 3408 x 784 on 128-token tiles: 69 us, 45 without
+// the term; the pair kernel 55).
 // `tiles` of this product among `all` of the launch.
-double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int64_t resident,
-                  int64_t all) {
+double small_time(Epi epi, int64_t tiles, int64_t kblocks, const SmallPlan &plan,
+                  int64_t resident, int64_t all) {
   const double nt = plan.nt, share = plan.per_sm, stage = (128 + nt) * 128 * plan.kd;
   const int64_t parts = (kblocks + plan.splits - 1) / plan.splits;
   const int64_t waves = (all + resident - 1) / resident;
@@ -59,7 +64,8 @@ double small_time(int64_t tiles, int64_t kblocks, const SmallPlan &plan, int64_t
   if (per < stage * share / 312e3) per = stage * share / 312e3;
   const double loads = waves * (2.18 + parts * per);
   const double l2 = parts * stage * (all > tiles ? all : tiles) * plan.splits / 17.8e6;
-  const double tail = plan.splits > 1 ? 0.0283 * nt + 1.61 : 0.0124 * nt;
+  double tail = plan.splits > 1 ? 0.0283 * nt + 1.61 : 0.0124 * nt;
+  if (epi == Epi::kGatedBwd) tail += 0.037 * nt / plan.splits;
   return 1.27 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
 }
 
@@ -134,8 +140,8 @@ double small_plan(const FusedGemm *ps, int n, const Residency &res, SmallPlan *b
       }
       double t = 0;
       for (int j = 0; j < n; ++j) {
-        const double tj = small_time(tiles_of(ps[j], plans[j].nt), kblocks_of(ps[j], plans[j].kd),
-                                     plans[j], resident, tiles);
+        const double tj = small_time(ps[j].epi, tiles_of(ps[j], plans[j].nt),
+                                     kblocks_of(ps[j], plans[j].kd), plans[j], resident, tiles);
         t = t > tj ? t : tj;
       }
       if (best == 0 || t < best) {
