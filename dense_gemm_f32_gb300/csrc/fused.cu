@@ -50,11 +50,13 @@ double pair_time(const FusedGemm &p, int num_sms) {
 // the stages in flight), its bytes at 96 GB/s, or its share of the SM's 312
 // GB/s when two run there; all together at most 17.8 TB/s from L2; a tile's
 // drain and epilogue grow with its tokens, and joining the parts of a K split
-// costs 1.6 us.  The gate gradient's epilogue, shared by the parts, is three
-// times a linear layer's (5136 x 3408 x 784 on 128-token tiles: 69 us, 45 without
-// the term; the pair kernel 55).
+// costs 1.6 us, and with two CTAs per SM, whose clusters join at different
+// times, 0.05 us more per token (1 x 4096 x 14336: 21.5 us in 4 parts, 20.1 in
+// 8; 64 x 4096 x 14336: 24.1 and 26.7).  The gate gradient's epilogue, shared
+// by the parts, is three times a linear layer's (5136 x 3408 x 784 on 128-token
+// tiles: 69 us, 45 without the term; the pair kernel 55).
 // `tiles` of this product among `all` of the launch.
-double small_time(Epi epi, int64_t tiles, int64_t kblocks, const SmallPlan &plan,
+double small_time(const FusedGemm &p, int64_t tiles, int64_t kblocks, const SmallPlan &plan,
                   int64_t resident, int64_t all) {
   const double nt = plan.nt, share = plan.per_sm, stage = (128 + nt) * 128 * plan.kd;
   const int64_t parts = (kblocks + plan.splits - 1) / plan.splits;
@@ -65,7 +67,8 @@ double small_time(Epi epi, int64_t tiles, int64_t kblocks, const SmallPlan &plan
   const double loads = waves * (2.18 + parts * per);
   const double l2 = parts * stage * (all > tiles ? all : tiles) * plan.splits / 17.8e6;
   double tail = plan.splits > 1 ? 0.0283 * nt + 1.61 : 0.0124 * nt;
-  if (epi == Epi::kGatedBwd) tail += 0.037 * nt / plan.splits;
+  if (plan.splits > 1 && plan.per_sm == 2) tail += 0.05 * (p.M < plan.nt ? p.M : plan.nt);
+  if (p.epi == Epi::kGatedBwd) tail += 0.037 * nt / plan.splits;
   return 1.27 + (loads > l2 ? loads : l2) + waves * (share > 1 ? 1.414 : 1.0) * tail;
 }
 
@@ -140,7 +143,7 @@ double small_plan(const FusedGemm *ps, int n, const Residency &res, SmallPlan *b
       }
       double t = 0;
       for (int j = 0; j < n; ++j) {
-        const double tj = small_time(ps[j].epi, tiles_of(ps[j], plans[j].nt),
+        const double tj = small_time(ps[j], tiles_of(ps[j], plans[j].nt),
                                      kblocks_of(ps[j], plans[j].kd), plans[j], resident, tiles);
         t = t > tj ? t : tj;
       }

@@ -21,7 +21,7 @@
 //  * kGated: the tile's 128 rows are 64 features of Wg and the same 64 of Wu,
 //    so one MMA stream gives both projections of a hidden unit in one tile.
 //  * Bound by HBM for single tokens: 4096 -> 14336 features in bf16 20.1 us, 5.8
-//    TB/s of 6.8, 14336 -> 4096 21.5 us with K split; below that by latency:
+//    TB/s of 6.8, 14336 -> 4096 20.0 us with K split; below that by latency:
 //    1024 -> 1024 6.9 us a call in a graph, weights from HBM.
 //  * Up to three independent products (a backward pass's) go out as one launch,
 //    their tiles one after the other in one grid.
@@ -623,16 +623,25 @@ int small_stages(const SmallPlan &plan) {
   return n < G::MAX_STAGES ? n : G::MAX_STAGES;
 }
 
-// By the occupancy query, once per device, cluster size and share of an SM
-// (every instance of the kernel has the same block and bounds; a cluster has
-// to fit in one GPC, which holds a few SMs more than a multiple of its size).
+// By the occupancy query, once per device and cluster size (every instance of
+// the kernel has the same block and bounds; a cluster has to fit in one GPC,
+// which holds a few SMs more than a multiple of its size).  The query knows of
+// one CTA of this kernel per SM only, whatever its shared memory, though two
+// run (1 x 4096 x 14336 in 32 clusters of 8: 20.1 us; in 32 of 4: 21.5); a
+// GPC with two per SM holds as many clusters of 2 s as it holds clusters of s
+// with one.
 int64_t small_resident(const SmallPlan &plan, int num_sms) {
   using G = SmallCfg;
   if (plan.splits == 1) return (int64_t)plan.per_sm * num_sms;
-  static std::atomic<int> cache[64][3][G::MAX_SPLITS + 1] = {};
+  if (plan.per_sm == 2) {
+    const bool even = plan.splits % 2 == 0;
+    const int64_t one = small_resident({plan.nt, plan.kd, even ? plan.splits / 2 : plan.splits, 1}, num_sms);
+    return even ? one : 2 * one;
+  }
+  static std::atomic<int> cache[64][G::MAX_SPLITS + 1] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / plan.splits;
-  std::atomic<int> &slot = cache[dev][plan.per_sm][plan.splits];
+  std::atomic<int> &slot = cache[dev][plan.splits];
   int n = slot.load(std::memory_order_relaxed);
   if (n == 0) {
     auto kern = fused_small_kernel<Elem, Epi::kLinear, true, true, 1, 0>;
@@ -644,14 +653,14 @@ int64_t small_resident(const SmallPlan &plan, int num_sms) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)plan.splits);
     cfg.blockDim = dim3(kThreads<true>);
-    cfg.dynamicSmemBytes = (size_t)((plan.per_sm == 2 ? G::BUDGET2 : G::BUDGET1) + G::TAIL_BYTES);
+    cfg.dynamicSmemBytes = G::BUDGET1 + G::TAIL_BYTES;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              G::BUDGET1 + G::TAIL_BYTES) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();  // not sticky; an estimate will do
-      n = plan.per_sm * num_sms / plan.splits;
+      n = num_sms / plan.splits;
     }
     slot.store(n, std::memory_order_relaxed);
   }
