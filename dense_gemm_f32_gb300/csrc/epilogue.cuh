@@ -19,7 +19,7 @@ __device__ __noinline__ void load32_unaligned(const T *row, int col, int cols, u
   const int valid = min(32, cols - col);
   const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);
   const uint4 *block = reinterpret_cast<const uint4 *>(
-      reinterpret_cast<const uint8_t *>(row) - off + col * (int)sizeof(T));
+      reinterpret_cast<const uint8_t *>(row) - off + (int64_t)col * (int)sizeof(T));
   const int blocks = valid > 0 ? (off + 2 * valid + 15) / 16 : 0;
   uint4 b[5];
 #pragma unroll

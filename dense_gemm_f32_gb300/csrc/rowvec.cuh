@@ -109,7 +109,7 @@ __device__ __forceinline__ void store_row16(T *row, int col, int cols, const uin
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int c = col + k * LANES * V;
-      uint8_t *dst = reinterpret_cast<uint8_t *>(row) - off + c * (int)sizeof(T);
+      uint8_t *dst = reinterpret_cast<uint8_t *>(row) - off + (int64_t)c * (int)sizeof(T);
       // the vector before: the lane before's, and for the first lane the last
       // lane's of the round before
       const uint4 send = k > 0 && lane == LANES - 1 ? v[k > 0 ? k - 1 : 0] : v[k];
