@@ -512,7 +512,7 @@ int dgemm_gemm_ex(int path, int op_a, int op_b, int M, int N, int K, const void 
 const char *dgemm_status_string(int status) {
   switch (status) {
     case DGEMM_OK: return "success";
-    case DGEMM_ERR_INVALID_VALUE: return "invalid value: negative size, leading dimension too small, or eps not finite and >= 0";
+    case DGEMM_ERR_INVALID_VALUE: return "invalid value: negative or too large size, leading dimension too small, or eps not finite and >= 0";
     case DGEMM_ERR_NULL_POINTER: return "null pointer for A, B or C, or for an argument that is not optional";
     case DGEMM_ERR_ALIAS: return "C (or another output) overlaps another argument";
     case DGEMM_ERR_UNSUPPORTED: return "unsupported mode, element type, activation or layout";

@@ -12,6 +12,7 @@
 //   8. every pointer is device memory of this device  -> DGEMM_ERR_INVALID_POINTER
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <cuda_runtime.h>
 
 #include "../../include/dgemm.h"
@@ -43,6 +44,14 @@ bool ok_dtype(int dtype, bool f32) {
 bool ok_act(int act) { return act >= DGEMM_ACT_NONE && act <= DGEMM_ACT_SILU; }
 bool ok_op(int op) { return op == DGEMM_OP_N || op == DGEMM_OP_T; }
 int elem_bytes(int dtype) { return dtype == DGEMM_DTYPE_F32 ? 4 : 2; }
+
+// Step 2 for the sizes that the kernels count in 32 bits: a round-up to whole
+// tiles or vectors, and a step past the end, stay below 2^31.
+bool ok_counts(std::initializer_list<int> sizes) {
+  for (int n : sizes)
+    if (n > DGEMM_OPS_MAX_SIZE) return false;
+  return true;
+}
 
 // Step 2 for the matrices (an absent optional one is not looked at).
 bool ok_sizes(const Arg *a, int n) {
@@ -115,7 +124,8 @@ int dgemm_layer_norm(int dtype, int rows, int cols, float eps, const void *X, in
   const Arg a[] = {{X, rows, cols, ldx, es, false, false}, vec(weight, cols, es, false),
                    vec(bias, cols, es, false),   {Y, rows, cols, ldy, es, true, false},
                    vec(mean, rows, 4, true),     vec(rstd, rows, 4, true)};
-  if (!ok_sizes(a, 4) || !(eps >= 0.f) || std::isinf(eps)) return DGEMM_ERR_INVALID_VALUE;
+  if (!ok_counts({cols}) || !ok_sizes(a, 4) || !(eps >= 0.f) || std::isinf(eps))
+    return DGEMM_ERR_INVALID_VALUE;
   if (rows == 0 || cols == 0) return DGEMM_OK;
   int dev = 0, sms = 0;
   const int st = check_args(a, 6, -1, -1, &dev, &sms);
@@ -136,6 +146,7 @@ int dgemm_layer_norm_backward(int dtype, int rows, int cols, const void *dY, int
                    {rstd, 1, rows, rows, 4, false, false},   {dR, rows, cols, lddr, es, false, true},
                    {dX, rows, cols, lddx, es, true, false},  vec(dweight, cols, es, true),
                    vec(dbias, cols, es, true)};
+  if (!ok_counts({cols})) return DGEMM_ERR_INVALID_VALUE;
   for (int i : {0, 1, 2, 5, 6, 7, 8})
     if (!ok_sizes(a + i, 1)) return DGEMM_ERR_INVALID_VALUE;
   if (cols == 0 || (rows == 0 && !dweight && !dbias)) return DGEMM_OK;
@@ -162,6 +173,7 @@ int dgemm_linear(int dtype, int activation, int op_w, int M, int N, int K, const
                    {R, M, N, ldr, es, false, true},
                    {D, M, N, ldd, es, true, false},
                    {Z, M, N, ldz, es, true, true}};
+  if (!ok_counts({M, N, K})) return DGEMM_ERR_INVALID_VALUE;
   for (int i : {0, 1, 3, 4, 5})
     if (!ok_sizes(a + i, 1)) return DGEMM_ERR_INVALID_VALUE;
   if (M == 0 || N == 0) return DGEMM_OK;
@@ -192,6 +204,7 @@ int dgemm_linear_backward(int dtype, int activation, int op_w, int M, int N, int
                    {dX, M, K, lddx, es, true, true},
                    {dW, wr, wc, lddw, es, true, true},
                    vec(dbias, N, es, true)};
+  if (!ok_counts({M, N, K})) return DGEMM_ERR_INVALID_VALUE;
   for (int i = 0; i < 7; ++i)
     if (!ok_sizes(a + i, 1)) return DGEMM_ERR_INVALID_VALUE;
   const bool want_dx = dX && M > 0 && K > 0, want_dw = dW && N > 0 && K > 0;
@@ -250,7 +263,7 @@ int dgemm_gated_ffn(int dtype, int activation, int op_w, int M, int D, int F, co
                    {R, M, D, ldr, es, false, true},    {H, M, F, ldh, es, true, false},
                    {G, M, F, ldg, es, true, U == nullptr}, {U, M, F, ldu, es, true, G == nullptr},
                    {Y, M, D, ldy, es, true, false}};
-  if (!ok_sizes(a, 9)) return DGEMM_ERR_INVALID_VALUE;
+  if (!ok_counts({M, D, F}) || !ok_sizes(a, 9)) return DGEMM_ERR_INVALID_VALUE;
   if (M == 0 || (D == 0 && F == 0)) return DGEMM_OK;
   int dev = 0, sms = 0;
   int st = check_args(a, 9, 8, 4, &dev, &sms);  // Y may be R itself
@@ -304,7 +317,7 @@ int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, 
                    {dX, M, D, lddx, es, true, true},    {dWg, ur, uc, lddwg, es, true, dWu == nullptr},
                    {dWu, ur, uc, lddwu, es, true, dWg == nullptr},
                    {dWd, uc, ur, lddwd, es, true, true}};
-  if (!ok_sizes(a, 14)) return DGEMM_ERR_INVALID_VALUE;
+  if (!ok_counts({M, D, F}) || !ok_sizes(a, 14)) return DGEMM_ERR_INVALID_VALUE;
   const bool want_dx = dX && M > 0, want_up = dWg && F > 0, want_down = dWd && F > 0;
   if (D == 0 || (!want_dx && !want_up && !want_down)) return DGEMM_OK;
   int dev = 0, sms = 0;

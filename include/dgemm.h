@@ -68,7 +68,7 @@ extern "C" {
  * was enqueued. */
 typedef enum {
     DGEMM_OK = 0,
-    DGEMM_ERR_INVALID_VALUE = 1,   /* negative size, leading dimension too small, bad eps */
+    DGEMM_ERR_INVALID_VALUE = 1,   /* negative or too large size, leading dimension too small, bad eps */
     DGEMM_ERR_NULL_POINTER = 2,    /* NULL A, B or C (or a matrix that is not optional) with work to do */
     DGEMM_ERR_ALIAS = 3,           /* an output overlaps another argument        */
     DGEMM_ERR_UNSUPPORTED = 4,     /* unknown mode, element type or activation   */
@@ -316,7 +316,12 @@ int dgemm_gemm_ex(int path, int op_a, int op_b, int M, int N, int K,
  * (DGEMM_ERR_ALIAS) except where an entry point says so.  Matrices marked
  * "workspace" are outputs whose contents are unspecified afterwards beyond
  * what is stated.  A sum over nothing (K == 0, no rows) is zero.
+ *
+ * The sizes of a product and the columns of a layer norm are at most
+ * DGEMM_OPS_MAX_SIZE (beyond it DGEMM_ERR_INVALID_VALUE): the kernels count
+ * columns and tiles in 32 bits, and this leaves room for the last tile.
  */
+#define DGEMM_OPS_MAX_SIZE 2147482624 /* 2^31 - 1024 */
 
 /* Element types of the feed-forward operators. */
 typedef enum {
