@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(S::BLOCK)
 // of threads that shares rows.  A stage holds NIN matrices' rows, each copied
 // as the whole 16-byte blocks it lies in; a row starts `offset` bytes into its
 // place.  Every wait is bounded; a group whose wait gave up records it, stops
-// waiting and finishes with incomplete results.
+// copying and waiting and finishes with incomplete results.
 template <class S, int NIN>
 struct Ring {
   using T = typename S::T;
@@ -199,11 +199,12 @@ struct Ring {
     for (int i = 0; i < NIN; ++i)
       if (bytes[i]) bulk_load(data + (uint32_t)((stage * NIN + i) * place), from[i], bytes[i], bar);
   }
-  __device__ void wait(int stage, uint32_t parity) {
-    if (!dead && !mbar_wait(bars + 8u * (uint32_t)stage, parity)) {
-      dead = true;
-      if (leader) atomicCAS(watchdog, 0, kSiteNormRow);
-    }
+  // False when this wait is the one that gave up.
+  __device__ bool wait(int stage, uint32_t parity) {
+    if (dead || mbar_wait(bars + 8u * (uint32_t)stage, parity)) return true;
+    dead = true;
+    if (leader) atomicCAS(watchdog, 0, kSiteNormRow);
+    return false;
   }
   // Matrix i's copy of `row` in `stage`.
   __device__ const T *row_at(int stage, int i, int64_t row) const {
@@ -227,6 +228,12 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
   constexpr int V = S::V, CH = S::CH, GROUP = S::GROUP, ROWS = S::BWD_ROWS;
   __shared__ float red[GROUP > 32 ? ROWS : 1][2][2][32];
   __shared__ uint64_t bars[ROWS * kMaxStages];
+  struct GaveUp {
+    int64_t row;
+    int stage, stages;
+    uint32_t phase;
+  };
+  __shared__ GaveUp gave_up[ROWS];  // where a ring's wait gave up (in registers it cost spills)
   extern __shared__ __align__(16) uint8_t rows_smem[];
   pdl_launch_dependents();
   const int t = threadIdx.x % GROUP, sub = threadIdx.x / GROUP;
@@ -267,7 +274,8 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
   for (; row < rows; row += step) {
     const float mu = mu_next, r = r_next;
     if (row + step < rows) mu_next = mean[row + step], r_next = rstd[row + step];
-    ring.wait(stage, phase);
+    if (!ring.wait(stage, phase) && t == 0)  // all stages are full but for the last row's
+      gave_up[sub] = {row, stage, stages - (last >= 0 ? 1 : 0), phase};
     const T *dy = ring.row_at(stage, 0, row), *x = ring.row_at(stage, 1, row);
     float p[S::KEEP ? CH : 1][V], xh[S::KEEP ? CH : 1][V], s[2] = {0.f, 0.f};
     // p = dy w and xh of vector c
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
     row_sum<S>(s, red[GROUP > 32 ? sub : 0][buf], sub);
     buf ^= 1;
     if (GROUP == 32) __syncwarp();
-    if (t == 0 && last >= 0 && row + (stages - 1) * step < rows)
+    if (t == 0 && !ring.dead && last >= 0 && row + (stages - 1) * step < rows)
       ring.fill(last, row + (stages - 1) * step);
     last = stage;
     const float m1 = s[0] * inv, m2 = s[1] * inv;
@@ -324,9 +332,16 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
       phase ^= 1u;
     }
   }
-  if (ring.dead && t == 0)  // no copy lands after the block has left (2 s have passed by now)
-    for (int s = 0; s < stages; ++s)
-      if (!mbar_wait(ring.bars + 8u * s, phase ^ (s < stage ? 1u : 0u))) break;
+  if (ring.dead && t == 0) {
+    // No copy was begun after the wait that gave up; those begun before it land
+    // (a bounded wait each) before the block leaves or puts its memory to other use.
+    const GaveUp g = gave_up[sub];
+    for (int k = 0; k < g.stages && g.row + k * step < rows; ++k) {
+      const bool wrap = g.stage + k >= stages;
+      mbar_wait(ring.bars + 8u * (uint32_t)(wrap ? g.stage + k - stages : g.stage + k),
+                g.phase ^ (wrap ? 1u : 0u));
+    }
+  }
   if (!grads) return;
   // the block's rows side by side, added in their order (the ring is idle now)
   float *fold = reinterpret_cast<float *>(rows_smem);
