@@ -407,6 +407,8 @@ __global__ void __launch_bounds__(PairCfg<T, EPI>::THREADS, 1)
         if (G::INS > 0 && in_tma) {
           const bool got = !*abort_flag && mbar_wait(my_bar, in_phase);
           if (!got && lane == 0 && !*abort_flag) watchdog_trip(p.watchdog, kSite3EpiInput, abort_flag);
+          // nothing more is sent for: the copy in flight is waited for at the end
+          if (!__all_sync(0xffffffffu, got)) break;
           in_phase ^= 1u;
           take_piece(smem + (in_buf - base), lane, i0);
           take_piece(smem + (in_buf - base) + G::PIECE_BYTES, lane, i1);
