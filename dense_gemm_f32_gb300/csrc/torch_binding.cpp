@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "../../include/dgemm.h"
@@ -237,7 +238,9 @@ PyObject *layer_norm(PyObject *const *a) {
   }
   const auto sizes = x.sizes().slice(0, x.dim() - 1);
   const auto options = x.options().dtype(at::kFloat);
-  const Tensor mean = at::empty(sizes, options), rstd = at::empty(sizes, options);
+  // rows without columns have no statistics, and the library writes none
+  auto stat = [&] { return m.cols > 0 ? at::empty(sizes, options) : at::full(sizes, NAN, options); };
+  const Tensor mean = stat(), rstd = stat();
   check(dgemm_layer_norm(dt, m.rows, m.cols, (float)eps, m.p, m.ld, w, b, y.p, y.ld,
                          static_cast<float *>(mean.data_ptr()),
                          static_cast<float *>(rstd.data_ptr()), stream),

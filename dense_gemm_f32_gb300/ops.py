@@ -74,7 +74,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, return_stats=False, out=None
     x: (..., n) bfloat16, float16 or float32.  weight, bias: n elements of the
     same type, or None.  out: optional tensor of x's shape and type to write.
     Returns y, or (y, mean, rstd) with the float32 statistics of every row
-    (shape x.shape[:-1]) that layer_norm_backward takes.
+    (shape x.shape[:-1]) that layer_norm_backward takes; rows without columns
+    have none (NaN).
     """
     if stream is not None:
         with _on(stream, x):

@@ -345,7 +345,8 @@ typedef enum {
  * mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps), in two passes over
  * the row held on the SM (the variance is of the centred values).
  * X, Y: rows x cols.  weight, bias: cols elements, or NULL (1 and 0).
- * mean, rstd: rows floats, or NULL when the backward pass is not wanted.
+ * mean, rstd: rows floats, or NULL when the backward pass is not wanted; with
+ * cols == 0 nothing is written, the statistics of no values included.
  * eps >= 0 and finite, else DGEMM_ERR_INVALID_VALUE.
  */
 int dgemm_layer_norm(int dtype, int rows, int cols, float eps,
