@@ -278,16 +278,25 @@ __global__ void __launch_bounds__(S::BWD_BLOCK, 1)
       gave_up[sub] = {row, stage, stages - (last >= 0 ? 1 : 0), phase};
     const T *dy = ring.row_at(stage, 0, row), *x = ring.row_at(stage, 1, row);
     float p[S::KEEP ? CH : 1][V], xh[S::KEEP ? CH : 1][V], s[2] = {0.f, 0.f};
-    // p = dy w and xh of vector c
+    // p = dy w and xh of vector c.  Past the row's end p is 0, and so has xh to
+    // be: -mu r may be past fp32's range, and 0 times that NaN.  (A vector of an
+    // aligned row is all inside or all past; others take a branch that few warps
+    // enter, as a select per element cost odd rows 3%.)
     auto read = [&](int c, float(&d)[V], float(&pc)[V], float(&hc)[V]) {
       float g[V];
       widen16<T>(load_row16<T, S::ALIGNED>(dy, S::col(c, t), cols), d);
       widen16<T>(load_row16<T, S::ALIGNED>(x, S::col(c, t), cols), hc);
       weights(c, g);
+      const float rc = !S::ALIGNED || S::col(c, t) < cols ? r : 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        hc[j] = (hc[j] - mu) * r;
+        hc[j] = (hc[j] - mu) * rc;
         pc[j] = d[j] * g[j];
+      }
+      if (!S::ALIGNED && S::col(c, t) + V > cols) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (S::col(c, t) + j >= cols) hc[j] = 0.f;
       }
     };
 #pragma unroll
