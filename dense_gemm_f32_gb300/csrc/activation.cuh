@@ -158,7 +158,8 @@ __device__ __forceinline__ void act_grad_f32(float z, float &value, float &slope
     const float z2 = z * z;
     const float s = sigmoid2(z * fmaf(2.f * kGeluA * kGeluB * kLog2e, z2, 2.f * kGeluA * kLog2e));
     value = z * s;
-    slope = fmaf(value * (1.f - s), fmaf(6.f * kGeluA * kGeluB, z2, 2.f * kGeluA), s);
+    // where z^2 is past fp32's range value (1 - s) is 0, and has to stay 0
+    slope = fmaf(value * (1.f - s), fmaf(6.f * kGeluA * kGeluB, fminf(z2, 1e30f), 2.f * kGeluA), s);
   } else if constexpr (ACT == DGEMM_ACT_SILU) {
     const float s = sigmoid2(kLog2e * z);
     value = z * s;
