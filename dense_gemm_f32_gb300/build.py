@@ -22,6 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdgemm.so")
 BINDING = os.path.join(PKG, "_torch_binding.so")
 HEADER = os.path.join(ROOT, "include", "dgemm.h")
+BINDING_SOURCE = "torch_binding.cpp"
 # (source, object name, defines): simt.cu and tc.cu are compiled once per
 # operand layout so that the four layouts build in parallel.
 UNITS = ([("api.cu", "api", []), ("staging.cu", "staging", []), ("ops_api.cu", "ops_api", []),
@@ -46,36 +47,57 @@ def _nvcc():
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libdgemm.so")
 
 
-def _sources():
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [HEADER, __file__]
-    return [d for d in deps if os.path.isfile(d)]
-
-
-def _stale():
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _newer(path, sources):
+    """Whether a source is newer than the built file, or there is none."""
+    if not os.path.exists(path):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(s) > t for s in _sources())
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(s) > t for s in sources if os.path.isfile(s))
+
+
+def _library_stale():
+    sources = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SOURCE]
+    return _newer(LIB, sources + [HEADER, __file__])
+
+
+def _binding_stale():
+    return _newer(BINDING, [os.path.join(CSRC, BINDING_SOURCE), HEADER, __file__])
+
+
+def _run(cmd, what):
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{what}: {cmd[0]}: {e.strerror}") from e
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stderr[-6000:]}")
+    return r.stdout + r.stderr
 
 
 def _compile_binding(nvcc):
     """The tensor calls' object file, and the directory of PyTorch's libraries."""
     spec = importlib.util.find_spec("torch")
     if spec is None:
-        raise RuntimeError("PyTorch is required to build the operators' tensor calls")
+        raise RuntimeError("the tensor calls need PyTorch, which is not installed")
     torch = os.path.dirname(spec.origin)
     obj = os.path.join(BUILD, "torch_binding.o")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
     include = os.path.join(torch, "include")
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
-           "-isystem", include,
-           "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
-           "-c", os.path.join(CSRC, "torch_binding.cpp"), "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"the host compiler failed on torch_binding.cpp:\n{r.stderr[-6000:]}")
+    _run([os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+          "-isystem", include,
+          "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+          "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj],
+         "the host compiler failed on the tensor calls")
     return obj, os.path.join(torch, "lib")
+
+
+def _link_binding(obj, torch_lib):
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, LIB, "-L", torch_lib,
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+          "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], "link of the tensor calls failed")
+    os.replace(tmp, BINDING)
 
 
 def _compile(nvcc, unit):
@@ -92,34 +114,57 @@ def _compile(nvcc, unit):
     return obj
 
 
-def build(force=False, verbose=False):
-    """Compile (if stale) and return the path of libdgemm.so."""
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding, nvcc)
-        objs = list(ex.map(lambda u: _compile(nvcc, u), UNITS))
-        binding_obj, torch_lib = binding.result()
+def _link_library(nvcc, objs):
     vs = os.path.join(BUILD, "exports.map")
     with open(vs, "w") as f:
         f.write("{\n  global:\n" + "".join(f"    {s};\n" for s in EXPORTS) + "  local: *;\n};\n")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libdgemm.so", "-Xlinker",
-           f"--version-script={vs}", *objs, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr[-6000:]}")
+    _run([nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libdgemm.so", "-Xlinker",
+          f"--version-script={vs}", *objs, "-o", tmp], "link failed")
     os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", binding_obj, "-o", tmp, LIB, "-L", torch_lib,
-           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10",
-           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the tensor calls failed:\n{r.stderr[-6000:]}")
-    os.replace(tmp, BINDING)
+
+
+def _build(force, library, binding):
+    """Build what is asked for and stale, in parallel.  Returns why the tensor calls could not be
+    built, or None; the library never waits for them."""
+    library, binding = library and (force or _library_stale()), binding and (force or _binding_stale())
+    if not library and not binding:
+        return None
+    os.makedirs(BUILD, exist_ok=True)
+    nvcc = _nvcc()
+    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS) + 1, os.cpu_count() or 4)) as ex:
+        compiled = ex.submit(_compile_binding, nvcc) if binding else None
+        if library:
+            _link_library(nvcc, list(ex.map(lambda u: _compile(nvcc, u), UNITS)))
+        try:
+            if compiled is not None:
+                _link_binding(*compiled.result())
+        except RuntimeError as e:
+            return str(e)
+    return None
+
+
+def build_library(force=False):
+    """Compile libdgemm.so (if stale) and return its path; needs no PyTorch."""
+    _build(force, True, False)
+    return LIB
+
+
+def build_binding(force=False):
+    """Compile the tensor calls (if stale), and the library that they call, and return their path."""
+    why = _build(force, True, True)
+    if why is not None:
+        raise RuntimeError(f"the operators' tensor calls were not built: {why}")
+    return BINDING
+
+
+def build(force=False, verbose=False):
+    """Compile (if stale) the library and the tensor calls, and return the path of libdgemm.so.
+    Where the tensor calls cannot be built (no PyTorch, say), that is reported and the library
+    serves without them."""
+    why = _build(force, True, True)
+    if why is not None:
+        print(f"the operators' tensor calls were not built: {why}", file=sys.stderr)
     if verbose:
         for _, name, _ in UNITS:
             with open(os.path.join(BUILD, f"ptxas_{name}.log")) as f:
