@@ -10,6 +10,8 @@ _build/ptxas_<unit>.log next to the objects.
 import concurrent.futures as cf
 import importlib.util
 import os
+import platform
+import re
 import shutil
 import subprocess
 import sys
@@ -60,8 +62,29 @@ def _library_stale():
     return _newer(LIB, sources + [HEADER, __file__])
 
 
-def _binding_stale():
-    return _newer(BINDING, [os.path.join(CSRC, BINDING_SOURCE), HEADER, __file__])
+def binding_key():
+    """The PyTorch, Python and machine that the tensor calls are compiled for; they are C++ against
+    PyTorch's own types and do not serve another.  None without PyTorch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py"), encoding="utf-8") as f:
+        version = re.search(r"^__version__ = ['\"]([^'\"]+)", f.read(), re.M)
+    return f"PyTorch {version and version.group(1)}, Python {sys.implementation.cache_tag}, {platform.machine()}"
+
+
+def built_key(binding):
+    """The key that a built file of the tensor calls has beside it, or None."""
+    try:
+        with open(binding + ".key", encoding="utf-8") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def binding_stale():
+    return (_newer(BINDING, [os.path.join(CSRC, BINDING_SOURCE), HEADER, __file__])
+            or built_key(BINDING) != binding_key())
 
 
 def _run(cmd, what):
@@ -97,7 +120,11 @@ def _link_binding(obj, torch_lib):
     _run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, LIB, "-L", torch_lib,
           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10",
           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], "link of the tensor calls failed")
+    if os.path.exists(BINDING + ".key"):
+        os.remove(BINDING + ".key")  # never the new key beside the old file
     os.replace(tmp, BINDING)
+    with open(BINDING + ".key", "w", encoding="utf-8") as f:
+        f.write(binding_key())
 
 
 def _compile(nvcc, unit):
@@ -127,7 +154,7 @@ def _link_library(nvcc, objs):
 def _build(force, library, binding):
     """Build what is asked for and stale, in parallel.  Returns why the tensor calls could not be
     built, or None; the library never waits for them."""
-    library, binding = library and (force or _library_stale()), binding and (force or _binding_stale())
+    library, binding = library and (force or _library_stale()), binding and (force or binding_stale())
     if not library and not binding:
         return None
     os.makedirs(BUILD, exist_ok=True)

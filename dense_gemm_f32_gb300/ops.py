@@ -36,13 +36,21 @@ def _raise(status, what):
 
 
 def _load():
-    """Load _torch_binding.so (built by dense_gemm_f32_gb300.build); raise if absent."""
+    """Load _torch_binding.so (built by dense_gemm_f32_gb300.build); raise if it is absent or
+    was built for another PyTorch or Python."""
     global _binding
     if _binding is None:
         _lib.load()  # the same libdgemm.so serves both
         if not os.path.exists(BINDING_PATH):
             raise LibraryMissing(
                 f"{BINDING_PATH} is missing: build it first with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        from . import build
+
+        if build.built_key(BINDING_PATH) != build.binding_key():
+            raise LibraryMissing(
+                f"{BINDING_PATH} was built for {build.built_key(BINDING_PATH)}, this is "
+                f"{build.binding_key()}: build it again with "
                 "`python -c 'import __graft_entry__ as g; g.build()'`")
         name = "_torch_binding"
         loader = importlib.machinery.ExtensionFileLoader(name, BINDING_PATH)
