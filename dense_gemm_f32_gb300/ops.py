@@ -16,8 +16,6 @@ import importlib.machinery
 import importlib.util
 import os
 
-import torch
-
 from . import _lib
 from ._lib import ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, LibraryMissing
 
@@ -40,6 +38,8 @@ def _load():
     was built for another PyTorch or Python."""
     global _binding
     if _binding is None:
+        import torch  # noqa: F401  (the libraries that the module links to)
+
         _lib.load()  # the same libdgemm.so serves both
         if not os.path.exists(BINDING_PATH):
             raise LibraryMissing(
@@ -64,6 +64,8 @@ def _load():
 
 def _on(stream, x):
     """The given stream (object or raw handle) as a context."""
+    import torch
+
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(stream, device=x.device)
     return torch.cuda.stream(stream)
