@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -218,8 +219,20 @@ int integer(PyObject *o) {
   return (int)v;
 }
 
+// A forward call's results have no gradient function, so an argument that requires
+// gradients is refused where autograd would record.
+void refuse_recording(const char *what, PyObject *const *args, int n) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (int i = 0; i < n; ++i)
+    if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad())
+      throw Refused{PyExc_RuntimeError,
+                    std::string(what) + " does not record gradients, and an argument requires them: call "
+                    "it under torch.no_grad(), and " + what + "_backward for the gradients"};
+}
+
 // (x, weight, bias, eps, return_stats, out)
 PyObject *layer_norm(PyObject *const *a) {
+  refuse_recording("layer_norm", a, 6);
   const Tensor &x = tensor(a[0], "x");
   const int dt = type_code(x, "layer_norm", true);
   const auto type = x.scalar_type();
@@ -270,6 +283,7 @@ PyObject *layer_norm_backward(PyObject *const *a) {
 
 // (x, w, bias, activation, residual, trans_w, return_preact, out)
 PyObject *linear(PyObject *const *a) {
+  refuse_recording("linear", a, 8);
   const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
   const int dt = type_code(x, "linear", false), act = integer(a[3]);
   const bool t = flag(a[5]), keep = flag(a[6]);
@@ -342,6 +356,7 @@ Block block(const char *what, const Tensor &x, const Tensor &wg, const Tensor &w
 
 // (x, w_gate, w_up, w_down, activation, residual, trans_w, return_saved, out)
 PyObject *gated_ffn(PyObject *const *a) {
+  refuse_recording("gated_ffn", a, 9);
   const Tensor &x = tensor(a[0], "x");
   const bool t = flag(a[6]), keep = flag(a[7]);
   const int act = integer(a[4]);

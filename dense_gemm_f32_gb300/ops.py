@@ -11,6 +11,10 @@ is contiguous.  Outputs are allocated on the stream the call runs on
 (`stream`: a torch.cuda.Stream or raw handle, default the current one); tensors
 made on another stream must be ready there, as for any torch call.  Shapes and
 types that do not fit raise ValueError and TypeError before anything runs.
+
+Autograd records nothing of these calls: with gradients enabled, layer_norm,
+linear and gated_ffn refuse arguments that require them (RuntimeError); call them
+under torch.no_grad() and the `_backward` calls for the gradients.
 """
 import importlib.machinery
 import importlib.util
