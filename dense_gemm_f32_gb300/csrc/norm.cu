@@ -491,7 +491,9 @@ cudaError_t with_shape(int cols, F &&f) {
   if (cols <= 2048) return f(Shape<T, ALIGNED, 4 * K / W, 64 * W>{});
   if (cols <= 4096) return f(Shape<T, ALIGNED, 4 * K / W, 128 * W>{});
   if (cols <= 8192) return f(Shape<T, ALIGNED, 4 * K / W, 256 * W>{});
-  return f(Shape<T, ALIGNED, 4 * K, 512>{});
+  if constexpr (!BWD || sizeof(T) == 2) return f(Shape<T, ALIGNED, 4 * K, 512>{});
+  static_assert(kMaxRingBytes <= 8192 * 4, "backward, no fp32 row gets here");
+  return cudaErrorInvalidValue;
 }
 template <class T, bool BWD, class F>
 cudaError_t with_shape(int cols, bool aligned, F &&f) {
