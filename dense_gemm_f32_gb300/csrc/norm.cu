@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(S::BLOCK)
 #pragma unroll
     for (int j = 0; j < V; ++j) s[0] += v[c][j];
   row_sum<S>(s, red[0]);
-  const float mu = s[0] * inv;
+  const float mu = s[0] / cols;  // by 1 / cols a constant row's mean is not its value, and y not b
   s[0] = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
