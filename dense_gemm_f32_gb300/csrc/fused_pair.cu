@@ -542,10 +542,6 @@ bool pair_operand_maps(CUtensorMap *ta, CUtensorMap *tb, const FusedGemm &p, con
   return ok_a && ok_b;
 }
 
-inline bool rows_aligned(const void *p, int64_t ld) {
-  return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && ld % 8 == 0;
-}
-
 template <class T, Epi EPI>
 cudaError_t launch_pair(const FusedGemm &p, int *watchdog, cudaStream_t stream) {
   using G = PairCfg<T, EPI>;

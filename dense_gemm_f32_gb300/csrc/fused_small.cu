@@ -484,10 +484,6 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
 }
 
 // ------------------------------------------------------------- host side
-inline bool rows_aligned(const void *p, int64_t ld) {
-  return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && ld % 8 == 0;
-}
-
 // Maps of the weights (boxes of 64 k x `w_rows` features, or 64 features x bk
 // k) and the tokens.
 bool small_maps(CUtensorMap *tw, CUtensorMap *tx, CUtensorMapDataType dt, const FusedGemm &p,

@@ -500,11 +500,6 @@ cudaError_t with_shape(int cols, bool aligned, F &&f) {
   return aligned ? with_shape<T, true, BWD>(cols, f) : with_shape<T, false, BWD>(cols, f);
 }
 
-template <class T>
-bool vec_ok(const void *p, int64_t ld) {
-  return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
-}
-
 // Stages of the backward kernel's rings, and its dynamic shared memory: the
 // rings, and the fold of the column sums in their place.
 template <class S, int NIN>
@@ -546,8 +541,9 @@ cudaError_t fwd(int rows, int cols, float eps, const void *X, int64_t ldx, const
     e = launch_kernel(ln_fwd_long_kernel<T>, dim3((unsigned)rows), dim3(1024), 0, stream, 1u, cols,
                       eps, x, ldx, w, b, y, ldy, mean, rstd);
   } else {
-    const bool vec = vec_ok<T>(X, ldx) && vec_ok<T>(Y, ldy) && vec_ok<T>(w, 0) &&
-                     vec_ok<T>(b, 0) && (cols * (int)sizeof(T)) % 16 == 0;
+    constexpr int es = sizeof(T);
+    const bool vec = rows_aligned(X, ldx, es) && rows_aligned(Y, ldy, es) &&
+                     rows_aligned(w, 0, es) && rows_aligned(b, 0, es) && cols * es % 16 == 0;
     e = with_shape<T, false>(cols, vec, [&](auto shape) {
       using S = decltype(shape);
       const int64_t blocks = ((int64_t)rows + S::ROWS - 1) / S::ROWS;
@@ -594,9 +590,10 @@ cudaError_t bwd(int dtype, int rows, int cols, const void *dY, int64_t lddy, con
   }
   int *wd = watchdog_address();
   if (wd == nullptr) return cudaErrorInvalidSymbol;
-  const bool vec = vec_ok<T>(dY, lddy) && vec_ok<T>(X, ldx) && vec_ok<T>(w, 0) &&
-                   vec_ok<T>(dr, dr ? lddr : 0) && vec_ok<T>(dX, lddx) &&
-                   (cols * (int)sizeof(T)) % 16 == 0;
+  constexpr int es = sizeof(T);
+  const bool vec = rows_aligned(dY, lddy, es) && rows_aligned(X, ldx, es) &&
+                   rows_aligned(w, 0, es) && rows_aligned(dr, dr ? lddr : 0, es) &&
+                   rows_aligned(dX, lddx, es) && cols * es % 16 == 0;
   e = with_shape<T, true>(cols, vec, [&](auto shape) {
     using S = decltype(shape);
     parts = bwd_parts(rows, S::BWD_ROWS, num_sms);

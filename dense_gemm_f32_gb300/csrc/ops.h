@@ -6,6 +6,12 @@
 
 namespace dg {
 
+// Whether rows at pitch `ld` (elements of `es` bytes) all start on 16-byte
+// boundaries; an absent matrix (null, pitch 0) does.
+inline bool rows_aligned(const void *p, int64_t ld, int es = 2) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0;
+}
+
 // What a fused product does with its accumulator tile (all in fp32, rounded
 // once per stored element).
 enum class Epi {

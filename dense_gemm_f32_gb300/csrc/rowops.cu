@@ -215,10 +215,6 @@ cudaError_t act_grad(int act, int M, int N, const void *dD, int64_t lddd, const 
   return e;
 }
 
-inline bool vec_ok(const void *p, int64_t ld) {
-  return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && ld % 8 == 0;
-}
-
 }  // namespace
 
 cudaError_t launch_column_sums(int dtype, const float *partial, int parts, int cols, void *out0,
@@ -234,8 +230,8 @@ size_t act_grad_scratch(int M, int N, bool with_bias, int num_sms) {
 cudaError_t launch_act_grad(int dtype, int act, int M, int N, const void *dD, int64_t lddd,
                             const void *Z, int64_t ldz, void *dZ, int64_t lddz, void *dbias,
                             float *partial, int num_sms, cudaStream_t stream) {
-  const bool vec = N % 8 == 0 && vec_ok(dD, lddd) &&
-                   (act == DGEMM_ACT_NONE || (vec_ok(Z, ldz) && vec_ok(dZ, lddz)));
+  const bool vec = N % 8 == 0 && rows_aligned(dD, lddd) &&
+                   (act == DGEMM_ACT_NONE || (rows_aligned(Z, ldz) && rows_aligned(dZ, lddz)));
   const int parts = act_grad_parts(M, N, num_sms);
   auto f = dtype == DGEMM_DTYPE_BF16
                ? (vec ? act_grad<__nv_bfloat16, true> : act_grad<__nv_bfloat16, false>)
