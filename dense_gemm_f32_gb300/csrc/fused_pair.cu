@@ -24,8 +24,8 @@
 //    may not write go out element by element).  Each warp owns two 2 KB pieces
 //    and runs on its own, with no barrier among the epilogue warps.
 // Bound by the tensor pipe under the power limit: 16384 x 14336 x 4096 bf16
-// with bias, gelu_tanh and both outputs 1.19 ms, 1615 TFLOP/s, where a cuBLAS
-// product without an epilogue sustains 1736.  With little K (1024 and less) the
+// with bias, gelu_tanh and both outputs 1.20 ms, 1607 TFLOP/s, where a cuBLAS
+// product of 8192^3 without an epilogue sustains 1708.  With little K (1024 and less) the
 // epilogue bounds it: a warp's chain through one piece takes about 900 cycles.
 // Every wait is bounded (ptx.cuh).
 #include <atomic>

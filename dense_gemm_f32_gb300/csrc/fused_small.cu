@@ -621,11 +621,14 @@ int small_stages(const SmallPlan &plan) {
 
 // By the occupancy query, once per device and cluster size (every instance of
 // the kernel has the same block and bounds; a cluster has to fit in one GPC,
-// which holds a few SMs more than a multiple of its size).  The query knows of
-// one CTA of this kernel per SM only, whatever its shared memory, though two
-// run (1 x 4096 x 14336 in 32 clusters of 8: 20.1 us; in 32 of 4: 21.5); a
-// GPC with two per SM holds as many clusters of 2 s as it holds clusters of s
-// with one.
+// which holds a few SMs more than a multiple of its size).  The query counts a
+// kernel that allocates tensor memory as one CTA per SM whatever its shared
+// memory, but two run: with half an SM's memory each, 152 pairs of CTAs were seen
+// at work on one SM at the same time.  So clusters of s with two CTAs per SM are
+// taken to be as many as clusters of s / 2 with one.  For a kernel of the same
+// size without tensor memory the query says 152, 97, 74, 46 and 36 clusters of 2,
+// 3, 4, 6 and 8; this gives 152, 92, 76, 46 and 36.  (1 x 4096 x 14336 in 32
+// clusters of 8: 20.1 us; in 32 of 4: 21.5.)
 int64_t small_resident(const SmallPlan &plan, int num_sms) {
   using G = SmallCfg;
   if (plan.splits == 1) return (int64_t)plan.per_sm * num_sms;

@@ -13,12 +13,19 @@
 // costs a thread about 190 instructions besides the 9 to 12 per element, so a
 // thread takes 32 elements (16 in the backward pass, which has to hold column
 // sums too) and a row as few threads as that leaves: a warp up to 1024
-// elements, without a block barrier, then 64 to 512 threads.  Rows beyond
-// 16384 elements (backward: 32 KB) are read again for each pass, from L2.  The
+// elements, without a block barrier, then 64 to 512 threads.  The
 // backward kernel is persistent: a ring of rows per block is filled ahead by
 // bulk copies, and a thread keeps the same columns for every row, so the
 // column sums of dw and db stay in its registers and each block writes one
 // partial sum, which a second launch adds up in a fixed order.
+//
+// Not made fast: backward rows of 8193 to 16384 16-bit elements, whose 64 column
+// sums per thread spill (4096 x 16384 bf16 149 us, its bytes 59); rows beyond 16384
+// elements (backward: 32 KB), which go an element per load through one block per
+// row, several passes from L2 and the column sums from both whole matrices once more
+// (2048 x 32768 bf16 105 us forward, its bytes 40, 277 backward, 59; 4096 x 16384
+// fp32 backward 269, 119); and backward with fewer rows than SMs, where each row
+// writes its own fp32 partial sums (128 x 8192 bf16 22 us, its bytes 1).
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>

@@ -3,6 +3,8 @@
 // join of column sums that several blocks hold parts of, and the re-pitching
 // of 16-bit operands.
 //
+// dZ is rounded to 16 bits, as the products that read it multiply 16-bit operands;
+// the column sums add the values before that rounding.
 // Bound by memory: dZ is two reads and one write of an M x N matrix.  A thread
 // owns eight columns (16 bytes of a row) and walks every eighth row of its
 // block's share, so the column sums stay in registers; the eight row groups of

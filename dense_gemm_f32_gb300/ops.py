@@ -132,7 +132,8 @@ def linear_backward(dd, x, w, activation="none", preact=None, trans_w=False, wit
 
     dd: the gradient of linear's result (also that of its residual).  preact:
     what linear(..., return_preact=True) returned; needed unless activation is
-    "none".
+    "none".  dd act'(preact) is rounded to x's type before the two products (in
+    float16 it is infinite past 65504); dbias sums the values before that.
     """
     if stream is not None:
         with _on(stream, x):
@@ -148,7 +149,9 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu", residual=None, trans_w
     x: (..., D) bfloat16 or float16.  w_gate, w_up: D x F and w_down: F x D, or
     their transposes with trans_w.  residual: of x's shape; out may be it.
     Returns y, or (y, g, u) with the two projections, (..., F), which
-    gated_ffn_backward takes.
+    gated_ffn_backward takes.  The hidden units are computed in float32 and
+    rounded to x's type for the product with w_down (in float16 they are
+    infinite past 65504).
     """
     if stream is not None:
         with _on(stream, x):
@@ -162,7 +165,10 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, g, u, activation="silu", tra
                        stream=None):
     """(dx, dw_gate, dw_up, dw_down) of gated_ffn from its saved g and u.
 
-    dy: the gradient of gated_ffn's result (also that of its residual).
+    dy: the gradient of gated_ffn's result (also that of its residual).  The
+    gradients of g and u, and the hidden units computed again from them, are
+    rounded to x's type before the products that read them (in float16 they are
+    infinite past 65504).
     """
     if stream is not None:
         with _on(stream, x):
