@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
   };
   if (warp != 0) fetch_first();
 
+  bool all_sent = false;  // this thread is the producer and has sent for every stage
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
           phase ^= 1u;
         }
       }
+      all_sent = ok;
       if (!ok) {  // no TMA write lands after this CTA has left
         int s = stage;
         uint32_t ph = phase;
@@ -469,6 +471,12 @@ __global__ void __launch_bounds__(kThreads<SPLIT>, 2)
         }
       }
     }
+  }
+  if (aborted && all_sent) {  // nor where another thread's wait gave up
+    const int sent = kb_end - kb_begin;
+    for (int i = max(0, sent - p.stages); i < sent; ++i)
+      if (!mbar_wait(full_bar(i % p.stages), (uint32_t)(i / p.stages) & 1u))
+        atomicCAS(p.watchdog, 0, kSite4ProducerDrain);
   }
   if constexpr (SPLIT) {
     __syncwarp();
