@@ -18,7 +18,9 @@ from ._lib import (  # noqa: F401  (re-exported C entry points)
     PATH_F8_E4M3, PATH_F8_E5M2, PATH_FP16, PATH_SIMT, PATH_TF32, TC_3XTF32, TC_TF32,
     LibraryMissing, dgemm_gated_ffn, dgemm_gated_ffn_backward, dgemm_gemm_ex,
     dgemm_kernel_launches, dgemm_last_cuda_error, dgemm_layer_norm, dgemm_layer_norm_backward,
-    dgemm_linear, dgemm_linear_backward,
+    dgemm_linear, dgemm_linear_backward, dgemm_quantize_int8, dgemm_linear_int8,
+    dgemm_linear_int8_workspace, dgemm_gated_ffn_int8, dgemm_gated_ffn_int8_workspace,
+    dgemm_orthogonalize, dgemm_orthogonalize_workspace,
     dgemm_status_string, dgemm_version, dgemm_watchdog_status, gemm_bf16_tc, gemm_f16_tc,
     gemm_f32_simt, gemm_f32_tc, gemm_f32_tc_noalloc, gemm_f8_tc, load,
 )
@@ -119,6 +121,6 @@ def matmul(A, B, mode="tf32", out=None, stream=None, trans_a=False, trans_b=Fals
 
 
 from .ops import (  # noqa: E402,F401  (uses DgemmError and check above)
-    ACTIVATIONS, gated_ffn, gated_ffn_backward, layer_norm, layer_norm_backward, linear,
-    linear_backward,
+    ACTIVATIONS, gated_ffn, gated_ffn_backward, gated_ffn_int8, layer_norm, layer_norm_backward,
+    linear, linear_backward, linear_int8, orthogonalize, quantize_int8,
 )

@@ -41,7 +41,10 @@ EXPORTED = ("gemm_f32_simt", "gemm_f32_tc", "gemm_bf16_tc", "dgemm_status_string
             "dgemm_last_cuda_error", "dgemm_watchdog_status", "dgemm_version",
             "dgemm_kernel_launches", "gemm_f32_tc_noalloc", "gemm_f16_tc", "dgemm_gemm_ex",
             "gemm_f8_tc", "dgemm_layer_norm", "dgemm_layer_norm_backward", "dgemm_linear",
-            "dgemm_linear_backward", "dgemm_gated_ffn", "dgemm_gated_ffn_backward")
+            "dgemm_linear_backward", "dgemm_gated_ffn", "dgemm_gated_ffn_backward",
+            "dgemm_quantize_int8", "dgemm_linear_int8_workspace", "dgemm_linear_int8",
+            "dgemm_gated_ffn_int8_workspace", "dgemm_gated_ffn_int8",
+            "dgemm_orthogonalize_workspace", "dgemm_orthogonalize")
 
 _lib = None
 
@@ -94,9 +97,19 @@ def load():
     lib.dgemm_linear_backward.argtypes = [i] * 6 + m * 7 + [p, p]
     lib.dgemm_gated_ffn.argtypes = [i] * 6 + m * 9 + [p]
     lib.dgemm_gated_ffn_backward.argtypes = [i] * 6 + m * 14 + [p]
+    lib.dgemm_quantize_int8.argtypes = [i] * 4 + [*m, *m, p, p]
+    lib.dgemm_linear_int8.argtypes = [i] * 5 + [*m, p, *m, p, p, *m, *m, p, p]
+    lib.dgemm_gated_ffn_int8.argtypes = [i] * 5 + m + [*m, p] * 3 + [*m, *m, p, p]
     for name in ("layer_norm", "layer_norm_backward", "linear", "linear_backward", "gated_ffn",
-                 "gated_ffn_backward"):
+                 "gated_ffn_backward", "quantize_int8", "linear_int8", "gated_ffn_int8",
+                 "orthogonalize"):
         getattr(lib, "dgemm_" + name).restype = i
+    f = ctypes.c_float
+    lib.dgemm_orthogonalize.argtypes = [i, i, i, ctypes.POINTER(f), f, f, f, i, i, *m, *m, *m, p, p]
+    lib.dgemm_linear_int8_workspace.argtypes = lib.dgemm_orthogonalize_workspace.argtypes = [i] * 2
+    lib.dgemm_gated_ffn_int8_workspace.argtypes = [i] * 3
+    for name in ("linear_int8", "gated_ffn_int8", "orthogonalize"):
+        getattr(lib, f"dgemm_{name}_workspace").restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -167,6 +180,50 @@ def dgemm_gated_ffn_backward(dtype, activation, op_w, M, D, F, dY, lddy, X, ldx,
                                            ldwg, Wu, ldwu, Wd, ldwd, G, ldg, U, ldu, H, ldh, dG,
                                            lddg, dU, lddu, dX, lddx, dWg, lddwg, dWu, lddwu, dWd,
                                            lddwd, stream)
+
+
+def dgemm_quantize_int8(dtype, op, rows, cols, X, ldx, Q, ldq, scale, stream=0):
+    return load().dgemm_quantize_int8(dtype, op, rows, cols, X, ldx, Q, ldq, scale, stream)
+
+
+def dgemm_linear_int8_workspace(M, K):
+    """Bytes of `work` for dgemm_linear_int8."""
+    return load().dgemm_linear_int8_workspace(M, K)
+
+
+def dgemm_linear_int8(dtype, activation, M, N, K, X, ldx, x_scale, W, ldw, w_scale, bias, R, ldr,
+                      D, ldd, work, stream=0):
+    return load().dgemm_linear_int8(dtype, activation, M, N, K, X, ldx, x_scale, W, ldw, w_scale,
+                                    bias, R, ldr, D, ldd, work, stream)
+
+
+def dgemm_gated_ffn_int8_workspace(M, D, F):
+    """Bytes of `work` for dgemm_gated_ffn_int8."""
+    return load().dgemm_gated_ffn_int8_workspace(M, D, F)
+
+
+def dgemm_gated_ffn_int8(dtype, activation, M, D, F, X, ldx, Wg, ldwg, g_scale, Wu, ldwu, u_scale,
+                         Wd, ldwd, d_scale, R, ldr, Y, ldy, work, stream=0):
+    return load().dgemm_gated_ffn_int8(dtype, activation, M, D, F, X, ldx, Wg, ldwg, g_scale, Wu,
+                                       ldwu, u_scale, Wd, ldwd, d_scale, R, ldr, Y, ldy, work,
+                                       stream)
+
+
+def dgemm_orthogonalize_workspace(rows, cols):
+    """Bytes of `work` for dgemm_orthogonalize."""
+    return load().dgemm_orthogonalize_workspace(rows, cols)
+
+
+def dgemm_orthogonalize(x_dtype, dtype, steps, coefficients, eps, scale, residual_scale, rows, cols,
+                        X, ldx, R, ldr, D, ldd, work, stream=0):
+    """coefficients: a sequence of 3 * steps numbers, or None."""
+    if coefficients is not None:
+        if len(coefficients) < 3 * steps:
+            raise ValueError(f"{3 * steps} coefficients are needed, got {len(coefficients)}")
+        coefficients = (ctypes.c_float * len(coefficients))(*coefficients)
+    return load().dgemm_orthogonalize(x_dtype, dtype, steps, coefficients, eps, scale,
+                                      residual_scale, rows, cols, X, ldx, R, ldr, D, ldd, work,
+                                      stream)
 
 
 def dgemm_status_string(status):

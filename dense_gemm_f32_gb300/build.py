@@ -29,7 +29,9 @@ BINDING_SOURCE = "torch_binding.cpp"
 # operand layout so that the four layouts build in parallel.
 UNITS = ([("api.cu", "api", []), ("staging.cu", "staging", []), ("ops_api.cu", "ops_api", []),
           ("norm.cu", "norm", []), ("rowops.cu", "rowops", []),
-          ("fused.cu", "fused", [])]
+          ("fused.cu", "fused", []), ("quant.cu", "quant", []), ("int8.cu", "int8", []),
+          ("int8_small.cu", "int8_small", []), ("int8_pair.cu", "int8_pair", []), ("newton.cu", "newton", []),
+          ("newton_pair.cu", "newton_pair", [])]
          + [("fused_pair.cu", f"fused_pair_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(3)]
          + [("fused_small.cu", f"fused_small_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(4)]
          + [("simt.cu", f"simt_{u}", [f"-DDGEMM_SIMT_UNIT={u}"]) for u in range(4)]
@@ -39,7 +41,10 @@ EXPORTS = ["gemm_f32_simt", "gemm_f32_tc", "gemm_bf16_tc", "dgemm_status_string"
            "dgemm_last_cuda_error", "dgemm_watchdog_status", "dgemm_version",
            "dgemm_kernel_launches", "gemm_f32_tc_noalloc", "gemm_f16_tc", "dgemm_gemm_ex",
            "gemm_f8_tc", "dgemm_layer_norm", "dgemm_layer_norm_backward", "dgemm_linear",
-           "dgemm_linear_backward", "dgemm_gated_ffn", "dgemm_gated_ffn_backward"]
+           "dgemm_linear_backward", "dgemm_gated_ffn", "dgemm_gated_ffn_backward",
+           "dgemm_quantize_int8", "dgemm_linear_int8_workspace", "dgemm_linear_int8",
+           "dgemm_gated_ffn_int8_workspace", "dgemm_gated_ffn_int8",
+           "dgemm_orthogonalize_workspace", "dgemm_orthogonalize"]
 
 
 def _nvcc():

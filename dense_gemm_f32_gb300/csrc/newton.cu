@@ -1,0 +1,342 @@
+// newton.cu -- orthogonalising a matrix by a Newton-Schulz iteration:
+//
+//   X_0 = X / (|X| + eps),  |X| the root of the sum of squares,
+//   X_k+1 = a X_k + (b A + c A^2) X_k,  A = X_k X_k^T   (X_k^T X_k on the right
+//                                                        when X is taller than wide)
+//
+// which brings every singular value s to p(p(...p(s))), p(s) = a s + b s^3 + c s^5.
+//
+// Everything between X and the result is fp16 with fp32 accumulators: 11 bits, where
+// bf16 has 8, at the same rate, and with the scales below nothing that matters
+// leaves fp16's range.  Against 64 bits the result is off by 0.0012 to 0.003 of its
+// norm where one in bf16 is off by 0.01 to 0.05 (the small singular values, which
+// the iteration enlarges, sit in the rounding of the large ones), and storing the
+// result in bf16 by 0.0017.
+//  * X_0 is kept as X 2^(8 - e), 2^e the power of two next above |X| + eps: exact for
+//    16-bit X but for elements 2^-30 below the norm.  The factor 2^e / (|X| + eps) that is
+//    missing goes into the first Gram matrix and the first product with X, in
+//    fp32.  Later X_k are kept times 2^8, the m x m matrices times 2^6.
+//  * Steps in groups.  All m x m matrices here are polynomials in A, so they are
+//    symmetric and commute.  Within a group X stays where it is: with P = a I + b
+//    A + c A^2, the next step's Gram matrix is P A P, the product of the P so far is Q, and
+//    only the group's end forms Q X.  A step costs 4 products of m^3 / 2
+//    multiplications then, instead of one such, a Gram matrix (m^2 n / 2) and a
+//    product with X (m^2 n).  A rounding of A off the true Gram matrix is not
+//    noticed before the group ends, though, and grows by a^2 at the small
+//    singular values in every step.  So a group ends before that growth passes a
+//    limit: 2^8 in the first group of a matrix with m >= 512, where A's rounding
+//    is small because its trace of 1 is spread (three steps with the usual a =
+//    3.4445), 2^4 in the first of a smaller one and in later ones, where the large
+//    singular values are about 1 (two steps), one step at a time in a smaller
+//    matrix's later ones.  In 64-bit simulations of these roundings over spectra from flat to i^-2
+//    that is off by 0.0006 to 0.008 of the norm (single steps: 0.0006 to 0.010; three
+//    steps first at m = 64: 0.004 to 0.014; all five in one group overflows).
+#include <cmath>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "activation.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "ops.h"
+#include "rowvec.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kAhead = 4;  // vectors of a thread in flight
+
+// Sums of squares in three scales, one of which neither overflows nor loses a
+// share that matters, whatever the elements' size.
+constexpr float kUp = 0x1p70f, kDown = 0x1p-70f;
+struct Squares {
+  float mid = 0.f, big = 0.f, small = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float u = x * kUp, d = x * kDown;
+    mid = fmaf(x, x, mid);
+    big = fmaf(d, d, big);
+    small = fmaf(u, u, small);
+  }
+};
+
+template <class T, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads)
+    squares_kernel(int rows, int cols, const T *X, int64_t ldx, float *partial) {
+  constexpr int V = kVec<T>;
+  __shared__ float fold[3][kThreads / 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int vecs = (cols + V - 1) / V;
+  const int64_t all = (int64_t)rows * vecs, step = (int64_t)gridDim.x * kThreads;
+  Squares s;
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < all; i0 += kAhead * step) {
+    RowBlocks b[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t i = i0 + k * step, row = i / vecs;
+      b[k] = fetch_row16<T, ALIGNED>(X + row * ldx, (int)(i - row * vecs) * V, i < all ? cols : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t i = i0 + k * step, row = i / vecs;
+      if (i >= all) break;
+      float f[V];
+      widen16<T>(take_row16<T, ALIGNED>(b[k], X + row * ldx, (int)(i - row * vecs) * V, cols), f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s.add(f[j]);
+    }
+  }
+  float v[3] = {s.mid, s.big, s.small};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+    if ((threadIdx.x & 31) == 0) fold[k][threadIdx.x >> 5] = v[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    float t = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) t += fold[threadIdx.x][w];
+    partial[blockIdx.x * 3 + threadIdx.x] = t;
+  }
+}
+
+// Every block adds the partial sums in the same order, then scales its share.
+template <class T, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads)
+    scale_kernel(int rows, int cols, const T *X, int64_t ldx, float eps, const float *partial, int parts,
+                 __half *out, int64_t ldo, float *factor) {
+  constexpr int V = kVec<T>;
+  __shared__ double fold[3][kThreads / 32];
+  __shared__ float up[2];
+  pdl_launch_dependents();
+  pdl_wait();
+  double v[3] = {0., 0., 0.};
+  for (int i = threadIdx.x; i < parts; i += kThreads)
+    for (int k = 0; k < 3; ++k) v[k] += partial[i * 3 + k];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+    if ((threadIdx.x & 31) == 0) fold[k][threadIdx.x >> 5] = v[k];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t[3] = {0., 0., 0.};
+    for (int k = 0; k < 3; ++k)
+      for (int w = 0; w < kThreads / 32; ++w) t[k] += fold[k][w];
+    // the plain sum where it is away from both ends of fp32's range
+    double norm = sqrt(t[0]);
+    if (!(t[0] < 0x1p100))
+      norm = sqrt(t[1]) * 0x1p70;
+    else if (t[0] < 0x1p-60)
+      norm = sqrt(t[2]) * 0x1p-70;
+    norm += (double)eps;
+    int e = 0;
+    const double f = frexp(norm, &e);  // norm = f 2^e, 1/2 <= f < 1
+    const bool none = !(norm > 0.) || isinf(norm);  // nothing to divide by, an infinity or NaN
+    if (blockIdx.x == 0) *factor = none ? __uint_as_float(0x7fc00000u) : (float)(1. / f);
+    // 2^(8 - e) in two factors that are fp32 numbers
+    const int k = none ? 0 : 8 - e, k1 = k / 2;
+    up[0] = ldexpf(1.f, k1), up[1] = ldexpf(1.f, k - k1);
+  }
+  __syncthreads();
+  const float u0 = up[0], u1 = up[1];
+  const int vecs = (cols + V - 1) / V;
+  const int64_t all = (int64_t)rows * vecs, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < all; i0 += kAhead * step) {
+    RowBlocks b[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t i = i0 + k * step, row = i / vecs;
+      b[k] = fetch_row16<T, ALIGNED>(X + row * ldx, (int)(i - row * vecs) * V, i < all ? cols : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t i = i0 + k * step, row = i / vecs;
+      const int col = (int)(i - row * vecs) * V;
+      if (i >= all) break;
+      float f[V];
+      widen16<T>(take_row16<T, ALIGNED>(b[k], X + row * ldx, col, cols), f);
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] = pack2<__half>(f[2 * j] * u0 * u1, f[2 * j + 1] * u0 * u1);
+      if constexpr (V == 8)  // rows of whole vectors, padded
+        *reinterpret_cast<uint4 *>(out + row * ldo + col) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2 *>(out + row * ldo + col) = make_uint2(w[0], w[1]);
+    }
+  }
+}
+
+int scale_blocks(int num_sms) { return 2 * num_sms; }
+
+template <class T>
+cudaError_t launch_scale(int rows, int cols, const void *X, int64_t ldx, float eps, void *out, int64_t ldo,
+                         float *factor, float *partial, int num_sms, cudaStream_t stream) {
+  const T *x = static_cast<const T *>(X);
+  const bool al = rows_aligned(X, ldx, sizeof(T)) && cols % kVec<T> == 0;
+  const int64_t vecs = (int64_t)rows * ((cols + kVec<T> - 1) / kVec<T>);
+  const int64_t want = (vecs + kThreads * kAhead - 1) / (kThreads * kAhead);
+  const int blocks = (int)(want < scale_blocks(num_sms) ? want : scale_blocks(num_sms));
+  cudaError_t e = launch_kernel(al ? squares_kernel<T, true> : squares_kernel<T, false>, dim3(blocks),
+                                dim3(kThreads), 0, stream, 1u, rows, cols, x, ldx, partial);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  e = launch_kernel(al ? scale_kernel<T, true> : scale_kernel<T, false>, dim3(blocks), dim3(kThreads), 0,
+                    stream, 1u, rows, cols, x, ldx, eps, static_cast<const float *>(partial), blocks,
+                    static_cast<__half *>(out), ldo, factor);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+// -------------------------------------------------------------- the iteration
+int64_t pitch8(int64_t cols) { return (cols + 7) / 8 * 8; }
+int64_t round256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// X, the next X, five m x m matrices, the factor and the partial sums (up to 512 SMs' worth).
+struct Work {
+  __half *x[2], *square[5];
+  float *factor, *partial;
+  size_t bytes;
+  Work(void *base, int rows, int cols) {
+    const int64_t m = rows < cols ? rows : cols;
+    const int64_t x_bytes = round256((int64_t)rows * pitch8(cols) * 2), s_bytes = round256(m * pitch8(m) * 2);
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(base);
+    uintptr_t p = begin;
+    auto take = [&](int64_t n) {
+      const uintptr_t at = p;
+      p += (uintptr_t)n;
+      return at;
+    };
+    for (auto &q : x) q = reinterpret_cast<__half *>(take(x_bytes));
+    for (auto &q : square) q = reinterpret_cast<__half *>(take(s_bytes));
+    factor = reinterpret_cast<float *>(take(256));
+    partial = reinterpret_cast<float *>(take(round256(scale_blocks(512) * 3 * 4)));
+    bytes = (size_t)(p - begin);
+  }
+};
+
+// Steps of the group that begins at step k.  (At m = n a step costs the same in a
+// group as alone, and the result is nearer.)
+int group_steps(const Orthogonalize &p, int k) {
+  const bool large = (p.rows < p.cols ? p.rows : p.cols) >= 512;
+  const double most = k == 0 ? (large ? 256. : 16.) : large ? 16. : 0.;
+  double growth = 1.;
+  int steps = 1;
+  while (k + steps < p.steps) {
+    const double a = p.coefficients[3 * (k + steps - 1)];
+    growth *= a * a;
+    if (!(growth <= most)) break;
+    ++steps;
+  }
+  return steps;
+}
+
+}  // namespace
+
+size_t newton_scale_scratch(int num_sms) { return (size_t)scale_blocks(num_sms) * 3 * 4; }
+
+cudaError_t launch_newton_scale(int dtype, int rows, int cols, const void *X, int64_t ldx, float eps,
+                                void *T, int64_t ldt, float *factor, float *partial, int num_sms,
+                                cudaStream_t stream) {
+  switch (dtype) {
+    case DGEMM_DTYPE_F32:
+      return launch_scale<float>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
+    case DGEMM_DTYPE_BF16:
+      return launch_scale<__nv_bfloat16>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
+    default:
+      return launch_scale<__half>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
+  }
+}
+
+size_t newton_workspace(int rows, int cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return Work(nullptr, rows, cols).bytes;
+}
+
+cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms, cudaStream_t stream) {
+  int *wd = watchdog_address();
+  if (wd == nullptr) return cudaErrorInvalidSymbol;
+  if (num_sms > 512) return cudaErrorInvalidDevice;
+  Work w(work, p.rows, p.cols);
+  const bool tall = p.rows > p.cols;
+  const int m = tall ? p.cols : p.rows, n = tall ? p.rows : p.cols;
+  const int64_t ldx = pitch8(p.cols), ldm = pitch8(m);
+  cudaError_t e = launch_newton_scale(p.x_dtype, p.rows, p.cols, p.X, p.ldx, p.eps, w.x[0], ldx, w.factor,
+                                      w.partial, num_sms, stream);
+  const float x_up = 0x1p8f, m_up = 0x1p6f;  // what X and the m x m matrices are kept times
+  __half *x = w.x[0], *x_next = w.x[1];
+  for (int k = 0; k < p.steps && e == cudaSuccess;) {
+    const int steps = group_steps(p, k);
+    __half *A = w.square[0], *W = w.square[1], *P = w.square[2], *Q = nullptr;
+    __half *spare[2] = {w.square[3], w.square[4]};
+    {  // A = X X^T, or X^T X
+      NewtonGemm g;
+      g.symmetric = true, g.dtype = DGEMM_DTYPE_F16;
+      g.layout = tall ? 2 : 1;
+      g.M = g.N = m, g.K = n;
+      g.A = g.B = x, g.lda = g.ldb = ldx;
+      g.alpha = m_up / (x_up * x_up);
+      if (k == 0) g.factor = w.factor, g.power = 2;
+      g.out = A, g.ldo = g.out_cols = ldm;
+      e = launch_newton_pair(g, wd, stream);
+    }
+    auto square = [&](const __half *left, const __half *right, __half *out, float alpha) {
+      NewtonGemm g;
+      g.symmetric = true, g.dtype = DGEMM_DTYPE_F16;
+      g.M = g.N = g.K = m;
+      g.A = left, g.B = right, g.lda = g.ldb = ldm;
+      g.alpha = alpha / m_up;
+      g.out = out, g.ldo = g.out_cols = ldm;
+      return g;
+    };
+    for (int i = 0; i < steps && e == cudaSuccess; ++i) {
+      const float *c = p.coefficients + 3 * (k + i);
+      __half *poly = i == 0 ? spare[0] : P;
+      NewtonGemm g = square(A, A, poly, c[2]);  // P = a I + b A + c A^2
+      g.in0 = A, g.ldi0 = ldm, g.beta = c[1], g.gamma = c[0] * m_up;
+      e = launch_newton_pair(g, wd, stream);
+      const bool more = i + 1 < steps;
+      if (e == cudaSuccess && (more || i > 0)) {  // W = A P and Q = Q P, together where both are wanted
+        NewtonGemm h = more ? square(A, poly, W, 1.f) : square(Q, poly, spare[1], 1.f);
+        if (more && i > 0) h.A2 = Q, h.out2 = spare[1];
+        e = launch_newton_pair(h, wd, stream);
+      }
+      if (i == 0) {
+        Q = poly;  // spare[0]
+      } else {
+        __half *old = Q;
+        Q = spare[1];
+        spare[1] = old;
+      }
+      if (e == cudaSuccess && more) e = launch_newton_pair(square(W, poly, A, 1.f), wd, stream);
+    }
+    if (e != cudaSuccess) break;
+    {  // X = Q X, or X Q
+      const bool last = k + steps == p.steps;
+      NewtonGemm g;
+      g.layout = tall ? 1 : 0;
+      g.M = p.rows, g.N = p.cols, g.K = m;
+      g.A = tall ? x : Q, g.lda = tall ? ldx : ldm;
+      g.B = tall ? Q : x, g.ldb = tall ? ldm : ldx;
+      if (k == 0) g.factor = w.factor, g.power = 1;
+      if (last) {
+        g.dtype = p.dtype;
+        g.alpha = p.scale / (x_up * m_up);
+        g.beta = p.residual_scale, g.in0 = p.R, g.ldi0 = p.ldr;
+        g.out = p.D, g.ldo = p.ldd, g.out_cols = p.cols;
+      } else {
+        g.dtype = DGEMM_DTYPE_F16;
+        g.alpha = 1.f / m_up;
+        g.out = x_next, g.ldo = g.out_cols = ldx;
+      }
+      e = launch_newton_pair(g, wd, stream);
+    }
+    __half *t = x;
+    x = x_next, x_next = t;
+    k += steps;
+  }
+  return e;
+}
+
+}  // namespace dg

@@ -152,4 +152,96 @@ cudaError_t launch_layer_norm_backward(int dtype, int rows, int cols, const void
                                        void *dbias, float *partial, int num_sms,
                                        cudaStream_t stream);
 
+// ------------------------------------------------- 8-bit integer products
+// Rows of X as integers (quant.cu): Q in 8 bits, or T in fp16 with rows of whole
+// 16-byte vectors (ldt a multiple of 8), and a scale for each row.
+cudaError_t launch_quantize_rows(int dtype, int rows, int cols, const void *X, int64_t ldx,
+                                 int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream);
+cudaError_t launch_quantize_tokens(int dtype, int rows, int cols, const void *X, int64_t ldx,
+                                   void *T, int64_t ldt, float *scale, cudaStream_t stream);
+// T = X, integers already.
+cudaError_t launch_expand_tokens(int rows, int cols, const int8_t *X, int64_t ldx, void *T,
+                                 int64_t ldt, int num_sms, cudaStream_t stream);
+// Columns of X (rows x cols) as rows of Q (cols x rows); `tops`: scratch of cols words.
+cudaError_t launch_quantize_columns(int dtype, int rows, int cols, const void *X, int64_t ldx,
+                                    int8_t *Q, int64_t ldq, float *scale, uint32_t *tops,
+                                    int num_sms, cudaStream_t stream);
+
+// z[i][j] = t_scale[i] w_scale[j] sum_k T[i][k] W[j][k], T the integers in fp16 (M x
+// K, a multiple of 8 as leading dimension, written by the kernel just before on
+// the stream, one of the two above), W in 8 bits (N x K, rows on 16-byte
+// boundaries).  out = act(z + bias) + in0, of `dtype`; gated: out = act(z) z2 in
+// fp32 (ldo a multiple of 8), z2 from W2 and w2_scale.
+struct Int8Gemm {
+  bool gated = false;
+  int dtype = 0, act = 0;
+  int M = 0, N = 0, K = 0;
+  const void *T = nullptr, *W = nullptr, *W2 = nullptr;
+  int64_t ldt = 0, ldw = 0, ldw2 = 0;
+  const float *t_scale = nullptr, *w_scale = nullptr, *w2_scale = nullptr;
+  const void *bias = nullptr, *in0 = nullptr;
+  int64_t ldi0 = 0;
+  void *out = nullptr;
+  int64_t ldo = 0;
+};
+cudaError_t launch_int8(const Int8Gemm &p, int num_sms, cudaStream_t stream);
+
+// How int8_small.cu cuts a product: tokens of a tile (a multiple of 16 up to
+// 128), CTAs that share a tile's K range (1 to 8), CTAs per SM whose stages have to fit.
+struct Int8Plan {
+  int nt, splits, per_sm;
+};
+cudaError_t launch_int8_small(const Int8Gemm &p, const Int8Plan &plan, int *watchdog,
+                              cudaStream_t stream);
+// int8_pair.cu, tiles of `nt` tokens (a multiple of 32 up to 192); K > 0.
+cudaError_t launch_int8_pair(const Int8Gemm &p, int nt, int *watchdog, cudaStream_t stream);
+
+// ------------------------------------------------- orthogonalised updates
+// The products of a Newton-Schulz iteration, fp16 operands:
+//   out = alpha f^power A B + beta in0 + gamma I,  f = *factor (1 where null)
+// layout 0: A M x K, B K x N; 1: A M x K, B N x K; 2: A K x M, B K x N; rows on
+// 16-byte boundaries.  symmetric: the result is (M = N), half of its tiles are
+// computed and written to both places; layouts 1 and 2, fp16 results.  With A2, a
+// second product A2 B goes to out2 in the same launch, without in0 and gamma
+// (symmetric ones only).  out and in0 are of `dtype`; out_cols: columns that may be
+// written, N or more (a workspace's padding).
+struct NewtonGemm {
+  int layout = 1;
+  bool symmetric = false;
+  int dtype = 0;  // dgemm_dtype_t
+  int M = 0, N = 0, K = 0;
+  const void *A = nullptr, *A2 = nullptr, *B = nullptr;
+  int64_t lda = 0, ldb = 0;
+  float alpha = 1.f, beta = 0.f, gamma = 0.f;
+  const float *factor = nullptr;
+  int power = 0;
+  const void *in0 = nullptr;
+  int64_t ldi0 = 0;
+  void *out = nullptr, *out2 = nullptr;
+  int64_t ldo = 0;
+  int64_t out_cols = 0;
+};
+cudaError_t launch_newton_pair(const NewtonGemm &p, int *watchdog, cudaStream_t stream);
+
+// X in fp16 (rows of `ldt`, a multiple of 8) as X 2^(8 - e), and *factor = 2^e /
+// (norm + eps), where 2^e is the power of two next above norm + eps, norm the root of the
+// sum of X's squares: X 2^(8 - e) factor / 256 is X / (norm + eps).  partial: scratch
+// of newton_scale_scratch() bytes.
+size_t newton_scale_scratch(int num_sms);
+cudaError_t launch_newton_scale(int dtype, int rows, int cols, const void *X, int64_t ldx, float eps,
+                                void *T, int64_t ldt, float *factor, float *partial, int num_sms,
+                                cudaStream_t stream);
+
+// The whole iteration (newton.cu); `work` of newton_workspace() bytes, 16-byte aligned.
+struct Orthogonalize {
+  int x_dtype = 0, dtype = 0, rows = 0, cols = 0, steps = 0;
+  const float *coefficients = nullptr;  // (a, b, c) per step, host memory
+  float eps = 0.f, scale = 1.f, residual_scale = 1.f;
+  const void *X = nullptr, *R = nullptr;
+  void *D = nullptr;
+  int64_t ldx = 0, ldr = 0, ldd = 0;
+};
+size_t newton_workspace(int rows, int cols);
+cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms, cudaStream_t stream);
+
 }  // namespace dg

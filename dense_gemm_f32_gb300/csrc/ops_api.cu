@@ -106,6 +106,63 @@ int with_scratch(size_t bytes, cudaStream_t stream, const char *what, F &&f) {
   return st;
 }
 
+// Copies of 8-bit weights whose rows TMA cannot read, in stream-ordered scratch:
+// add() them, run() copies all of them in one launch per two and points the
+// operands there; release() after the last launch that reads them.
+class ByteStager {
+ public:
+  ByteStager(int num_sms, cudaStream_t stream) : num_sms_(num_sms), stream_(stream) {}
+  void add(const void *&p, int64_t &ld, int rows, int cols) {
+    if (rows == 0 || cols == 0 || tma_ok(p, ld, 1)) return;
+    ops_[n_] = {&p, &ld};
+    jobs_[n_++] = {p, ld, nullptr, (cols + 15LL) / 16 * 16, rows, cols, false};
+  }
+  cudaError_t run() {
+    if (n_ == 0) return cudaSuccess;
+    size_t at[kMax], total = 0;
+    for (int i = 0; i < n_; ++i) {
+      at[i] = total;
+      total += (size_t)(jobs_[i].rows * jobs_[i].ldd + 255) / 256 * 256;
+    }
+    cudaError_t e = scratch_alloc(&scratch_, total, stream_);
+    if (e != cudaSuccess) {
+      scratch_ = nullptr;
+      return e;
+    }
+    for (int i = 0; i < n_; ++i) {
+      jobs_[i].dst = static_cast<char *>(scratch_) + at[i];
+      *ops_[i].p = jobs_[i].dst;
+      *ops_[i].ld = jobs_[i].ldd;
+    }
+    for (int i = 0; i < n_ && e == cudaSuccess; i += 2)
+      e = launch_stage(jobs_ + i, n_ - i < 2 ? n_ - i : 2, 1, num_sms_, stream_);
+    return e;
+  }
+  int release(int st) {
+    if (scratch_ == nullptr) return st;
+    const cudaError_t e = scratch_free(scratch_, stream_);
+    scratch_ = nullptr;
+    return st == DGEMM_OK ? done(e, "scratch release") : st;
+  }
+
+ private:
+  static constexpr int kMax = 3;
+  struct Operand {
+    const void **p;
+    int64_t *ld;
+  } ops_[kMax];
+  StageJob jobs_[kMax];
+  int n_ = 0, num_sms_;
+  cudaStream_t stream_;
+  void *scratch_ = nullptr;
+};
+
+// The parts of the integer products' workspaces: tokens in fp16 with their
+// scales behind them, and the gated block's H in front of those.
+int64_t pitch8(int cols) { return (cols + 7LL) / 8 * 8; }
+size_t tokens_bytes(int M, int cols) { return ((size_t)M * (size_t)pitch8(cols) * 2 + 255) / 256 * 256; }
+size_t hidden_bytes(int M, int F) { return ((size_t)M * (size_t)pitch8(F) * 4 + 255) / 256 * 256; }
+
 // The end of a call that staged operands.
 int release(Stager &stage, int st) {
   const cudaError_t e = stage.release();
@@ -377,6 +434,170 @@ int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, 
     p.out0 = dWd, p.ldo0 = lddwd;
   }
   return release(stage, done(launch_fused_batch(ps, n, sms, stream), "gradient launch"));
+}
+
+int dgemm_quantize_int8(int dtype, int op, int rows, int cols, const void *X, int ldx,
+                        signed char *Q, int ldq, float *scale, cudaStream_t stream) {
+  if (!ok_dtype(dtype, true) || !ok_op(op)) return DGEMM_ERR_UNSUPPORTED;
+  const bool t = op == DGEMM_OP_T;
+  const int qr = t ? cols : rows, qc = t ? rows : cols;
+  const Arg a[] = {{X, rows, cols, ldx, elem_bytes(dtype), false, false},
+                   {Q, qr, qc, ldq, 1, true, false},
+                   {scale, 1, qr, qr, 4, true, false}};
+  if (!ok_counts({rows, cols}) || !ok_sizes(a, 2)) return DGEMM_ERR_INVALID_VALUE;
+  if (qr == 0) return DGEMM_OK;
+  int dev = 0, sms = 0;
+  const int st = check_args(a, 3, -1, -1, &dev, &sms);
+  if (st != DGEMM_OK) return st;
+  if (!t)
+    return done(launch_quantize_rows(dtype, rows, cols, X, ldx, Q, ldq, scale, stream),
+                "quantisation launch");
+  return with_scratch((size_t)cols * 4, stream, "quantisation launch", [&](float *tops) {
+    return launch_quantize_columns(dtype, rows, cols, X, ldx, Q, ldq, scale,
+                                   reinterpret_cast<uint32_t *>(tops), sms, stream);
+  });
+}
+
+size_t dgemm_linear_int8_workspace(int M, int K) {
+  if (M <= 0 || K < 0) return 0;
+  return tokens_bytes(M, K) + (size_t)M * 4;
+}
+
+int dgemm_linear_int8(int dtype, int activation, int M, int N, int K, const void *X, int ldx,
+                      const float *x_scale, const signed char *W, int ldw, const float *w_scale,
+                      const void *bias, const void *R, int ldr, void *D, int ldd, void *work,
+                      cudaStream_t stream) {
+  if (!ok_dtype(dtype, false) || !ok_act(activation)) return DGEMM_ERR_UNSUPPORTED;
+  const int64_t work_bytes = (int64_t)dgemm_linear_int8_workspace(M, K);
+  const Arg a[] = {{X, M, K, ldx, x_scale ? 1 : 2, false, false},
+                   {W, N, K, ldw, 1, false, false},
+                   {R, M, N, ldr, 2, false, true},
+                   {D, M, N, ldd, 2, true, false},
+                   vec(x_scale, M, 4, false),
+                   {w_scale, 1, N, N, 4, false, false},
+                   vec(bias, N, 2, false),
+                   {work, 1, work_bytes, work_bytes, 1, true, false}};
+  if (!ok_counts({M, N, K}) || !ok_sizes(a, 4)) return DGEMM_ERR_INVALID_VALUE;
+  if (M == 0 || N == 0) return DGEMM_OK;
+  if (work != nullptr && !aligned(work, 16)) return DGEMM_ERR_MISALIGNED;
+  int dev = 0, sms = 0;
+  int st = check_args(a, 8, 3, 2, &dev, &sms);  // D may be R itself
+  if (st != DGEMM_OK) return st;
+  Int8Gemm p;
+  p.dtype = dtype, p.act = activation;
+  p.M = M, p.N = N, p.K = K;
+  p.T = work, p.ldt = pitch8(K);
+  float *scale = reinterpret_cast<float *>(static_cast<char *>(work) + tokens_bytes(M, K));
+  p.t_scale = x_scale ? x_scale : scale;
+  p.W = W, p.ldw = ldw, p.w_scale = w_scale;
+  p.bias = bias, p.in0 = R, p.ldi0 = ldr, p.out = D, p.ldo = ldd;
+  ByteStager stage(sms, stream);
+  stage.add(p.W, p.ldw, N, K);
+  if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
+  if (!x_scale)
+    st = done(launch_quantize_tokens(dtype, M, K, X, ldx, work, p.ldt, scale, stream), "token launch");
+  else if (K > 0)
+    st = done(launch_expand_tokens(M, K, static_cast<const int8_t *>(X), ldx, work, p.ldt, sms, stream),
+              "token launch");
+  if (st == DGEMM_OK) st = done(launch_int8(p, sms, stream), "integer product launch");
+  return stage.release(st);
+}
+
+size_t dgemm_gated_ffn_int8_workspace(int M, int D, int F) {
+  if (M <= 0 || D < 0 || F < 0) return 0;
+  return hidden_bytes(M, F) + tokens_bytes(M, D > F ? D : F) + (size_t)M * 4;
+}
+
+int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const void *X, int ldx,
+                         const signed char *Wg, int ldwg, const float *g_scale,
+                         const signed char *Wu, int ldwu, const float *u_scale,
+                         const signed char *Wd, int ldwd, const float *d_scale, const void *R,
+                         int ldr, void *Y, int ldy, void *work, cudaStream_t stream) {
+  if (!ok_dtype(dtype, false) || !ok_act(activation)) return DGEMM_ERR_UNSUPPORTED;
+  const int64_t work_bytes = (int64_t)dgemm_gated_ffn_int8_workspace(M, D, F);
+  const Arg a[] = {{X, M, D, ldx, 2, false, false},
+                   {Wg, F, D, ldwg, 1, false, false},
+                   {Wu, F, D, ldwu, 1, false, false},
+                   {Wd, D, F, ldwd, 1, false, false},
+                   {R, M, D, ldr, 2, false, true},
+                   {Y, M, D, ldy, 2, true, false},
+                   {g_scale, 1, F, F, 4, false, false},
+                   {u_scale, 1, F, F, 4, false, false},
+                   {d_scale, 1, D, D, 4, false, false},
+                   {work, 1, work_bytes, work_bytes, 1, true, false}};
+  if (!ok_counts({M, D, F}) || !ok_sizes(a, 6)) return DGEMM_ERR_INVALID_VALUE;
+  if (M == 0 || D == 0) return DGEMM_OK;
+  if (work != nullptr && !aligned(work, 16)) return DGEMM_ERR_MISALIGNED;
+  int dev = 0, sms = 0;
+  int st = check_args(a, 10, 5, 4, &dev, &sms);  // Y may be R itself
+  if (st != DGEMM_OK) return st;
+  char *w = static_cast<char *>(work);
+  float *h = reinterpret_cast<float *>(w);
+  void *tokens = w + hidden_bytes(M, F);
+  float *scale = reinterpret_cast<float *>(w + hidden_bytes(M, F) + tokens_bytes(M, D > F ? D : F));
+  const void *wg = Wg, *wu = Wu, *wd = Wd;
+  int64_t lg = ldwg, lu = ldwu, ld = ldwd;
+  ByteStager stage(sms, stream);
+  stage.add(wg, lg, F, D);
+  stage.add(wu, lu, F, D);
+  stage.add(wd, ld, D, F);
+  if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
+  if (F > 0) {
+    st = done(launch_quantize_tokens(dtype, M, D, X, ldx, tokens, pitch8(D), scale, stream), "token launch");
+    Int8Gemm p;
+    p.gated = true, p.dtype = dtype, p.act = activation;
+    p.M = M, p.N = F, p.K = D;
+    p.T = tokens, p.ldt = pitch8(D), p.t_scale = scale;
+    p.W = wg, p.ldw = lg, p.w_scale = g_scale;
+    p.W2 = wu, p.ldw2 = lu, p.w2_scale = u_scale;
+    p.out = h, p.ldo = pitch8(F);
+    if (st == DGEMM_OK) st = done(launch_int8(p, sms, stream), "gated integer product launch");
+  }
+  if (st == DGEMM_OK)
+    st = done(launch_quantize_tokens(DGEMM_DTYPE_F32, M, F, h, pitch8(F), tokens, pitch8(F), scale, stream),
+              "token launch");
+  if (st == DGEMM_OK) {
+    Int8Gemm p;
+    p.dtype = dtype;
+    p.M = M, p.N = D, p.K = F;
+    p.T = tokens, p.ldt = pitch8(F), p.t_scale = scale;
+    p.W = wd, p.ldw = ld, p.w_scale = d_scale;
+    p.in0 = R, p.ldi0 = ldr, p.out = Y, p.ldo = ldy;
+    st = done(launch_int8(p, sms, stream), "down integer product launch");
+  }
+  return stage.release(st);
+}
+
+size_t dgemm_orthogonalize_workspace(int rows, int cols) { return newton_workspace(rows, cols); }
+
+int dgemm_orthogonalize(int x_dtype, int dtype, int steps, const float *coefficients, float eps,
+                        float scale, float residual_scale, int rows, int cols, const void *X, int ldx,
+                        const void *R, int ldr, void *D, int ldd, void *work, cudaStream_t stream) {
+  if (!ok_dtype(x_dtype, true) || !ok_dtype(dtype, true)) return DGEMM_ERR_UNSUPPORTED;
+  const int es = elem_bytes(dtype);
+  const int64_t work_bytes = (int64_t)dgemm_orthogonalize_workspace(rows, cols);
+  const Arg a[] = {{X, rows, cols, ldx, elem_bytes(x_dtype), false, false},
+                   {R, rows, cols, ldr, es, false, true},
+                   {D, rows, cols, ldd, es, true, false},
+                   {work, 1, work_bytes, work_bytes, 1, true, false}};
+  if (!ok_counts({rows, cols}) || !ok_sizes(a, 3) || steps < 1 || steps > DGEMM_NEWTON_MAX_STEPS ||
+      !(eps >= 0.f) || std::isinf(eps) || !std::isfinite(scale) || !std::isfinite(residual_scale))
+    return DGEMM_ERR_INVALID_VALUE;
+  if (coefficients != nullptr)
+    for (int i = 0; i < 3 * steps; ++i)
+      if (!(std::fabs(coefficients[i]) <= 64.f)) return DGEMM_ERR_INVALID_VALUE;
+  if (rows == 0 || cols == 0) return DGEMM_OK;
+  if (coefficients == nullptr) return DGEMM_ERR_NULL_POINTER;
+  if (work != nullptr && !aligned(work, 16)) return DGEMM_ERR_MISALIGNED;
+  int dev = 0, sms = 0;
+  const int st = check_args(a, 4, 2, 1, &dev, &sms);  // D may be R itself
+  if (st != DGEMM_OK) return st;
+  Orthogonalize p;
+  p.x_dtype = x_dtype, p.dtype = dtype, p.rows = rows, p.cols = cols, p.steps = steps;
+  p.coefficients = coefficients;
+  p.eps = eps, p.scale = scale, p.residual_scale = residual_scale;
+  p.X = X, p.ldx = ldx, p.R = R, p.ldr = ldr, p.D = D, p.ldd = ldd;
+  return done(launch_orthogonalize(p, work, sms, stream), "orthogonalisation launch");
 }
 
 }  // extern "C"

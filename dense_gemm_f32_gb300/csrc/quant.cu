@@ -1,0 +1,354 @@
+// quant.cu -- rows in 8-bit integers with one scale each, and the forms of them
+// that the integer products read.
+//
+// A row x becomes q_j = round(127 x_j / top), top = max |x_j|, to the nearest
+// integer (ties to even), and its scale top / 127, so that x_j is about q_j scale.
+// The quotient's nearest integer is exact for 16-bit elements: with a power of
+// two that brings top into [1, 4), t = 127 x is exact in fp32 (7 + 11 bits), the
+// product with 127 / top finds an integer that is at most one off, next to a
+// half, and e = t - q top, exact as well, says on which side of it the quotient
+// lies.  (An element costs a product, a rounding by a large constant, a fused
+// multiply-add and a comparison; a division would cost twice as much.)  For
+// fp32 elements t is rounded once.  The maximum is taken of the bits of |x|, in
+// which NaN is the largest: a row with NaN or an infinity gets that as its scale
+// and zeros, so that what is computed from it is NaN.  A row of zeros has scale
+// 0.
+//
+// Bound by memory: a row is read once and held in registers up to 8192 elements
+// of 16 bits or 4096 of 32 (longer rows are read again, from L2 mostly).  Three
+// kinds of output: the integers, for a user; the integers in fp16, which hold
+// them exactly, for the products (int8_small.cu, int8_pair.cu multiply in fp16);
+// and columns instead of rows, transposed on the way, for weights stored in x
+// out.
+//
+// A kernel here signals its dependents only after its own wait, unlike the
+// library's other kernels: a product that follows may then read its weights
+// before this kernel is done, since all that came before it is.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "activation.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "ops.h"
+#include "rowvec.cuh"
+
+namespace dg {
+namespace {
+
+// What a row's largest size says about quantising it.
+struct RowScale {
+  float up, top, inv;  // a power of two; top times it; 127 / that
+  float scale;         // top / 127
+  bool none;           // zeros, an infinity or NaN: every q is 0
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t top_bits) {
+  RowScale r;
+  const float top = __uint_as_float(top_bits);
+  r.none = top_bits == 0u || top_bits >= 0x7f800000u;
+  r.scale = r.none ? top : __fdiv_rn(top, 127.f);
+  int e = (int)(top_bits >> 23);
+  e = e < 1 ? 1 : e > 253 ? 253 : e;
+  r.up = __uint_as_float((uint32_t)(254 - e) << 23);
+  r.top = top * r.up;
+  r.inv = r.none ? 0.f : __fdiv_rn(127.f, r.top);
+  return r;
+}
+
+__device__ __forceinline__ float quantised(float x, const RowScale &r) {
+  if (r.none) return 0.f;
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: a sum with it is rounded to an integer
+  x *= r.up;
+  const float t = 127.f * x, v = x * r.inv;
+  const float m = v + kRound, q = m - kRound;
+  const float e = fmaf(-q, r.top, t), twice = 2.f * fabsf(e);
+  const bool odd = __float_as_uint(m) & 1u;
+  return twice > r.top || (twice == r.top && odd) ? q + copysignf(1.f, e) : q;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// V integers to `out`: signed bytes, or fp16.
+template <int V>
+__device__ __forceinline__ void put(int8_t *out, const float (&q)[V], int valid, bool vec) {
+  uint32_t w[V / 4];
+#pragma unroll
+  for (int j = 0; j < V / 4; ++j) {
+    w[j] = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[j] |= ((uint32_t)(int)q[4 * j + k] & 0xFFu) << (8 * k);
+  }
+  if (vec && valid >= V) {
+    if constexpr (V == 8)
+      *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t *>(out) = w[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < valid) out[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
+  }
+}
+template <int V>
+__device__ __forceinline__ void put(__half *out, const float (&q)[V], int valid, bool) {
+  // the products' tokens: rows of whole vectors, padded
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) w[j] = pack2<__half>(q[2 * j], q[2 * j + 1]);
+  if constexpr (V == 8)
+    *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);
+}
+
+// Vectors of a row that a thread holds.
+constexpr int kHeld = 4;
+
+// One row per block.
+template <class T, class O, bool ALIGNED, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    quantize_rows_kernel(int cols, const T *X, int64_t ldx, O *Q, int64_t ldq, float *scale,
+                         bool vec) {
+  constexpr int V = kVec<T>;
+  __shared__ uint32_t tops[THREADS / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t row = blockIdx.x;
+  const T *x = X + row * ldx;
+  O *out = Q + row * ldq;
+  RowBlocks b[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    b[k] = fetch_row16<T, ALIGNED>(x, min((int)(threadIdx.x + k * THREADS), cols) * V, cols);
+  float f[kHeld][V];
+  uint32_t top = 0;
+  auto widest = [&](const float (&v)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = max(top, abs_bits(v[j]));
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int col = min((int)(threadIdx.x + k * THREADS), cols) * V;
+    if (col < cols) {
+      widen16<T>(take_row16<T, ALIGNED>(b[k], x, col, cols), f[k]);
+      widest(f[k]);
+    }
+  }
+  for (int64_t c = (int64_t)(threadIdx.x + kHeld * THREADS) * V; c < cols; c += THREADS * V) {
+    float v[V];
+    widen16<T>(load_row16<T, ALIGNED>(x, (int)c, cols), v);
+    widest(v);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < THREADS / 32 ? tops[threadIdx.x & 31] : 0u);
+  const RowScale r = row_scale(top);
+  if (threadIdx.x == 0) scale[row] = r.scale;
+  auto finish = [&](float (&v)[V], int col) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = quantised(v[j], r);
+    put<V>(out + col, v, cols - col, vec);
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int col = min((int)(threadIdx.x + k * THREADS), cols) * V;
+    if (col < cols) finish(f[k], col);
+  }
+  for (int64_t c = (int64_t)(threadIdx.x + kHeld * THREADS) * V; c < cols; c += THREADS * V) {
+    float v[V];
+    widen16<T>(load_row16<T, ALIGNED>(x, (int)c, cols), v);
+    finish(v, (int)c);
+  }
+}
+
+template <class T, class O>
+cudaError_t launch_rows(int rows, int cols, const void *X, int64_t ldx, O *Q, int64_t ldq,
+                        float *scale, cudaStream_t stream) {
+  const bool al = rows_aligned(X, ldx, sizeof(T)) && cols % kVec<T> == 0;
+  const bool vec = reinterpret_cast<uintptr_t>(Q) % kVec<T> == 0 && ldq % kVec<T> == 0;
+  // a row's threads: as many as hold it, up to 512; a block of 1024 for the few long rows of a
+  // decoding step would hold more, but a second vector per thread costs less than the wider join
+  const int vecs = (cols + kVec<T> - 1) / kVec<T>;
+  auto go = [&](auto kern, int threads) {
+    const cudaError_t e = launch_kernel(kern, dim3((unsigned)rows), dim3(threads), 0, stream, 1u, cols,
+                                        static_cast<const T *>(X), ldx, Q, ldq, scale, vec);
+    if (e == cudaSuccess) count_launch();
+    return e;
+  };
+  if (vecs <= 128 * kHeld)
+    return al ? go(quantize_rows_kernel<T, O, true, 128>, 128)
+              : go(quantize_rows_kernel<T, O, false, 128>, 128);
+  return al ? go(quantize_rows_kernel<T, O, true, 512>, 512)
+            : go(quantize_rows_kernel<T, O, false, 512>, 512);
+}
+
+// The integers of X (int8) in fp16.
+constexpr int kExpandThreads = 256;
+__global__ void __launch_bounds__(kExpandThreads)
+    expand_rows_kernel(int rows, int cols, const int8_t *X, int64_t ldx, __half *T, int64_t ldt,
+                       bool vec) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int vecs = (cols + 7) / 8;
+  for (int64_t i = (int64_t)blockIdx.x * kExpandThreads + threadIdx.x; i < (int64_t)rows * vecs;
+       i += (int64_t)gridDim.x * kExpandThreads) {
+    const int64_t row = i / vecs;
+    const int col = (int)(i - row * vecs) * 8;
+    const int8_t *x = X + row * ldx + col;
+    int8_t b[8] = {};
+    if (vec && col + 8 <= cols) {
+      const uint2 w = *reinterpret_cast<const uint2 *>(x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b[j] = (int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < cols) b[j] = x[j];
+    }
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = (float)b[j];
+    put<8>(T + row * ldt + col, q, 8, true);
+  }
+}
+
+// ------------------------------------------------------- columns, transposed
+// tops[c] = the largest |X[r][c]| over the rows, as bits (zero before).
+template <class T>
+__global__ void __launch_bounds__(256)
+    column_tops_kernel(int rows, int cols, const T *X, int64_t ldx, uint32_t *tops) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  if (col >= cols) return;
+  uint32_t top = 0;
+#pragma unroll 8
+  for (int64_t r = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.y * 4)
+    top = max(top, abs_bits(to_f32<T>(X[r * ldx + col])));
+  atomicMax(tops + col, top);  // of whole numbers: the same in any order
+}
+
+__global__ void clear_kernel(int n, uint32_t *p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    p[i] = 0;
+}
+
+// Q[c][r] = X[r][c] in column c's scale; tiles of 64 x 64.
+template <class T>
+__global__ void __launch_bounds__(256)
+    quantize_columns_kernel(int rows, int cols, const T *X, int64_t ldx, int8_t *Q, int64_t ldq,
+                            const uint32_t *tops, float *scale, bool vec) {
+  __shared__ int8_t tile[64][68];  // [column][row]
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t c0 = (int64_t)blockIdx.x * 64;
+  const int64_t col = c0 + (threadIdx.x & 63);
+  const bool in = col < cols;
+  const RowScale s = row_scale(in ? tops[col] : 0u);
+  if (in && blockIdx.y == 0 && threadIdx.x < 64) scale[col] = s.scale;
+  for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < rows; r0 += (int64_t)gridDim.y * 64) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t r = r0 + (threadIdx.x >> 6) * 16 + i;
+      x[i] = in && r < rows ? to_f32<T>(X[r * ldx + col]) : 0.f;
+    }
+    __syncthreads();  // the tile before has been stored
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w |= ((uint32_t)(int)quantised(x[i + k], s) & 0xFFu) << (8 * k);
+      *reinterpret_cast<uint32_t *>(&tile[threadIdx.x & 63][(threadIdx.x >> 6) * 16 + i]) = w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = (threadIdx.x >> 4) + 16 * i, r = (threadIdx.x & 15) * 4;
+      if (c0 + c >= cols) continue;
+      int8_t *out = Q + (c0 + c) * ldq + r0 + r;
+      if (vec && r0 + r + 4 <= rows) {
+        *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(&tile[c][r]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (r0 + r + k < rows) out[k] = tile[c][r + k];
+      }
+    }
+  }
+}
+
+template <class T>
+cudaError_t launch_columns(int rows, int cols, const void *X, int64_t ldx, int8_t *Q, int64_t ldq,
+                           float *scale, uint32_t *tops, int num_sms, cudaStream_t stream) {
+  const unsigned gx = (unsigned)((cols + 63LL) / 64);
+  // about eight blocks per SM, each with rows of its own
+  const int64_t want = (8LL * num_sms + gx - 1) / gx, most = (rows + 63LL) / 64;
+  const unsigned gy = (unsigned)(want < most ? want : most < 1 ? 1 : most);
+  const unsigned gc = (unsigned)((cols + 1023LL) / 1024);
+  cudaError_t e = launch_kernel(clear_kernel, dim3(gc < 1024 ? gc : 1024), dim3(256), 0, stream, 1u,
+                                cols, tops);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  e = launch_kernel(column_tops_kernel<T>, dim3(gx, gy), dim3(256), 0, stream, 1u, rows, cols,
+                    static_cast<const T *>(X), ldx, tops);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  const bool vec = reinterpret_cast<uintptr_t>(Q) % 4 == 0 && ldq % 4 == 0;
+  e = launch_kernel(quantize_columns_kernel<T>, dim3(gx, gy), dim3(256), 0, stream, 1u, rows, cols,
+                    static_cast<const T *>(X), ldx, Q, ldq, static_cast<const uint32_t *>(tops), scale,
+                    vec);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(int dtype, int rows, int cols, const void *X, int64_t ldx,
+                                 int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream) {
+  switch (dtype) {
+    case DGEMM_DTYPE_F32: return launch_rows<float>(rows, cols, X, ldx, Q, ldq, scale, stream);
+    case DGEMM_DTYPE_BF16: return launch_rows<__nv_bfloat16>(rows, cols, X, ldx, Q, ldq, scale, stream);
+    default: return launch_rows<__half>(rows, cols, X, ldx, Q, ldq, scale, stream);
+  }
+}
+
+cudaError_t launch_quantize_tokens(int dtype, int rows, int cols, const void *X, int64_t ldx,
+                                   void *T, int64_t ldt, float *scale, cudaStream_t stream) {
+  __half *t = static_cast<__half *>(T);
+  switch (dtype) {
+    case DGEMM_DTYPE_F32: return launch_rows<float>(rows, cols, X, ldx, t, ldt, scale, stream);
+    case DGEMM_DTYPE_BF16: return launch_rows<__nv_bfloat16>(rows, cols, X, ldx, t, ldt, scale, stream);
+    default: return launch_rows<__half>(rows, cols, X, ldx, t, ldt, scale, stream);
+  }
+}
+
+cudaError_t launch_expand_tokens(int rows, int cols, const int8_t *X, int64_t ldx, void *T,
+                                 int64_t ldt, int num_sms, cudaStream_t stream) {
+  const int64_t vecs = (int64_t)rows * ((cols + 7) / 8), blocks = (vecs + kExpandThreads - 1) / kExpandThreads;
+  const int64_t most = 8LL * num_sms;
+  const bool vec = reinterpret_cast<uintptr_t>(X) % 8 == 0 && ldx % 8 == 0;
+  const cudaError_t e = launch_kernel(expand_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)),
+                                      dim3(kExpandThreads), 0, stream, 1u, rows, cols, X, ldx,
+                                      static_cast<__half *>(T), ldt, vec);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+cudaError_t launch_quantize_columns(int dtype, int rows, int cols, const void *X, int64_t ldx,
+                                    int8_t *Q, int64_t ldq, float *scale, uint32_t *tops,
+                                    int num_sms, cudaStream_t stream) {
+  switch (dtype) {
+    case DGEMM_DTYPE_F32:
+      return launch_columns<float>(rows, cols, X, ldx, Q, ldq, scale, tops, num_sms, stream);
+    case DGEMM_DTYPE_BF16:
+      return launch_columns<__nv_bfloat16>(rows, cols, X, ldx, Q, ldq, scale, tops, num_sms, stream);
+    default:
+      return launch_columns<__half>(rows, cols, X, ldx, Q, ldq, scale, tops, num_sms, stream);
+  }
+}
+
+}  // namespace dg

@@ -1,4 +1,4 @@
-// torch_binding.cpp -- the feed-forward operators' tensor calls: shape and
+// torch_binding.cpp -- the operators' tensor calls: shape and
 // type checks, pointers, leading dimensions, the current stream, outputs and
 // workspaces, one call into the C ABI (include/dgemm.h).  No arithmetic.
 //
@@ -13,6 +13,7 @@
 #include <ATen/ATen.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -178,17 +179,30 @@ Tensor pitched(int64_t rows, int64_t cols, const Tensor &like, int *ld) {
   *ld = as_int(pitch > 0 ? pitch : 1, "a workspace's rows");
   return make({rows, pitch}, like);
 }
-// `out`, which has to have the given shape, or a new tensor of it.
-Tensor out_or_new(PyObject *out, const Tensor &x, int rows, int cols, Mat *m) {
-  Tensor t = given(out) ? tensor(out, "out") : make_rows(x, cols);
+// `out`, which has to have x's leading dimensions and `cols` columns of `type`, or a
+// new tensor like that.
+Tensor out_or_new(PyObject *out, const Tensor &x, int rows, int cols, Mat *m, at::ScalarType type) {
+  Tensor t;
+  if (given(out)) {
+    t = tensor(out, "out");
+  } else if (type == x.scalar_type()) {
+    t = make_rows(x, cols);
+  } else {
+    auto sizes = x.sizes().vec();
+    sizes.back() = cols;
+    t = at::empty(sizes, x.options().dtype(type));
+  }
   if (given(out)) {
     bool same = t.dim() == x.dim();
     for (int64_t i = 0; same && i < x.dim(); ++i)
       same = t.size(i) == (i + 1 < x.dim() ? x.size(i) : cols);
     if (!same) value_error("out: has another shape than the result");
   }
-  *m = like(t, "out", x.scalar_type(), rows, cols);
+  *m = like(t, "out", type, rows, cols);
   return t;
+}
+Tensor out_or_new(PyObject *out, const Tensor &x, int rows, int cols, Mat *m) {
+  return out_or_new(out, x, rows, cols, m, x.scalar_type());
 }
 
 int pos(int n) { return n > 0 ? n : 1; }
@@ -221,13 +235,14 @@ int integer(PyObject *o) {
 
 // A forward call's results have no gradient function, so an argument that requires
 // gradients is refused where autograd would record.
-void refuse_recording(const char *what, PyObject *const *args, int n) {
+void refuse_recording(const char *what, PyObject *const *args, int n, bool backward = true) {
   if (!c10::GradMode::is_enabled()) return;
   for (int i = 0; i < n; ++i)
     if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad())
       throw Refused{PyExc_RuntimeError,
                     std::string(what) + " does not record gradients, and an argument requires them: call "
-                    "it under torch.no_grad(), and " + what + "_backward for the gradients"};
+                    "it under torch.no_grad()" +
+                        (backward ? std::string(", and ") + what + "_backward for the gradients" : "")};
 }
 
 // (x, weight, bias, eps, return_stats, out)
@@ -407,6 +422,180 @@ PyObject *gated_ffn_backward(PyObject *const *a) {
   return tuple({&dx, &dwg, &dwu, &dwd});
 }
 
+// A scale for each of n rows, contiguous in any shape.
+const float *scales(PyObject *o, const char *name, int n) {
+  return static_cast<const float *>(stats(o, name, n));
+}
+Tensor bytes_like(size_t n, const Tensor &x) {
+  return at::empty({(int64_t)n}, x.options().dtype(at::kByte));
+}
+
+// (x, transpose)
+PyObject *quantize_int8(PyObject *const *a) {
+  refuse_recording("quantize_int8", a, 2, false);
+  const Tensor &x = tensor(a[0], "x");
+  const int dt = type_code(x, "quantize_int8", true);
+  const bool t = flag(a[1]);
+  const Mat m = rows_of(x, "x", x.scalar_type());
+  if (t && x.dim() != 2) value_error("x: expected a 2-D matrix");
+  const cudaStream_t stream = current_stream(x);
+  const auto bytes = x.options().dtype(at::kChar), floats = x.options().dtype(at::kFloat);
+  const int cols = t ? m.rows : m.cols;
+  const Tensor q = t ? at::empty({m.cols, m.rows}, bytes) : at::empty(x.sizes(), bytes);
+  const Tensor s = t ? at::empty({m.cols}, floats) : at::empty(x.sizes().slice(0, x.dim() - 1), floats);
+  check(dgemm_quantize_int8(dt, t ? DGEMM_OP_T : DGEMM_OP_N, m.rows, m.cols, m.p, m.ld,
+                            static_cast<signed char *>(q.data_ptr()), pos(cols),
+                            static_cast<float *>(s.data_ptr()), stream),
+        "quantize_int8");
+  return tuple({&q, &s});
+}
+
+// A weight in 8 bits, outer x inner.
+Mat weight_int8(const Tensor &w, const char *name, int outer, int inner) {
+  return weight(w, name, at::kChar, inner, outer, true);
+}
+
+// (x, w, w_scale, bias, activation, residual, x_scale, dtype, out)
+PyObject *linear_int8(PyObject *const *a) {
+  refuse_recording("linear_int8", a, 9, false);
+  const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
+  const bool ints = x.scalar_type() == at::kChar;
+  at::ScalarType type = ints ? at::kBFloat16 : x.scalar_type();
+  if (given(a[7])) {
+    if (!THPDtype_Check(a[7])) type_error("dtype: expected a torch.dtype");
+    const auto want = reinterpret_cast<THPDtype *>(a[7])->scalar_type;
+    if (!ints && want != type) type_error("dtype: the result has x's type, " + name_of(type));
+    type = want;
+  }
+  if (ints != given(a[6])) type_error("x_scale comes with an int8 x, and with no other");
+  if (!ints && type != at::kBFloat16 && type != at::kHalf)
+    type_error("linear_int8 takes torch.bfloat16, torch.float16, torch.int8, got " + name_of(type));
+  if (type != at::kBFloat16 && type != at::kHalf)
+    type_error("dtype: torch.bfloat16 or torch.float16, got " + name_of(type));
+  const int dt = type == at::kHalf ? DGEMM_DTYPE_F16 : DGEMM_DTYPE_BF16, act = integer(a[4]);
+  const Mat m = rows_of(x, "x", x.scalar_type());
+  const int N = outer_of(w, "w", true);
+  const Mat mw = weight_int8(w, "w", N, m.cols);
+  const float *ws = scales(a[2], "w_scale", N);
+  const float *xs = ints ? scales(a[6], "x_scale", m.rows) : nullptr;
+  void *b = vector_or_none(a[3], "bias", type, N);
+  const Mat r = like_or_none(a[5], "residual", type, m.rows, N);
+  if (given(a[8])) (void)like(tensor(a[8], "out"), "out", type, m.rows, N);
+  const cudaStream_t stream = current_stream(x);
+  Mat d;
+  const Tensor out = out_or_new(a[8], x, m.rows, N, &d, type);
+  const Tensor work = bytes_like(dgemm_linear_int8_workspace(m.rows, m.cols), x);
+  check(dgemm_linear_int8(dt, act, m.rows, N, m.cols, m.p, m.ld, xs,
+                          static_cast<const signed char *>(mw.p), mw.ld, ws, b, r.p, r.ld, d.p, d.ld,
+                          work.data_ptr(), stream),
+        "linear_int8");
+  return THPVariable_Wrap(out);
+}
+
+// (x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, activation, residual, out)
+PyObject *gated_ffn_int8(PyObject *const *a) {
+  refuse_recording("gated_ffn_int8", a, 10, false);
+  const Tensor &x = tensor(a[0], "x"), &wg = tensor(a[1], "w_gate");
+  const int dt = type_code(x, "gated_ffn_int8", false), act = integer(a[7]);
+  const auto type = x.scalar_type();
+  const Mat m = rows_of(x, "x", type);
+  const int F = outer_of(wg, "w_gate", true);
+  const Mat mg = weight_int8(wg, "w_gate", F, m.cols);
+  const Mat mu = weight_int8(tensor(a[3], "w_up"), "w_up", F, m.cols);
+  const Mat md = weight_int8(tensor(a[5], "w_down"), "w_down", m.cols, F);
+  const float *sg = scales(a[2], "gate_scale", F), *su = scales(a[4], "up_scale", F);
+  const float *sd = scales(a[6], "down_scale", m.cols);
+  const Mat r = like_or_none(a[8], "residual", type, m.rows, m.cols);
+  if (given(a[9])) (void)like(tensor(a[9], "out"), "out", type, m.rows, m.cols);
+  const cudaStream_t stream = current_stream(x);
+  Mat y;
+  const Tensor out = out_or_new(a[9], x, m.rows, m.cols, &y);
+  const Tensor work = bytes_like(dgemm_gated_ffn_int8_workspace(m.rows, m.cols, F), x);
+  auto bytes = [](const Mat &w) { return static_cast<const signed char *>(w.p); };
+  check(dgemm_gated_ffn_int8(dt, act, m.rows, m.cols, F, m.p, m.ld, bytes(mg), mg.ld, sg, bytes(mu),
+                             mu.ld, su, bytes(md), md.ld, sd, r.p, r.ld, y.p, y.ld, work.data_ptr(),
+                             stream),
+        "gated_ffn_int8");
+  return THPVariable_Wrap(out);
+}
+
+double number(PyObject *o, const char *name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    if (!PyErr_ExceptionMatches(PyExc_TypeError)) throw PythonError{};
+    PyErr_Clear();
+    type_error(std::string(name) + ": expected a number");
+  }
+  return v;
+}
+
+// A new reference to a list or tuple of `o`'s items, released with the object.
+struct Items {
+  PyObject *seq;
+  Items(PyObject *o, const char *name) : seq(PySequence_Fast(o, "")) {
+    if (seq == nullptr) {
+      PyErr_Clear();
+      type_error(std::string(name) + ": expected a sequence of numbers");
+    }
+  }
+  ~Items() { Py_XDECREF(seq); }
+  Items(const Items &) = delete;
+  Items &operator=(const Items &) = delete;
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
+  PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+};
+
+// (x, steps, coefficients, eps, scale, residual, residual_scale, out)
+PyObject *orthogonalize(PyObject *const *a) {
+  refuse_recording("orthogonalize", a, 8, false);
+  const Tensor &x = tensor(a[0], "x");
+  const int dx = type_code(x, "orthogonalize", true);
+  if (x.dim() != 2) value_error("x: expected a 2-D matrix");
+  const long steps = PyLong_AsLong(a[1]);
+  if (steps == -1 && PyErr_Occurred()) throw PythonError{};
+  if (steps < 1 || steps > DGEMM_NEWTON_MAX_STEPS)
+    value_error("steps: 1 to " + std::to_string(DGEMM_NEWTON_MAX_STEPS));
+  float c[3 * DGEMM_NEWTON_MAX_STEPS];
+  {
+    const Items items(a[2], "coefficients");
+    const bool each = items.size() > 0 && !PyNumber_Check(items[0]);
+    if (items.size() != (each ? steps : 3))
+      value_error("coefficients: three numbers, or three for each step");
+    for (long k = 0; k < steps; ++k) {
+      auto fill = [&](const Items &t) {
+        if (t.size() != 3) value_error("coefficients: three numbers, or three for each step");
+        for (int j = 0; j < 3; ++j) {
+          const double v = number(t[j], "coefficients");
+          if (!(std::fabs(v) <= 64.0)) value_error("coefficients: at most 64 in size");
+          c[3 * k + j] = (float)v;
+        }
+      };
+      if (each)
+        fill(Items(items[k], "coefficients"));
+      else
+        fill(items);
+    }
+  }
+  const double eps = number(a[3], "eps"), scale = number(a[4], "scale"), keep = number(a[6], "residual_scale");
+  const Mat m = rows_of(x, "x", x.scalar_type());
+  const auto type = given(a[5])   ? tensor(a[5], "residual").scalar_type()
+                    : given(a[7]) ? tensor(a[7], "out").scalar_type()
+                                  : x.scalar_type();
+  const int dt = given(a[5])   ? type_code(tensor(a[5], "residual"), "residual", true)
+                 : given(a[7]) ? type_code(tensor(a[7], "out"), "out", true)
+                               : dx;
+  const Mat r = like_or_none(a[5], "residual", type, m.rows, m.cols);
+  if (given(a[7])) (void)like(tensor(a[7], "out"), "out", type, m.rows, m.cols);
+  const cudaStream_t stream = current_stream(x);
+  Mat d;
+  const Tensor out = out_or_new(a[7], x, m.rows, m.cols, &d, type);
+  const Tensor work = bytes_like(dgemm_orthogonalize_workspace(m.rows, m.cols), x);
+  check(dgemm_orthogonalize(dx, dt, (int)steps, c, (float)eps, (float)scale, (float)keep, m.rows, m.cols,
+                            m.p, m.ld, r.p, r.ld, d.p, d.ld, work.data_ptr(), stream),
+        "orthogonalize");
+  return THPVariable_Wrap(out);
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -434,6 +623,8 @@ PyObject *on_error(PyObject *, PyObject *f) {
 PyMethodDef g_methods[] = {DG_FAST(layer_norm, 6),       DG_FAST(layer_norm_backward, 6),
                            DG_FAST(linear, 8),           DG_FAST(linear_backward, 7),
                            DG_FAST(gated_ffn, 9),        DG_FAST(gated_ffn_backward, 9),
+                           DG_FAST(quantize_int8, 2),    DG_FAST(linear_int8, 9),
+                           DG_FAST(gated_ffn_int8, 10),  DG_FAST(orthogonalize, 8),
                            {"on_error", &on_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, g_methods,

@@ -1,6 +1,7 @@
 """The feed-forward operators over torch CUDA tensors: layer norm, the linear
 layer with bias, activation and residual in its epilogue, and the gated
-feed-forward block, each with its backward pass.
+feed-forward block, each with its backward pass; the two products with weights in
+8-bit integers; and the orthogonalised update of a weight.
 
 Like `matmul`, these only check shapes and types, derive pointers, leading
 dimensions and the stream, allocate outputs and workspaces, and raise on a
@@ -175,3 +176,76 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, g, u, activation="silu", tra
             return gated_ffn_backward(dy, x, w_gate, w_up, w_down, g, u, activation, trans_w)
     return (_binding or _load()).gated_ffn_backward(dy, x, w_gate, w_up, w_down, g, u,
                                                     _activation(activation), trans_w)
+
+
+def quantize_int8(x, transpose=False, stream=None):
+    """(q, scale): every row of x as 8-bit integers, x about q * scale[..., None].
+
+    x: (..., n) bfloat16, float16 or float32.  q: int8 of x's shape, at most 127
+    in size, round(127 x / max|x|) with ties to even; scale: float32, max|x| / 127
+    of every row (shape x.shape[:-1]).  transpose: x is a K x N matrix whose
+    columns are meant: q is N x K and scale has N elements, the form in which
+    linear_int8 and gated_ffn_int8 take weights that linear and gated_ffn have as
+    K x N.  A row with NaN or an infinity gets that for its scale, and zeros.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return quantize_int8(x, transpose)
+    return (_binding or _load()).quantize_int8(x, transpose)
+
+
+def linear_int8(x, w, w_scale, bias=None, activation="none", residual=None, x_scale=None, dtype=None,
+                out=None, stream=None):
+    """act(x @ (w * w_scale[:, None]).T + bias) + residual, multiplied in 8-bit integers.
+
+    w: N x K int8 and w_scale: N float32, as quantize_int8 gives them (w.T of what
+    linear takes).  x: (..., K) bfloat16 or float16, put into 8 bits in the call,
+    each row with a scale of its own; or int8 with x_scale, float32 of shape
+    x.shape[:-1], to use the integers for several products.  bias: N elements;
+    residual, and out if given (it may be `residual` itself): (..., N); all of the
+    result's type, which is x's, or for an int8 x `dtype` (default bfloat16).
+    Sums of integers are exact within 2^24 and rounded to float32 beyond.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return linear_int8(x, w, w_scale, bias, activation, residual, x_scale, dtype, out)
+    return (_binding or _load()).linear_int8(x, w, w_scale, bias, _activation(activation), residual,
+                                             x_scale, dtype, out)
+
+
+def gated_ffn_int8(x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, activation="silu",
+                   residual=None, out=None, stream=None):
+    """gated_ffn with its weights, and the rows they multiply, in 8-bit integers.
+
+    x: (..., D) bfloat16 or float16.  w_gate, w_up: F x D and w_down: D x F int8,
+    with the float32 scales of their rows, as quantize_int8 gives them.  residual:
+    of x's shape; out may be it.  The hidden units are float32 until they are put
+    into 8 bits, each row with a scale of its own.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gated_ffn_int8(x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale,
+                                  activation, residual, out)
+    return (_binding or _load()).gated_ffn_int8(x, w_gate, gate_scale, w_up, up_scale, w_down,
+                                                down_scale, _activation(activation), residual, out)
+
+
+def orthogonalize(x, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, residual=None,
+                  residual_scale=1.0, out=None, stream=None):
+    """scale * orthogonalised(x) + residual_scale * residual, x's singular values brought towards 1
+    by `steps` Newton-Schulz steps (the Muon optimiser's update of a weight matrix):
+
+        x0 = x / (|x| + eps);  x <- a x + (b A + c A A) x,  A = x x^T.
+
+    x: a 2-D matrix, bfloat16, float16 or float32 (a momentum).  coefficients: (a, b,
+    c), or a sequence of `steps` such triples.  residual (the weights) and out: x's shape
+    and either of these types; out may be residual itself; the result has residual's type,
+    else out's, else x's.  So orthogonalize(m, scale=-lr, residual=w,
+    residual_scale=1 - lr * decay, out=w) is a step of the optimiser.  The products
+    are fp16 with float32 sums, whatever the types: the update is off by some 0.002 of its norm.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return orthogonalize(x, steps, coefficients, eps, scale, residual, residual_scale, out)
+    return (_binding or _load()).orthogonalize(x, steps, coefficients, eps, scale, residual,
+                                               residual_scale, out)

@@ -58,6 +58,7 @@
 #ifndef DGEMM_H
 #define DGEMM_H
 
+#include <stddef.h>              /* size_t */
 #include <cuda_runtime_api.h>   /* cudaStream_t */
 
 #ifdef __cplusplus
@@ -325,7 +326,7 @@ int dgemm_gemm_ex(int path, int op_a, int op_b, int M, int N, int K,
 
 /* Element types of the feed-forward operators. */
 typedef enum {
-    DGEMM_DTYPE_F32 = 0,  /* layer norm only */
+    DGEMM_DTYPE_F32 = 0,  /* layer norm, dgemm_quantize_int8, dgemm_orthogonalize */
     DGEMM_DTYPE_BF16 = 1,
     DGEMM_DTYPE_F16 = 2
 } dgemm_dtype_t;
@@ -434,6 +435,99 @@ int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, 
                              void *dX, int lddx, void *dWg, int lddwg,
                              void *dWu, int lddwu, void *dWd, int lddwd,
                              cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Products with weights in 8-bit integers, and the rows in 8-bit integers
+ * that they multiply.
+ *
+ * A row x is held as integers q of at most 127 in size and one float, its
+ * scale: x_j is about q_j scale.  Weights are stored out x in (N x K), a row and
+ * a scale for each output feature; tokens get theirs in the call.  Integers
+ * are multiplied and summed in fp32, exactly while the partial sums stay
+ * within 2^24 (any 1040 products do) and with fp32's rounding beyond.
+ * A row with NaN or an infinity gets that as its scale and zeros as integers;
+ * results computed from it are NaN.
+ */
+
+/*
+ * dgemm_quantize_int8 -- q_j = round(127 x_j / top) to the nearest integer,
+ * ties to even, and scale = top / 127, top = max |x_j| over a row (0, and scale
+ * 0, where there is nothing but zeros).  The rounding is that of the exact
+ * quotient for bf16 and fp16, of an fp32 one for fp32.
+ *
+ * X: rows x cols, of `dtype`.  op = DGEMM_OP_N: Q is rows x cols, scale rows floats.
+ * op = DGEMM_OP_T: the rows are X's columns, Q is cols x rows and scale cols
+ * floats (weights stored in x out, once, for the products below).
+ */
+int dgemm_quantize_int8(int dtype, int op, int rows, int cols,
+                        const void *X, int ldx,
+                        signed char *Q, int ldq, float *scale,
+                        cudaStream_t stream);
+
+/*
+ * dgemm_linear_int8 -- D = act(Z + bias) + R with Z_ij = s_i w_scale_j
+ * sum_k q_ik W_jk, q and s the rows of X in 8 bits.
+ *
+ * X: M x K of `dtype` (BF16 or F16), put into 8 bits here as dgemm_quantize_int8
+ * does; or, with x_scale (M floats) not NULL, M x K signed bytes.  W: N x K
+ * signed bytes, w_scale: N floats.  bias: N elements of dtype, or NULL.  R: M x
+ * N, or NULL; D: M x N, may be R itself.  work: dgemm_linear_int8_workspace(M,
+ * K) bytes on a 16-byte boundary.
+ */
+size_t dgemm_linear_int8_workspace(int M, int K);
+int dgemm_linear_int8(int dtype, int activation, int M, int N, int K,
+                      const void *X, int ldx, const float *x_scale,
+                      const signed char *W, int ldw, const float *w_scale,
+                      const void *bias, const void *R, int ldr,
+                      void *D, int ldd, void *work,
+                      cudaStream_t stream);
+
+/*
+ * dgemm_gated_ffn_int8 -- H = act(G) U with G and U the products above of X and
+ * Wg, Wu (one kernel), Y = the product of H and Wd, plus R.
+ *
+ * X, Y, R: M x D of `dtype`; R or NULL, Y may be R itself.  Wg, Wu: F x D, Wd: D x
+ * F signed bytes, their scales F, F and D floats.  H is kept in fp32 and put into
+ * 8 bits row by row like X.  work: dgemm_gated_ffn_int8_workspace(M, D, F)
+ * bytes on a 16-byte boundary.
+ */
+size_t dgemm_gated_ffn_int8_workspace(int M, int D, int F);
+int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F,
+                         const void *X, int ldx,
+                         const signed char *Wg, int ldwg, const float *g_scale,
+                         const signed char *Wu, int ldwu, const float *u_scale,
+                         const signed char *Wd, int ldwd, const float *d_scale,
+                         const void *R, int ldr, void *Y, int ldy, void *work,
+                         cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dgemm_orthogonalize -- a matrix with its singular values brought towards 1
+ * (what the Muon optimiser makes of a weight's momentum), and the update of a
+ * weight by it, by a Newton-Schulz iteration:
+ *
+ *   X_0 = X / (|X| + eps), |X| the root of the sum of squares,
+ *   X_k+1 = a_k X_k + (b_k A + c_k A A) X_k, A = X_k X_k^T (X_k^T X_k on the right
+ *           where X has more rows than columns: the same result),
+ *   D = scale X_steps + residual_scale R.
+ *
+ * X: rows x cols of x_dtype; R (or NULL) and D: rows x cols of dtype; both any of
+ * the three types; D may be R itself (w <- (1 - lr decay) w - lr update in place).
+ * coefficients: 3 * steps finite floats in HOST memory, a_k, b_k, c_k in turn,
+ * read during the call; at most 64 in size.  steps: 1 to DGEMM_NEWTON_MAX_STEPS.  eps >=
+ * 0 and finite.  Anything else: DGEMM_ERR_INVALID_VALUE.
+ * The iteration runs in fp16 with fp32 sums, whatever the types: D is off by some
+ * 0.002 of the update's norm (bf16 products would be off by 0.02).  With eps = 0 a
+ * matrix of zeros, and always one with NaN or an infinity, gives NaN.  Coefficients
+ * under which the iteration diverges give infinities and NaN past 2^7 or so.
+ * work: dgemm_orthogonalize_workspace(rows, cols) bytes on a 16-byte boundary.
+ */
+#define DGEMM_NEWTON_MAX_STEPS 64
+size_t dgemm_orthogonalize_workspace(int rows, int cols);
+int dgemm_orthogonalize(int x_dtype, int dtype, int steps, const float *coefficients, float eps,
+                        float scale, float residual_scale, int rows, int cols,
+                        const void *X, int ldx, const void *R, int ldr,
+                        void *D, int ldd, void *work,
+                        cudaStream_t stream);
 
 /* Static English text for a status code (never NULL). */
 const char *dgemm_status_string(int status);
