@@ -31,13 +31,10 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
-// sum * x * y of a row's and a feature's scale: the smaller first, so that nothing
-// overflows that the result does not, and a sum of 0 with a scale that is not
-// finite is NaN.
-__device__ __forceinline__ float scaled(float sum, float x, float y) {
-  const bool less = x < y;
-  return sum * (less ? x : y) * (less ? y : x);
-}
+// What a sum of integer products stands for: the feature's scale first, so that a
+// row's scale at either end of fp32's range neither overflows nor vanishes before the
+// result does; a sum of 0 in a row whose scale is not finite is NaN.
+__device__ __forceinline__ float scaled(float sum, float row, float feature) { return sum * feature * row; }
 
 // A whole warp's wait for a phase of a barrier.  False after `site` was recorded or
 // another wait of the CTA had given up.

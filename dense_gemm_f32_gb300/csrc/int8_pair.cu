@@ -8,9 +8,9 @@
 // the tile's to each CTA.  The weights are the operand in tensor memory because
 // they are the ones that are widened on the SM (int8.cuh), and 192 tokens because
 // that is what two accumulators leave room for.
-//  * Warp 0 loads weights (16 KB per 128 k), warp 14 tokens, warps 2-9 widen half a
+//  * Warp 0 loads weights (16 KB per 128 k), warp 2 tokens, warps 4-11 widen half a
 //    row of weights per thread, one thread of the even CTA issues
-//    tcgen05.mma.cta_group::2 with A in tensor memory, four warps run the epilogue.
+//    tcgen05.mma.cta_group::2 with A in tensor memory, eight warps run the epilogue.
 //  * The epilogue: a thread holds a feature's sums; a warp turns a 32 x 32 piece over
 //    through its 4 KB of shared memory, after which a thread has eight neighbouring
 //    features of a token: scales, bias, activation and residual in fp32, one
@@ -46,13 +46,23 @@ struct Cfg {
   static constexpr int PLACES = 2, PLACE_COLS = BK / 2;
   static constexpr int ACC_COLS = MAX_NT, TMEM_COLS = 512;
   static_assert(2 * ACC_COLS + PLACES * PLACE_COLS <= TMEM_COLS, "tensor memory of an SM");
-  static constexpr int CONV_WARP = 2, CONV_WARPS = 8, EPI_WARP = 10, EPI_WARPS = 4, TOKEN_WARP = 14;
-  static constexpr int THREADS = 32 * 15;
+  // Warps in fours, which hand registers to each other: weights, MMA, tokens, scales;
+  // converters; epilogue.  96 registers each at launch; the sum of what they go to is
+  // no more.
+  static constexpr int TOKEN_WARP = 2, SCALE_WARP = 3, CONV_WARP = 4, CONV_WARPS = 8, EPI_WARP = 12, EPI_WARPS = 8;
+  static constexpr int THREADS = 32 * (EPI_WARP + EPI_WARPS);
+  static constexpr int LAUNCH_REGS = 96, LOAD_REGS = 56, CONV_REGS = 80, EPI_REGS = 128;
+  static_assert(THREADS * LAUNCH_REGS <= 65536 && 32 * (CONV_WARP * LOAD_REGS + CONV_WARPS * CONV_REGS +
+                                                        EPI_WARPS * EPI_REGS) <= THREADS * LAUNCH_REGS,
+                "registers of an SM");
   static constexpr int PIECE_BYTES = 32 * 32 * 4;
   static constexpr int EPI_BYTES = EPI_WARPS * PIECE_BYTES;
-  // wfull, wempty, ready, tempty, accf[2], acce[2], drain, stall
-  static constexpr int NUM_BARS = 2 * W_STAGES + 2 * T_MAX_STAGES + 6;
-  static constexpr int TAIL_BYTES = NUM_BARS * 8 + 16 + 1024;
+  // Scales of a tile, for the epilogue: its features' (or bias or second scales behind),
+  // and its tokens'; two tiles'.
+  static constexpr int SCALE_FLOATS = 2 * HM + MAX_NT;
+  // wfull, wempty, ready, tempty, accf[2], acce[2], sfull[2], sempty[2], drain, stall
+  static constexpr int NUM_BARS = 2 * W_STAGES + 2 * T_MAX_STAGES + 10;
+  static constexpr int TAIL_BYTES = 2 * SCALE_FLOATS * 4 + NUM_BARS * 8 + 16 + 1024;
   static constexpr int FIXED_BYTES = W_STAGES * W_BYTES + EPI_BYTES + TAIL_BYTES;
   static constexpr int BUDGET = 232448 - FIXED_BYTES;
 };
@@ -70,6 +80,8 @@ enum : int {
   kSite7MmaDrain = 0xfa,
   kSite7MmaTail = 0xfb,
   kSite7EpiAccFull = 0xfc,
+  kSite7EpiScales = 0xfe,
+  kSite7ScalesEmpty = 0xff,
   kSite7TestStall = 0xfd,  // DGEMM_TC_TEST_STALL: the MMA thread's test wait ran out
 };
 
@@ -103,7 +115,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const uint32_t t_bytes = (uint32_t)p.nt * 128u;  // this CTA's half of the tokens, 128 k
   const uint32_t t_base = base + G::W_STAGES * G::W_BYTES;
   const uint32_t epi_base = t_base + (uint32_t)p.t_stages * t_bytes;
-  const uint32_t bars = epi_base + G::EPI_BYTES;
+  const uint32_t bars = epi_base + G::EPI_BYTES + 2 * G::SCALE_FLOATS * 4;
+  float *scales = reinterpret_cast<float *>(smem + (epi_base - base) + G::EPI_BYTES);
   auto wfull_bar = [&](int s) { return bars + 8u * s; };
   auto wempty_bar = [&](int s) { return bars + 8u * (G::W_STAGES + s); };
   auto ready_bar = [&](int s) { return bars + 8u * (2 * G::W_STAGES + s); };
@@ -111,8 +124,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const uint32_t more = bars + 8u * (2 * G::W_STAGES + 2 * G::T_MAX_STAGES);
   auto accf_bar = [&](int b) { return more + 8u * b; };
   auto acce_bar = [&](int b) { return more + 8u * (2 + b); };
-  const uint32_t drain_bar = more + 8u * 4;
-  const uint32_t stall_bar = more + 8u * 5;  // nothing ever arrives here
+  auto sfull_bar = [&](int b) { return more + 8u * (4 + b); };
+  auto sempty_bar = [&](int b) { return more + 8u * (6 + b); };
+  const uint32_t drain_bar = more + 8u * 8;
+  const uint32_t stall_bar = more + 8u * 9;  // nothing ever arrives here
   uint8_t *tail = smem + (bars - base) + 8 * G::NUM_BARS;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
@@ -141,6 +156,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
       mbar_init(acce_bar(b), 2 * G::EPI_WARPS);
+      mbar_init(sfull_bar(b), 1);
+      mbar_init(sempty_bar(b), G::EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     mbar_init(stall_bar, 1);
@@ -166,139 +183,171 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tile_coords(tile, tiles_f, tiles_t, p.group, tf, tt);
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------- weights
-    if (lane == 0) {
-      int s = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
-        int tf, tt;
-        coords(tile, tf, tt);
-        const int f0 = (2 * tf + (int)rank) * HF;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_try_wait(wempty_bar(s), phase ^ 1u) &&
-              (*abort_flag || !mbar_wait(wempty_bar(s), phase ^ 1u))) {
-            if (!*abort_flag) watchdog_trip(p.watchdog, kSite7WeightsEmpty, abort_flag);
-            ok = false;
+  if (warp < G::CONV_WARP) {
+    setmaxnreg_dec<G::LOAD_REGS>();
+    if (warp == 0) {
+      // ------------------------------------------------------------- weights
+      if (lane == 0) {
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+          int tf, tt;
+          coords(tile, tf, tt);
+          const int f0 = (2 * tf + (int)rank) * HF;
+          for (int kb = 0; kb < kblocks; ++kb) {
+            if (!mbar_try_wait(wempty_bar(s), phase ^ 1u) &&
+                (*abort_flag || !mbar_wait(wempty_bar(s), phase ^ 1u))) {
+              if (!*abort_flag) watchdog_trip(p.watchdog, kSite7WeightsEmpty, abort_flag);
+              ok = false;
+              break;
+            }
+            tma_load_2d(w_tile(s), &maps.w, wfull_bar(s), kb * G::BK, f0);
+            if constexpr (GATED)
+              tma_load_2d(w_tile(s) + G::W_BYTES / 2, &maps.w2, wfull_bar(s), kb * G::BK, f0);
+            mbar_arrive_expect_tx(wfull_bar(s), G::W_BYTES);
+            if (++s == G::W_STAGES) s = 0, phase ^= 1u;
+          }
+        }
+        // Tail: no copy is still writing this CTA's shared memory.
+        for (int i = 0; i < G::W_STAGES; ++i) {
+          if (!mbar_wait(wempty_bar(s), phase ^ 1u)) {
+            atomicCAS(p.watchdog, 0, kSite7WeightsTail);
             break;
           }
-          tma_load_2d(w_tile(s), &maps.w, wfull_bar(s), kb * G::BK, f0);
-          if constexpr (GATED)
-            tma_load_2d(w_tile(s) + G::W_BYTES / 2, &maps.w2, wfull_bar(s), kb * G::BK, f0);
-          mbar_arrive_expect_tx(wfull_bar(s), G::W_BYTES);
           if (++s == G::W_STAGES) s = 0, phase ^= 1u;
         }
       }
-      // Tail: no copy is still writing this CTA's shared memory.
-      for (int i = 0; i < G::W_STAGES; ++i) {
-        if (!mbar_wait(wempty_bar(s), phase ^ 1u)) {
-          atomicCAS(p.watchdog, 0, kSite7WeightsTail);
-          break;
+    } else if (warp == G::TOKEN_WARP) {
+      // -------------------------------------------------------------- tokens
+      if (lane == 0) {
+        pdl_wait();
+        const uint32_t fb0 = mapa_shared(ready_bar(0), 0);
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+          int tf, tt;
+          coords(tile, tf, tt);
+          const int t0 = tt * p.nt + (int)rank * (p.nt / 2);
+          for (int kb = 0; kb < kblocks; ++kb) {
+            if (!mbar_try_wait(tempty_bar(s), phase ^ 1u) &&
+                (*abort_flag || !mbar_wait(tempty_bar(s), phase ^ 1u))) {
+              if (!*abort_flag) watchdog_trip(p.watchdog, kSite7TokensEmpty, abort_flag);
+              ok = false;
+              break;
+            }
+            tma_load_2d_pair(t_tile(s), &maps.t, fb0 + 8u * (uint32_t)s, kb * G::BK, t0);
+            tma_load_2d_pair(t_tile(s) + t_bytes / 2, &maps.t, fb0 + 8u * (uint32_t)s, kb * G::BK + 64, t0);
+            if (leader) mbar_arrive_expect_tx(ready_bar(s), 2u * t_bytes);
+            if (++s == p.t_stages) s = 0, phase ^= 1u;
+          }
         }
-        if (++s == G::W_STAGES) s = 0, phase ^= 1u;
-      }
-    }
-  } else if (warp == G::TOKEN_WARP) {
-    // -------------------------------------------------------------- tokens
-    if (lane == 0) {
-      pdl_wait();
-      const uint32_t fb0 = mapa_shared(ready_bar(0), 0);
-      int s = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
-        int tf, tt;
-        coords(tile, tf, tt);
-        const int t0 = tt * p.nt + (int)rank * (p.nt / 2);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_try_wait(tempty_bar(s), phase ^ 1u) &&
-              (*abort_flag || !mbar_wait(tempty_bar(s), phase ^ 1u))) {
-            if (!*abort_flag) watchdog_trip(p.watchdog, kSite7TokensEmpty, abort_flag);
-            ok = false;
+        // Tail: every stage-free signal aimed at this CTA has landed, and no
+        // copy is still writing its shared memory.
+        for (int i = 0; i < p.t_stages; ++i) {
+          if (!mbar_wait(tempty_bar(s), phase ^ 1u)) {
+            atomicCAS(p.watchdog, 0, kSite7TokensTail);
             break;
           }
-          tma_load_2d_pair(t_tile(s), &maps.t, fb0 + 8u * (uint32_t)s, kb * G::BK, t0);
-          tma_load_2d_pair(t_tile(s) + t_bytes / 2, &maps.t, fb0 + 8u * (uint32_t)s, kb * G::BK + 64, t0);
-          if (leader) mbar_arrive_expect_tx(ready_bar(s), 2u * t_bytes);
           if (++s == p.t_stages) s = 0, phase ^= 1u;
         }
       }
-      // Tail: every stage-free signal aimed at this CTA has landed, and no
-      // copy is still writing its shared memory.
-      for (int i = 0; i < p.t_stages; ++i) {
-        if (!mbar_wait(tempty_bar(s), phase ^ 1u)) {
-          atomicCAS(p.watchdog, 0, kSite7TokensTail);
-          break;
-        }
-        if (++s == p.t_stages) s = 0, phase ^= 1u;
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------- MMA (even CTA only)
-    if (lane == 0 && leader) {
-      int s = 0;
-      uint32_t phase = 0, place = place0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      // Descriptors of stage 0's tokens; stages and steps of k are added to their
-      // address field (a thread's chain through computing them anew for every MMA is
-      // as long as the MMA).
-      const uint64_t desc0 = smem_desc(t_tile(0), 16u, 1024u);
-      const uint32_t stage16 = t_bytes >> 4, box16 = t_bytes >> 5;
-      uint64_t desc = desc0;
-      bool ok = true;
-      if (p.stall && cluster == 0) {  // test hook: a wait that runs out
-        if (!mbar_wait(stall_bar, 0)) watchdog_trip(p.watchdog, kSite7TestStall, abort_flag);
-        ok = false;
-      }
-      for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
-        if (*abort_flag || !mbar_wait(acce_bar(acc), acc_phase ^ 1u)) {
-          if (!*abort_flag) watchdog_trip(p.watchdog, kSite7MmaAccEmpty, abort_flag);
+    } else if (warp == 1) {
+      // ------------------------------------------------- MMA (even CTA only)
+      // The whole warp goes through the loop, so that one elected lane issues the MMAs
+      // from uniform registers.
+      if (leader) {
+        int s = 0;
+        uint32_t phase = 0, place = place0;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        // Descriptors of stage 0's tokens; stages and steps of k are added to their
+        // address field (a thread's chain through computing them anew for every MMA is
+        // as long as the MMA).
+        const uint64_t desc0 = smem_desc(t_tile(0), 16u, 1024u);
+        const uint32_t stage16 = t_bytes >> 4, box16 = t_bytes >> 5;
+        uint64_t desc = desc0;
+        bool ok = true;
+        if (p.stall && cluster == 0) {  // test hook: a wait that runs out
+          warp_wait(stall_bar, 0, lane, p.watchdog, kSite7TestStall, abort_flag);
           ok = false;
-          break;
         }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * G::ACC_COLS);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_try_wait(ready_bar(s), phase) && (*abort_flag || !mbar_wait(ready_bar(s), phase))) {
-            if (!*abort_flag) watchdog_trip(p.watchdog, kSite7MmaReady, abort_flag);
-            ok = false;
+        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+          if (!warp_wait(acce_bar(acc), acc_phase ^ 1u, lane, p.watchdog, kSite7MmaAccEmpty, abort_flag)) break;
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * G::ACC_COLS);
+          for (int kb = 0; kb < kblocks; ++kb) {
+            ok = warp_wait(ready_bar(s), phase, lane, p.watchdog, kSite7MmaReady, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < G::BK / 16; ++k)
+                umma_f16_ta_pair(d_tmem, place + 8u * k, desc + (k >> 2) * box16 + 2u * (k & 3), p.idesc,
+                                 k > 0 ? 1u : kb > 0 ? 1u : 0u);
+              umma_commit_pair(tempty_bar(s), 0x3);  // frees the tokens and the place in both CTAs
+            }
+            __syncwarp();
+            place ^= place0 ^ place1;
+            desc += stage16;
+            if (++s == p.t_stages) s = 0, phase ^= 1u, desc = desc0;
+          }
+          if (!ok) break;
+          if (elect_one()) umma_commit_pair(accf_bar(acc), 0x3);  // accumulator ready in both CTAs
+          __syncwarp();
+          if (++acc == 2) acc = 0, acc_phase ^= 1u;
+        }
+        // by the lane that issued the MMAs (elect_one names the same one every time)
+        if (elect_one()) umma_commit_pair(drain_bar, 0x1);
+        __syncwarp();
+        if (!mbar_wait(drain_bar, 0)) atomicCAS(p.watchdog, 0, kSite7MmaDrain);
+        // Tail: both accumulators released by both epilogues.
+        for (int i = 0; i < 2; ++i) {
+          if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u)) {
+            atomicCAS(p.watchdog, 0, kSite7MmaTail);
             break;
           }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < G::BK / 16; ++k)
-            umma_f16_ta_pair(d_tmem, place + 8u * k, desc + (k >> 2) * box16 + 2u * (k & 3), p.idesc,
-                             k > 0 ? 1u : kb > 0 ? 1u : 0u);
-          umma_commit_pair(tempty_bar(s), 0x3);  // frees the tokens and the place in both CTAs
-          place ^= place0 ^ place1;
-          desc += stage16;
-          if (++s == p.t_stages) s = 0, phase ^= 1u, desc = desc0;
+          if (++acc == 2) acc = 0, acc_phase ^= 1u;
         }
-        if (!ok) break;
-        umma_commit_pair(accf_bar(acc), 0x3);  // accumulator ready in both CTAs
-        if (++acc == 2) acc = 0, acc_phase ^= 1u;
-      }
-      umma_commit_pair(drain_bar, 0x1);
-      if (!mbar_wait(drain_bar, 0)) atomicCAS(p.watchdog, 0, kSite7MmaDrain);
-      // Tail: both accumulators released by both epilogues.
-      for (int i = 0; i < 2; ++i) {
-        if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u)) {
-          atomicCAS(p.watchdog, 0, kSite7MmaTail);
-          break;
-        }
-        if (++acc == 2) acc = 0, acc_phase ^= 1u;
       }
     }
-  } else if (warp < G::CONV_WARP + G::CONV_WARPS) {
+    if (warp == G::SCALE_WARP) {
+      // ------------------------------------------------------------ scales
+      pdl_wait();
+      int b = 0;
+      uint32_t phase = 0;
+      for (int tile = cluster; tile < num_tiles; tile += clusters) {
+        int tf, tt;
+        coords(tile, tf, tt);
+        if (!warp_wait(sempty_bar(b), phase ^ 1u, lane, p.watchdog, kSite7ScalesEmpty, abort_flag)) break;
+        float *to = scales + b * G::SCALE_FLOATS;
+        const int f0 = (2 * tf + (int)rank) * HF, t0 = tt * p.nt;
+        for (int i = lane; i < HF; i += 32) {
+          const bool in = f0 + i < p.N;
+          to[i] = in ? p.w_scale[f0 + i] : 0.f;
+          float more = 0.f;  // the other projection's scale, or the bias
+          if (GATED)
+            more = in ? p.w2_scale[f0 + i] : 0.f;
+          else if (p.bias != nullptr)
+            more = in ? to_f32<T>(static_cast<const T *>(p.bias)[f0 + i]) : 0.f;
+          to[G::HM + i] = more;
+        }
+        for (int i = lane; i < p.nt; i += 32) to[2 * G::HM + i] = t0 + i < p.M ? p.t_scale[t0 + i] : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull_bar(b));
+        if (++b == 2) b = 0, phase ^= 1u;
+      }
+    }
+  } else if (warp < G::EPI_WARP) {
+    setmaxnreg_dec<G::CONV_REGS>();
     // --------------------------------------------------- widen the weights
     // four warps for each half of a stage's k
-    const int quarter = warp & 3, half = (warp - G::CONV_WARP) >> 2;
+    const int quarter = warp & 3, half_k = (warp - G::CONV_WARP) >> 2;
     // gated: of a quarter's 32 lanes 16 features of Wg, then the same of Wu
     const int row = !GATED ? quarter * 32 + lane
                            : (lane < 16 ? quarter * 16 + lane : G::HM / 2 + quarter * 16 + lane - 16);
-    const uint32_t lanes = ((uint32_t)(quarter * 32) << 16) + (uint32_t)(32 * half);
+    const uint32_t lanes = ((uint32_t)(quarter * 32) << 16) + (uint32_t)(32 * half_k);
     const uint32_t ready_leader = mapa_shared(ready_bar(0), 0);
     const int64_t tiles = cluster < num_tiles ? (num_tiles - 1 - cluster) / clusters + 1 : 0;
     const int64_t blocks = tiles * kblocks;
@@ -306,8 +355,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint32_t phase = 0, free_phase = 0, place = place0;
     for (int64_t i = 0; i < blocks; ++i) {
       if (!warp_wait(wfull_bar(s), phase, lane, p.watchdog, kSite7ConvFull, abort_flag)) break;
+      const uint8_t *w = smem + (w_tile(s) - base) + row * G::BK;
       uint32_t r[32];
-      widen64(smem + (w_tile(s) - base) + row * G::BK, 4 * half, row & 7, r);
+      widen64(w, 4 * half_k, row & 7, r);
       __syncwarp();
       if (lane == 0) mbar_arrive(wempty_bar(s));
       if (++s == G::W_STAGES) s = 0, phase ^= 1u;
@@ -325,6 +375,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       place ^= place0 ^ place1;
     }
   } else {
+    setmaxnreg_inc<G::EPI_REGS>();
     // ------------------------------------------------------------ epilogue
     pdl_wait();
     const int quarter = warp & 3;
@@ -336,94 +387,101 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int chunk = lane % Q, token = lane / Q;
     int acc = 0;
     uint32_t acc_phase = 0;
+    const int half = (warp - G::EPI_WARP) >> 2;  // which of the two warps of the quarter
+    const bool has_in0 = !GATED && p.in0 != nullptr;
     for (int tile = cluster; tile < num_tiles; tile += clusters) {
       int tf, tt;
       coords(tile, tf, tt);
       const int t0 = tt * p.nt, live = min(p.nt, p.M - t0);
-      const int col = (2 * tf + (int)rank) * HF + quarter * (HF / 4) + 8 * chunk;
-      float ws[8], ws2[8], bias[8];
+      const int f = quarter * (HF / 4) + 8 * chunk, col = (2 * tf + (int)rank) * HF + f;
+      if (!warp_wait(sfull_bar(acc), acc_phase, lane, p.watchdog, kSite7EpiScales, abort_flag)) break;
+      const float *sc = scales + acc * G::SCALE_FLOATS;
+      float ws[8], more[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = col + j < p.N;
-        ws[j] = in ? p.w_scale[col + j] : 0.f;
-        ws2[j] = GATED && in ? p.w2_scale[col + j] : 0.f;
-        bias[j] = !GATED && in && p.bias != nullptr ? to_f32<T>(static_cast<const T *>(p.bias)[col + j]) : 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = *reinterpret_cast<const float4 *>(sc + f + 4 * h);
+        const float4 y = *reinterpret_cast<const float4 *>(sc + G::HM + f + 4 * h);
+        ws[4 * h] = x.x, ws[4 * h + 1] = x.y, ws[4 * h + 2] = x.z, ws[4 * h + 3] = x.w;
+        more[4 * h] = y.x, more[4 * h + 1] = y.y, more[4 * h + 2] = y.z, more[4 * h + 3] = y.w;
       }
       if (!warp_wait(accf_bar(acc), acc_phase, lane, p.watchdog, kSite7EpiAccFull, abort_flag)) break;
       tc_fence_after();
       const uint32_t t_row =
           tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * G::ACC_COLS);
 #pragma unroll 1
-      for (int c0 = 0; c0 < live; c0 += 32) {
+      for (int c0 = 32 * half; c0 < live; c0 += 64) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_row + (uint32_t)c0, r);
-        float ts[ROUNDS];
-        RowBlocks res[ROUNDS];
+        const T *res_row = static_cast<const T *>(p.in0) + (int64_t)(t0 + c0 + token) * p.ldi0;
+        RowBlocks res[GATED ? 1 : ROUNDS];
+        if (has_in0) {
 #pragma unroll
-        for (int i = 0; i < ROUNDS; ++i) {
-          const int t = c0 + token + i * STEP;
-          const int64_t row = t0 + t;
-          ts[i] = t < live ? p.t_scale[row] : 0.f;
-          if (!GATED && p.in0 != nullptr)
-            res[i] = fetch_row16<T, AL>(static_cast<const T *>(p.in0) + row * p.ldi0, col, t < live ? p.N : 0);
+          for (int i = 0; i < ROUNDS; ++i)
+            res[GATED ? 0 : i] = fetch_row16<T, AL>(res_row + i * STEP * p.ldi0, col,
+                                                    c0 + token + i * STEP < live ? p.N : 0);
         }
         tmem_wait_ld();
         __syncwarp();  // the piece before has been read
 #pragma unroll
         for (int j = 0; j < 32; ++j) piece[j * 32 + lane] = __uint_as_float(r[j]);
         __syncwarp();
+        const float *ts = sc + 2 * G::HM + c0 + token;
+        const int left = col < p.N ? live - c0 - token : 0;  // of this thread's tokens, STEP apart
+        char *out = static_cast<char *>(p.out) +
+                    ((int64_t)(t0 + c0 + token) * p.ldo + col) * (GATED ? 4 : (int)sizeof(T));
+        const int64_t step_bytes = (int64_t)STEP * p.ldo * (GATED ? 4 : (int)sizeof(T));
+        // halves in an order that keeps the eight lanes of a phase on different banks
+        const int first = (lane / Q) & 1;
+        auto take = [&](int tp, int at, float (&v)[8]) {
+          const float4 x = *reinterpret_cast<const float4 *>(piece + tp * 32 + at + 4 * first);
+          const float4 y = *reinterpret_cast<const float4 *>(piece + tp * 32 + at + 4 * (first ^ 1));
+          v[0] = first ? y.x : x.x, v[1] = first ? y.y : x.y, v[2] = first ? y.z : x.z, v[3] = first ? y.w : x.w;
+          v[4] = first ? x.x : y.x, v[5] = first ? x.y : y.y, v[6] = first ? x.z : y.z, v[7] = first ? x.w : y.w;
+        };
+        with_act(p.act, [&](auto c) {
+          constexpr int ACT = decltype(c)::value;
 #pragma unroll
-        for (int i = 0; i < ROUNDS; ++i) {
-          const int tp = token + i * STEP, t = c0 + tp;
-          const bool in = t < live && col < p.N;
-          const int64_t row = t0 + t;
-          float a[8], b[8];
-          // halves in an order that keeps the eight lanes of a phase on different banks
-          auto take = [&](int f, float (&v)[8]) {
-            const int first = (lane / Q) & 1;
+          for (int i = 0; i < ROUNDS; ++i) {
+            float a[8];
+            take(token + i * STEP, 8 * chunk, a);
+            const float row_scale = ts[i * STEP];
+            if constexpr (GATED) {
+              float b[8];
+              take(token + i * STEP, 16 + 8 * chunk, b);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int k = h ^ first;
-              const float4 x = *reinterpret_cast<const float4 *>(piece + tp * 32 + f + 4 * k);
-              if (k == 0)
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-              else
-                v[4] = x.x, v[5] = x.y, v[6] = x.z, v[7] = x.w;
+              for (int j = 0; j < 8; ++j)
+                a[j] = act_f32<ACT>(scaled(a[j], row_scale, ws[j])) * scaled(b[j], row_scale, more[j]);
+              if (i * STEP < left) {
+                float4 *h = reinterpret_cast<float4 *>(out + i * step_bytes);
+                h[0] = make_float4(a[0], a[1], a[2], a[3]);
+                h[1] = make_float4(a[4], a[5], a[6], a[7]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) a[j] = act_f32<ACT>(scaled(a[j], row_scale, ws[j]) + more[j]);
+              if (has_in0) {
+                float x[8];
+                widen16<T>(take_row16<T, AL>(res[GATED ? 0 : i], res_row + i * STEP * p.ldi0, col, p.N), x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[j] += x[j];
+              }
+              const uint4 v[1] = {narrow16<T>(a)};
+              if constexpr (AL) {
+                if (i * STEP < left) *reinterpret_cast<uint4 *>(out + i * step_bytes) = v[0];
+              } else {
+                store_row16<T, AL, 1, Q>(static_cast<T *>(p.out) + (int64_t)(t0 + c0 + token + i * STEP) * p.ldo,
+                                         i * STEP < left ? col : p.N, p.N, v);
+              }
             }
-          };
-          take(8 * chunk, a);
-          if constexpr (GATED) take(16 + 8 * chunk, b);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) a[j] = scaled(a[j], ts[i], ws[j]) + bias[j];
-          if constexpr (GATED) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) b[j] = scaled(b[j], ts[i], ws2[j]);
-            with_act(p.act, [&](auto c) {
-              constexpr int ACT = decltype(c)::value;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) a[j] = act_f32<ACT>(a[j]) * b[j];
-            });
-            if (in) {
-              float4 *h = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * p.ldo + col);
-              h[0] = make_float4(a[0], a[1], a[2], a[3]);
-              h[1] = make_float4(a[4], a[5], a[6], a[7]);
-            }
-          } else {
-            const bool has_in0 = p.in0 != nullptr;
-            uint32_t i0[4], w0[4], w1[4], w2[4];
-            if (has_in0) {
-              const uint4 x = take_row16<T, AL>(res[i], static_cast<const T *>(p.in0) + row * p.ldi0, col, p.N);
-              i0[0] = x.x, i0[1] = x.y, i0[2] = x.z, i0[3] = x.w;
-            }
-            epilogue_row<Epi::kLinear, T, 4>(p.act, has_in0, false, a, a, i0, i0, w0, w1, w2);
-            const uint4 v[1] = {make_uint4(w0[0], w0[1], w0[2], w0[3])};
-            store_row16<T, AL, 1, Q>(static_cast<T *>(p.out) + row * p.ldo, in ? col : p.N, p.N, v);
           }
-        }
+        });
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc ? acce_leader1 : acce_leader0);
+      if (lane == 0) {
+        mbar_arrive(sempty_bar(acc));
+        mbar_arrive_cluster_tmem(acc ? acce_leader1 : acce_leader0);
+      }
       if (++acc == 2) acc = 0, acc_phase ^= 1u;
     }
   }

@@ -7,8 +7,8 @@
 // where there are few tiles, partial tiles joined through distributed shared
 // memory in part order.  T holds the tokens' integers in fp16 (quant.cu).
 //  * Warp 0 loads stages of 128 k by TMA (16 KB of weights, the tokens' 256
-//    bytes each); warps 2-5 widen the weights into one of two places in tensor
-//    memory (int8.cuh); warp 1 issues tcgen05.mma with A from there.
+//    bytes each); warps 2-9 widen the weights into one of two places in tensor
+//    memory (int8.cuh), half a row each; warp 1 issues tcgen05.mma with A from there.
 //  * The first stages of weights are loaded before the kernel ahead on the
 //    stream, which quantises the tokens, is done: it signals only after its own
 //    wait, so whatever wrote the weights is done by then.
@@ -40,7 +40,7 @@ struct Cfg {
   static constexpr int W_BYTES = TF * BK;
   static constexpr int MAX_STAGES = 10, MAX_SPLITS = 8;
   static constexpr int A_COLS = 64;           // tensor memory of widened weights of 128 k
-  static constexpr int CONV_WARPS = 4, THREADS = 32 * (2 + CONV_WARPS);
+  static constexpr int CONV_WARPS = 8, THREADS = 32 * (2 + CONV_WARPS);
   // bars (full, empty, conv[2], accf, stall), TMEM slot, abort flag; 1024 for alignment
   static constexpr int NUM_BARS = 2 * MAX_STAGES + 4;
   static constexpr int TAIL_BYTES = NUM_BARS * 8 + 16 + 1024;
@@ -135,6 +135,40 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t a_tmem = tmem_base + (p.tmem_cols - 2u * G::A_COLS);  // behind the accumulator
 
+  // What the epilogue needs of a thread's features, and of its first token, is read
+  // now.
+  constexpr int Q = TF / 8;  // threads per token
+  const int live = min(p.nt, p.M - t0), feats = min(TF, p.N - f0), end = f0 + feats;
+  const int n = live * Q, round = splits * G::THREADS, e0 = part * G::THREADS + threadIdx.x;
+  static_assert(G::THREADS % Q == 0, "a thread keeps its features from round to round");
+  const int f = 8 * (e0 % Q), col = f0 + f;
+  float ws[8], ws2[8], bias[8];
+  struct Inputs {
+    float ts;
+    RowBlocks res;
+  } ahead;
+  const T *in0 = static_cast<const T *>(p.in0);
+  auto fetch = [&](int e) {
+    const int t = e / Q;
+    const bool in = t < live && f < feats;
+    const int64_t row = t0 + t;
+    Inputs x = {};
+    x.ts = in ? p.t_scale[row] : 0.f;
+    if (!GATED && in0 != nullptr) x.res = fetch_row16<T, AL>(in0 + row * p.ldi0, col, in ? end : 0);
+    return x;
+  };
+  auto fetch_first = [&] {
+    const bool mine = e0 < n;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = mine && f + j < feats;
+      ws[j] = in ? p.w_scale[col + j] : 0.f;
+      ws2[j] = GATED && in ? p.w2_scale[col + j] : 0.f;
+      bias[j] = !GATED && in && p.bias != nullptr ? to_f32<T>(static_cast<const T *>(p.bias)[col + j]) : 0.f;
+    }
+    ahead = fetch(e0);
+  };
+
   bool all_sent = false;  // this thread is the producer and has sent for every stage
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -174,64 +208,64 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
     } else {
       pdl_wait();
     }
+    __syncwarp();
+    fetch_first();
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
+    // (the whole warp in the loop, descriptors by addition: as in int8_pair.cu)
     pdl_wait();
-    if (lane == 0) {
-      bool ok = true;
-      if (p.stall && blockIdx.x == 0) {  // test hook: a wait that runs out
-        if (!mbar_wait(stall_bar, 0)) watchdog_trip(p.watchdog, kSite5TestStall, abort_flag);
-        ok = false;
-      }
-      int s = 0;
-      uint32_t phase = 0;
-      // as in int8_pair.cu: descriptors by addition
-      const uint64_t desc0 = smem_desc(t_tile(0), 16u, 1024u);
-      const uint32_t stage16 = stage_bytes >> 4, box16 = t_bytes >> 5;
-      uint64_t desc = desc0;
-      for (int i = 0; i < blocks && ok; ++i) {
-        // the converters have seen the stage full; so does this thread, for the tokens
-        const uint32_t conv_phase = (uint32_t)(i >> 1) & 1u;
-        if ((!mbar_try_wait(full_bar(s), phase) && (*abort_flag || !mbar_wait(full_bar(s), phase))) ||
-            (!mbar_try_wait(conv_bar(i & 1), conv_phase) &&
-             (*abort_flag || !mbar_wait(conv_bar(i & 1), conv_phase)))) {
-          if (!*abort_flag) watchdog_trip(p.watchdog, kSite5MmaConv, abort_flag);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a = a_tmem + (uint32_t)((i & 1) * G::A_COLS);
+    fetch_first();
+    bool ok = true;
+    if (p.stall && blockIdx.x == 0) {  // test hook: a wait that runs out
+      warp_wait(stall_bar, 0, lane, p.watchdog, kSite5TestStall, abort_flag);
+      ok = false;
+    }
+    int s = 0;
+    uint32_t phase = 0;
+    const uint64_t desc0 = smem_desc(t_tile(0), 16u, 1024u);
+    const uint32_t stage16 = stage_bytes >> 4, box16 = t_bytes >> 5;
+    uint64_t desc = desc0;
+    for (int i = 0; i < blocks && ok; ++i) {
+      // the converters have seen the stage full; so does this warp, for the tokens
+      ok = warp_wait(full_bar(s), phase, lane, p.watchdog, kSite5MmaConv, abort_flag) &&
+           warp_wait(conv_bar(i & 1), (uint32_t)(i >> 1) & 1u, lane, p.watchdog, kSite5MmaConv, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t a = a_tmem + (uint32_t)((i & 1) * G::A_COLS);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < G::BK / 16; ++k)
           umma_f16_ta(tmem_base, a + 8u * k, desc + (k >> 2) * box16 + 2u * (k & 3), p.idesc,
                       k > 0 ? 1u : i > 0 ? 1u : 0u);
         umma_commit(empty_bar(s));
-        desc += stage16;
-        if (++s == p.stages) s = 0, phase ^= 1u, desc = desc0;
       }
-      umma_commit(accf_bar);  // every MMA issued above has completed
-      if (!mbar_wait(accf_bar, 0)) atomicCAS(p.watchdog, 0, kSite5MmaDrain);
+      __syncwarp();
+      desc += stage16;
+      if (++s == p.stages) s = 0, phase ^= 1u, desc = desc0;
     }
+    if (elect_one()) umma_commit(accf_bar);  // every MMA issued above has completed
+    __syncwarp();
+    if (!mbar_wait(accf_bar, 0)) atomicCAS(p.watchdog, 0, kSite5MmaDrain);
   } else {
     // ---------------------------- widen the weights, then drain the accumulator
     pdl_wait();
-    const int quarter = warp & 3, row = quarter * 32 + lane;
+    fetch_first();
+    // four warps for each half of a stage's k
+    const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     int s = 0, free_s = 0;
     uint32_t phase = 0, free_phase = 0;
     for (int i = 0; i < blocks; ++i) {
       if (!warp_wait(full_bar(s), phase, lane, p.watchdog, kSite5ConvFull, abort_flag)) break;
       const uint8_t *w = smem + (w_tile(s) - base) + row * G::BK;
-      uint32_t r0[32], r1[32];
-      widen64(w, 0, row & 7, r0);
-      widen64(w, 4, row & 7, r1);
+      uint32_t r[32];
+      widen64(w, 4 * half, row & 7, r);
       if (i >= 2) {  // the MMAs that read this place two blocks ago are done
         if (!warp_wait(empty_bar(free_s), free_phase, lane, p.watchdog, kSite5ConvSlot, abort_flag)) break;
         if (++free_s == p.stages) free_s = 0, free_phase ^= 1u;
         tc_fence_after();
       }
-      const uint32_t to = a_tmem + lanes + (uint32_t)((i & 1) * G::A_COLS);
-      tmem_st_32x32b_x32(to, r0);
-      tmem_st_32x32b_x32(to + 32u, r1);
+      tmem_st_32x32b_x32(a_tmem + lanes + (uint32_t)((i & 1) * G::A_COLS + 32 * half), r);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -242,8 +276,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
       tc_fence_after();
       // Every MMA has completed, so the stage area is idle: partial[t][f]
       float *col = reinterpret_cast<float *>(smem) + row;
-      const int live = min(p.nt, p.M - t0);
-      for (int c0 = 0; c0 < live; c0 += 16) {
+      for (int c0 = 16 * half; c0 < live; c0 += 32) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(tmem_base + lanes + (uint32_t)c0, r);
         tmem_wait_ld();
@@ -266,6 +299,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
 #pragma unroll
     for (int s = 0; s < G::MAX_SPLITS; ++s)
       at[s] = s < splits ? mapa_shared(base, (uint32_t)s) : 0u;
+    // looked at before anything is stored, so that these loads and those of the
+    // partials are in flight together
     const uint32_t flag = smem_u32(const_cast<int *>(abort_flag)) - base;
 #pragma unroll
     for (int s = 0; s < G::MAX_SPLITS; ++s)
@@ -273,7 +308,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
   } else {
     aborted = *abort_flag != 0;
   }
-  if (!aborted) {  // the same for the whole cluster
+  {
     auto sum4 = [&](uint32_t off) {  // parts added in K order
       if constexpr (SPLIT) {
         float4 v[G::MAX_SPLITS];
@@ -296,19 +331,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
         a[4 * h] = v.x, a[4 * h + 1] = v.y, a[4 * h + 2] = v.z, a[4 * h + 3] = v.w;
       }
     };
-    constexpr int Q = TF / 8;  // threads per token
-    const int live = min(p.nt, p.M - t0), feats = min(TF, p.N - f0), end = f0 + feats;
-    const int n = live * Q, round = splits * G::THREADS, e0 = part * G::THREADS + threadIdx.x;
-    static_assert(G::THREADS % Q == 0, "a thread keeps its features from round to round");
-    const int f = 8 * (e0 % Q), col = f0 + f;
-    float ws[8], ws2[8], bias[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = f + j < feats;
-      ws[j] = in ? p.w_scale[col + j] : 0.f;
-      ws2[j] = GATED && in ? p.w2_scale[col + j] : 0.f;
-      bias[j] = !GATED && in && p.bias != nullptr ? to_f32<T>(static_cast<const T *>(p.bias)[col + j]) : 0.f;
-    }
     // whole warps go round together: their stores put blocks together
 #pragma unroll 1
     for (int e = e0; e - lane < n; e += round) {
@@ -317,9 +339,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
       const int64_t row = t0 + t;
       float a[8], b[8];
       uint32_t i0[4], w0[4], w1[4], w2[4];
-      const T *res = static_cast<const T *>(p.in0) + row * p.ldi0;
+      const Inputs now = ahead;
+      ahead = fetch(e + round);
       if (in) {
-        const float ts = p.t_scale[row];
+        const float ts = now.ts;
         sum8(t, f, a);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = scaled(a[j], ts, ws[j]) + bias[j];
@@ -337,18 +360,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
             for (int j = 0; j < 8; ++j) a[j] = act_f32<ACT>(a[j]) * b[j];
           });
           float4 *h = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * p.ldo + col);
+          if (aborted) break;  // the same for the whole cluster
           h[0] = make_float4(a[0], a[1], a[2], a[3]);
           h[1] = make_float4(a[4], a[5], a[6], a[7]);
         }
       } else {
-        const bool has_in0 = p.in0 != nullptr;
+        const bool has_in0 = in0 != nullptr;
         if (in) {
           if (has_in0) {
-            const uint4 x = load_row16<T, AL>(res, col, end);
+            const uint4 x = take_row16<T, AL>(now.res, in0 + row * p.ldi0, col, end);
             i0[0] = x.x, i0[1] = x.y, i0[2] = x.z, i0[3] = x.w;
           }
           epilogue_row<Epi::kLinear, T, 4>(p.act, has_in0, false, a, a, i0, i0, w0, w1, w2);
         }
+        if (aborted) break;
         const uint4 v[1] = {make_uint4(w0[0], w0[1], w0[2], w0[3])};
         store_row16<T, AL, 1, Q>(static_cast<T *>(p.out) + row * p.ldo, in ? col : end, end, v);
       }
@@ -359,9 +384,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
       if (!mbar_wait(full_bar(i % p.stages), (uint32_t)(i / p.stages) & 1u))
         atomicCAS(p.watchdog, 0, kSite5ProducerDrain);
   }
-  if constexpr (SPLIT) {
+  if constexpr (SPLIT) {  // no CTA leaves while a peer may still read its partial
     __syncwarp();
-    cluster_sync();  // no CTA leaves while a peer may still read its partial
+    cluster_arrive_relaxed();
+    cluster_wait();
   }
   tc_fence_before();
   __syncthreads();

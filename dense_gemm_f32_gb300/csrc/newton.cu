@@ -33,6 +33,7 @@
 //    steps first at m = 64: 0.004 to 0.014; all five in one group overflows).
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "activation.cuh"
@@ -216,6 +217,42 @@ struct Work {
   }
 };
 
+// DGEMM_NEWTON_*: an environment variable's value in lo .. hi, or -1 (read at
+// every launch, for tests and tuning).
+int knob(const char *name, int lo, int hi) {
+  const char *e = getenv(name);
+  if (e == nullptr || e[0] < '0' || e[0] > '9') return -1;
+  const int v = atoi(e);
+  return v >= lo && v <= hi ? v : -1;
+}
+
+// The quicker kernel and K split by time models (microseconds; graph replays on
+// GB300).  Small kernel: 3.6 us of launch, first load, and epilogue, 0.37 us for a
+// CTA's stage of 64 k or its share where two run on an SM, 2.6 us for joining the
+// parts of a K split.  Pair kernel: 5.5 us, and 0.31 us per 64 k of a wave of 256 x
+// 256 tiles.
+cudaError_t run(const NewtonGemm &p, int num_sms, int *wd, cudaStream_t stream) {
+  const int f_pair = knob("DGEMM_NEWTON_PAIR", 0, 1), f_splits = knob("DGEMM_NEWTON_SPLITS", 1, 8);
+  auto tiles_of = [&](int t) {
+    const int64_t tm = (p.M + t - 1) / t, tn = (p.N + t - 1) / t;
+    return p.symmetric ? tm * (tm + 1) / 2 * (p.A2 != nullptr ? 2 : 1) : tm * tn;
+  };
+  const int64_t small = tiles_of(128), large = tiles_of(256), kblocks = (p.K + 63) / 64;
+  const int64_t waves = (large + num_sms / 2 - 1) / (num_sms / 2);
+  const double pair_time = 5.5 + 0.31 * (double)(waves * kblocks);
+  double best = 0;
+  int splits = 1;
+  for (int s = 1; s <= 8; s *= 2) {
+    const int64_t ctas = small * s, per = (kblocks + s - 1) / s;
+    const int64_t rounds = (ctas + num_sms - 1) / num_sms;
+    const double t = 3.6 + (s > 1 ? 2.6 : 0.) + 0.37 * (double)(per * rounds);
+    if (s == 1 || t < best) best = t, splits = s;
+  }
+  if (f_splits >= 0) splits = f_splits;
+  const bool pair = f_pair >= 0 ? f_pair == 1 : pair_time < best;
+  return pair ? launch_newton_pair(p, wd, stream) : launch_newton_small(p, splits, num_sms, wd, stream);
+}
+
 // Steps of the group that begins at step k.  (At m = n a step costs the same in a
 // group as alone, and the result is nearer.)
 int group_steps(const Orthogonalize &p, int k) {
@@ -279,7 +316,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
       g.alpha = m_up / (x_up * x_up);
       if (k == 0) g.factor = w.factor, g.power = 2;
       g.out = A, g.ldo = g.out_cols = ldm;
-      e = launch_newton_pair(g, wd, stream);
+      e = run(g, num_sms, wd, stream);
     }
     auto square = [&](const __half *left, const __half *right, __half *out, float alpha) {
       NewtonGemm g;
@@ -295,12 +332,12 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
       __half *poly = i == 0 ? spare[0] : P;
       NewtonGemm g = square(A, A, poly, c[2]);  // P = a I + b A + c A^2
       g.in0 = A, g.ldi0 = ldm, g.beta = c[1], g.gamma = c[0] * m_up;
-      e = launch_newton_pair(g, wd, stream);
+      e = run(g, num_sms, wd, stream);
       const bool more = i + 1 < steps;
       if (e == cudaSuccess && (more || i > 0)) {  // W = A P and Q = Q P, together where both are wanted
         NewtonGemm h = more ? square(A, poly, W, 1.f) : square(Q, poly, spare[1], 1.f);
         if (more && i > 0) h.A2 = Q, h.out2 = spare[1];
-        e = launch_newton_pair(h, wd, stream);
+        e = run(h, num_sms, wd, stream);
       }
       if (i == 0) {
         Q = poly;  // spare[0]
@@ -309,7 +346,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
         Q = spare[1];
         spare[1] = old;
       }
-      if (e == cudaSuccess && more) e = launch_newton_pair(square(W, poly, A, 1.f), wd, stream);
+      if (e == cudaSuccess && more) e = run(square(W, poly, A, 1.f), num_sms, wd, stream);
     }
     if (e != cudaSuccess) break;
     {  // X = Q X, or X Q
@@ -330,7 +367,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
         g.alpha = 1.f / m_up;
         g.out = x_next, g.ldo = g.out_cols = ldx;
       }
-      e = launch_newton_pair(g, wd, stream);
+      e = run(g, num_sms, wd, stream);
     }
     __half *t = x;
     x = x_next, x_next = t;

@@ -284,52 +284,56 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------- MMA (even CTA only)
-    if (lane == 0 && leader) {
+    // The whole warp goes through the loop, so that one elected lane issues the MMAs
+    // from uniform registers.
+    if (leader) {
+      auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        const bool got = !*abort_flag && mbar_wait(bar, parity);
+        if (!got && lane == 0 && !*abort_flag) watchdog_trip(p.watchdog, site, abort_flag);
+        return __all_sync(0xffffffffu, got) != 0;
+      };
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
       if (p.stall && cluster == 0) {  // test hook: a wait that runs out
-        if (!mbar_wait(stall_bar, 0)) watchdog_trip(p.watchdog, kSite6TestStall, abort_flag);
+        wait(stall_bar, 0, kSite6TestStall);
         ok = false;
       }
       for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
-        if (*abort_flag || !mbar_wait(acce_bar(acc), acc_phase ^ 1u)) {
-          if (!*abort_flag) watchdog_trip(p.watchdog, kSite6MmaAccEmpty, abort_flag);
-          ok = false;
-          break;
-        }
+        if (!wait(acce_bar(acc), acc_phase ^ 1u, kSite6MmaAccEmpty)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * G::BN);
         for (int kb = 0; kb < kblocks; ++kb) {
-          const bool got = mbar_try_wait(full_bar(stage), phase) ||
-                           (!*abort_flag && mbar_wait(full_bar(stage), phase));
-          if (!got) {
-            if (!*abort_flag) watchdog_trip(p.watchdog, kSite6MmaFull, abort_flag);
-            ok = false;
-            break;
-          }
+          ok = wait(full_bar(stage), phase, kSite6MmaFull);
+          if (!ok) break;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < G::KSTEPS; ++k)
-            umma_f16_pair(d_tmem, operand_desc<G, kAT>(a_tile(stage), k, G::A_BOX_BYTES),
-                          operand_desc<G, !kBT>(b_tile(stage), k, G::B_BOX_BYTES), G::IDESC,
-                          (kb > 0 || k > 0) ? 1u : 0u);
-          umma_commit_pair(empty_bar(stage), 0x3);  // frees the stage in both CTAs
+            for (int k = 0; k < G::KSTEPS; ++k)
+              umma_f16_pair(d_tmem, operand_desc<G, kAT>(a_tile(stage), k, G::A_BOX_BYTES),
+                            operand_desc<G, !kBT>(b_tile(stage), k, G::B_BOX_BYTES), G::IDESC,
+                            (kb > 0 || k > 0) ? 1u : 0u);
+            umma_commit_pair(empty_bar(stage), 0x3);  // frees the stage in both CTAs
+          }
+          __syncwarp();
           if (++stage == G::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair(accf_bar(acc), 0x3);  // accumulator ready in both CTAs
+        if (elect_one()) umma_commit_pair(accf_bar(acc), 0x3);  // accumulator ready in both CTAs
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      umma_commit_pair(drain_bar, 0x1);
+      if (elect_one()) umma_commit_pair(drain_bar, 0x1);
+      __syncwarp();
       if (!mbar_wait(drain_bar, 0)) atomicCAS(p.watchdog, 0, kSite6MmaDrain);
       // Tail: both accumulators released by both epilogues.
       for (int i = 0; i < 2; ++i) {

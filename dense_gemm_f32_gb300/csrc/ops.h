@@ -156,9 +156,11 @@ cudaError_t launch_layer_norm_backward(int dtype, int rows, int cols, const void
 // Rows of X as integers (quant.cu): Q in 8 bits, or T in fp16 with rows of whole
 // 16-byte vectors (ldt a multiple of 8), and a scale for each row.
 cudaError_t launch_quantize_rows(int dtype, int rows, int cols, const void *X, int64_t ldx,
-                                 int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream);
+                                 int8_t *Q, int64_t ldq, float *scale, int num_sms,
+                                 cudaStream_t stream);
 cudaError_t launch_quantize_tokens(int dtype, int rows, int cols, const void *X, int64_t ldx,
-                                   void *T, int64_t ldt, float *scale, cudaStream_t stream);
+                                   void *T, int64_t ldt, float *scale, int num_sms,
+                                   cudaStream_t stream);
 // T = X, integers already.
 cudaError_t launch_expand_tokens(int rows, int cols, const int8_t *X, int64_t ldx, void *T,
                                  int64_t ldt, int num_sms, cudaStream_t stream);
@@ -222,6 +224,9 @@ struct NewtonGemm {
   int64_t out_cols = 0;
 };
 cudaError_t launch_newton_pair(const NewtonGemm &p, int *watchdog, cudaStream_t stream);
+// The same on 128 x 128 tiles, the K range of each shared by `splits` (1, 2, 4 or 8) CTAs.
+cudaError_t launch_newton_small(const NewtonGemm &p, int splits, int num_sms, int *watchdog,
+                                cudaStream_t stream);
 
 // X in fp16 (rows of `ldt`, a multiple of 8) as X 2^(8 - e), and *factor = 2^e /
 // (norm + eps), where 2^e is the power of two next above norm + eps, norm the root of the

@@ -450,7 +450,7 @@ int dgemm_quantize_int8(int dtype, int op, int rows, int cols, const void *X, in
   const int st = check_args(a, 3, -1, -1, &dev, &sms);
   if (st != DGEMM_OK) return st;
   if (!t)
-    return done(launch_quantize_rows(dtype, rows, cols, X, ldx, Q, ldq, scale, stream),
+    return done(launch_quantize_rows(dtype, rows, cols, X, ldx, Q, ldq, scale, sms, stream),
                 "quantisation launch");
   return with_scratch((size_t)cols * 4, stream, "quantisation launch", [&](float *tops) {
     return launch_quantize_columns(dtype, rows, cols, X, ldx, Q, ldq, scale,
@@ -495,7 +495,8 @@ int dgemm_linear_int8(int dtype, int activation, int M, int N, int K, const void
   stage.add(p.W, p.ldw, N, K);
   if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
   if (!x_scale)
-    st = done(launch_quantize_tokens(dtype, M, K, X, ldx, work, p.ldt, scale, stream), "token launch");
+    st = done(launch_quantize_tokens(dtype, M, K, X, ldx, work, p.ldt, scale, sms, stream),
+              "token launch");
   else if (K > 0)
     st = done(launch_expand_tokens(M, K, static_cast<const int8_t *>(X), ldx, work, p.ldt, sms, stream),
               "token launch");
@@ -543,7 +544,8 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
   stage.add(wd, ld, D, F);
   if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
   if (F > 0) {
-    st = done(launch_quantize_tokens(dtype, M, D, X, ldx, tokens, pitch8(D), scale, stream), "token launch");
+    st = done(launch_quantize_tokens(dtype, M, D, X, ldx, tokens, pitch8(D), scale, sms, stream),
+              "token launch");
     Int8Gemm p;
     p.gated = true, p.dtype = dtype, p.act = activation;
     p.M = M, p.N = F, p.K = D;
@@ -554,7 +556,8 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
     if (st == DGEMM_OK) st = done(launch_int8(p, sms, stream), "gated integer product launch");
   }
   if (st == DGEMM_OK)
-    st = done(launch_quantize_tokens(DGEMM_DTYPE_F32, M, F, h, pitch8(F), tokens, pitch8(F), scale, stream),
+    st = done(launch_quantize_tokens(DGEMM_DTYPE_F32, M, F, h, pitch8(F), tokens, pitch8(F), scale, sms,
+                                     stream),
               "token launch");
   if (st == DGEMM_OK) {
     Int8Gemm p;

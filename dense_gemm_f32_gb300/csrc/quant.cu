@@ -164,19 +164,20 @@ __global__ void __launch_bounds__(THREADS)
 
 template <class T, class O>
 cudaError_t launch_rows(int rows, int cols, const void *X, int64_t ldx, O *Q, int64_t ldq,
-                        float *scale, cudaStream_t stream) {
+                        float *scale, int num_sms, cudaStream_t stream) {
   const bool al = rows_aligned(X, ldx, sizeof(T)) && cols % kVec<T> == 0;
   const bool vec = reinterpret_cast<uintptr_t>(Q) % kVec<T> == 0 && ldq % kVec<T> == 0;
-  // a row's threads: as many as hold it, up to 512; a block of 1024 for the few long rows of a
-  // decoding step would hold more, but a second vector per thread costs less than the wider join
+  // few rows, as in a decoding step: a thread per vector up to 512, for the shortest
+  // chain; else threads that hold four each
   const int vecs = (cols + kVec<T> - 1) / kVec<T>;
+  const bool few = rows <= 2 * num_sms;
   auto go = [&](auto kern, int threads) {
     const cudaError_t e = launch_kernel(kern, dim3((unsigned)rows), dim3(threads), 0, stream, 1u, cols,
                                         static_cast<const T *>(X), ldx, Q, ldq, scale, vec);
     if (e == cudaSuccess) count_launch();
     return e;
   };
-  if (vecs <= 128 * kHeld)
+  if (vecs <= (few ? 128 : 128 * kHeld))
     return al ? go(quantize_rows_kernel<T, O, true, 128>, 128)
               : go(quantize_rows_kernel<T, O, false, 128>, 128);
   return al ? go(quantize_rows_kernel<T, O, true, 512>, 512)
@@ -308,21 +309,23 @@ cudaError_t launch_columns(int rows, int cols, const void *X, int64_t ldx, int8_
 }  // namespace
 
 cudaError_t launch_quantize_rows(int dtype, int rows, int cols, const void *X, int64_t ldx,
-                                 int8_t *Q, int64_t ldq, float *scale, cudaStream_t stream) {
+                                 int8_t *Q, int64_t ldq, float *scale, int num_sms,
+                                 cudaStream_t stream) {
   switch (dtype) {
-    case DGEMM_DTYPE_F32: return launch_rows<float>(rows, cols, X, ldx, Q, ldq, scale, stream);
-    case DGEMM_DTYPE_BF16: return launch_rows<__nv_bfloat16>(rows, cols, X, ldx, Q, ldq, scale, stream);
-    default: return launch_rows<__half>(rows, cols, X, ldx, Q, ldq, scale, stream);
+    case DGEMM_DTYPE_F32: return launch_rows<float>(rows, cols, X, ldx, Q, ldq, scale, num_sms, stream);
+    case DGEMM_DTYPE_BF16: return launch_rows<__nv_bfloat16>(rows, cols, X, ldx, Q, ldq, scale, num_sms, stream);
+    default: return launch_rows<__half>(rows, cols, X, ldx, Q, ldq, scale, num_sms, stream);
   }
 }
 
 cudaError_t launch_quantize_tokens(int dtype, int rows, int cols, const void *X, int64_t ldx,
-                                   void *T, int64_t ldt, float *scale, cudaStream_t stream) {
+                                   void *T, int64_t ldt, float *scale, int num_sms,
+                                   cudaStream_t stream) {
   __half *t = static_cast<__half *>(T);
   switch (dtype) {
-    case DGEMM_DTYPE_F32: return launch_rows<float>(rows, cols, X, ldx, t, ldt, scale, stream);
-    case DGEMM_DTYPE_BF16: return launch_rows<__nv_bfloat16>(rows, cols, X, ldx, t, ldt, scale, stream);
-    default: return launch_rows<__half>(rows, cols, X, ldx, t, ldt, scale, stream);
+    case DGEMM_DTYPE_F32: return launch_rows<float>(rows, cols, X, ldx, t, ldt, scale, num_sms, stream);
+    case DGEMM_DTYPE_BF16: return launch_rows<__nv_bfloat16>(rows, cols, X, ldx, t, ldt, scale, num_sms, stream);
+    default: return launch_rows<__half>(rows, cols, X, ldx, t, ldt, scale, num_sms, stream);
   }
 }
 

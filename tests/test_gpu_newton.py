@@ -64,6 +64,19 @@ def test_coefficients_of_each_step(rows, cols):
     nr.check(dg.orthogonalize(x, steps=3, coefficients=[0.0, 0.0, 0.0]), x, 3, (0.0, 0.0, 0.0))
 
 
+@pytest.mark.parametrize("plan", [dict(PAIR=1), dict(PAIR=0, SPLITS=1), dict(PAIR=0, SPLITS=2), dict(PAIR=0, SPLITS=4),
+                                  dict(PAIR=0, SPLITS=8)], ids=str)
+@pytest.mark.parametrize("rows, cols", [(40, 60), (260, 700), (700, 260), (530, 520), (513, 1030)])
+def test_every_kernel_and_cut(rows, cols, plan, monkeypatch):
+    for k, v in plan.items():
+        monkeypatch.setenv("DGEMM_NEWTON_" + k, str(v))
+    for x_type, w_type in ((torch.bfloat16, torch.float32), (torch.float16, torch.float16)):
+        x, w = _gradient(rows, cols, x_type, 1), ref.make(2)((rows, cols), w_type, rows ** -0.5)
+        got = dg.orthogonalize(x, scale=-0.02, residual=w, residual_scale=0.998)
+        nr.check(got, x, scale=-0.02, residual=w, keep=0.998)
+        assert torch.equal(dg.orthogonalize(x, scale=-0.02, residual=w, residual_scale=0.998), got)
+
+
 @pytest.mark.parametrize("x_type", TYPES, ids=str)
 @pytest.mark.parametrize("w_type", TYPES, ids=str)
 @pytest.mark.parametrize("rows, cols", [(130, 520), (520, 130), (300, 1001)])
