@@ -43,15 +43,19 @@ struct Cfg {
   static constexpr int A_BOXES = kAT ? HM / BOX : 1, B_BOXES = kBT ? 1 : HN / BOX;
   static constexpr int A_BOX_BYTES = kAT ? BK * 128 : A_BYTES;
   static constexpr int B_BOX_BYTES = kBT ? B_BYTES : BK * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, STAGES = 6;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, MAX_STAGES = 6;
   static constexpr int TMEM_COLS = 512;
   static constexpr int kEpiWarps = 8, kProdBWarp = 2 + kEpiWarps;
   static constexpr int THREADS = 32 * (3 + kEpiWarps);
-  static constexpr int NUM_BARS = 2 * STAGES + 6;  // full, empty, accf[2], acce[2], drain, stall
+  // full, empty, accf[2], acce[2], drain, stall, two per epilogue warp
+  static constexpr int NUM_BARS = 2 * MAX_STAGES + 6 + 2 * kEpiWarps;
   static constexpr int PIECE_BYTES = 32 * 64;      // 32 rows of 64 bytes
   static constexpr int EPI_BYTES = kEpiWarps * 2 * PIECE_BYTES;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + NUM_BARS * 8 + 16 + 1024;
-  static_assert(SMEM_BYTES <= 232448, "fits the 227 KB opt-in shared memory of a CTA");
+  static constexpr int TAIL_BYTES = NUM_BARS * 8 + 16 + 1024;
+  // in0's pieces, 4 KB for a warp, take a stage's place
+  static constexpr int SMEM_BYTES = MAX_STAGES * STAGE_BYTES + EPI_BYTES + TAIL_BYTES;
+  static_assert(SMEM_BYTES <= 232448 && kEpiWarps * 4096 <= STAGE_BYTES,
+                "fits the 227 KB opt-in shared memory of a CTA");
   static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
   static constexpr uint32_t IDESC = (1u << 4) | ((kAT ? 1u : 0u) << 15) | ((kBT ? 0u : 1u) << 16) |
                                     ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
@@ -66,18 +70,20 @@ enum : int {
   kSite6MmaDrain = 0xe5,
   kSite6MmaTail = 0xe6,
   kSite6EpiAccFull = 0xe7,
+  kSite6EpiInput = 0xe9,
   kSite6TestStall = 0xe8,  // DGEMM_TC_TEST_STALL: the MMA thread's test wait ran out
 };
 
 struct Maps {
-  CUtensorMap a, a2, b, o[2];
+  CUtensorMap a, a2, b, o[2], in;
 };
 
 struct Args {
   int M, N, K;
   int group_m, mn3d, stall, products;
   int o_tma;  // outputs may be written by TMA
-  int in_vec;
+  int in_vec, in_tma;  // rows of in0 are aligned; it may be read by TMA
+  int stages;
   float alpha, beta, gamma;
   const float *factor;
   int power;
@@ -138,6 +144,15 @@ __device__ __forceinline__ void load_piece(const O *row, int col, int cols, bool
   }
 }
 
+// Row `lane` of a 32 x 64-byte piece that TMA loaded (64-byte swizzle).
+__device__ __forceinline__ void take_piece(const uint8_t *piece, int lane, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(piece + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+    w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+  }
+}
+
 // A staged piece written element by element, a row per instruction: pieces that TMA may not write.
 template <class O>
 __device__ __noinline__ void store_piece(const uint8_t *piece, O *out, int64_t ld, int rows, int valid,
@@ -161,15 +176,16 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw_base);
-  const uint32_t epi_base = base + G::STAGES * G::STAGE_BYTES;
+  const uint32_t epi_base = base + G::MAX_STAGES * G::STAGE_BYTES;
   const uint32_t bars = epi_base + G::EPI_BYTES;
   auto full_bar = [&](int s) { return bars + 8u * s; };
-  auto empty_bar = [&](int s) { return bars + 8u * (G::STAGES + s); };
-  auto accf_bar = [&](int b) { return bars + 8u * (2 * G::STAGES + b); };
-  auto acce_bar = [&](int b) { return bars + 8u * (2 * G::STAGES + 2 + b); };
-  const uint32_t drain_bar = bars + 8u * (2 * G::STAGES + 4);
-  const uint32_t stall_bar = bars + 8u * (2 * G::STAGES + 5);  // nothing ever arrives here
-  uint8_t *tail = smem + G::STAGES * G::STAGE_BYTES + G::EPI_BYTES + G::NUM_BARS * 8;
+  auto empty_bar = [&](int s) { return bars + 8u * (G::MAX_STAGES + s); };
+  auto accf_bar = [&](int b) { return bars + 8u * (2 * G::MAX_STAGES + b); };
+  auto acce_bar = [&](int b) { return bars + 8u * (2 * G::MAX_STAGES + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (2 * G::MAX_STAGES + 4);
+  const uint32_t stall_bar = bars + 8u * (2 * G::MAX_STAGES + 5);  // nothing ever arrives here
+  auto in_bar = [&](int i) { return bars + 8u * (2 * G::MAX_STAGES + 6 + i); };
+  uint8_t *tail = smem + G::MAX_STAGES * G::STAGE_BYTES + G::EPI_BYTES + G::NUM_BARS * 8;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
   auto a_tile = [&](int s) { return base + (uint32_t)(s * G::STAGE_BYTES); };
@@ -191,7 +207,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
   };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < G::STAGES; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(full_bar(s), 2);  // one arrival per producer thread
       mbar_init(empty_bar(s), 1);
     }
@@ -201,6 +217,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     mbar_init(stall_bar, 1);
+    for (int i = 0; i < 2 * G::kEpiWarps; ++i) mbar_init(in_bar(i), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -263,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
             }
           }
           if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
-          if (++stage == G::STAGES) {
+          if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -271,12 +288,12 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
       }
       // Tail: every stage-free signal aimed at this CTA has landed, and no
       // copy is still writing its shared memory.
-      for (int i = 0; i < G::STAGES; ++i) {
+      for (int i = 0; i < p.stages; ++i) {
         if (!mbar_wait(empty_bar(stage), phase ^ 1u)) {
           atomicCAS(p.watchdog, 0, kSite6ProducerTail);
           break;
         }
-        if (++stage == G::STAGES) {
+        if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -319,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
             umma_commit_pair(empty_bar(stage), 0x3);  // frees the stage in both CTAs
           }
           __syncwarp();
-          if (++stage == G::STAGES) {
+          if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -363,8 +380,44 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
     int stores = 0;  // pieces staged by this warp
     int acc = 0;
     uint32_t acc_phase = 0;
+    // in0 comes by TMA where its rows are aligned, IN_AHEAD pieces of 32 x 32 ahead of
+    // the epilogue.  (A row per thread read directly is 32 lines of memory for an
+    // instruction.)  in_tile, in_c0: the next piece to send for, `sent` how many were.
+    constexpr int IN_BYTES = 32 * 32 * (int)sizeof(O), IN_AHEAD = 4096 / IN_BYTES;
+    const uint32_t in_buf = base + (uint32_t)(p.stages * G::STAGE_BYTES + (warp - 2) * 4096);
+    int in_tile = cluster, in_c0 = 32 * half, sent = 0, taken = 0;
+    auto send_for_input = [&] {
+      while (in_tile < num_tiles && !(SYM && in_tile >= tiles1)) {
+        int tm, tn;
+        coords(in_tile, tm, tn);
+        const int r0 = tm * G::BM + (int)rank * G::HM + quarter * 32;
+        while (SYM && in_c0 < G::BN && tn * G::BN + in_c0 < r0) in_c0 += 64;  // below the diagonal
+        const int col = tn * G::BN + in_c0;
+        if (in_c0 >= G::BN || col >= p.N || r0 >= p.M) {
+          in_tile += clusters, in_c0 = 32 * half;
+          continue;
+        }
+        const int slot = sent % IN_AHEAD;
+        const uint32_t bar = in_bar(2 * (warp - 2) + slot), to = in_buf + (uint32_t)(slot * IN_BYTES);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, IN_BYTES);
+          for (int h = 0; h < 32 / C; ++h)
+            tma_load_2d(to + (uint32_t)(h * G::PIECE_BYTES), &maps.in, bar, col + h * C, r0);
+        }
+        ++sent;
+        in_c0 += 64;
+        return;
+      }
+    };
+    if (p.in_tma)
+      for (int i = 0; i < IN_AHEAD; ++i) send_for_input();
+    // After the last tile's products the stages are idle: its pieces are staged there, each in
+    // a place of its own, and none waits for a store.
+    int idle = -1;
     // The next of this warp's two pieces, free to be written.
     auto next_piece = [&] {
+      if (idle >= 0)
+        return base + (uint32_t)((warp - 2) * (4 * (32 / C) * (SYM ? 2 : 1)) + idle++) * (uint32_t)G::PIECE_BYTES;
       if (lane == 0 && stores >= 2) bulk_wait_group_read<1>();  // the store two pieces ago
       __syncwarp();
       return slots + (uint32_t)((stores & 1) * G::PIECE_BYTES);
@@ -394,6 +447,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
       if (!ok && lane == 0 && !*abort_flag) watchdog_trip(p.watchdog, kSite6EpiAccFull, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      if (tile + clusters >= num_tiles) idle = 0;
       const int row0 = tm * G::BM + (int)rank * G::HM + quarter * 32;  // the warp's first row
       const int row = row0 + lane;
       const uint32_t t_row =
@@ -410,11 +464,26 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(r[j]);
         if (p.in0 != nullptr && o == 0) {
+          const int slot = taken % IN_AHEAD;
+          if (p.in_tma) {
+            const uint32_t bar = in_bar(2 * (warp - 2) + slot), phase = (uint32_t)(taken / IN_AHEAD) & 1u;
+            bool got = __all_sync(0xffffffffu, mbar_try_wait(bar, phase));
+            if (!got) {
+              got = !*abort_flag && mbar_wait(bar, phase);
+              if (!got && lane == 0 && !*abort_flag) watchdog_trip(p.watchdog, kSite6EpiInput, abort_flag);
+              // nothing more is sent for: the copies in flight are waited for at the end
+              if (!__all_sync(0xffffffffu, got)) break;
+            }
+            ++taken;
+          }
           const O *in = static_cast<const O *>(p.in0) + (int64_t)row * p.ldi0;
 #pragma unroll
           for (int h = 0; h < 32 / C; ++h) {
             uint32_t w[16];
-            load_piece<O>(in, col + h * C, row < p.M ? p.N : 0, p.in_vec, w);
+            if (p.in_tma)
+              take_piece(smem + (in_buf - base) + slot * IN_BYTES + h * G::PIECE_BYTES, lane, w);
+            else
+              load_piece<O>(in, col + h * C, row < p.M ? p.N : 0, p.in_vec, w);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               if constexpr (sizeof(O) == 2) {
@@ -424,6 +493,10 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
                 v[h * C + j] += p.beta * __uint_as_float(w[j]);
               }
             }
+          }
+          if (p.in_tma) {
+            __syncwarp();
+            send_for_input();
           }
         }
         if (SYM && o == 0 && p.gamma != 0.f && col < row0 + 32 && row0 < col + 32) {
@@ -480,7 +553,11 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
         acc_phase ^= 1u;
       }
     }
-    if (lane == 0) bulk_wait_group<0>();  // every TMA store of this warp complete
+    if (lane == 0) {
+      bulk_wait_group<0>();  // every TMA store of this warp complete
+      for (; taken < sent; ++taken)  // after an abort: its inputs have landed
+        mbar_wait(in_bar(2 * (warp - 2) + taken % IN_AHEAD), (uint32_t)(taken / IN_AHEAD) & 1u);
+    }
     __syncwarp();
   }
 
@@ -537,6 +614,10 @@ cudaError_t launch(const NewtonGemm &p, int *watchdog, cudaStream_t stream) {
   a.factor = p.factor, a.power = p.power;
   a.in0 = p.in0, a.ldi0 = p.ldi0;
   a.in_vec = rows_aligned(p.in0, p.ldi0, sizeof(O));
+  a.in_tma = p.in0 != nullptr && a.in_vec &&
+             make_map(&maps.in, p.in0, map_type<O>(), sizeof(O), p.M, p.N, p.ldi0, kPieceCols<O>, 32,
+                      CU_TENSOR_MAP_SWIZZLE_64B);
+  a.stages = a.in_tma ? G::MAX_STAGES - 1 : G::MAX_STAGES;
   a.out[0] = p.out, a.out[1] = p.out2;
   a.ldo = p.ldo, a.out_cols = (int)p.out_cols;
   a.o_tma = rows_aligned(p.out, p.ldo, sizeof(O)) && rows_aligned(p.out2, p.ldo, sizeof(O));
