@@ -180,24 +180,22 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
       const int early = min(blocks, p.stages);
       for (int i = 0; i < early; ++i) weights(i, (kb_begin + i) * G::BK);
       pdl_wait();  // the tokens are there
-      int issued = 0;
+      int issued = 0, s = 0;
+      uint32_t phase = 1;  // a fresh barrier's phase before is complete
       bool ok = true;
       for (int i = 0; i < blocks; ++i) {
-        const int s = i % p.stages, round = i / p.stages;
         const int k0 = (kb_begin + i) * G::BK;
-        if (round > 0) {
-          if (!mbar_try_wait(empty_bar(s), (uint32_t)(round - 1) & 1u) &&
-              (*abort_flag || !mbar_wait(empty_bar(s), (uint32_t)(round - 1) & 1u))) {
-            if (!*abort_flag) watchdog_trip(p.watchdog, kSite5ProducerEmpty, abort_flag);
-            ok = false;
-            break;
-          }
-          weights(s, k0);
+        if (!mbar_try_wait(empty_bar(s), phase) && (*abort_flag || !mbar_wait(empty_bar(s), phase))) {
+          if (!*abort_flag) watchdog_trip(p.watchdog, kSite5ProducerEmpty, abort_flag);
+          ok = false;
+          break;
         }
+        if (i >= early) weights(s, k0);
         tma_load_2d(t_tile(s), &maps.t, full_bar(s), k0, t0);
         tma_load_2d(t_tile(s) + t_bytes / 2, &maps.t, full_bar(s), k0 + 64, t0);
         mbar_arrive_expect_tx(full_bar(s), stage_bytes);  // announced after the copies are issued
         ++issued;
+        if (++s == p.stages) s = 0, phase ^= 1u;
       }
       all_sent = ok;
       if (!ok) {  // no TMA write lands after this CTA has left

@@ -191,7 +191,6 @@ cudaError_t launch_scale(int rows, int cols, const void *X, int64_t ldx, float e
 }
 
 // -------------------------------------------------------------- the iteration
-int64_t pitch8(int64_t cols) { return (cols + 7) / 8 * 8; }
 int64_t round256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // X, the next X, five m x m matrices, the factor and the partial sums (up to 512 SMs' worth).
@@ -201,7 +200,7 @@ struct Work {
   size_t bytes;
   Work(void *base, int rows, int cols) {
     const int64_t m = rows < cols ? rows : cols;
-    const int64_t x_bytes = round256((int64_t)rows * pitch8(cols) * 2), s_bytes = round256(m * pitch8(m) * 2);
+    const int64_t x_bytes = round256((int64_t)rows * line_pitch(cols, 2) * 2), s_bytes = round256(m * line_pitch(m, 2) * 2);
     const uintptr_t begin = reinterpret_cast<uintptr_t>(base);
     uintptr_t p = begin;
     auto take = [&](int64_t n) {
@@ -227,10 +226,10 @@ int knob(const char *name, int lo, int hi) {
 }
 
 // The quicker kernel and K split by time models (microseconds; graph replays on
-// GB300).  Small kernel: 3.6 us of launch, first load, and epilogue, 0.37 us for a
-// CTA's stage of 64 k or its share where two run on an SM, 2.6 us for joining the
-// parts of a K split.  Pair kernel: 5.5 us, and 0.31 us per 64 k of a wave of 256 x
-// 256 tiles.
+// GB300).  Small kernel: 3.4 us of launch, first load and epilogue, 0.27 us for a
+// CTA's stage of 64 k or its share where two run on an SM, 5 to 6.5 us for joining the
+// parts of a K split.  Pair kernel: 8 us, and 0.28 us per 64 k of a wave of 256 x 256
+// tiles.
 cudaError_t run(const NewtonGemm &p, int num_sms, int *wd, cudaStream_t stream) {
   const int f_pair = knob("DGEMM_NEWTON_PAIR", 0, 1), f_splits = knob("DGEMM_NEWTON_SPLITS", 1, 8);
   auto tiles_of = [&](int t) {
@@ -239,13 +238,13 @@ cudaError_t run(const NewtonGemm &p, int num_sms, int *wd, cudaStream_t stream) 
   };
   const int64_t small = tiles_of(128), large = tiles_of(256), kblocks = (p.K + 63) / 64;
   const int64_t waves = (large + num_sms / 2 - 1) / (num_sms / 2);
-  const double pair_time = 5.5 + 0.31 * (double)(waves * kblocks);
+  const double pair_time = 8.0 + 0.28 * (double)(waves * kblocks);
   double best = 0;
   int splits = 1;
   for (int s = 1; s <= 8; s *= 2) {
     const int64_t ctas = small * s, per = (kblocks + s - 1) / s;
     const int64_t rounds = (ctas + num_sms - 1) / num_sms;
-    const double t = 3.6 + (s > 1 ? 2.6 : 0.) + 0.37 * (double)(per * rounds);
+    const double t = 3.4 + (s > 1 ? 4.5 + 0.25 * s : 0.) + 0.27 * (double)(per * rounds);
     if (s == 1 || t < best) best = t, splits = s;
   }
   if (f_splits >= 0) splits = f_splits;
@@ -298,7 +297,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
   Work w(work, p.rows, p.cols);
   const bool tall = p.rows > p.cols;
   const int m = tall ? p.cols : p.rows, n = tall ? p.rows : p.cols;
-  const int64_t ldx = pitch8(p.cols), ldm = pitch8(m);
+  const int64_t ldx = line_pitch(p.cols, 2), ldm = line_pitch(m, 2);
   cudaError_t e = launch_newton_scale(p.x_dtype, p.rows, p.cols, p.X, p.ldx, p.eps, w.x[0], ldx, w.factor,
                                       w.partial, num_sms, stream);
   const float x_up = 0x1p8f, m_up = 0x1p6f;  // what X and the m x m matrices are kept times

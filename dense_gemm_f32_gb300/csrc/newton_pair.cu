@@ -25,6 +25,7 @@
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "newton.cuh"
 #include "ops.h"
 #include "ptx.cuh"
 #include "tc_tile.cuh"
@@ -56,7 +57,7 @@ struct Cfg {
   static constexpr int SMEM_BYTES = MAX_STAGES * STAGE_BYTES + EPI_BYTES + TAIL_BYTES;
   static_assert(SMEM_BYTES <= 232448 && kEpiWarps * 4096 <= STAGE_BYTES,
                 "fits the 227 KB opt-in shared memory of a CTA");
-  static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
+  [[maybe_unused]] static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
   static constexpr uint32_t IDESC = (1u << 4) | ((kAT ? 1u : 0u) << 15) | ((kBT ? 0u : 1u) << 16) |
                                     ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 };
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
       return slots + (uint32_t)((stores & 1) * G::PIECE_BYTES);
     };
     auto send_piece = [&](int o, uint32_t buf, int row0, int col) {
+      if (idle >= 0) return;  // all together at the tile's end
       const int valid = min(C, p.out_cols - col);
       // TMA writes whole 16-byte granules: a piece that ends inside one goes
       // out element by element.
@@ -499,11 +501,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
             send_for_input();
           }
         }
-        if (SYM && o == 0 && p.gamma != 0.f && col < row0 + 32 && row0 < col + 32) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (col + j == row) v[j] += p.gamma;
-        }
+        if (SYM && o == 0 && col == row0) add_diagonal(v, lane, p.gamma);
 #pragma unroll
         for (int h = 0; h < 32 / C; ++h) {
           if (h > 0 && col + h * C >= p.N) break;
@@ -516,38 +514,51 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
               w[j] = __float_as_uint(v[h * C + j]);
           }
           uint32_t buf = next_piece();
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             buf + (uint32_t)(lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4))),
-                         "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
-                         : "memory");
-          // row j of the mirrored piece is this one's column j; from row `first` on
-          auto mirror = [&](uint32_t piece, int first) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j >= first)
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(
-                                 piece + (uint32_t)(j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) +
-                                                    ((lane & 7) << 1))),
-                             "h"((uint16_t)(w[j >> 1] >> (16 * (j & 1))))
-                             : "memory");
-          };
-          if (SYM && col == row0) {  // below the diagonal what is above it
-            __syncwarp();
-            mirror(buf, lane + 1);
+          if constexpr (SYM) {
+            if (col == row0) {  // below the diagonal what is above it
+              piece_store_turned(buf, lane, w);
+              piece_mirror(buf, lane, w);
+              __syncwarp();
+            }
           }
+          piece_store_row(buf, lane, w);
           send_piece(o, buf, row0, col + h * C);
-          if (SYM && col > row0) {  // the mirrored place
-            buf = next_piece();
-            mirror(buf, 0);
-            send_piece(o, buf, col, row0);
+          if constexpr (SYM) {
+            if (col > row0) {  // the mirrored place
+              buf = next_piece();
+              piece_store_turned(buf, lane, w);
+              send_piece(o, buf, col, row0);
+            }
+          }
+        }
+      }
+      if (idle > 0) {
+        // the last tile's pieces, in the order in which they were staged, after one fence
+        const int last = idle;
+        idle = -1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        uint32_t buf = base + (uint32_t)((warp - 2) * (4 * (32 / C) * (SYM ? 2 : 1))) * (uint32_t)G::PIECE_BYTES;
+        int n = 0;
+#pragma unroll 1
+        for (int c0 = 32 * half; c0 < G::BN; c0 += 64) {
+          const int col = tn * G::BN + c0;
+          if (col >= p.N || row0 >= p.M) break;
+          if (SYM && col < row0) continue;
+#pragma unroll 1
+          for (int h = 0; h < 32 / C && col + h * C < p.N && n < last; ++h) {
+            send_piece(o, buf, row0, col + h * C);
+            buf += G::PIECE_BYTES, ++n;
+            if (SYM && col > row0) {
+              send_piece(o, buf, col, row0);
+              buf += G::PIECE_BYTES, ++n;
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc ? acce_leader1 : acce_leader0);
+      if (lane == 0) mbar_arrive_cluster_tmem(acc ? acce_leader1 : acce_leader0);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;

@@ -20,6 +20,7 @@
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "newton.cuh"
 #include "ops.h"
 #include "ptx.cuh"
 #include "rowvec.cuh"
@@ -167,6 +168,8 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(o ? &maps.a2 : &maps.a);
     tma_prefetch_desc(&maps.b);
+    if (!SPLIT && p.o_tma) tma_prefetch_desc(&maps.o[o]);
+    if (!SPLIT && p.in_tma) tma_prefetch_desc(&maps.in);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), G::T);
@@ -221,12 +224,11 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const CUtensorMap *map_a = o ? &maps.a2 : &maps.a;
-      int issued = 0;
+      int issued = 0, s = 0;
+      uint32_t phase = 1;  // a fresh barrier's phase before is complete
       bool ok = true;
       for (int i = 0; i < blocks; ++i) {
-        const int s = i % p.stages, round = i / p.stages;
-        if (round > 0 && !mbar_try_wait(empty_bar(s), (uint32_t)(round - 1) & 1u) &&
-            (*abort_flag || !mbar_wait(empty_bar(s), (uint32_t)(round - 1) & 1u))) {
+        if (!mbar_try_wait(empty_bar(s), phase) && (*abort_flag || !mbar_wait(empty_bar(s), phase))) {
           if (!*abort_flag) watchdog_trip(p.watchdog, kSite8ProducerEmpty, abort_flag);
           ok = false;
           break;
@@ -247,6 +249,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
         }
         mbar_arrive_expect_tx(fb, G::STAGE_BYTES);  // announced after the copies are issued
         ++issued;
+        if (++s == p.stages) s = 0, phase ^= 1u;
       }
       all_sent = ok;
       if (!ok) {  // no TMA write lands after this CTA has left
@@ -263,9 +266,9 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
       if (!mbar_wait(stall_bar, 0) && lane == 0) watchdog_trip(p.watchdog, kSite8TestStall, abort_flag);
       ok = false;
     }
+    int s = 0;
+    uint32_t phase = 0;
     for (int i = 0; i < blocks && ok; ++i) {
-      const int s = i % p.stages;
-      const uint32_t phase = (uint32_t)(i / p.stages) & 1u;
       if (!__all_sync(0xffffffffu, mbar_try_wait(full_bar(s), phase))) {
         ok = !*abort_flag && mbar_wait(full_bar(s), phase);
         if (!ok && lane == 0 && !*abort_flag) watchdog_trip(p.watchdog, kSite8MmaFull, abort_flag);
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
         umma_commit(empty_bar(s));
       }
       __syncwarp();
+      if (++s == p.stages) s = 0, phase ^= 1u;
     }
     if (elect_one()) umma_commit(accf_bar);  // every MMA issued above has completed
     __syncwarp();
@@ -346,16 +350,14 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
         const O *src = in0 + (int64_t)r_first * p.ldi0 + c0;
         const int rows = c0 < p.N ? p.M - r_first : 0;
         uint8_t *dst = smem + (in_buf - base) + h * P::BYTES;
-#pragma unroll 8
-        for (int r = 0; r < 32; ++r)
-          *reinterpret_cast<O *>(dst + P::at(r, lane)) = r < rows ? src[r * p.ldi0] : from_f32<O>(0.f);
+        O x[32];  // all in flight
+#pragma unroll
+        for (int r = 0; r < 32; ++r) x[r] = r < rows ? src[r * p.ldi0] : from_f32<O>(0.f);
+#pragma unroll
+        for (int r = 0; r < 32; ++r) *reinterpret_cast<O *>(dst + P::at(r, lane)) = x[r];
       }
       __syncwarp();
     }
-    if (in_sent > 0) wait(in_bar(warp));
-    if (ok) wait(accf_bar);
-    ok = ok && !__any_sync(0xffffffffu, *abort_flag != 0);
-    tc_fence_after();
     // the stages are done with: two pieces for every two results
     uint8_t *buf = smem + warp * (SYM ? 4 : 2) * P::BYTES;
     // A staged piece to rows row0.. and columns col0.. of the result
@@ -376,6 +378,10 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
           if (r < rows) dst[r * p.ldo] = *reinterpret_cast<const O *>(piece + P::at(r, lane));
       }
     };
+    if (in_sent > 0) wait(in_bar(warp));
+    if (ok) wait(accf_bar);
+    ok = ok && !__any_sync(0xffffffffu, *abort_flag != 0);
+    tc_fence_after();
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       if (!ok || !wanted(h)) continue;  // the same for the whole warp
@@ -397,30 +403,24 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
         }
       }
       const bool cross = SYM && col0 == r_first;
-      if (cross && o == 0) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == lane) v[j] += p.gamma;
-      }
-#pragma unroll
-      for (int q = 0; q < P::PARTS; ++q)
-        *reinterpret_cast<uint4 *>(buf + P::part(lane, q)) = narrow16<O>(v + kVec<O> * q);
+      if (cross && o == 0) add_diagonal(v, lane, p.gamma);
       if constexpr (SYM) {
-        // Column j turned over: row j of the mirrored piece; on the diagonal of this one,
-        // below the diagonal.
-        uint8_t *turned = cross ? buf : buf + P::BYTES;
-        const int first = cross ? lane + 1 : 0;
-        __syncwarp();
+        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j >= first) *reinterpret_cast<O *>(turned + P::at(j, lane)) = from_f32<O>(v[j]);
+        for (int j = 0; j < 16; ++j) w[j] = pack2<O>(v[2 * j], v[2 * j + 1]);
+        const uint32_t turned = smem_u32(buf) + P::BYTES;
+        piece_store_turned(turned, lane, w);
+        if (cross) piece_mirror(turned, lane, w);
+        piece_store_row(smem_u32(buf), lane, w);
         send(buf, r_first, col0);
         if (!cross) send(buf + P::BYTES, col0, r_first);
-        buf += 2 * P::BYTES;
       } else {
+#pragma unroll
+        for (int q = 0; q < P::PARTS; ++q)
+          *reinterpret_cast<uint4 *>(buf + P::part(lane, q)) = narrow16<O>(v + kVec<O> * q);
         send(buf, r_first, col0);
-        buf += P::BYTES;
       }
+      buf += (SYM ? 2 : 1) * P::BYTES;
     }
     if (lane == 0) {
       bulk_commit_group();
@@ -489,8 +489,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
       }
       if (SYM && diagonal && o == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c + j == tr) v[j] += p.gamma;
+        for (int j = 0; j < 8; ++j) v[j] = fmaf(p.gamma, c + j == tr ? 1.f : 0.f, v[j]);
       }
       if constexpr (sizeof(O) == 2) {
         const uint4 w[1] = {narrow16<O>(v)};

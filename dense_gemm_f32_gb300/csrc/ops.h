@@ -12,6 +12,11 @@ inline bool rows_aligned(const void *p, int64_t ld, int es = 2) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0;
 }
 
+// Pitch of a workspace's rows, in elements of `es` bytes: whole 128-byte lines (TMA reads
+// a box's rows of 128 bytes at half the rate where each lies in two lines: 16 products
+// of 997^2 took 172 us at a pitch of 1000 halves, of 1024^2 135).
+inline int64_t line_pitch(int64_t cols, int es) { return (cols * es + 127) / 128 * 128 / es; }
+
 // What a fused product does with its accumulator tile (all in fp32, rounded
 // once per stored element).
 enum class Epi {

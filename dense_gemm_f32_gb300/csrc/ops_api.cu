@@ -115,7 +115,7 @@ class ByteStager {
   void add(const void *&p, int64_t &ld, int rows, int cols) {
     if (rows == 0 || cols == 0 || tma_ok(p, ld, 1)) return;
     ops_[n_] = {&p, &ld};
-    jobs_[n_++] = {p, ld, nullptr, (cols + 15LL) / 16 * 16, rows, cols, false};
+    jobs_[n_++] = {p, ld, nullptr, line_pitch(cols, 1), rows, cols, false};
   }
   cudaError_t run() {
     if (n_ == 0) return cudaSuccess;
@@ -159,9 +159,8 @@ class ByteStager {
 
 // The parts of the integer products' workspaces: tokens in fp16 with their
 // scales behind them, and the gated block's H in front of those.
-int64_t pitch8(int cols) { return (cols + 7LL) / 8 * 8; }
-size_t tokens_bytes(int M, int cols) { return ((size_t)M * (size_t)pitch8(cols) * 2 + 255) / 256 * 256; }
-size_t hidden_bytes(int M, int F) { return ((size_t)M * (size_t)pitch8(F) * 4 + 255) / 256 * 256; }
+size_t tokens_bytes(int M, int cols) { return ((size_t)M * (size_t)line_pitch(cols, 2) * 2 + 255) / 256 * 256; }
+size_t hidden_bytes(int M, int F) { return ((size_t)M * (size_t)line_pitch(F, 4) * 4 + 255) / 256 * 256; }
 
 // The end of a call that staged operands.
 int release(Stager &stage, int st) {
@@ -486,7 +485,7 @@ int dgemm_linear_int8(int dtype, int activation, int M, int N, int K, const void
   Int8Gemm p;
   p.dtype = dtype, p.act = activation;
   p.M = M, p.N = N, p.K = K;
-  p.T = work, p.ldt = pitch8(K);
+  p.T = work, p.ldt = line_pitch(K, 2);
   float *scale = reinterpret_cast<float *>(static_cast<char *>(work) + tokens_bytes(M, K));
   p.t_scale = x_scale ? x_scale : scale;
   p.W = W, p.ldw = ldw, p.w_scale = w_scale;
@@ -544,26 +543,26 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
   stage.add(wd, ld, D, F);
   if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
   if (F > 0) {
-    st = done(launch_quantize_tokens(dtype, M, D, X, ldx, tokens, pitch8(D), scale, sms, stream),
+    st = done(launch_quantize_tokens(dtype, M, D, X, ldx, tokens, line_pitch(D, 2), scale, sms, stream),
               "token launch");
     Int8Gemm p;
     p.gated = true, p.dtype = dtype, p.act = activation;
     p.M = M, p.N = F, p.K = D;
-    p.T = tokens, p.ldt = pitch8(D), p.t_scale = scale;
+    p.T = tokens, p.ldt = line_pitch(D, 2), p.t_scale = scale;
     p.W = wg, p.ldw = lg, p.w_scale = g_scale;
     p.W2 = wu, p.ldw2 = lu, p.w2_scale = u_scale;
-    p.out = h, p.ldo = pitch8(F);
+    p.out = h, p.ldo = line_pitch(F, 4);
     if (st == DGEMM_OK) st = done(launch_int8(p, sms, stream), "gated integer product launch");
   }
   if (st == DGEMM_OK)
-    st = done(launch_quantize_tokens(DGEMM_DTYPE_F32, M, F, h, pitch8(F), tokens, pitch8(F), scale, sms,
+    st = done(launch_quantize_tokens(DGEMM_DTYPE_F32, M, F, h, line_pitch(F, 4), tokens, line_pitch(F, 2), scale, sms,
                                      stream),
               "token launch");
   if (st == DGEMM_OK) {
     Int8Gemm p;
     p.dtype = dtype;
     p.M = M, p.N = D, p.K = F;
-    p.T = tokens, p.ldt = pitch8(F), p.t_scale = scale;
+    p.T = tokens, p.ldt = line_pitch(F, 2), p.t_scale = scale;
     p.W = wd, p.ldw = ld, p.w_scale = d_scale;
     p.in0 = R, p.ldi0 = ldr, p.out = Y, p.ldo = ldy;
     st = done(launch_int8(p, sms, stream), "down integer product launch");
