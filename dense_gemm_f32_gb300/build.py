@@ -30,7 +30,7 @@ BINDING_SOURCE = "torch_binding.cpp"
 UNITS = ([("api.cu", "api", []), ("staging.cu", "staging", []), ("ops_api.cu", "ops_api", []),
           ("norm.cu", "norm", []), ("rowops.cu", "rowops", []),
           ("fused.cu", "fused", []), ("quant.cu", "quant", []), ("int8.cu", "int8", []),
-          ("int8_small.cu", "int8_small", []), ("int8_pair.cu", "int8_pair", []), ("newton.cu", "newton", []),
+          ("int8_small.cu", "int8_small", []), ("int8_pair.cu", "int8_pair", []), ("int8_row.cu", "int8_row", []), ("newton.cu", "newton", []),
           ("newton_pair.cu", "newton_pair", []), ("newton_small.cu", "newton_small", [])]
          + [("fused_pair.cu", f"fused_pair_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(3)]
          + [("fused_small.cu", f"fused_small_{u}", [f"-DDGEMM_FUSED_UNIT={u}"]) for u in range(4)]

@@ -92,6 +92,10 @@ double pair_plan(const Int8Gemm &p, int num_sms, int *best_nt) {
 
 }  // namespace
 
+bool int8_use_row(int M, int K) {
+  return int8_row_takes(M, K) && knob("DGEMM_INT8_ROW", 0, 1) != 0;
+}
+
 cudaError_t launch_int8(const Int8Gemm &p, int num_sms, cudaStream_t stream) {
   int *wd = watchdog_address();
   if (wd == nullptr) return cudaErrorInvalidSymbol;

@@ -490,6 +490,10 @@ int dgemm_linear_int8(int dtype, int activation, int M, int N, int K, const void
   p.t_scale = x_scale ? x_scale : scale;
   p.W = W, p.ldw = ldw, p.w_scale = w_scale;
   p.bias = bias, p.in0 = R, p.ldi0 = ldr, p.out = D, p.ldo = ldd;
+  if (int8_use_row(M, K)) {
+    p.t_scale = x_scale;
+    return done(launch_int8_row(p, X, ldx, dtype, false, sms, stream), "integer product launch");
+  }
   ByteStager stage(sms, stream);
   stage.add(p.W, p.ldw, N, K);
   if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
@@ -535,6 +539,23 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
   float *h = reinterpret_cast<float *>(w);
   void *tokens = w + hidden_bytes(M, F);
   float *scale = reinterpret_cast<float *>(w + hidden_bytes(M, F) + tokens_bytes(M, D > F ? D : F));
+  if (int8_use_row(M, D) && int8_use_row(M, F)) {
+    Int8Gemm p;
+    p.gated = true, p.dtype = dtype, p.act = activation;
+    p.M = M, p.N = F, p.K = D;
+    p.W = Wg, p.ldw = ldwg, p.w_scale = g_scale;
+    p.W2 = Wu, p.ldw2 = ldwu, p.w2_scale = u_scale;
+    p.out = h, p.ldo = line_pitch(F, 4);
+    st = done(launch_int8_row(p, X, ldx, dtype, false, sms, stream), "gated integer product launch");
+    if (st != DGEMM_OK) return st;
+    Int8Gemm q;
+    q.dtype = dtype;
+    q.M = M, q.N = D, q.K = F;
+    q.W = Wd, q.ldw = ldwd, q.w_scale = d_scale;
+    q.in0 = R, q.ldi0 = ldr, q.out = Y, q.ldo = ldy;
+    return done(launch_int8_row(q, h, line_pitch(F, 4), DGEMM_DTYPE_F32, true, sms, stream),
+                "down integer product launch");
+  }
   const void *wg = Wg, *wu = Wu, *wd = Wd;
   int64_t lg = ldwg, lu = ldwu, ld = ldwd;
   ByteStager stage(sms, stream);

@@ -289,3 +289,63 @@ def test_every_cut_gives_the_same(M, N, K, plan, monkeypatch):
         monkeypatch.setenv("DGEMM_INT8_" + k, str(v))
     assert torch.equal(dg.linear_int8(x, w, ws, activation="gelu"), want)
     assert torch.equal(dg.gated_ffn_int8(x, w, ws, wu, su, wd, sd, residual=r), block)
+
+
+@pytest.mark.parametrize("row", ["0", "1"])
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+@pytest.mark.parametrize("N, K", [(5, 1), (40, 15), (33, 16), (300, 31), (700, 130), (64, 511), (1300, 997), (2500, 1024),
+                                  (100, 4096), (90, 4099), (50, 14336), (30, 20001), (9, 32768), (7, 40000)])
+def test_few_tokens(M, N, K, row, monkeypatch):
+    """Rows of every length that a warp, several warps or none of them hold, on either kernel."""
+    monkeypatch.setenv("DGEMM_INT8_ROW", row)
+    n = ref.make(M + N + K)
+    dtype = DTYPES[(M + K) % 2]
+    x, (w, ws) = n((M, K), dtype), _ints(n, N, K)
+    b, r = n((N,), dtype, 0.5), n((M, N), dtype)
+    q, s = ref8.quantize(x)
+    want = ref8.linear(q, s, _d(w), _d(ws), _d(b), "silu", _d(r), dtype)
+    got = dg.linear_int8(x, w, ws, b, "silu", r)
+    ref.check(got, want, "x")
+    xq, xs = dg.quantize_int8(x)
+    assert torch.equal(dg.linear_int8(xq, w, ws, b, "silu", r, x_scale=xs, dtype=dtype), got)
+    wide = torch.full((N * (K + 5) + 3,), 77, dtype=torch.int8, device="cuda")
+    w2 = wide.as_strided((N, K), (K + 5, 1), 3)
+    w2.copy_(w)
+    assert torch.equal(dg.linear_int8(x, w2, ws, b, "silu", r), got)
+
+
+@pytest.mark.parametrize("row", ["0", "1"])
+@pytest.mark.parametrize("M, D, F", [(1, 64, 96), (2, 1000, 3000), (3, 257, 131), (4, 512, 1408), (1, 2048, 33000)])
+def test_few_tokens_through_the_block(M, D, F, row, monkeypatch):
+    monkeypatch.setenv("DGEMM_INT8_ROW", row)
+    n = ref.make(M + D + F)
+    dtype = DTYPES[M % 2]
+    x, r = n((M, D), dtype), n((M, D), dtype)
+    (wg, sg), (wu, su), (wd, sd) = _ints(n, F, D), _ints(n, F, D, 1), _ints(n, D, F, 2)
+    want = ref8.gated(_d(x), _d(wg), _d(sg), _d(wu), _d(su), _d(wd), _d(sd), "gelu", _d(r), dtype)
+    ref.check(dg.gated_ffn_int8(x, wg, sg, wu, su, wd, sd, "gelu", r), want, "y")
+    x[0] = 0
+    y = dg.gated_ffn_int8(x, wg, sg, wu, su, wd, sd, "gelu", r)
+    assert torch.equal(y[0], r[0])
+
+
+def test_few_tokens_rows_without_a_scale():
+    n = ref.make(21)
+    x, (w, ws) = n((4, 300), torch.bfloat16), _ints(n, 70, 300)
+    x[1], x[2, 9], x[3, 1] = 0, float("inf"), float("nan")
+    y = dg.linear_int8(x, w, ws)
+    assert bool((y[1] == 0).all()) and bool(torch.isnan(y[2:]).all()) and bool(torch.isfinite(y[0]).all())
+
+
+def test_weights_quantised_just_before_a_single_token():
+    """The kernel that writes the weights is the one ahead of the product that reads them."""
+    n = ref.make(22)
+    x, w = n((1, 2048), torch.bfloat16), n((4096, 2048), torch.bfloat16)
+    q, s = dg.quantize_int8(w)
+    want = dg.linear_int8(x, q, s)
+    for M in (1, 8, 300):
+        xs = x.expand(M, -1).contiguous()
+        for _ in range(10):
+            again, scale = dg.quantize_int8(w)
+            assert torch.equal(dg.linear_int8(xs, again, scale)[M - 1:], want)
+            again.zero_()
