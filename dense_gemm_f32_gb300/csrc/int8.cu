@@ -92,8 +92,20 @@ double pair_plan(const Int8Gemm &p, int num_sms, int *best_nt) {
 
 }  // namespace
 
-bool int8_use_row(int M, int K) {
-  return int8_row_takes(M, K) && knob("DGEMM_INT8_ROW", 0, 1) != 0;
+bool int8_use_row(const Int8Gemm *p, int n, int num_sms) {
+  const int force = knob("DGEMM_INT8_ROW", 0, 1);
+  if (force == 0) return false;
+  double row = 0, other = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!int8_row_takes(p[i].M, p[i].K)) return false;
+    row += int8_row_time(p[i]);
+    Int8Plan plan;
+    other += small_plan(p[i], num_sms, &plan) + 3.0;  // the tokens' kernel
+    // the copy of weights on other than 16-byte boundaries
+    const int mats = p[i].gated ? 2 : 1;
+    if (!rows_aligned(p[i].W, p[i].ldw, 1)) other += 3.0 + (double)p[i].N * p[i].K * mats / 2e6;
+  }
+  return force == 1 || row < other;
 }
 
 cudaError_t launch_int8(const Int8Gemm &p, int num_sms, cudaStream_t stream) {

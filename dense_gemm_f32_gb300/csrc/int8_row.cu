@@ -27,19 +27,19 @@
 namespace dg {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;  // one block per SM
 constexpr int kMaxVecs = 8;    // 16-byte loads of a lane for its part of a row
 constexpr int kMaxTokens = 4;
-constexpr int kChunk = 512;    // rows whose sums are kept before they are finished
+constexpr int kChunk = 1024;   // parts of rows whose sums are kept before they are finished
 
 struct Args {
   int M, N, K;
   int act, parts, vecs;  // warps per row, loads per lane
   int early;             // the weights may be read before the kernel ahead is done
+  int x_aligned;         // rows of X are, and whole vectors
   int pitch;             // bytes of a token in shared memory
   const void *X;         // the tokens, of type `x_type`, or integers with x_scale
   int64_t ldx;
-  int x_type;
   const float *x_scale;
   const uint8_t *W, *W2;
   int64_t ldw, ldw2;
@@ -50,47 +50,106 @@ struct Args {
   int64_t ldo;
 };
 
-// Rows of tokens in 8 bits in shared memory, zeros behind them; their scales.
-template <class X>
-__device__ void quantise_tokens(const Args &p, int8_t *tokens, float *scales, uint32_t *tops, int mt) {
-  constexpr int V = kVec<X>;
-  for (int m = 0; m < mt; ++m) {
-    const X *x = static_cast<const X *>(p.X) + m * p.ldx;
-    const int cols = m < p.M ? p.K : 0;
-    uint32_t top = 0;
-#pragma unroll 4
-    for (int c = threadIdx.x * V; c < cols; c += kThreads * V) {
-      float f[V];
-      widen16<X>(load_row16<X, false>(x, c, cols), f);
+// f(column, elements) for this thread's vectors of a row, four of them in flight.
+template <class X, bool AL, class F>
+__device__ __forceinline__ void for_vectors(const X *x, int cols, int end, F &&f) {
+  constexpr int V = kVec<X>, AHEAD = 4;
+  for (int c0 = threadIdx.x * V; c0 < end; c0 += AHEAD * kThreads * V) {
+    RowBlocks b[AHEAD];
 #pragma unroll
-      for (int j = 0; j < V; ++j) top = max(top, abs_bits(f[j]));
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) tops[m * kWarps + (threadIdx.x >> 5)] = top;
-  }
-  __syncthreads();
-  for (int m = 0; m < mt; ++m) {
-    const X *x = static_cast<const X *>(p.X) + m * p.ldx;
-    const int cols = m < p.M ? p.K : 0;
-    const RowScale r =
-        row_scale(__reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? tops[m * kWarps + (threadIdx.x & 31)] : 0u));
-    if (threadIdx.x == 0) scales[m] = r.scale;
-    int8_t *to = tokens + m * p.pitch;
-#pragma unroll 4
-    for (int c = threadIdx.x * V; c < p.pitch; c += kThreads * V) {
-      float f[V];
-      widen16<X>(load_row16<X, false>(x, c, cols), f);
+    for (int k = 0; k < AHEAD; ++k) b[k] = fetch_row16<X, AL>(x, c0 + k * kThreads * V, cols);
 #pragma unroll
-      for (int j = 0; j < V; ++j) f[j] = quantised(f[j], r);
-      put<V>(to + c, f, V, true);
+    for (int k = 0; k < AHEAD; ++k) {
+      const int c = c0 + k * kThreads * V;
+      if (c >= end) break;
+      float v[V];
+      widen16<X>(take_row16<X, AL>(b[k], x, c, cols), v);
+      f(c, v);
     }
   }
 }
 
+// Rows of tokens in 8 bits in shared memory, zeros behind them; their scales.  Their
+// largest first (before the weights are sent for, or the tokens' few bytes come after
+// those), then the integers.  A single token on aligned rows is held in between.
+template <class X, int MT>
+struct Tokens {
+  static constexpr int V = kVec<X>, HELD = 8;
+  RowBlocks held[HELD];
+
+  __device__ __forceinline__ bool holds(const Args &p) const {
+    return MT == 1 && p.x_aligned && p.K <= HELD * kThreads * V;
+  }
+  __device__ __forceinline__ void send(const Args &p) {
+    if (holds(p)) {
+#pragma unroll
+      for (int k = 0; k < HELD; ++k)
+        held[k] = fetch_row16<X, true>(static_cast<const X *>(p.X), min((int)(threadIdx.x + k * kThreads) * V, p.K), p.K);
+    }
+  }
+  __device__ __forceinline__ void largest(const Args &p, uint32_t *tops) {
+    for (int m = 0; m < MT; ++m) {
+      const X *x = static_cast<const X *>(p.X) + m * p.ldx;
+      const int cols = m < p.M ? p.K : 0;
+      uint32_t top = 0;
+      auto widest = [&](int, const float (&v)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) top = max(top, abs_bits(v[j]));
+      };
+      if (holds(p)) {
+#pragma unroll
+        for (int k = 0; k < HELD; ++k) {
+          float v[V];
+          widen16<X>(held[k].a, v);  // zeros past the row
+          widest(0, v);
+        }
+      } else if (p.x_aligned) {
+        for_vectors<X, true>(x, cols, cols, widest);
+      } else {
+        for_vectors<X, false>(x, cols, cols, widest);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if ((threadIdx.x & 31) == 0) tops[m * kWarps + (threadIdx.x >> 5)] = top;
+    }
+  }
+  __device__ __forceinline__ void quantise(const Args &p, int8_t *tokens, float *scales, const uint32_t *tops) {
+    for (int m = 0; m < MT; ++m) {
+      const X *x = static_cast<const X *>(p.X) + m * p.ldx;
+      const int cols = m < p.M ? p.K : 0;
+      const RowScale r = row_scale(
+          __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? tops[m * kWarps + (threadIdx.x & 31)] : 0u));
+      if (threadIdx.x == 0) scales[m] = r.scale;
+      int8_t *to = tokens + m * p.pitch;
+      auto put_one = [&](int c, float (&v)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = quantised(v[j], r);
+        put<V>(to + c, v, V, true);
+      };
+      if (holds(p)) {
+#pragma unroll
+        for (int k = 0; k < HELD; ++k) {
+          const int c = (int)(threadIdx.x + k * kThreads) * V;
+          if (c >= p.pitch) break;
+          float v[V];
+          widen16<X>(held[k].a, v);
+          put_one(c, v);
+        }
+        // what no held vector covers is behind the row
+        for (int c = HELD * kThreads * V + (int)threadIdx.x * 4; c < p.pitch; c += kThreads * 4)
+          *reinterpret_cast<uint32_t *>(to + c) = 0u;
+      } else if (p.x_aligned) {
+        for_vectors<X, true>(x, cols, p.pitch, put_one);
+      } else {
+        for_vectors<X, false>(x, cols, p.pitch, put_one);
+      }
+    }
+  }
+};
+
 // X: the tokens' type (int8_t: given as integers); T: the result's; GATED: H = act(g)
 // u in fp32.  MT: tokens, 1, 2 or 4.  AL: rows of weights on 16-byte boundaries.
 template <class X, class T, bool GATED, int MT, bool AL>
-__global__ void __launch_bounds__(kThreads, 2) int8_row_kernel(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(kThreads, 1) int8_row_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(16) uint8_t smem[];
   int8_t *tokens = reinterpret_cast<int8_t *>(smem);
   int *sums = reinterpret_cast<int *>(smem + MT * p.pitch);  // [row of the chunk][part][token]
@@ -129,14 +188,29 @@ __global__ void __launch_bounds__(kThreads, 2) int8_row_kernel(const __grid_cons
   };
 
   Row now, next;
-  const int tasks_all = mine * MATS;  // of the block; a group's are interleaved by feature
   auto task_of = [&](int k) { return (k / MATS * groups + group) * MATS + k % MATS; };
   if (p.early) load(task_of(0), now);
   pdl_wait();
   pdl_launch_dependents();
-  if (!p.early) load(task_of(0), now);
-  load(task_of(1), next);
-
+  // this thread's first output of the finish below, for which it reads now what it needs
+  auto feature_at = [&](int at) { return blockIdx.x + (int64_t)at * step; };
+  struct Rest {
+    float ws, ws2, bias, res;
+  };
+  auto rest_of = [&](int at, int m) {
+    Rest r = {0.f, 0.f, 0.f, 0.f};
+    if (at >= mine || m >= p.M) return r;
+    const int64_t f = feature_at(at);
+    r.ws = p.w_scale[f];
+    if constexpr (GATED) {
+      r.ws2 = p.w2_scale[f];
+    } else {
+      if (p.bias != nullptr) r.bias = to_f32<T>(static_cast<const T *>(p.bias)[f]);
+      if (p.in0 != nullptr) r.res = to_f32<T>(static_cast<const T *>(p.in0)[m * p.ldi0 + f]);
+    }
+    return r;
+  };
+  const Rest first = rest_of(threadIdx.x / MT, threadIdx.x % MT);
   if constexpr (sizeof(X) == 1) {
     for (int m = 0; m < MT; ++m) {
       const int8_t *x = static_cast<const int8_t *>(p.X) + m * p.ldx;
@@ -144,14 +218,21 @@ __global__ void __launch_bounds__(kThreads, 2) int8_row_kernel(const __grid_cons
         tokens[m * p.pitch + c] = m < p.M && c < p.K ? x[c] : (int8_t)0;
       if (threadIdx.x == 0) scales[m] = m < p.M ? p.x_scale[m] : 0.f;
     }
+    if (!p.early) load(task_of(0), now);
   } else {
-    quantise_tokens<X>(p, tokens, scales, tops, MT);
+    Tokens<X, MT> t;
+    t.send(p);
+    if (!t.holds(p)) t.largest(p, tops);
+    if (!p.early) load(task_of(0), now);
+    if (t.holds(p)) t.largest(p, tops);
+    __syncthreads();
+    t.quantise(p, tokens, scales, tops);
   }
+  load(task_of(1), next);
   __syncthreads();
 
   const int per_group = (mine + groups - 1) / groups * MATS;  // rounds of the longest group
-  constexpr int CHUNK_ROWS = kChunk;
-  const int chunk = CHUNK_ROWS / (p.parts * groups * MATS) * MATS;  // rounds between flushes
+  const int chunk = kChunk / (p.parts * groups * MATS) * MATS;  // rounds between flushes
   for (int k0 = 0; k0 < per_group; k0 += chunk) {
     const int k1 = min(per_group, k0 + chunk);
 #pragma unroll 1
@@ -204,28 +285,24 @@ __global__ void __launch_bounds__(kThreads, 2) int8_row_kernel(const __grid_cons
       const int m = e % MT, i = e / MT, round = i / groups, g = i % groups;
       const int at = k0 / MATS * groups + i;
       if (at >= mine || m >= p.M) continue;
-      const int64_t f = blockIdx.x + (int64_t)at * step;
+      const int64_t f = feature_at(at);
       auto sum = [&](int mat) {
         int s = 0;  // any order gives the same integer
         for (int q = 0; q < p.parts; ++q)
           s += sums[(((round * MATS + mat) * groups + g) * p.parts + q) * MT + m];
         return (float)s;
       };
-      float z = scaled(sum(0), scales[m], p.w_scale[f]);
-      if constexpr (GATED) {
-        const float u = scaled(sum(1), scales[m], p.w2_scale[f]);
-        with_act(p.act, [&](auto c) { z = act_f32<decltype(c)::value>(z); });
+      const Rest r = e == (int)threadIdx.x && k0 == 0 ? first : rest_of(at, m);
+      float z = scaled(sum(0), scales[m], r.ws) + r.bias;
+      const float u = GATED ? scaled(sum(1), scales[m], r.ws2) : 0.f;
+      with_act(p.act, [&](auto c) { z = act_f32<decltype(c)::value>(z); });
+      if constexpr (GATED)
         static_cast<float *>(p.out)[m * p.ldo + f] = z * u;
-      } else {
-        if (p.bias != nullptr) z += to_f32<T>(static_cast<const T *>(p.bias)[f]);
-        with_act(p.act, [&](auto c) { z = act_f32<decltype(c)::value>(z); });
-        if (p.in0 != nullptr) z += to_f32<T>(static_cast<const T *>(p.in0)[m * p.ldi0 + f]);
-        static_cast<T *>(p.out)[m * p.ldo + f] = from_f32<T>(z);
-      }
+      else
+        static_cast<T *>(p.out)[m * p.ldo + f] = from_f32<T>(z + r.res);
     }
     __syncthreads();
   }
-  (void)tasks_all;
 }
 
 // Warps per row: the fewest whose lanes hold their parts in kMaxVecs loads.
@@ -244,13 +321,13 @@ cudaError_t launch_one(const Args &a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 190 * 1024);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
   const size_t smem = (size_t)MT * a.pitch + kChunk * MT * 4 + kMaxTokens * 4 + kMaxTokens * kWarps * 4;
-  // two blocks per SM, each with the same number of rounds where there are many
-  const int groups = kWarps / a.parts, most = 2 * num_sms;
+  // one block per SM, each with the same number of rounds where there are many
+  const int groups = kWarps / a.parts, most = num_sms;
   int64_t grid = ((int64_t)a.N + groups - 1) / groups;
   if (grid > most) {
     const int64_t rounds = ((int64_t)a.N + (int64_t)most * groups - 1) / ((int64_t)most * groups);
@@ -277,10 +354,18 @@ cudaError_t launch_x(const Args &a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
+// Whether it can, and its time (microseconds, fitted like those of int8.cu): the
+// weights', and for each token the shared memory's and the integer units'.
+double int8_row_time(const Int8Gemm &p) {
+  const bool aligned = rows_aligned(p.W, p.ldw, 1) && (!p.gated || rows_aligned(p.W2, p.ldw2, 1));
+  const double weights = (double)p.N * p.K * (p.gated ? 2 : 1) / 6.6e6;
+  return 2.8 + weights * (0.95 + 0.22 * p.M) * (aligned ? 1.0 : 1.8);
+}
+
 bool int8_row_takes(int M, int K) {
   const int64_t pitch = ((int64_t)K + 15) / 16 * 16 + 16;
   return M >= 1 && M <= kMaxTokens && K >= 1 && (K + 15) / 16 <= kWarps * 32 * kMaxVecs &&
-         (M == 3 ? 4 : M) * pitch <= 96 * 1024;
+         (M == 3 ? 4 : M) * pitch <= 160 * 1024;
 }
 
 cudaError_t launch_int8_row(const Int8Gemm &p, const void *X, int64_t ldx, int x_type, bool early, int num_sms,
@@ -292,7 +377,9 @@ cudaError_t launch_int8_row(const Int8Gemm &p, const void *X, int64_t ldx, int x
   a.vecs = ((p.K + 15) / 16 + a.parts * 32 - 1) / (a.parts * 32);
   a.early = early;
   a.pitch = (p.K + 15) / 16 * 16 + 16;  // a vector of zeros behind
-  a.X = X, a.ldx = ldx, a.x_type = x_type, a.x_scale = p.t_scale;
+  a.X = X, a.ldx = ldx, a.x_scale = p.t_scale;
+  const int xs = x_type == DGEMM_DTYPE_F32 ? 4 : 2;
+  a.x_aligned = rows_aligned(X, ldx, xs) && p.K % (16 / xs) == 0;
   a.W = static_cast<const uint8_t *>(p.W), a.W2 = static_cast<const uint8_t *>(p.W2);
   a.ldw = p.ldw, a.ldw2 = p.ldw2, a.w_scale = p.w_scale, a.w2_scale = p.w2_scale;
   a.bias = p.bias, a.in0 = p.in0, a.ldi0 = p.ldi0, a.out = p.out, a.ldo = p.ldo;

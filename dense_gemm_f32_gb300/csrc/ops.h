@@ -192,14 +192,17 @@ struct Int8Gemm {
   int64_t ldo = 0;
 };
 cudaError_t launch_int8(const Int8Gemm &p, int num_sms, cudaStream_t stream);
-// Whether a product goes to int8_row.cu instead (DGEMM_INT8_ROW=0 / =1 forces it where it can).
-bool int8_use_row(int M, int K);
+// Whether a product (or two, one after the other) goes to int8_row.cu instead: where it
+// can and is the quicker way, weights that TMA cannot read being copied for the others.
+// DGEMM_INT8_ROW=0 / =1 forces it.
+bool int8_use_row(const Int8Gemm *p, int n, int num_sms);
 
 // The same for one to four tokens X of x_type (or integers, with p.t_scale their
 // scales), quantised in the kernel: p.T and p.ldt are not looked at, p.t_scale is
 // null for X to be quantised; W on any alignment.  early: the kernel ahead on the
 // stream is another of these, so the weights may be read before it is done.
 bool int8_row_takes(int M, int K);
+double int8_row_time(const Int8Gemm &p);
 cudaError_t launch_int8_row(const Int8Gemm &p, const void *X, int64_t ldx, int x_type, bool early, int num_sms,
                             cudaStream_t stream);
 

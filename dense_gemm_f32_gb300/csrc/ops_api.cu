@@ -490,7 +490,7 @@ int dgemm_linear_int8(int dtype, int activation, int M, int N, int K, const void
   p.t_scale = x_scale ? x_scale : scale;
   p.W = W, p.ldw = ldw, p.w_scale = w_scale;
   p.bias = bias, p.in0 = R, p.ldi0 = ldr, p.out = D, p.ldo = ldd;
-  if (int8_use_row(M, K)) {
+  if (int8_use_row(&p, 1, sms)) {
     p.t_scale = x_scale;
     return done(launch_int8_row(p, X, ldx, dtype, false, sms, stream), "integer product launch");
   }
@@ -539,21 +539,20 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
   float *h = reinterpret_cast<float *>(w);
   void *tokens = w + hidden_bytes(M, F);
   float *scale = reinterpret_cast<float *>(w + hidden_bytes(M, F) + tokens_bytes(M, D > F ? D : F));
-  if (int8_use_row(M, D) && int8_use_row(M, F)) {
-    Int8Gemm p;
-    p.gated = true, p.dtype = dtype, p.act = activation;
-    p.M = M, p.N = F, p.K = D;
-    p.W = Wg, p.ldw = ldwg, p.w_scale = g_scale;
-    p.W2 = Wu, p.ldw2 = ldwu, p.w2_scale = u_scale;
-    p.out = h, p.ldo = line_pitch(F, 4);
-    st = done(launch_int8_row(p, X, ldx, dtype, false, sms, stream), "gated integer product launch");
+  Int8Gemm two[2];  // for few tokens: both products in a launch each, nothing in between
+  two[0].gated = true, two[0].act = activation;
+  two[0].N = F, two[0].K = D;
+  two[0].W = Wg, two[0].ldw = ldwg, two[0].w_scale = g_scale;
+  two[0].W2 = Wu, two[0].ldw2 = ldwu, two[0].w2_scale = u_scale;
+  two[0].out = h, two[0].ldo = line_pitch(F, 4);
+  two[1].N = D, two[1].K = F;
+  two[1].W = Wd, two[1].ldw = ldwd, two[1].w_scale = d_scale;
+  two[1].in0 = R, two[1].ldi0 = ldr, two[1].out = Y, two[1].ldo = ldy;
+  two[0].M = two[1].M = M, two[0].dtype = two[1].dtype = dtype;
+  if (int8_use_row(two, 2, sms)) {
+    st = done(launch_int8_row(two[0], X, ldx, dtype, false, sms, stream), "gated integer product launch");
     if (st != DGEMM_OK) return st;
-    Int8Gemm q;
-    q.dtype = dtype;
-    q.M = M, q.N = D, q.K = F;
-    q.W = Wd, q.ldw = ldwd, q.w_scale = d_scale;
-    q.in0 = R, q.ldi0 = ldr, q.out = Y, q.ldo = ldy;
-    return done(launch_int8_row(q, h, line_pitch(F, 4), DGEMM_DTYPE_F32, true, sms, stream),
+    return done(launch_int8_row(two[1], h, line_pitch(F, 4), DGEMM_DTYPE_F32, true, sms, stream),
                 "down integer product launch");
   }
   const void *wg = Wg, *wu = Wu, *wd = Wd;

@@ -19,6 +19,7 @@
 
 #include <cmath>
 #include <string>
+#include <vector>
 
 #include "../../include/dgemm.h"
 
@@ -430,6 +431,18 @@ Tensor bytes_like(size_t n, const Tensor &x) {
   return at::empty({(int64_t)n}, x.options().dtype(at::kByte));
 }
 
+// A tensor of the given sizes whose rows start on 16-byte boundaries, in 8 bits.
+Tensor rows_of_bytes(at::IntArrayRef sizes, const Tensor &like) {
+  const int64_t cols = sizes.back(), pitch = (cols + 15) / 16 * 16;
+  int64_t rows = 1;
+  std::vector<int64_t> strides(sizes.size(), 1);
+  for (int64_t i = (int64_t)sizes.size() - 2; i >= 0; --i) {
+    strides[i] = pitch * rows;
+    rows *= sizes[i];
+  }
+  return at::empty({rows * pitch}, like.options().dtype(at::kChar)).as_strided(sizes, strides);
+}
+
 // (x, transpose)
 PyObject *quantize_int8(PyObject *const *a) {
   refuse_recording("quantize_int8", a, 2, false);
@@ -439,12 +452,12 @@ PyObject *quantize_int8(PyObject *const *a) {
   const Mat m = rows_of(x, "x", x.scalar_type());
   if (t && x.dim() != 2) value_error("x: expected a 2-D matrix");
   const cudaStream_t stream = current_stream(x);
-  const auto bytes = x.options().dtype(at::kChar), floats = x.options().dtype(at::kFloat);
+  const auto floats = x.options().dtype(at::kFloat);
   const int cols = t ? m.rows : m.cols;
-  const Tensor q = t ? at::empty({m.cols, m.rows}, bytes) : at::empty(x.sizes(), bytes);
+  const Tensor q = t ? rows_of_bytes({m.cols, m.rows}, x) : rows_of_bytes(x.sizes(), x);
   const Tensor s = t ? at::empty({m.cols}, floats) : at::empty(x.sizes().slice(0, x.dim() - 1), floats);
   check(dgemm_quantize_int8(dt, t ? DGEMM_OP_T : DGEMM_OP_N, m.rows, m.cols, m.p, m.ld,
-                            static_cast<signed char *>(q.data_ptr()), pos(cols),
+                            static_cast<signed char *>(q.data_ptr()), pos((cols + 15) / 16 * 16),
                             static_cast<float *>(s.data_ptr()), stream),
         "quantize_int8");
   return tuple({&q, &s});

@@ -186,7 +186,10 @@ def quantize_int8(x, transpose=False, stream=None):
     of every row (shape x.shape[:-1]).  transpose: x is a K x N matrix whose
     columns are meant: q is N x K and scale has N elements, the form in which
     linear_int8 and gated_ffn_int8 take weights that linear and gated_ffn have as
-    K x N.  A row with NaN or an infinity gets that for its scale, and zeros.
+    K x N.  A row with NaN or an infinity gets that for its scale, and zeros.  The rows
+    of q start on 16-byte boundaries, as the products read weights best (so q is
+    contiguous where they are a multiple of 16 long; other weights are copied first, in
+    every call).
     """
     if stream is not None:
         with _on(stream, x):

@@ -349,3 +349,15 @@ def test_weights_quantised_just_before_a_single_token():
             again, scale = dg.quantize_int8(w)
             assert torch.equal(dg.linear_int8(xs, again, scale)[M - 1:], want)
             again.zero_()
+
+
+def test_rows_of_quantised_weights_are_aligned():
+    n = ref.make(23)
+    for x in (n((7, 33), torch.float16), n((2, 3, 50), torch.bfloat16), n((5,), torch.float32), n((4, 32), torch.float32)):
+        q, s = dg.quantize_int8(x)
+        assert q.shape == x.shape and q.stride(-1) == 1 and q.data_ptr() % 16 == 0
+        assert x.dim() == 1 or q.stride(-2) % 16 == 0
+        same, again = dg.quantize_int8(x.clone())
+        assert torch.equal(q, same) and torch.equal(s, again)
+    q, _ = dg.quantize_int8(n((33, 7), torch.float16), transpose=True)
+    assert q.shape == (7, 33) and q.stride() == (48, 1)
