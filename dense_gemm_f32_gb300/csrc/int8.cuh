@@ -61,4 +61,11 @@ __device__ __forceinline__ void widen64(const uint8_t *at, int first, int swizzl
   }
 }
 
+// True once every lane of the warp holds what widen64 loads: a vote over a value of each of
+// the four loads.  A widened integer is no NaN, so the vote is always true, but the
+// compiler cannot know that and what depends on it waits for the loads.
+__device__ __forceinline__ bool warp_has(const uint32_t (&r)[32]) {
+  return __all_sync(0xffffffffu, (r[0] & r[8] & r[16] & r[24]) != 0x7fff7fffu);
+}
+
 }  // namespace dg

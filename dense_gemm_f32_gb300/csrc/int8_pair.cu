@@ -358,8 +358,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const uint8_t *w = smem + (w_tile(s) - base) + row * G::BK;
       uint32_t r[32];
       widen64(w, 4 * half_k, row & 7, r);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(wempty_bar(s));
+      // The stage is given back once the values are here: an arrival that is only issued
+      // after the loads can be seen before they have read, and the next copy then lands
+      // under them.
+      const bool here = warp_has(r);
+      if (lane == 0 && here) mbar_arrive(wempty_bar(s));
       if (++s == G::W_STAGES) s = 0, phase ^= 1u;
       if (i >= G::PLACES) {  // the MMAs that read this place PLACES blocks ago are done
         if (!warp_wait(tempty_bar(free_t), free_phase, lane, p.watchdog, kSite7ConvPlace, abort_flag)) break;

@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
             }
           }
           if (p.in_tma) {
+            fence_proxy_async_smem();  // the next copy comes after these reads
             __syncwarp();
             send_for_input();
           }

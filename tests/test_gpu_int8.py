@@ -361,3 +361,34 @@ def test_rows_of_quantised_weights_are_aligned():
         assert torch.equal(q, same) and torch.equal(s, again)
     q, _ = dg.quantize_int8(n((33, 7), torch.float16), transpose=True)
     assert q.shape == (7, 33) and q.stride() == (48, 1)
+
+
+@pytest.mark.parametrize("M, K, N", [(2048, 4096, 14336), (1000, 1008, 30000)])
+def test_many_tokens_with_one_weight_after_the_other(M, K, N):
+    """Weights that alternate come from memory, not from L2: nothing is read before it
+    has arrived, or after its place was given to the next block."""
+    n = ref.make(M + N)
+    x = n((M, K), torch.bfloat16)
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    # |q w| sums to at most 2^24: the integers' sums are exact
+    top = min(127, 2 ** 24 // (127 * K))
+    ws = [torch.randint(-top, top + 1, (N, K), generator=gen, dtype=torch.int8, device="cuda") for _ in range(4)]
+    scale = n((N,), torch.float32, 0.001, 0.002).abs() + 1e-4
+    want = [ref8.linear(*ref8.quantize(x), w.double(), scale.double(), None, "none", None, torch.bfloat16) for w in ws]
+    for _ in range(4):
+        got = [dg.linear_int8(x, w, scale) for w in ws]
+        for y, (d, bound) in zip(got, want):
+            assert bool(((y.double() - d).abs() <= bound).all())
+
+
+def test_many_tokens_through_one_block_after_the_other():
+    M, D, F = 700, 2048, 8192
+    n = ref.make(M)
+    x = n((M, D), torch.bfloat16)
+    blocks = [[t for w in (n((F, D), torch.bfloat16, 0.05), n((F, D), torch.bfloat16, 0.05),
+                           n((D, F), torch.bfloat16, 0.05)) for t in dg.quantize_int8(w)] for _ in range(4)]
+    want = [ref8.gated(x, *(_d(t) for t in b), "silu", None, torch.bfloat16) for b in blocks]
+    for _ in range(4):
+        got = [dg.gated_ffn_int8(x, *b, "silu") for b in blocks]
+        for y, (d, bound) in zip(got, want):
+            assert bool(((y.double() - d).abs() <= bound).all())
