@@ -108,11 +108,11 @@ __global__ void __launch_bounds__(kThreads)
     scale_kernel(int rows, int cols, const T *X, int64_t ldx, float eps, const float *partial, int parts,
                  __half *out, int64_t ldo, float *factor) {
   constexpr int V = kVec<T>;
-  __shared__ double fold[3][kThreads / 32];
+  __shared__ float fold[3][kThreads / 32];
   __shared__ float up[2];
   pdl_launch_dependents();
   pdl_wait();
-  double v[3] = {0., 0., 0.};
+  float v[3] = {0.f, 0.f, 0.f};
   for (int i = threadIdx.x; i < parts; i += kThreads)
     for (int k = 0; k < 3; ++k) v[k] += partial[i * 3 + k];
 #pragma unroll
@@ -121,24 +121,30 @@ __global__ void __launch_bounds__(kThreads)
     if ((threadIdx.x & 31) == 0) fold[k][threadIdx.x >> 5] = v[k];
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double t[3] = {0., 0., 0.};
-    for (int k = 0; k < 3; ++k)
-      for (int w = 0; w < kThreads / 32; ++w) t[k] += fold[k][w];
-    // the plain sum where it is away from both ends of fp32's range
-    double norm = sqrt(t[0]);
-    if (!(t[0] < 0x1p100))
-      norm = sqrt(t[1]) * 0x1p70;
-    else if (t[0] < 0x1p-60)
-      norm = sqrt(t[2]) * 0x1p-70;
+  if (threadIdx.x < 32) {
+    float t[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      t[k] = fold[k][threadIdx.x % (kThreads / 32)];
+      for (int m = kThreads / 64; m; m >>= 1) t[k] += __shfl_xor_sync(0xffffffffu, t[k], m);
+    }
+    // The plain sum where it is away from both ends of fp32's range.  64 bits from here, for
+    // their range alone: sums in them took 3 us more.
+    double norm;
+    if (!(t[0] < 0x1p100f))
+      norm = sqrtf(t[1]) * 0x1p70;
+    else if (t[0] < 0x1p-60f)
+      norm = sqrtf(t[2]) * 0x1p-70;
+    else
+      norm = sqrtf(t[0]);
     norm += (double)eps;
     int e = 0;
     const double f = frexp(norm, &e);  // norm = f 2^e, 1/2 <= f < 1
     const bool none = !(norm > 0.) || isinf(norm);  // nothing to divide by, an infinity or NaN
-    if (blockIdx.x == 0) *factor = none ? __uint_as_float(0x7fc00000u) : (float)(1. / f);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *factor = none ? __uint_as_float(0x7fc00000u) : 1.f / (float)f;
     // 2^(8 - e) in two factors that are fp32 numbers
     const int k = none ? 0 : 8 - e, k1 = k / 2;
-    up[0] = ldexpf(1.f, k1), up[1] = ldexpf(1.f, k - k1);
+    if (threadIdx.x == 0) up[0] = ldexpf(1.f, k1), up[1] = ldexpf(1.f, k - k1);
   }
   __syncthreads();
   const float u0 = up[0], u1 = up[1];
@@ -268,13 +274,11 @@ int group_steps(const Orthogonalize &p, int k) {
   return steps;
 }
 
-}  // namespace
-
-size_t newton_scale_scratch(int num_sms) { return (size_t)scale_blocks(num_sms) * 3 * 4; }
-
-cudaError_t launch_newton_scale(int dtype, int rows, int cols, const void *X, int64_t ldx, float eps,
-                                void *T, int64_t ldt, float *factor, float *partial, int num_sms,
-                                cudaStream_t stream) {
+// X in fp16 (rows of `ldt`, a multiple of 8) as X 2^(8 - e), and *factor = 2^e /
+// (norm + eps): X 2^(8 - e) factor / 256 is X / (norm + eps).  partial: three floats for
+// each of scale_blocks() blocks.
+cudaError_t scale_to_fp16(int dtype, int rows, int cols, const void *X, int64_t ldx, float eps, void *T,
+                          int64_t ldt, float *factor, float *partial, int num_sms, cudaStream_t stream) {
   switch (dtype) {
     case DGEMM_DTYPE_F32:
       return launch_scale<float>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
@@ -284,6 +288,8 @@ cudaError_t launch_newton_scale(int dtype, int rows, int cols, const void *X, in
       return launch_scale<__half>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
   }
 }
+
+}  // namespace
 
 size_t newton_workspace(int rows, int cols) {
   if (rows <= 0 || cols <= 0) return 0;
@@ -298,7 +304,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
   const bool tall = p.rows > p.cols;
   const int m = tall ? p.cols : p.rows, n = tall ? p.rows : p.cols;
   const int64_t ldx = line_pitch(p.cols, 2), ldm = line_pitch(m, 2);
-  cudaError_t e = launch_newton_scale(p.x_dtype, p.rows, p.cols, p.X, p.ldx, p.eps, w.x[0], ldx, w.factor,
+  cudaError_t e = scale_to_fp16(p.x_dtype, p.rows, p.cols, p.X, p.ldx, p.eps, w.x[0], ldx, w.factor,
                                       w.partial, num_sms, stream);
   const float x_up = 0x1p8f, m_up = 0x1p6f;  // what X and the m x m matrices are kept times
   __half *x = w.x[0], *x_next = w.x[1];

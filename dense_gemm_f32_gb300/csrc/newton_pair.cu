@@ -81,7 +81,7 @@ struct Maps {
 
 struct Args {
   int M, N, K;
-  int group_m, mn3d, stall, products;
+  int mn3d, stall, products;
   int o_tma;  // outputs may be written by TMA
   int in_vec, in_tma;  // rows of in0 are aligned; it may be read by TMA
   int stages;

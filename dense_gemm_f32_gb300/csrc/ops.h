@@ -246,15 +246,6 @@ cudaError_t launch_newton_pair(const NewtonGemm &p, int *watchdog, cudaStream_t 
 cudaError_t launch_newton_small(const NewtonGemm &p, int splits, int num_sms, int *watchdog,
                                 cudaStream_t stream);
 
-// X in fp16 (rows of `ldt`, a multiple of 8) as X 2^(8 - e), and *factor = 2^e /
-// (norm + eps), where 2^e is the power of two next above norm + eps, norm the root of the
-// sum of X's squares: X 2^(8 - e) factor / 256 is X / (norm + eps).  partial: scratch
-// of newton_scale_scratch() bytes.
-size_t newton_scale_scratch(int num_sms);
-cudaError_t launch_newton_scale(int dtype, int rows, int cols, const void *X, int64_t ldx, float eps,
-                                void *T, int64_t ldt, float *factor, float *partial, int num_sms,
-                                cudaStream_t stream);
-
 // The whole iteration (newton.cu); `work` of newton_workspace() bytes, 16-byte aligned.
 struct Orthogonalize {
   int x_dtype = 0, dtype = 0, rows = 0, cols = 0, steps = 0;
