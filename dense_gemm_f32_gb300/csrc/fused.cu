@@ -12,6 +12,28 @@
 #include "ops.h"
 
 namespace dg {
+
+Residency::Residency(int num_sms) {
+  for (int per_sm = 1; per_sm <= 2; ++per_sm)
+    for (int s = 1; s <= 8; ++s) tiles[per_sm][s] = small_resident({16, 1, s, per_sm}, num_sms);
+}
+
+const Residency *residency(int num_sms) {
+  static std::atomic<const Residency *> made[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  const Residency *r = made[dev].load(std::memory_order_acquire);
+  if (r == nullptr) {
+    const Residency *mine = new (std::nothrow) Residency(num_sms);
+    if (mine == nullptr) return nullptr;
+    if (made[dev].compare_exchange_strong(r, mine, std::memory_order_acq_rel))
+      r = mine;
+    else
+      delete mine;
+  }
+  return r;
+}
+
 namespace {
 
 // DGEMM_FUSED_*: an environment variable's value in lo .. hi, or -1 (read at
@@ -78,31 +100,6 @@ int64_t tiles_of(const FusedGemm &p, int nt) {
 }
 int64_t kblocks_of(const FusedGemm &p, int kd) {
   return (int64_t)((p.K + 64 * kd - 1) / (64 * kd)) * (p.dual == Dual::kSum ? 2 : 1);
-}
-
-// Tiles of the small kernel resident at once, by CTAs per SM and K split.
-struct Residency {
-  int64_t tiles[3][9];
-  explicit Residency(int num_sms) {
-    for (int per_sm = 1; per_sm <= 2; ++per_sm)
-      for (int s = 1; s <= 8; ++s) tiles[per_sm][s] = small_resident({16, 1, s, per_sm}, num_sms);
-  }
-};
-// The current device's, made once.
-const Residency *residency(int num_sms) {
-  static std::atomic<const Residency *> made[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  const Residency *r = made[dev].load(std::memory_order_acquire);
-  if (r == nullptr) {
-    const Residency *mine = new (std::nothrow) Residency(num_sms);
-    if (mine == nullptr) return nullptr;
-    if (made[dev].compare_exchange_strong(r, mine, std::memory_order_acq_rel))
-      r = mine;
-    else
-      delete mine;
-  }
-  return r;
 }
 
 // The best cut of `n` products as one launch of the small kernel, and its time.

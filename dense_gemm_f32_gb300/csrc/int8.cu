@@ -38,11 +38,11 @@ double pair_time(const Int8Gemm &p, int nt, int num_sms) {
 // Small kernel: a block takes a CTA its chain of hand-overs, or its bytes' time at
 // an SM's 135 GB/s (101 where two CTAs share it); the epilogue 0.054 per token of a tile,
 // and joining the parts of a K split 0.72 for each.
-double small_time(const Int8Gemm &p, const Int8Plan &plan, int num_sms) {
+double small_time(const Int8Gemm &p, const Int8Plan &plan, const Residency &res, int num_sms) {
   const int tf = p.gated ? 64 : 128;
   const int64_t tiles_t = (p.M + plan.nt - 1) / plan.nt;
   const int64_t ctas = (int64_t)((p.N + tf - 1) / tf) * tiles_t * plan.splits;
-  const int64_t slots = small_resident({plan.nt, 1, plan.splits, plan.per_sm}, num_sms) * plan.splits;
+  const int64_t slots = res.tiles[plan.per_sm][plan.splits] * plan.splits;
   const int64_t waves = (ctas + slots - 1) / slots;
   const int64_t blocks = ((p.K + 127) / 128 + plan.splits - 1) / plan.splits;
   const bool two = (ctas < slots ? ctas : slots) > num_sms;  // on the fullest SM
@@ -54,7 +54,7 @@ double small_time(const Int8Gemm &p, const Int8Plan &plan, int num_sms) {
 }
 
 // The best cut of each kernel; DGEMM_INT8_NT / _SPLITS force parts of it.
-double small_plan(const Int8Gemm &p, int num_sms, Int8Plan *best_plan) {
+double small_plan(const Int8Gemm &p, const Residency &res, int num_sms, Int8Plan *best_plan) {
   const int f_nt = knob("DGEMM_INT8_NT", 16, 128), f_splits = knob("DGEMM_INT8_SPLITS", 1, 8);
   const int64_t kblocks = (p.K + 127) / 128;
   double best = 0;
@@ -68,8 +68,8 @@ double small_plan(const Int8Gemm &p, int num_sms, Int8Plan *best_plan) {
       const int tf = p.gated ? 64 : 128;
       const int64_t tiles = (int64_t)((p.N + tf - 1) / tf) * ((p.M + plan.nt - 1) / plan.nt);
       // all of an SM's shared memory for one CTA's stages where that holds every tile at once
-      plan.per_sm = tiles > small_resident({plan.nt, 1, s, 1}, num_sms) ? 2 : 1;
-      const double t = small_time(p, plan, num_sms);
+      plan.per_sm = tiles > res.tiles[1][s] ? 2 : 1;
+      const double t = small_time(p, plan, res, num_sms);
       if (best == 0 || t < best) best = t, *best_plan = plan;
       if (f_splits >= 0) break;
     }
@@ -94,13 +94,15 @@ double pair_plan(const Int8Gemm &p, int num_sms, int *best_nt) {
 
 bool int8_use_row(const Int8Gemm *p, int n, int num_sms) {
   const int force = knob("DGEMM_INT8_ROW", 0, 1);
-  if (force == 0) return false;
+  for (int i = 0; i < n; ++i)
+    if (!int8_row_takes(p[i].M, p[i].K)) return false;
+  const Residency *res = residency(num_sms);
+  if (force == 0 || res == nullptr) return false;
   double row = 0, other = 0;
   for (int i = 0; i < n; ++i) {
-    if (!int8_row_takes(p[i].M, p[i].K)) return false;
     row += int8_row_time(p[i]);
     Int8Plan plan;
-    other += small_plan(p[i], num_sms, &plan) + 3.0;  // the tokens' kernel
+    other += small_plan(p[i], *res, num_sms, &plan) + 3.0;  // the tokens' kernel
     // the copy of weights on other than 16-byte boundaries
     const int mats = p[i].gated ? 2 : 1;
     if (!rows_aligned(p[i].W, p[i].ldw, 1)) other += 3.0 + (double)p[i].N * p[i].K * mats / 2e6;
@@ -111,9 +113,11 @@ bool int8_use_row(const Int8Gemm *p, int n, int num_sms) {
 cudaError_t launch_int8(const Int8Gemm &p, int num_sms, cudaStream_t stream) {
   int *wd = watchdog_address();
   if (wd == nullptr) return cudaErrorInvalidSymbol;
+  const Residency *res = residency(num_sms);
+  if (res == nullptr) return cudaErrorInvalidDevice;
   Int8Plan plan;
   int nt = 0;
-  const double small = small_plan(p, num_sms, &plan), pair = pair_plan(p, num_sms, &nt);
+  const double small = small_plan(p, *res, num_sms, &plan), pair = pair_plan(p, num_sms, &nt);
   // DGEMM_INT8_PAIR=0 / =1 forces the kernel; an empty sum is the small one's
   const int force = p.K > 0 ? knob("DGEMM_INT8_PAIR", 0, 1) : 0;
   return (force >= 0 ? force == 1 : pair < small) ? launch_int8_pair(p, nt, wd, stream)

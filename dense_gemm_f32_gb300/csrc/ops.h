@@ -117,6 +117,13 @@ struct SmallPlan {
 // `splits` CTAs) the device holds at once.
 int small_stages(const SmallPlan &plan);
 int64_t small_resident(const SmallPlan &plan, int num_sms);
+// The same by CTAs per SM and K split; the current device's, made once (null: no device, no
+// memory).
+struct Residency {
+  int64_t tiles[3][9];
+  explicit Residency(int num_sms);
+};
+const Residency *residency(int num_sms);
 // `n` products in one launch (three at most for Epi::kLinear, one otherwise;
 // their plans agree in splits and per_sm).  0: bf16 linear, 1: fp16 linear, 2:
 // bf16 gated, 3: fp16 gated.
