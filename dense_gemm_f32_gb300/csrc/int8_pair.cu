@@ -8,9 +8,10 @@
 // the tile's to each CTA.  The weights are the operand in tensor memory because
 // they are the ones that are widened on the SM (int8.cuh), and 192 tokens because
 // that is what two accumulators leave room for.
-//  * Warp 0 loads weights (16 KB per 128 k), warp 2 tokens, warps 4-11 widen half a
-//    row of weights per thread, one thread of the even CTA issues
-//    tcgen05.mma.cta_group::2 with A in tensor memory, eight warps run the epilogue.
+//  * Warp 0 loads weights (16 KB per 128 k), warp 2 tokens, warp 3 the scales of the
+//    next tile, warps 4-11 widen half a row of weights per thread, one lane of warp 1 of
+//    the even CTA issues tcgen05.mma.cta_group::2 with A in tensor memory, warps 12-19 run
+//    the epilogue, with registers that the others hand over.
 //  * The epilogue: a thread holds a feature's sums; a warp turns a 32 x 32 piece over
 //    through its 4 KB of shared memory, after which a thread has eight neighbouring
 //    features of a token: scales, bias, activation and residual in fp32, one
@@ -20,6 +21,12 @@
 //    out in fp32 (int8_small.cu says why).
 //  * Weights are loaded before the kernel ahead on the stream is done, as in
 //    int8_small.cu.
+// Bound by the tensor pipe from about 140 tokens in a tile (0.0024 us per token and 128 k),
+// below that by the hand-over from the loads through the converters to the MMA (0.3 us).
+// 8192 x 4096 x 14336 takes 490 to 520 us (494 at cuBLAS's measured fp16 rate).  On the same
+// box: four warps for the even blocks and four for the odd, whole rows each, 524 for 504;
+// three or four places behind narrower accumulators 516 for 490; MMAs issued by a lane under
+// `if (lane == 0)` 640, as their descriptors go through that lane's registers one by one.
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>

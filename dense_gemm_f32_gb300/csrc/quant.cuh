@@ -6,8 +6,8 @@
 // two that brings top into [1, 4), t = 127 x is exact in fp32 (7 + 11 bits), the
 // product with 127 / top finds an integer that is at most one off, next to a
 // half, and e = t - q top, exact as well, says on which side of it the quotient
-// lies.  (An element costs a product, a rounding by a large constant, a fused
-// multiply-add and a comparison; a division would cost twice as much.)  For
+// lies.  (An element costs three products, two of them with a sum, a subtraction and a
+// comparison; a division would cost several times that.)  For
 // fp32 elements t is rounded once.  The maximum is taken of the bits of |x|, in
 // which NaN is the largest: a row with NaN or an infinity gets that as its scale
 // and zeros, so that what is computed from it is NaN.  A row of zeros has scale
@@ -39,15 +39,37 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top_bits) {
   return r;
 }
 
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23: a sum with it is rounded to an integer
+
+// The integer of one element.
 __device__ __forceinline__ float quantised(float x, const RowScale &r) {
   if (r.none) return 0.f;
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: a sum with it is rounded to an integer
   x *= r.up;
-  const float t = 127.f * x, v = x * r.inv;
-  const float m = v + kRound, q = m - kRound;
+  const float t = 127.f * x, m = fmaf(x, r.inv, kRound), q = m - kRound;
   const float e = fmaf(-q, r.top, t), twice = 2.f * fabsf(e);
   const bool odd = __float_as_uint(m) & 1u;
   return twice > r.top || (twice == r.top && odd) ? q + copysignf(1.f, e) : q;
+}
+
+// The integers of N elements: the side of the half is looked at only where an element
+// lies on one or beyond, which takes half the instructions.
+template <int N>
+__device__ __forceinline__ void quantise_vec(float (&v)[N], const RowScale &r) {
+  const float half = 0.5f * r.top;
+  bool off = r.none;
+  float q[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float x = v[j] * r.up;
+    q[j] = fmaf(x, r.inv, kRound) - kRound;
+    off |= fabsf(fmaf(-q[j], r.top, 127.f * x)) >= half;
+  }
+  if (off) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) q[j] = quantised(v[j], r);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = q[j];
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
