@@ -26,7 +26,7 @@
 // 8192 x 4096 x 14336 takes 490 to 520 us (494 at cuBLAS's measured fp16 rate).  On the same
 // box: four warps for the even blocks and four for the odd, whole rows each, 524 for 504;
 // three or four places behind narrower accumulators 516 for 490; MMAs issued by a lane under
-// `if (lane == 0)` 640, as their descriptors go through that lane's registers one by one.
+// `if (lane == 0)` 613 for 543, as their descriptors are put together by that lane one by one.
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>

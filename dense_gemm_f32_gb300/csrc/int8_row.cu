@@ -10,8 +10,9 @@
 //    its first rows are on their way.
 //  * Rows on any alignment: a lane's aligned 16 bytes are put together with its
 //    neighbour's, so weights need no copy.
-//  * 1 x 4096 x 14336 in 13.3 us (floor 8.8), with a tokens' kernel ahead of int8_small.cu's
-//    17.9; the rule between them is int8_use_row's.
+//  * One token, 4096 -> 14336: 13.3 us (floor 8.8), 15.6 by a tokens' kernel and
+//    int8_small.cu; 1000 -> 1000 4.2 and 8.8; four tokens, 4096 -> 14336, 18.9 and 16.4: a
+//    token costs every weight another dp4a, so int8_use_row weighs both.
 //  * The product after another of this kind (the gated block's second) sends for its
 //    weights before the first is done, which signals after its own wait.
 #include <atomic>

@@ -15,9 +15,8 @@
 //    fp16, or for the last product to the type of the update.
 //  * A second product with the same B in one launch (the next Gram matrix's and
 //    the polynomials' products read the same polynomial).
-// Bound by the tensor pipe: 4096^3 symmetric in 52 us (36 at cuBLAS's measured rate for the
-// triangle), 17 of them and 3 products with X make the five steps of 4096 x 4096, 1.0 ms.
-// The epilogue's input comes by TMA ahead: a row per thread read from memory took 30 us more a product.
+// Bound by the tensor pipe: 4096^3 symmetric takes 48 to 51 us (37 at cuBLAS's measured rate
+// for the 136 tiles, which are 1.8 waves of 76 pairs; tensor pipe 62 to 65% busy), with X 83 (71; 72%).
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>

@@ -516,7 +516,8 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F,
  * read during the call; at most 64 in size.  steps: 1 to DGEMM_NEWTON_MAX_STEPS.  eps >=
  * 0 and finite.  Anything else: DGEMM_ERR_INVALID_VALUE.
  * The iteration runs in fp16 with fp32 sums, whatever the types: D is off by some
- * 0.002 of the update's norm (bf16 products would be off by 0.02).  With eps = 0 a
+ * 0.002 of the update's norm, up to 0.008 where a small matrix's singular values fall
+ * steeply (bf16 products would be off by 0.01 to 0.05).  With eps = 0 a
  * matrix of zeros, and always one with NaN or an infinity, gives NaN.  Coefficients
  * under which the iteration diverges give infinities and NaN past 2^7 or so.
  * work: dgemm_orthogonalize_workspace(rows, cols) bytes on a 16-byte boundary.
