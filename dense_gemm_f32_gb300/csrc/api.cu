@@ -175,10 +175,16 @@ cudaError_t scratch_alloc(void **ptr, size_t bytes, cudaStream_t stream) {
       props.location.type = cudaMemLocationTypeDevice;
       props.location.id = dev;
       cudaMemPool_t p = nullptr;
-      if ((e = cudaMemPoolCreate(&p, &props)) != cudaSuccess) return e;
       uint64_t keep = pool_keep_bytes();
-      if ((e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess) {
-        cudaMemPoolDestroy(p);
+      // Making the pool is no work on the stream: it is allowed while this thread captures one.
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+      if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
+      e = cudaMemPoolCreate(&p, &props);
+      if (e == cudaSuccess) e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+      const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+      if (e == cudaSuccess) e = back;
+      if (e != cudaSuccess) {
+        if (p != nullptr) cudaMemPoolDestroy(p);
         return e;
       }
       g_pools[dev] = p;

@@ -453,11 +453,12 @@ PyObject *quantize_int8(PyObject *const *a) {
   if (t && x.dim() != 2) value_error("x: expected a 2-D matrix");
   const cudaStream_t stream = current_stream(x);
   const auto floats = x.options().dtype(at::kFloat);
-  const int cols = t ? m.rows : m.cols;
+  // (longer rows than the library takes are refused by it)
+  const int pitch = (int)std::min<int64_t>(((int64_t)(t ? m.rows : m.cols) + 15) / 16 * 16, INT_MAX);
   const Tensor q = t ? rows_of_bytes({m.cols, m.rows}, x) : rows_of_bytes(x.sizes(), x);
   const Tensor s = t ? at::empty({m.cols}, floats) : at::empty(x.sizes().slice(0, x.dim() - 1), floats);
   check(dgemm_quantize_int8(dt, t ? DGEMM_OP_T : DGEMM_OP_N, m.rows, m.cols, m.p, m.ld,
-                            static_cast<signed char *>(q.data_ptr()), pos((cols + 15) / 16 * 16),
+                            static_cast<signed char *>(q.data_ptr()), pos(pitch),
                             static_cast<float *>(s.data_ptr()), stream),
         "quantize_int8");
   return tuple({&q, &s});
