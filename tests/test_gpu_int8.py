@@ -363,8 +363,9 @@ def test_rows_of_quantised_weights_are_aligned():
     assert q.shape == (7, 33) and q.stride() == (48, 1)
 
 
-@pytest.mark.parametrize("M, K, N", [(2048, 4096, 14336), (1000, 1008, 30000)])
-def test_many_tokens_with_one_weight_after_the_other(M, K, N):
+@pytest.mark.parametrize("M, K, N", [(2048, 4096, 14336), (1000, 1008, 30000), (3, 4096, 14336), (64, 14336, 4096),
+                                     (64, 4096, 14336), (200, 4096, 14336)])
+def test_one_weight_after_the_other(M, K, N):
     """Weights that alternate come from memory, not from L2: nothing is read before it
     has arrived, or after its place was given to the next block."""
     n = ref.make(M + N)
@@ -381,7 +382,7 @@ def test_many_tokens_with_one_weight_after_the_other(M, K, N):
             assert bool(((y.double() - d).abs() <= bound).all())
 
 
-def test_many_tokens_through_one_block_after_the_other():
+def test_one_block_after_the_other():
     M, D, F = 700, 2048, 8192
     n = ref.make(M)
     x = n((M, D), torch.bfloat16)
@@ -392,3 +393,44 @@ def test_many_tokens_through_one_block_after_the_other():
         got = [dg.gated_ffn_int8(x, *b, "silu") for b in blocks]
         for y, (d, bound) in zip(got, want):
             assert bool(((y.double() - d).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("nt", [32, 64, 96, 128, 160, 192])
+@pytest.mark.parametrize("M, N, K", [(70, 300, 1500), (500, 900, 384), (33, 4, 20), (191, 513, 129)])
+def test_every_pair_cut_gives_the_same(M, N, K, nt, monkeypatch):
+    n = ref.make(M)
+    x, (w, ws) = n((M, K), torch.float16), _ints(n, N, K)
+    (wu, su), (wd, sd) = _ints(n, N, K, 1), _ints(n, K, N, 2)
+    w, wu, wd = (torch.div(t, 16, rounding_mode="trunc") for t in (w, wu, wd))  # 127 * 8 * 1500 < 2^24
+    r, b = n((M, K), torch.float16), n((N,), torch.float16)
+    monkeypatch.setenv("DGEMM_INT8_ROW", "0")
+    monkeypatch.setenv("DGEMM_INT8_PAIR", "0")
+    want = dg.linear_int8(x, w, ws, bias=b, activation="silu")
+    block = dg.gated_ffn_int8(x, w, ws, wu, su, wd, sd, residual=r)
+    monkeypatch.setenv("DGEMM_INT8_PAIR", "1")
+    monkeypatch.setenv("DGEMM_INT8_NT", str(nt))
+    assert torch.equal(dg.linear_int8(x, w, ws, bias=b, activation="silu"), want)
+    assert torch.equal(dg.gated_ffn_int8(x, w, ws, wu, su, wd, sd, residual=r), block)
+
+
+def test_blocks_on_streams_and_graphs_at_once():
+    M, D, F = 96, 512, 1408
+    n = ref.make(3)
+    xs = [n((M, D), torch.bfloat16) for _ in range(4)]
+    weights = [t for s in ((F, D), (F, D), (D, F)) for t in dg.quantize_int8(n(s, torch.bfloat16, 0.05))]
+    want = [dg.gated_ffn_int8(x, *weights, residual=x) for x in xs]
+    graphs, outs = [], []
+    for x in xs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(dg.gated_ffn_int8(x, *weights, residual=x))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        late = [dg.gated_ffn_int8(x, *weights, residual=x, stream=s) for x, s in zip(xs[2:], streams[2:])]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs + late, want))

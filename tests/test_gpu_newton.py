@@ -210,3 +210,25 @@ def test_a_block_trained_with_orthogonalised_updates():
         lr = 0.02 * math.sqrt(max(1.0, p.shape[0] / p.shape[1]))
         dg.orthogonalize(grad, scale=-lr, residual=p, residual_scale=1 - 0.002, out=p)
         nr.check(p, grad, scale=-lr, residual=before, keep=1 - 0.002)
+
+
+@pytest.mark.parametrize("shape", [(2048, 4096), (4096, 2048), (600, 1500)])
+def test_updates_one_after_the_other(shape):
+    """Matrices that alternate, larger together than L2, on one stream and on two at once: every
+    result is the one of a call alone, to the last bit."""
+    n = ref.make(shape[0])
+    xs = [n(shape, torch.bfloat16) for _ in range(6)]
+    rs = [n(shape, torch.float32) for _ in range(6)]
+    want = []
+    for x, r in zip(xs, rs):
+        want.append(dg.orthogonalize(x, scale=-0.1, residual=r))
+        torch.cuda.synchronize()
+    for _ in range(3):
+        got = [dg.orthogonalize(x, scale=-0.1, residual=r) for x, r in zip(xs, rs)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [dg.orthogonalize(x, scale=-0.1, residual=r, stream=streams[i % 3]) for i, (x, r) in enumerate(zip(xs, rs))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
