@@ -231,31 +231,40 @@ int knob(const char *name, int lo, int hi) {
   return v >= lo && v <= hi ? v : -1;
 }
 
-// The quicker kernel and K split by time models (microseconds; graph replays on
-// GB300).  Small kernel: 3.4 us of launch, first load and epilogue, 0.27 us for a
-// CTA's stage of 64 k or its share where two run on an SM, 5 to 6.5 us for joining the
-// parts of a K split.  Pair kernel: 8 us, and 0.28 us per 64 k of a wave of 256 x 256
-// tiles.
+// The quicker kernel, tile and K split by time models (microseconds; graph replays on
+// GB300).  Small kernel: on 128 x 128 tiles 3.4 us of launch, first load and epilogue, and
+// 0.27 us for a CTA's stage of 64 k or its share where two run on an SM, 5 to 6.5 us for
+// joining the parts of a K split; on 128 x 64 tiles, half an epilogue on twice as many SMs,
+// 2.7 us and 0.255 for a stage, 0.165 its share.  (Five steps of 512 x 1408: 91 us on the
+// narrow tiles, 107 on the square ones; 1013 x 997: 116, 133; of 2048 x 2048, where the narrow
+// ones are two to an SM: 241, 215.)  Pair kernel: 8 us, and 0.28 us per 64 k of a wave of
+// 256 x 256 tiles.
 cudaError_t run(const NewtonGemm &p, int num_sms, int *wd, cudaStream_t stream) {
   const int f_pair = knob("DGEMM_NEWTON_PAIR", 0, 1), f_splits = knob("DGEMM_NEWTON_SPLITS", 1, 8);
-  auto tiles_of = [&](int t) {
-    const int64_t tm = (p.M + t - 1) / t, tn = (p.N + t - 1) / t;
-    return p.symmetric ? tm * (tm + 1) / 2 * (p.A2 != nullptr ? 2 : 1) : tm * tn;
+  const int f_tn = knob("DGEMM_NEWTON_TN", 64, 128);
+  auto tiles_of = [&](int t, int w) {  // t x w
+    const int64_t tm = (p.M + t - 1) / t, tn = (p.N + w - 1) / w;
+    return p.symmetric ? (tm * tn - t / w * (tm * (tm - 1) / 2)) * (p.A2 != nullptr ? 2 : 1) : tm * tn;
   };
-  const int64_t small = tiles_of(128), large = tiles_of(256), kblocks = (p.K + 63) / 64;
+  const int64_t small = tiles_of(128, 128), narrow = tiles_of(128, 64), large = tiles_of(256, 256), kblocks = (p.K + 63) / 64;
   const int64_t waves = (large + num_sms / 2 - 1) / (num_sms / 2);
   const double pair_time = 8.0 + 0.28 * (double)(waves * kblocks);
   double best = 0;
-  int splits = 1;
+  int splits = 1, tn = 128;
   for (int s = 1; s <= 8; s *= 2) {
     const int64_t ctas = small * s, per = (kblocks + s - 1) / s;
     const int64_t rounds = (ctas + num_sms - 1) / num_sms;
     const double t = 3.4 + (s > 1 ? 4.5 + 0.25 * s : 0.) + 0.27 * (double)(per * rounds);
     if (s == 1 || t < best) best = t, splits = s;
   }
+  const double share = 0.165 * (double)((narrow + num_sms - 1) / num_sms);
+  const double t64 = 2.7 + (share > 0.255 ? share : 0.255) * (double)kblocks;
+  if (t64 < best) best = t64, splits = 1, tn = 64;
   if (f_splits >= 0) splits = f_splits;
+  if (f_tn >= 0) tn = f_tn / 64 * 64;
+  if (splits > 1) tn = 128;
   const bool pair = f_pair >= 0 ? f_pair == 1 : pair_time < best;
-  return pair ? launch_newton_pair(p, wd, stream) : launch_newton_small(p, splits, num_sms, wd, stream);
+  return pair ? launch_newton_pair(p, wd, stream) : launch_newton_small(p, tn, splits, num_sms, wd, stream);
 }
 
 // Steps of the group that begins at step k.  (At m = n a step costs the same in a

@@ -2,8 +2,8 @@
 //
 // An iteration is a chain of some 16 products, each needing the one before, so with
 // few tiles its time is the latency of one product 16 times over.  Tiles here are
-// 128 x 128 on one CTA (tcgen05.mma.cta_group::1), one or two CTAs per SM, finished by
-// eight warps straight from the accumulator.  Where few tiles have a long K range, it
+// 128 x 128 or, on twice as many SMs, 128 x 64, on one CTA (tcgen05.mma.cta_group::1), one or
+// two CTAs per SM, finished by eight warps straight from the accumulator.  Where few tiles have a long K range, it
 // is split over a cluster of up to 8 CTAs, whose partial tiles are added through
 // distributed shared memory in K order, each CTA finishing a share of the tile's
 // rows.  Symmetric results: as in newton_pair.cu only the tiles on and above the diagonal
@@ -30,13 +30,14 @@
 namespace dg {
 namespace {
 
-template <int LAYOUT>
+template <int LAYOUT, int TN>  // tiles of 128 x TN
 struct Cfg {
   static constexpr bool kAT = LAYOUT == 2, kBT = LAYOUT == 1;
   static constexpr int T = 128, BK = 64, UMMA_K = 16;
   static constexpr int BOX = 64;  // elements in one 128-byte swizzle row
-  static constexpr int TILE_BYTES = T * 128, STAGE_BYTES = 2 * TILE_BYTES;
-  static constexpr int MAX_STAGES = 6;
+  static constexpr int TILE_BYTES = T * 128, STAGE_BYTES = TILE_BYTES + TN * 128;
+  static constexpr int MAX_STAGES = 8;
+  static constexpr int PIECES = TN / 64;  // of 32 x 32, a warp's
   static constexpr int BOX_BYTES = BK * 128;  // of an MN-major operand
   static constexpr int THREADS = 256;
   static constexpr int PARKED_BYTES = T * T * 4, TURN_PITCH = T + 8;  // the fp16 rows of a share
@@ -48,7 +49,7 @@ struct Cfg {
   static_assert(2 * (MIN_AREA + TAIL_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
   [[maybe_unused]] static constexpr uint32_t MN_LAYOUT = 2u, MN_SBO = 1024u;
   static constexpr uint32_t IDESC = (1u << 4) | ((kAT ? 1u : 0u) << 15) | ((kBT ? 0u : 1u) << 16) |
-                                    ((uint32_t)(T >> 3) << 17) | ((uint32_t)(T >> 4) << 24);
+                                    ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(T >> 4) << 24);
 };
 
 constexpr int kMaxSplits = 8;
@@ -86,6 +87,13 @@ struct Piece {
   }
 };
 
+// Tiles on and above the diagonal of a symmetric result.
+template <int TN>
+__host__ __device__ __forceinline__ int upper_tiles(int M, int tiles_n) {
+  const int tiles_m = (M + 127) / 128;
+  return tiles_m * tiles_n - 128 / TN * (tiles_m * (tiles_m - 1) / 2);
+}
+
 struct Args {
   int M, N, K;
   int splits, products, stall, stages, area;
@@ -113,27 +121,29 @@ __device__ __forceinline__ void load8(const O *row, int col, int cols, float (&f
   }
 }
 
-template <class O, int LAYOUT, bool SYM, bool SPLIT, bool AL>
-__global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
+template <class O, int LAYOUT, int TN, bool SYM, bool SPLIT, bool AL>
+__global__ void __launch_bounds__(Cfg<LAYOUT, TN>::THREADS, 2)
     newton_small_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
-  using G = Cfg<LAYOUT>;
+  using G = Cfg<LAYOUT, TN>;
+  static_assert(!SPLIT || TN == G::T, "a K split is of square tiles");
   constexpr bool kAT = G::kAT, kBT = G::kBT;
   pdl_launch_dependents();
   const int splits = SPLIT ? p.splits : 1;
   const int part = SPLIT ? blockIdx.x % splits : 0;
   int tile = SPLIT ? blockIdx.x / splits : blockIdx.x;
-  const int tiles_n = (p.N + G::T - 1) / G::T;
+  const int tiles_n = (p.N + TN - 1) / TN;
   int o = 0, tm, tn;
   if constexpr (SYM) {  // row by row on and above the diagonal
-    const int tiles1 = tiles_n * (tiles_n + 1) / 2;
+    constexpr int STEP = G::T / TN;
+    const int tiles1 = upper_tiles<TN>(p.M, tiles_n);
     if (tile >= tiles1) o = 1, tile -= tiles1;
     tm = 0;
-    while (tile >= tiles_n - tm) tile -= tiles_n - tm++;
-    tn = tm + tile;
+    while (tile >= tiles_n - STEP * tm) tile -= tiles_n - STEP * tm++;
+    tn = STEP * tm + tile;
   } else {
     tm = tile / tiles_n, tn = tile % tiles_n;
   }
-  const int m0 = tm * G::T, n0 = tn * G::T;
+  const int m0 = tm * G::T, n0 = tn * TN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -172,7 +182,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
     if (!SPLIT && p.in_tma) tma_prefetch_desc(&maps.in);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), G::T);
+    tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), TN);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();  // set-up done; the previous kernel on the stream has completed
 
-  // Without a K split a warp finishes two pieces of 32 x 32: rows of its quarter of the
+  // Without a K split a warp finishes one or two pieces of 32 x 32: rows of its quarter of the
   // tensor memory's lanes, columns of one half of the tile.  Those of in0 are sent
   // for now.  (A thread has a row of a piece; global memory is left to TMA, for whose
   // loads and stores the rows need not be neighbours: with the threads' own, 1024^2 took
@@ -190,16 +200,16 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
   const bool has_in0 = p.in0 != nullptr && o == 0;
   const O *in0 = static_cast<const O *>(p.in0);
   const int quarter = warp & 3, r_first = m0 + quarter * 32;
-  auto piece_col = [&](int h) { return n0 + 64 * (warp >> 2) + 32 * h; };
+  auto piece_col = [&](int h) { return n0 + (TN / 2) * (warp >> 2) + 32 * h; };
   // pieces below the diagonal come from those above it
   auto wanted = [&](int h) { return r_first < p.M && piece_col(h) < p.N && (!SYM || piece_col(h) >= r_first); };
-  const uint32_t in_buf = base + (uint32_t)(p.stages * G::STAGE_BYTES + warp * 2 * P::BYTES);
+  const uint32_t in_buf = base + (uint32_t)(p.stages * G::STAGE_BYTES + warp * G::PIECES * P::BYTES);
   int in_sent = 0;
   if (!SPLIT && has_in0 && p.in_tma) {
-    for (int h = 0; h < 2; ++h) in_sent += wanted(h) ? 1 : 0;
+    for (int h = 0; h < G::PIECES; ++h) in_sent += wanted(h) ? 1 : 0;
     if (lane == 0 && in_sent > 0) {
       mbar_arrive_expect_tx(in_bar(warp), (uint32_t)(in_sent * P::BYTES));
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < G::PIECES; ++h)
         if (wanted(h)) tma_load_2d(in_buf + (uint32_t)(h * P::BYTES), &maps.in, in_bar(warp), piece_col(h), r_first);
     }
     __syncwarp();
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
           tma_load_2d(a_tile(s), map_a, fb, k0, m0);
         }
         if (!kBT) {
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < TN / G::BOX; ++j)
             tma_load_2d(b_tile(s) + j * G::BOX_BYTES, &maps.b, fb, n0 + j * G::BOX, k0);
         } else {
           tma_load_2d(b_tile(s), &maps.b, fb, k0, n0);
@@ -344,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
     };
     if (has_in0 && !p.in_tma) {  // a row of a piece per instruction
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < G::PIECES; ++h) {
         if (!wanted(h)) continue;
         const int64_t c0 = piece_col(h) + lane;
         const O *src = in0 + (int64_t)r_first * p.ldi0 + c0;
@@ -358,8 +368,8 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
       }
       __syncwarp();
     }
-    // the stages are done with: two pieces for every two results
-    uint8_t *buf = smem + warp * (SYM ? 4 : 2) * P::BYTES;
+    // the stages are done with: a piece for every result, and for its mirrored place
+    uint8_t *buf = smem + warp * G::PIECES * (SYM ? 2 : 1) * P::BYTES;
     // A staged piece to rows row0.. and columns col0.. of the result
     auto send = [&](const uint8_t *piece, int row0, int col0) {
       const int valid = min(32, p.out_cols - col0);
@@ -383,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
     ok = ok && !__any_sync(0xffffffffu, *abort_flag != 0);
     tc_fence_after();
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < G::PIECES; ++h) {
       if (!ok || !wanted(h)) continue;  // the same for the whole warp
       const int col0 = piece_col(h);
       uint32_t x[32];
@@ -558,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 2)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, G::T);
+    tmem_dealloc(tmem_base, TN);
   }
 }
 
@@ -588,9 +598,9 @@ cudaError_t launch_one(unsigned grid, size_t smem, cudaStream_t stream, unsigned
   return e;
 }
 
-template <class O, int LAYOUT, bool SYM>
+template <class O, int LAYOUT, int TN, bool SYM>
 cudaError_t launch(const NewtonGemm &p, int splits, int num_sms, int *watchdog, cudaStream_t stream) {
-  using G = Cfg<LAYOUT>;
+  using G = Cfg<LAYOUT, TN>;
   Maps maps;
   memset(&maps, 0, sizeof maps);
   Args a;
@@ -603,12 +613,12 @@ cudaError_t launch(const NewtonGemm &p, int splits, int num_sms, int *watchdog, 
   };
   bool ok = map_a(&maps.a, p.A);
   if (p.A2 != nullptr) ok = ok && SYM && map_a(&maps.a2, p.A2);
-  ok = ok && (G::kBT ? make_map(&maps.b, p.B, dt, 2, p.N, p.K, p.ldb, G::BOX, G::T, swz)
+  ok = ok && (G::kBT ? make_map(&maps.b, p.B, dt, 2, p.N, p.K, p.ldb, G::BOX, TN, swz)
                      : make_map(&maps.b, p.B, dt, 2, p.K, p.N, p.ldb, G::BOX, G::BK, swz));
   // symmetric results are workspaces: rows of whole vectors
   const bool out_al = rows_aligned(p.out, p.ldo, sizeof(O)) && rows_aligned(p.out2, p.ldo, sizeof(O));
   if (!ok || p.K < 1 || (SYM && (p.M != p.N || !out_al || p.out_cols % 8 != 0)) ||
-      (splits != 1 && splits != 2 && splits != 4 && splits != 8))
+      (splits != 1 && (TN != G::T || (splits != 2 && splits != 4 && splits != 8))))
     return cudaErrorInvalidValue;
   a.M = p.M, a.N = p.N, a.K = p.K;
   a.splits = splits, a.products = p.A2 != nullptr ? 2 : 1;
@@ -619,15 +629,16 @@ cudaError_t launch(const NewtonGemm &p, int splits, int num_sms, int *watchdog, 
   a.out[0] = p.out, a.out[1] = p.out2;
   a.ldo = p.ldo, a.out_cols = (int)p.out_cols;
   a.watchdog = watchdog;
-  const int64_t tm = (p.M + G::T - 1) / G::T, tn = (p.N + G::T - 1) / G::T;
-  const int64_t tiles = SYM ? a.products * (tm * (tm + 1) / 2) : tm * tn;
+  const int64_t tm = (p.M + G::T - 1) / G::T, tn = (p.N + TN - 1) / TN;
+  if (tm * tn > 0x1fffffff) return cudaErrorInvalidValue;
+  const int64_t tiles = SYM ? (int64_t)a.products * upper_tiles<TN>(p.M, (int)tn) : tm * tn;
   if (tiles * splits > 0x3fffffff) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(tiles * splits), cluster = (unsigned)splits;
   // all of an SM's shared memory for one CTA's stages where that holds every CTA at once
   // (or where half of it is too little)
-  const int in_bytes = splits == 1 && p.in0 != nullptr ? G::WARPS * 2 * Piece<O>::BYTES : 0;
+  const int in_bytes = splits == 1 && p.in0 != nullptr ? G::WARPS * G::PIECES * Piece<O>::BYTES : 0;
   // without a K split the results' pieces take the stages' place, with one the parked tile
-  const int least = splits == 1 ? G::WARPS * (SYM ? 4 : 2) * Piece<O>::BYTES : G::MIN_AREA;
+  const int least = splits == 1 ? G::WARPS * G::PIECES * (SYM ? 2 : 1) * Piece<O>::BYTES : G::MIN_AREA;
   for (int half = grid > (unsigned)num_sms; half >= 0; --half) {
     const int budget = (half ? 113 * 1024 : 232448) - G::TAIL_BYTES;
     a.stages = (budget - in_bytes) / G::STAGE_BYTES;
@@ -636,8 +647,8 @@ cudaError_t launch(const NewtonGemm &p, int splits, int num_sms, int *watchdog, 
     if (splits > 1 && a.area < least) a.area = least;
     if (a.stages >= 2 && (splits > 1 || a.stages * G::STAGE_BYTES >= least)) break;
   }
-  static_assert(2 * G::STAGE_BYTES >= G::WARPS * 4 * Piece<__half>::BYTES && G::MIN_AREA + G::TAIL_BYTES <= 113 * 1024 &&
-                    4 * G::STAGE_BYTES + G::WARPS * 2 * Piece<O>::BYTES + G::TAIL_BYTES <= 232448,
+  static_assert(2 * G::STAGE_BYTES >= G::WARPS * G::PIECES * 2 * Piece<__half>::BYTES && G::MIN_AREA + G::TAIL_BYTES <= 113 * 1024 &&
+                    4 * G::STAGE_BYTES + G::WARPS * G::PIECES * Piece<O>::BYTES + G::TAIL_BYTES <= 232448,
                 "what is least always fits");
   if (splits == 1) {
     a.o_tma = out_al;
@@ -651,36 +662,43 @@ cudaError_t launch(const NewtonGemm &p, int splits, int num_sms, int *watchdog, 
   constexpr int B = 232448, T = G::THREADS;
   const bool al = SYM || (p.out_cols % (16 / (int)sizeof(O)) == 0 && out_al &&
                           (p.in0 == nullptr || rows_aligned(p.in0, p.ldi0, sizeof(O))));
-  if constexpr (SYM) {
-    return splits > 1 ? launch_one<newton_small_kernel<O, LAYOUT, true, true, true>, B, T>(grid, smem, stream, cluster, maps, a)
-                      : launch_one<newton_small_kernel<O, LAYOUT, true, false, true>, B, T>(grid, smem, stream, 1u, maps, a);
-  } else {
-    if (splits > 1)
-      return al ? launch_one<newton_small_kernel<O, LAYOUT, false, true, true>, B, T>(grid, smem, stream, cluster, maps, a)
-                : launch_one<newton_small_kernel<O, LAYOUT, false, true, false>, B, T>(grid, smem, stream, cluster, maps, a);
-    return launch_one<newton_small_kernel<O, LAYOUT, false, false, true>, B, T>(grid, smem, stream, 1u, maps, a);
+  if constexpr (TN == G::T) {
+    if (splits > 1) {
+      if constexpr (SYM)
+        return launch_one<newton_small_kernel<O, LAYOUT, TN, true, true, true>, B, T>(grid, smem, stream, cluster, maps, a);
+      else
+        return al ? launch_one<newton_small_kernel<O, LAYOUT, TN, false, true, true>, B, T>(grid, smem, stream, cluster, maps, a)
+                  : launch_one<newton_small_kernel<O, LAYOUT, TN, false, true, false>, B, T>(grid, smem, stream, cluster, maps, a);
+    }
   }
+  return launch_one<newton_small_kernel<O, LAYOUT, TN, SYM, false, true>, B, T>(grid, smem, stream, 1u, maps, a);
 }
 
+template <class O, int LAYOUT, bool SYM>
+cudaError_t launch_wide(const NewtonGemm &p, int tn, int splits, int num_sms, int *watchdog, cudaStream_t stream) {
+  return tn == 64 ? launch<O, LAYOUT, 64, SYM>(p, splits, num_sms, watchdog, stream)
+                  : launch<O, LAYOUT, 128, SYM>(p, splits, num_sms, watchdog, stream);
+}
 template <class O>
-cudaError_t launch_plain(const NewtonGemm &p, int splits, int num_sms, int *watchdog, cudaStream_t stream) {
-  return p.layout == 0 ? launch<O, 0, false>(p, splits, num_sms, watchdog, stream)
-                       : launch<O, 1, false>(p, splits, num_sms, watchdog, stream);
+cudaError_t launch_plain(const NewtonGemm &p, int tn, int splits, int num_sms, int *watchdog, cudaStream_t stream) {
+  return p.layout == 0 ? launch_wide<O, 0, false>(p, tn, splits, num_sms, watchdog, stream)
+                       : launch_wide<O, 1, false>(p, tn, splits, num_sms, watchdog, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_newton_small(const NewtonGemm &p, int splits, int num_sms, int *watchdog, cudaStream_t stream) {
+cudaError_t launch_newton_small(const NewtonGemm &p, int tn, int splits, int num_sms, int *watchdog,
+                                cudaStream_t stream) {
   if (p.symmetric) {
     if (p.dtype != DGEMM_DTYPE_F16 || p.layout == 0) return cudaErrorInvalidValue;
-    return p.layout == 1 ? launch<__half, 1, true>(p, splits, num_sms, watchdog, stream)
-                         : launch<__half, 2, true>(p, splits, num_sms, watchdog, stream);
+    return p.layout == 1 ? launch_wide<__half, 1, true>(p, tn, splits, num_sms, watchdog, stream)
+                         : launch_wide<__half, 2, true>(p, tn, splits, num_sms, watchdog, stream);
   }
   if (p.layout == 2) return cudaErrorInvalidValue;
   switch (p.dtype) {
-    case DGEMM_DTYPE_F32: return launch_plain<float>(p, splits, num_sms, watchdog, stream);
-    case DGEMM_DTYPE_BF16: return launch_plain<__nv_bfloat16>(p, splits, num_sms, watchdog, stream);
-    default: return launch_plain<__half>(p, splits, num_sms, watchdog, stream);
+    case DGEMM_DTYPE_F32: return launch_plain<float>(p, tn, splits, num_sms, watchdog, stream);
+    case DGEMM_DTYPE_BF16: return launch_plain<__nv_bfloat16>(p, tn, splits, num_sms, watchdog, stream);
+    default: return launch_plain<__half>(p, tn, splits, num_sms, watchdog, stream);
   }
 }
 

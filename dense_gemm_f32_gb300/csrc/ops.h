@@ -249,8 +249,9 @@ struct NewtonGemm {
   int64_t out_cols = 0;
 };
 cudaError_t launch_newton_pair(const NewtonGemm &p, int *watchdog, cudaStream_t stream);
-// The same on 128 x 128 tiles, the K range of each shared by `splits` (1, 2, 4 or 8) CTAs.
-cudaError_t launch_newton_small(const NewtonGemm &p, int splits, int num_sms, int *watchdog,
+// The same on 128 x tn tiles (128, or 64 without a split), the K range of each shared by
+// `splits` (1, 2, 4 or 8) CTAs.
+cudaError_t launch_newton_small(const NewtonGemm &p, int tn, int splits, int num_sms, int *watchdog,
                                 cudaStream_t stream);
 
 // The whole iteration (newton.cu); `work` of newton_workspace() bytes, 16-byte aligned.

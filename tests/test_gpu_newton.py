@@ -232,3 +232,19 @@ def test_updates_one_after_the_other(shape):
     got = [dg.orthogonalize(x, scale=-0.1, residual=r, stream=streams[i % 3]) for i, (x, r) in enumerate(zip(xs, rs))]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("plan", [dict(TN=64, SPLITS=1), dict(TN=128, SPLITS=1)], ids=str)
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows, cols", [(1, 1), (65, 64), (129, 200), (200, 129), (191, 193), (300, 700), (513, 520)])
+def test_every_tile_gives_the_same(rows, cols, dtype, plan, monkeypatch):
+    """Whatever the tiles, an element is the same sum in the same order of K."""
+    x, r = _gradient(rows, cols, dtype), ref.make(5)((rows, cols), dtype)
+    monkeypatch.setenv("DGEMM_NEWTON_PAIR", "0")
+    monkeypatch.setenv("DGEMM_NEWTON_TN", "64")
+    monkeypatch.setenv("DGEMM_NEWTON_SPLITS", "1")
+    want = dg.orthogonalize(x, scale=0.5, residual=r)
+    for k, v in plan.items():
+        monkeypatch.setenv("DGEMM_NEWTON_" + k, str(v))
+    assert torch.equal(dg.orthogonalize(x, scale=0.5, residual=r), want)
+    assert torch.equal(dg.orthogonalize(x, scale=0.5, residual=r), want)
