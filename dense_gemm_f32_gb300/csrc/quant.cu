@@ -24,34 +24,30 @@
 namespace dg {
 namespace {
 
-// Vectors of a row that a thread holds: 32 elements.
-template <class T>
-constexpr int kHolds = 32 / kVec<T>;
-
-// One row per block.
-template <class T, class O, bool ALIGNED, int THREADS>
+// One row per block, whose threads hold HELD vectors of it each.
+template <class T, class O, bool ALIGNED, int THREADS, int HELD>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     quantize_rows_kernel(int cols, const T *X, int64_t ldx, O *Q, int64_t ldq, float *scale,
                          bool vec) {
-  constexpr int V = kVec<T>, kHeld = kHolds<T>;
+  constexpr int V = kVec<T>;
   __shared__ uint32_t tops[THREADS / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t row = blockIdx.x;
   const T *x = X + row * ldx;
   O *out = Q + row * ldq;
-  RowBlocks b[kHeld];
+  RowBlocks b[HELD];
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k)
+  for (int k = 0; k < HELD; ++k)
     b[k] = fetch_row16<T, ALIGNED>(x, min((int)(threadIdx.x + k * THREADS), cols) * V, cols);
-  uint4 held[kHeld];
+  uint4 held[HELD];
   uint32_t top = 0;
   auto widest = [&](const float (&v)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) top = max(top, abs_bits(v[j]));
   };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
+  for (int k = 0; k < HELD; ++k) {
     const int col = min((int)(threadIdx.x + k * THREADS), cols) * V;
     if (col < cols) {
       float v[V];
@@ -60,7 +56,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       widest(v);
     }
   }
-  for (int64_t c = (int64_t)(threadIdx.x + kHeld * THREADS) * V; c < cols; c += THREADS * V) {
+  for (int64_t c = (int64_t)(threadIdx.x + HELD * THREADS) * V; c < cols; c += THREADS * V) {
     float v[V];
     widen16<T>(load_row16<T, ALIGNED>(x, (int)c, cols), v);
     widest(v);
@@ -76,7 +72,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     put<V>(out + col, v, cols - col, vec);
   };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
+  for (int k = 0; k < HELD; ++k) {
     const int col = min((int)(threadIdx.x + k * THREADS), cols) * V;
     if (col < cols) {
       float v[V];
@@ -84,7 +80,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       finish(v, col);
     }
   }
-  for (int64_t c = (int64_t)(threadIdx.x + kHeld * THREADS) * V; c < cols; c += THREADS * V) {
+  for (int64_t c = (int64_t)(threadIdx.x + HELD * THREADS) * V; c < cols; c += THREADS * V) {
     float v[V];
     widen16<T>(load_row16<T, ALIGNED>(x, (int)c, cols), v);
     finish(v, (int)c);
@@ -96,8 +92,9 @@ cudaError_t launch_rows(int rows, int cols, const void *X, int64_t ldx, O *Q, in
                         float *scale, int num_sms, cudaStream_t stream) {
   const bool al = rows_aligned(X, ldx, sizeof(T)) && cols % kVec<T> == 0;
   const bool vec = reinterpret_cast<uintptr_t>(Q) % kVec<T> == 0 && ldq % kVec<T> == 0;
-  // few rows, as in a decoding step: a thread per vector up to 512, then up to four in
-  // 1024, for the shortest chain; else threads that hold as many as they can
+  // Few rows, as in a decoding step: as many threads as hold one or two vectors each, for the
+  // shortest chain (64 rows of 4096 fp32 in 1.8 us, 2.1 with eight held); else threads that
+  // hold 32 elements.
   const int vecs = (cols + kVec<T> - 1) / kVec<T>;
   const bool few = rows <= 2 * num_sms;
   auto go = [&](auto kern, int threads) {
@@ -106,14 +103,17 @@ cudaError_t launch_rows(int rows, int cols, const void *X, int64_t ldx, O *Q, in
     if (e == cudaSuccess) count_launch();
     return e;
   };
-  if (vecs <= (few ? 128 : 128 * kHolds<T>))
-    return al ? go(quantize_rows_kernel<T, O, true, 128>, 128)
-              : go(quantize_rows_kernel<T, O, false, 128>, 128);
-  if (few && vecs > 512 * 2)
-    return al ? go(quantize_rows_kernel<T, O, true, 1024>, 1024)
-              : go(quantize_rows_kernel<T, O, false, 1024>, 1024);
-  return al ? go(quantize_rows_kernel<T, O, true, 512>, 512)
-            : go(quantize_rows_kernel<T, O, false, 512>, 512);
+#define DG_ROWS(threads, held)                                                \
+  (al ? go(quantize_rows_kernel<T, O, true, threads, held>, threads)        \
+      : go(quantize_rows_kernel<T, O, false, threads, held>, threads))
+  constexpr int MANY = 32 / kVec<T>;
+  if (few) {
+    if (vecs <= 128) return DG_ROWS(128, 1);
+    if (vecs <= 512 * 2) return DG_ROWS(512, 2);
+    return DG_ROWS(1024, MANY / 2);
+  }
+  return vecs <= 128 * MANY ? DG_ROWS(128, MANY) : DG_ROWS(512, MANY);
+#undef DG_ROWS
 }
 
 // The integers of X (int8) in fp16.
