@@ -105,7 +105,7 @@ bool int8_use_row(const Int8Gemm *p, int n, int num_sms) {
     other += small_plan(p[i], *res, num_sms, &plan) + 3.0;  // the tokens' kernel
     // the copy of weights on other than 16-byte boundaries
     const int mats = p[i].gated ? 2 : 1;
-    if (!rows_aligned(p[i].W, p[i].ldw, 1)) other += 3.0 + (double)p[i].N * p[i].K * mats / 2e6;
+    if (!rows_aligned(p[i].W, p[i].ldw, 1)) other += 1.0 + (double)p[i].N * p[i].K * mats / 3.5e6;
   }
   return force == 1 || row < other;
 }

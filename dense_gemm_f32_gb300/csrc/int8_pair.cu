@@ -98,7 +98,7 @@ struct Maps {
 
 struct Args {
   int M, N, K;
-  int act, nt, t_stages, group, stall;
+  int act, nt, t_stages, group, stall, early;
   uint32_t idesc;
   const float *t_scale, *w_scale, *w2_scale;
   const void *in0, *bias;
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if (warp == 0) {
       // ------------------------------------------------------------- weights
       if (lane == 0) {
+        if (!p.early) pdl_wait();
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -524,6 +525,7 @@ cudaError_t launch(const Int8Gemm &p, int nt, int *watchdog, cudaStream_t stream
     return cudaErrorInvalidValue;
   a.M = p.M, a.N = p.N, a.K = p.K;
   a.act = p.act, a.nt = nt;
+  a.early = p.early;
   a.t_stages = G::BUDGET / (nt * 128);
   if (a.t_stages > G::T_MAX_STAGES) a.t_stages = G::T_MAX_STAGES;
   static_assert(G::BUDGET / (G::MAX_NT * 128) >= G::T_MIN_STAGES, "a place is free when its tokens are");

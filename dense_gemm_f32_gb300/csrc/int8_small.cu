@@ -11,7 +11,8 @@
 //    memory (int8.cuh), half a row each; warp 1 issues tcgen05.mma with A from there.
 //  * The first stages of weights are loaded before the kernel ahead on the
 //    stream, which quantises the tokens, is done: it signals only after its own
-//    wait, so whatever wrote the weights is done by then.
+//    wait, so whatever wrote the weights is done by then.  (Not where that kernel also
+//    copies weights to rows that TMA can read.)
 //  * kGated: rows 0-63 are features of Wg, 64-127 the same of Wu; the hidden
 //    units go out in fp32, as the next step quantises them against the largest
 //    of their row: rounded to 16 bits before that, one in a hundred would become
@@ -71,7 +72,7 @@ struct Maps {
 
 struct Args {
   int M, N, K;
-  int act, nt, stages, splits, stall;
+  int act, nt, stages, splits, stall, early;
   uint32_t idesc, tmem_cols;
   const float *t_scale, *w_scale, *w2_scale;
   const void *in0, *bias;
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2)
         tma_load_2d(w_tile(s), &maps.w, full_bar(s), k0, f0);
         if constexpr (GATED) tma_load_2d(w_tile(s) + G::W_BYTES / 2, &maps.w2, full_bar(s), k0, f0);
       };
-      const int early = min(blocks, p.stages);
+      const int early = p.early ? min(blocks, p.stages) : 0;
       for (int i = 0; i < early; ++i) weights(i, (kb_begin + i) * G::BK);
       pdl_wait();  // the tokens are there
       int issued = 0, s = 0;
@@ -445,6 +446,7 @@ cudaError_t launch_small(const Int8Gemm &p, const Int8Plan &plan, int *watchdog,
   }
   a.M = p.M, a.N = p.N, a.K = p.K;
   a.act = p.act, a.nt = plan.nt, a.splits = plan.splits;
+  a.early = p.early;
   a.stages = stages_of(plan);
   a.stall = test_stall();
   // fp16 operands, both K-major, fp32 accumulator

@@ -165,17 +165,29 @@ cudaError_t launch_layer_norm_backward(int dtype, int rows, int cols, const void
                                        cudaStream_t stream);
 
 // ------------------------------------------------- 8-bit integer products
+// Copies of weights whose rows TMA cannot read to rows of `ldd` bytes (a multiple of 16), made
+// by the launch that puts the tokens into 8 bits.
+struct ByteCopies {
+  struct Job {
+    const uint8_t *src;
+    uint8_t *dst;
+    int64_t lds, ldd;
+    int rows, cols;
+  } job[3];
+  int n = 0;
+};
 // Rows of X as integers (quant.cu): Q in 8 bits, or T in fp16 with rows of whole
 // 16-byte vectors (ldt a multiple of 8), and a scale for each row.
 cudaError_t launch_quantize_rows(int dtype, int rows, int cols, const void *X, int64_t ldx,
                                  int8_t *Q, int64_t ldq, float *scale, int num_sms,
                                  cudaStream_t stream);
 cudaError_t launch_quantize_tokens(int dtype, int rows, int cols, const void *X, int64_t ldx,
-                                   void *T, int64_t ldt, float *scale, int num_sms,
-                                   cudaStream_t stream);
+                                   void *T, int64_t ldt, float *scale, const ByteCopies &copies,
+                                   int num_sms, cudaStream_t stream);
 // T = X, integers already.
 cudaError_t launch_expand_tokens(int rows, int cols, const int8_t *X, int64_t ldx, void *T,
-                                 int64_t ldt, int num_sms, cudaStream_t stream);
+                                 int64_t ldt, const ByteCopies &copies, int num_sms,
+                                 cudaStream_t stream);
 // Columns of X (rows x cols) as rows of Q (cols x rows); `tops`: scratch of cols words.
 cudaError_t launch_quantize_columns(int dtype, int rows, int cols, const void *X, int64_t ldx,
                                     int8_t *Q, int64_t ldq, float *scale, uint32_t *tops,
@@ -184,10 +196,10 @@ cudaError_t launch_quantize_columns(int dtype, int rows, int cols, const void *X
 // z[i][j] = t_scale[i] w_scale[j] sum_k T[i][k] W[j][k], T the integers in fp16 (M x
 // K, a multiple of 8 as leading dimension, written by the kernel just before on
 // the stream, one of the two above), W in 8 bits (N x K, rows on 16-byte
-// boundaries).  out = act(z + bias) + in0, of `dtype`; gated: out = act(z) z2 in
+// boundaries; early: they may be read before that kernel is done).  out = act(z + bias) + in0, of `dtype`; gated: out = act(z) z2 in
 // fp32 (ldo a multiple of 8), z2 from W2 and w2_scale.
 struct Int8Gemm {
-  bool gated = false;
+  bool gated = false, early = true;
   int dtype = 0, act = 0;
   int M = 0, N = 0, K = 0;
   const void *T = nullptr, *W = nullptr, *W2 = nullptr;

@@ -107,37 +107,36 @@ int with_scratch(size_t bytes, cudaStream_t stream, const char *what, F &&f) {
 }
 
 // Copies of 8-bit weights whose rows TMA cannot read, in stream-ordered scratch:
-// add() them, run() copies all of them in one launch per two and points the
-// operands there; release() after the last launch that reads them.
+// add() them, allocate() points the operands there and says what has to be copied (by the
+// tokens' launch), release() after the last launch that reads them.
 class ByteStager {
  public:
-  ByteStager(int num_sms, cudaStream_t stream) : num_sms_(num_sms), stream_(stream) {}
+  explicit ByteStager(cudaStream_t stream) : stream_(stream) {}
   void add(const void *&p, int64_t &ld, int rows, int cols) {
     if (rows == 0 || cols == 0 || tma_ok(p, ld, 1)) return;
-    ops_[n_] = {&p, &ld};
-    jobs_[n_++] = {p, ld, nullptr, line_pitch(cols, 1), rows, cols, false};
+    ops_[copies_.n] = {&p, &ld};
+    copies_.job[copies_.n++] = {static_cast<const uint8_t *>(p), nullptr, ld, line_pitch(cols, 1), rows, cols};
   }
-  cudaError_t run() {
-    if (n_ == 0) return cudaSuccess;
-    size_t at[kMax], total = 0;
-    for (int i = 0; i < n_; ++i) {
+  cudaError_t allocate() {
+    if (copies_.n == 0) return cudaSuccess;
+    size_t at[3], total = 0;
+    for (int i = 0; i < copies_.n; ++i) {
       at[i] = total;
-      total += (size_t)(jobs_[i].rows * jobs_[i].ldd + 255) / 256 * 256;
+      total += (size_t)(copies_.job[i].rows * copies_.job[i].ldd + 255) / 256 * 256;
     }
-    cudaError_t e = scratch_alloc(&scratch_, total, stream_);
+    const cudaError_t e = scratch_alloc(&scratch_, total, stream_);
     if (e != cudaSuccess) {
       scratch_ = nullptr;
       return e;
     }
-    for (int i = 0; i < n_; ++i) {
-      jobs_[i].dst = static_cast<char *>(scratch_) + at[i];
-      *ops_[i].p = jobs_[i].dst;
-      *ops_[i].ld = jobs_[i].ldd;
+    for (int i = 0; i < copies_.n; ++i) {
+      copies_.job[i].dst = static_cast<uint8_t *>(scratch_) + at[i];
+      *ops_[i].p = copies_.job[i].dst;
+      *ops_[i].ld = copies_.job[i].ldd;
     }
-    for (int i = 0; i < n_ && e == cudaSuccess; i += 2)
-      e = launch_stage(jobs_ + i, n_ - i < 2 ? n_ - i : 2, 1, num_sms_, stream_);
-    return e;
+    return cudaSuccess;
   }
+  const ByteCopies &copies() const { return copies_; }
   int release(int st) {
     if (scratch_ == nullptr) return st;
     const cudaError_t e = scratch_free(scratch_, stream_);
@@ -146,13 +145,11 @@ class ByteStager {
   }
 
  private:
-  static constexpr int kMax = 3;
   struct Operand {
     const void **p;
     int64_t *ld;
-  } ops_[kMax];
-  StageJob jobs_[kMax];
-  int n_ = 0, num_sms_;
+  } ops_[3];
+  ByteCopies copies_;
   cudaStream_t stream_;
   void *scratch_ = nullptr;
 };
@@ -494,15 +491,17 @@ int dgemm_linear_int8(int dtype, int activation, int M, int N, int K, const void
     p.t_scale = x_scale;
     return done(launch_int8_row(p, X, ldx, dtype, false, sms, stream), "integer product launch");
   }
-  ByteStager stage(sms, stream);
+  ByteStager stage(stream);
   stage.add(p.W, p.ldw, N, K);
-  if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
+  if ((st = done(stage.allocate(), "weight staging")) != DGEMM_OK) return stage.release(st);
   if (!x_scale)
-    st = done(launch_quantize_tokens(dtype, M, K, X, ldx, work, p.ldt, scale, sms, stream),
+    st = done(launch_quantize_tokens(dtype, M, K, X, ldx, work, p.ldt, scale, stage.copies(), sms, stream),
               "token launch");
   else if (K > 0)
-    st = done(launch_expand_tokens(M, K, static_cast<const int8_t *>(X), ldx, work, p.ldt, sms, stream),
+    st = done(launch_expand_tokens(M, K, static_cast<const int8_t *>(X), ldx, work, p.ldt, stage.copies(), sms,
+                                   stream),
               "token launch");
+  p.early = stage.copies().n == 0;  // else that launch writes the weights
   if (st == DGEMM_OK) st = done(launch_int8(p, sms, stream), "integer product launch");
   return stage.release(st);
 }
@@ -557,16 +556,18 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
   }
   const void *wg = Wg, *wu = Wu, *wd = Wd;
   int64_t lg = ldwg, lu = ldwu, ld = ldwd;
-  ByteStager stage(sms, stream);
+  ByteStager stage(stream);
   stage.add(wg, lg, F, D);
   stage.add(wu, lu, F, D);
   stage.add(wd, ld, D, F);
-  if ((st = done(stage.run(), "weight staging")) != DGEMM_OK) return stage.release(st);
+  if ((st = done(stage.allocate(), "weight staging")) != DGEMM_OK) return stage.release(st);
   if (F > 0) {
-    st = done(launch_quantize_tokens(dtype, M, D, X, ldx, tokens, line_pitch(D, 2), scale, sms, stream),
+    st = done(launch_quantize_tokens(dtype, M, D, X, ldx, tokens, line_pitch(D, 2), scale, stage.copies(), sms,
+                                     stream),
               "token launch");
     Int8Gemm p;
     p.gated = true, p.dtype = dtype, p.act = activation;
+    p.early = stage.copies().n == 0;  // else the tokens' launch writes weights
     p.M = M, p.N = F, p.K = D;
     p.T = tokens, p.ldt = line_pitch(D, 2), p.t_scale = scale;
     p.W = wg, p.ldw = lg, p.w_scale = g_scale;
@@ -575,7 +576,7 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
     if (st == DGEMM_OK) st = done(launch_int8(p, sms, stream), "gated integer product launch");
   }
   if (st == DGEMM_OK)
-    st = done(launch_quantize_tokens(DGEMM_DTYPE_F32, M, F, h, line_pitch(F, 4), tokens, line_pitch(F, 2), scale, sms,
+    st = done(launch_quantize_tokens(DGEMM_DTYPE_F32, M, F, h, line_pitch(F, 4), tokens, line_pitch(F, 2), scale, {}, sms,
                                      stream),
               "token launch");
   if (st == DGEMM_OK) {
