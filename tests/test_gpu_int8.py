@@ -364,7 +364,8 @@ def test_rows_of_quantised_weights_are_aligned():
 
 
 @pytest.mark.parametrize("M, K, N", [(2048, 4096, 14336), (1000, 1008, 30000), (3, 4096, 14336), (64, 14336, 4096),
-                                     (64, 4096, 14336), (200, 4096, 14336)])
+                                     (64, 4096, 14336), (200, 4096, 14336), (40, 2001, 20000),
+                                     (600, 2001, 20000)])
 def test_one_weight_after_the_other(M, K, N):
     """Weights that alternate come from memory, not from L2: nothing is read before it
     has arrived, or after its place was given to the next block."""
@@ -382,12 +383,13 @@ def test_one_weight_after_the_other(M, K, N):
             assert bool(((y.double() - d).abs() <= bound).all())
 
 
-def test_one_block_after_the_other():
-    M, D, F = 700, 2048, 8192
+@pytest.mark.parametrize("M, D, F", [(700, 2048, 8192), (700, 1001, 6007), (30, 1001, 6007)])
+def test_one_block_after_the_other(M, D, F):
     n = ref.make(M)
     x = n((M, D), torch.bfloat16)
     blocks = [[t for w in (n((F, D), torch.bfloat16, 0.05), n((F, D), torch.bfloat16, 0.05),
-                           n((D, F), torch.bfloat16, 0.05)) for t in dg.quantize_int8(w)] for _ in range(4)]
+                           n((D, F), torch.bfloat16, 0.05)) for t in (v.contiguous() for v in dg.quantize_int8(w))]
+              for _ in range(4)]
     want = [ref8.gated(x, *(_d(t) for t in b), "silu", None, torch.bfloat16) for b in blocks]
     for _ in range(4):
         got = [dg.gated_ffn_int8(x, *b, "silu") for b in blocks]
