@@ -13,7 +13,7 @@
 // the iteration enlarges, sit in the rounding of the large ones), and storing the
 // result in bf16 by 0.0017.
 //  * X_0 is kept as X 2^(8 - e), 2^e the power of two next above |X| + eps: exact for
-//    16-bit X but for elements 2^-30 below the norm.  The factor 2^e / (|X| + eps) that is
+//    16-bit X but for elements 2^-22 (fp16) or 2^-25 (bf16) of the norm and less.  The factor 2^e / (|X| + eps) that is
 //    missing goes into the first Gram matrix and the first product with X, in
 //    fp32.  Later X_k are kept times 2^8, the m x m matrices times 2^6.
 //  * Steps in groups.  All m x m matrices here are polynomials in A, so they are
@@ -21,16 +21,20 @@
 //    A + c A^2, the next step's Gram matrix is P A P, the product of the P so far is Q, and
 //    only the group's end forms Q X.  A step costs 4 products of m^3 / 2
 //    multiplications then, instead of one such, a Gram matrix (m^2 n / 2) and a
-//    product with X (m^2 n).  A rounding of A off the true Gram matrix is not
-//    noticed before the group ends, though, and grows by a^2 at the small
-//    singular values in every step.  So a group ends before that growth passes a
-//    limit: 2^8 in the first group of a matrix with m >= 512, where A's rounding
-//    is small because its trace of 1 is spread (three steps with the usual a =
-//    3.4445), 2^4 in the first of a smaller one and in later ones, where the large
-//    singular values are about 1 (two steps), one step at a time in a smaller
-//    matrix's later ones.  In 64-bit simulations of these roundings over spectra from flat to i^-2
-//    that is off by 0.0006 to 0.008 of the norm (single steps: 0.0006 to 0.010; three
-//    steps first at m = 64: 0.004 to 0.014; all five in one group overflows).
+//    product with X (m^2 n).  Two roundings work against each other.  One of A off
+//    the true Gram matrix is not noticed before the group ends, and grows by a^2 in every step
+//    where the singular values are small; how much of it is there depends on X, whose elements may
+//    all round alike (a few distinct values, low rank), not on its size.  And X is rounded
+//    when a group ends, which the steps after it enlarge by their a where X has no direction of its
+//    own.  So the first group takes steps while that growth is at most 2^4 (two with the usual a =
+//    3.4445; three, a growth of 2^7, put matrices of rank 1 and 2 off by 0.03 to 0.09), the second
+//    is one step (as two it put gradients off by 0.005 for 0.0014: it is there that most of the
+//    singular values come up to 1), and later ones take steps up to 2^4 again where that
+//    saves work, in wide matrices: at n = 1.25 m five steps as 2 + 1 + 2 cost 2% less than as 2 + 1 + 1 +
+//    1, at 3.5 m 15%.  In a small matrix, whose time is its launches, single steps are nearer.
+//    In 64-bit simulations of these roundings five steps are off by 0.0003 to 0.004 of the norm
+//    over spectra from flat to i^-1.5, 0.008 at i^-4, and at most 0.016, a matrix of rank one
+//    (the limit that include/dgemm.h states, 0.02, is what the roundings can add up to).
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -267,11 +271,10 @@ cudaError_t run(const NewtonGemm &p, int num_sms, int *wd, cudaStream_t stream) 
   return pair ? launch_newton_pair(p, wd, stream) : launch_newton_small(p, tn, splits, num_sms, wd, stream);
 }
 
-// Steps of the group that begins at step k.  (At m = n a step costs the same in a
-// group as alone, and the result is nearer.)
-int group_steps(const Orthogonalize &p, int k) {
-  const bool large = (p.rows < p.cols ? p.rows : p.cols) >= 512;
-  const double most = k == 0 ? (large ? 256. : 16.) : large ? 16. : 0.;
+// Steps of group number `group`, which begins at step k.
+int group_steps(const Orthogonalize &p, int k, int group) {
+  const int64_t m = p.rows < p.cols ? p.rows : p.cols, n = p.rows < p.cols ? p.cols : p.rows;
+  const double most = group == 0 || (group > 1 && m >= 512 && 4 * n > 5 * m) ? 16. : 0.;
   double growth = 1.;
   int steps = 1;
   while (k + steps < p.steps) {
@@ -317,8 +320,8 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
                                       w.partial, num_sms, stream);
   const float x_up = 0x1p8f, m_up = 0x1p6f;  // what X and the m x m matrices are kept times
   __half *x = w.x[0], *x_next = w.x[1];
-  for (int k = 0; k < p.steps && e == cudaSuccess;) {
-    const int steps = group_steps(p, k);
+  for (int k = 0, group = 0; k < p.steps && e == cudaSuccess; ++group) {
+    const int steps = group_steps(p, k, group);
     __half *A = w.square[0], *W = w.square[1], *P = w.square[2], *Q = nullptr;
     __half *spare[2] = {w.square[3], w.square[4]};
     {  // A = X X^T, or X^T X
