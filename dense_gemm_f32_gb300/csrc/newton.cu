@@ -15,7 +15,12 @@
 //  * X_0 is kept as X 2^(8 - e), 2^e the power of two next above |X| + eps: exact for
 //    16-bit X but for elements 2^-22 (fp16) or 2^-25 (bf16) of the norm and less.  The factor 2^e / (|X| + eps) that is
 //    missing goes into the first Gram matrix and the first product with X, in
-//    fp32.  Later X_k are kept times 2^8, the m x m matrices times 2^6.
+//    fp32.  An fp32 X is kept in two fp16 terms until the first group ends, 22 bits of it: its Gram
+//    matrix is then H H^T + H L^T + L H^T and the product Q H + Q L, the terms blocks of K of one
+//    product.  (Rounded to 11 bits an fp32 matrix of rank one was off by 0.15 of the result's norm,
+//    eight directions over a floor of 10^-3 by 0.03: the five steps enlarge what is rounded
+//    where X has no direction by a^5 = 485.  The second terms cost 4096 x 4096 171 us of 1082,
+//    14336 x 4096 738 of 2643.)  Later X_k are kept times 2^8, the m x m matrices times 2^6.
 //  * Steps in groups.  All m x m matrices here are polynomials in A, so they are
 //    symmetric and commute.  Within a group X stays where it is: with P = a I + b
 //    A + c A^2, the next step's Gram matrix is P A P, the product of the P so far is Q, and
@@ -38,6 +43,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "activation.cuh"
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(kThreads)
 template <class T, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads)
     scale_kernel(int rows, int cols, const T *X, int64_t ldx, float eps, const float *partial, int parts,
-                 __half *out, int64_t ldo, float *factor) {
+                 __half *out, __half *out_lo, int64_t ldo, float *factor) {
   constexpr int V = kVec<T>;
   __shared__ float fold[3][kThreads / 32];
   __shared__ float up[2];
@@ -170,11 +176,21 @@ __global__ void __launch_bounds__(kThreads)
       widen16<T>(take_row16<T, ALIGNED>(b[k], X + row * ldx, col, cols), f);
       uint32_t w[V / 2];
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) w[j] = pack2<__half>(f[2 * j] * u0 * u1, f[2 * j + 1] * u0 * u1);
+      for (int j = 0; j < V; ++j) f[j] = f[j] * u0 * u1;
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] = pack2<__half>(f[2 * j], f[2 * j + 1]);
       if constexpr (V == 8)  // rows of whole vectors, padded
         *reinterpret_cast<uint4 *>(out + row * ldo + col) = make_uint4(w[0], w[1], w[2], w[3]);
       else
         *reinterpret_cast<uint2 *>(out + row * ldo + col) = make_uint2(w[0], w[1]);
+      if constexpr (std::is_same<T, float>::value) {  // what fp16 leaves of an element
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 hi = unpack2<__half>(w[j]);
+          w[j] = pack2<__half>(f[2 * j] - hi.x, f[2 * j + 1] - hi.y);
+        }
+        *reinterpret_cast<uint2 *>(out_lo + row * ldo + col) = make_uint2(w[0], w[1]);
+      }
     }
   }
 }
@@ -182,8 +198,8 @@ __global__ void __launch_bounds__(kThreads)
 int scale_blocks(int num_sms) { return 2 * num_sms; }
 
 template <class T>
-cudaError_t launch_scale(int rows, int cols, const void *X, int64_t ldx, float eps, void *out, int64_t ldo,
-                         float *factor, float *partial, int num_sms, cudaStream_t stream) {
+cudaError_t launch_scale(int rows, int cols, const void *X, int64_t ldx, float eps, __half *out, __half *out_lo,
+                         int64_t ldo, float *factor, float *partial, int num_sms, cudaStream_t stream) {
   const T *x = static_cast<const T *>(X);
   const bool al = rows_aligned(X, ldx, sizeof(T)) && cols % kVec<T> == 0;
   const int64_t vecs = (int64_t)rows * ((cols + kVec<T> - 1) / kVec<T>);
@@ -195,7 +211,7 @@ cudaError_t launch_scale(int rows, int cols, const void *X, int64_t ldx, float e
   count_launch();
   e = launch_kernel(al ? scale_kernel<T, true> : scale_kernel<T, false>, dim3(blocks), dim3(kThreads), 0,
                     stream, 1u, rows, cols, x, ldx, eps, static_cast<const float *>(partial), blocks,
-                    static_cast<__half *>(out), ldo, factor);
+                    out, out_lo, ldo, factor);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -203,9 +219,10 @@ cudaError_t launch_scale(int rows, int cols, const void *X, int64_t ldx, float e
 // -------------------------------------------------------------- the iteration
 int64_t round256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
-// X, the next X, five m x m matrices, the factor and the partial sums (up to 512 SMs' worth).
+// X, the next X, what fp16 leaves of an fp32 X, five m x m matrices, the factor and the partial
+// sums (up to 512 SMs' worth).
 struct Work {
-  __half *x[2], *square[5];
+  __half *x[3], *square[5];
   float *factor, *partial;
   size_t bytes;
   Work(void *base, int rows, int cols) {
@@ -250,7 +267,8 @@ cudaError_t run(const NewtonGemm &p, int num_sms, int *wd, cudaStream_t stream) 
     const int64_t tm = (p.M + t - 1) / t, tn = (p.N + w - 1) / w;
     return p.symmetric ? (tm * tn - t / w * (tm * (tm - 1) / 2)) * (p.A2 != nullptr ? 2 : 1) : tm * tn;
   };
-  const int64_t small = tiles_of(128, 128), narrow = tiles_of(128, 64), large = tiles_of(256, 256), kblocks = (p.K + 63) / 64;
+  const int64_t small = tiles_of(128, 128), narrow = tiles_of(128, 64), large = tiles_of(256, 256);
+  const int64_t kblocks = (p.K + 63) / 64 * (1 + (p.A_lo != nullptr) + (p.B_lo != nullptr));
   const int64_t waves = (large + num_sms / 2 - 1) / (num_sms / 2);
   const double pair_time = 8.0 + 0.28 * (double)(waves * kblocks);
   double best = 0;
@@ -287,17 +305,17 @@ int group_steps(const Orthogonalize &p, int k, int group) {
 }
 
 // X in fp16 (rows of `ldt`, a multiple of 8) as X 2^(8 - e), and *factor = 2^e /
-// (norm + eps): X 2^(8 - e) factor / 256 is X / (norm + eps).  partial: three floats for
-// each of scale_blocks() blocks.
-cudaError_t scale_to_fp16(int dtype, int rows, int cols, const void *X, int64_t ldx, float eps, void *T,
-                          int64_t ldt, float *factor, float *partial, int num_sms, cudaStream_t stream) {
+// (norm + eps): X 2^(8 - e) factor / 256 is X / (norm + eps).  Of an fp32 X, T_lo is what T
+// leaves.  partial: three floats for each of scale_blocks() blocks.
+cudaError_t scale_to_fp16(int dtype, int rows, int cols, const void *X, int64_t ldx, float eps, __half *T,
+                          __half *T_lo, int64_t ldt, float *factor, float *partial, int num_sms, cudaStream_t stream) {
   switch (dtype) {
     case DGEMM_DTYPE_F32:
-      return launch_scale<float>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
+      return launch_scale<float>(rows, cols, X, ldx, eps, T, T_lo, ldt, factor, partial, num_sms, stream);
     case DGEMM_DTYPE_BF16:
-      return launch_scale<__nv_bfloat16>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
+      return launch_scale<__nv_bfloat16>(rows, cols, X, ldx, eps, T, nullptr, ldt, factor, partial, num_sms, stream);
     default:
-      return launch_scale<__half>(rows, cols, X, ldx, eps, T, ldt, factor, partial, num_sms, stream);
+      return launch_scale<__half>(rows, cols, X, ldx, eps, T, nullptr, ldt, factor, partial, num_sms, stream);
   }
 }
 
@@ -316,10 +334,12 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
   const bool tall = p.rows > p.cols;
   const int m = tall ? p.cols : p.rows, n = tall ? p.rows : p.cols;
   const int64_t ldx = line_pitch(p.cols, 2), ldm = line_pitch(m, 2);
-  cudaError_t e = scale_to_fp16(p.x_dtype, p.rows, p.cols, p.X, p.ldx, p.eps, w.x[0], ldx, w.factor,
-                                      w.partial, num_sms, stream);
+  cudaError_t e = scale_to_fp16(p.x_dtype, p.rows, p.cols, p.X, p.ldx, p.eps, w.x[0], w.x[2], ldx,
+                                w.factor, w.partial, num_sms, stream);
   const float x_up = 0x1p8f, m_up = 0x1p6f;  // what X and the m x m matrices are kept times
   __half *x = w.x[0], *x_next = w.x[1];
+  // (one row or column has no other directions in which its rounding would be enlarged)
+  const __half *lo = p.x_dtype == DGEMM_DTYPE_F32 && m > 1 ? w.x[2] : nullptr;
   for (int k = 0, group = 0; k < p.steps && e == cudaSuccess; ++group) {
     const int steps = group_steps(p, k, group);
     __half *A = w.square[0], *W = w.square[1], *P = w.square[2], *Q = nullptr;
@@ -332,6 +352,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
       g.A = g.B = x, g.lda = g.ldb = ldx;
       g.alpha = m_up / (x_up * x_up);
       if (k == 0) g.factor = w.factor, g.power = 2;
+      if (k == 0) g.A_lo = g.B_lo = lo;
       g.out = A, g.ldo = g.out_cols = ldm;
       e = run(g, num_sms, wd, stream);
     }
@@ -374,6 +395,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &p, void *work, int num_sms
       g.A = tall ? x : Q, g.lda = tall ? ldx : ldm;
       g.B = tall ? Q : x, g.ldb = tall ? ldm : ldx;
       if (k == 0) g.factor = w.factor, g.power = 1;
+      if (k == 0) (tall ? g.A_lo : g.B_lo) = lo;
       if (last) {
         g.dtype = p.dtype;
         g.alpha = p.scale / (x_up * m_up);

@@ -9,6 +9,18 @@
 
 namespace dg {
 
+// Blocks of K in the order in which a product with operands of two terms goes through them:
+// A B, then A B_lo (bit 0 of `lo`), then A_lo B (bit 1), `one` blocks each.
+struct TermBlock {
+  int k;              // block of K
+  bool a_lo, b_lo;    // of A_lo, B_lo
+};
+__host__ __device__ __forceinline__ int terms_of(int lo) { return 1 + (lo & 1) + (lo >> 1); }
+__device__ __forceinline__ TermBlock term_block(int kq, int one, int lo) {
+  const int all = one * terms_of(lo), k = kq >= 2 * one ? kq - 2 * one : kq >= one ? kq - one : kq;
+  return {k, (lo & 2) && kq >= all - one, (lo & 1) && kq >= one && kq < 2 * one};
+}
+
 // gamma on the diagonal of a piece.  As a choice of what is added: a choice of where to
 // is compiled into a branch for every lane, 1400 cycles.
 __device__ __forceinline__ void add_diagonal(float (&v)[32], int lane, float gamma) {

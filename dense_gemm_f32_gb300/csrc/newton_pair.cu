@@ -78,7 +78,7 @@ enum : int {
 };
 
 struct Maps {
-  CUtensorMap a, a2, b, o[2], in;
+  CUtensorMap a, a2, b, b2, o[2], in;  // a2: of A2, or of A_lo; b2: of B_lo
 };
 
 struct Args {
@@ -87,6 +87,7 @@ struct Args {
   int o_tma;  // outputs may be written by TMA
   int in_vec, in_tma;  // rows of in0 are aligned; it may be read by TMA
   int stages;
+  int lo;  // B_lo (1), A_lo (2)
   float alpha, beta, gamma;
   const float *factor;
   int power;
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
   const int tiles_m = (p.M + G::BM - 1) / G::BM, tiles_n = (p.N + G::BN - 1) / G::BN;
   const int tiles1 = SYM ? upper_tiles(tiles_m) : tiles_m * tiles_n;  // of one product
   const int num_tiles = SYM ? p.products * tiles1 : tiles1;
-  const int kblocks = (p.K + G::BK - 1) / G::BK;
+  const int kblocks1 = (p.K + G::BK - 1) / G::BK, kblocks = kblocks1 * terms_of(p.lo);
   auto coords = [&](int tile, int &tm, int &tn) {
     if constexpr (SYM)
       upper_coords(tile >= tiles1 ? tile - tiles1 : tile, tiles_m, tm, tn);
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
       for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
         int tm, tn;
         coords(tile, tm, tn);
-        const CUtensorMap *map_a = SYM && tile >= tiles1 ? &maps.a2 : &maps.a;
+        const bool second = SYM && tile >= tiles1;
         const int m0 = tm * G::BM + (int)rank * G::HM, n0 = tn * G::BN + (int)rank * G::HN;
         for (int kq = 0; kq < kblocks; ++kq) {
           if (!mbar_try_wait(empty_bar(stage), phase ^ 1u) &&
@@ -262,7 +263,10 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
             break;
           }
           const uint32_t fb = fb0 + 8u * (uint32_t)stage;
-          const int k0 = kq * G::BK;
+          const TermBlock at = term_block(kq, kblocks1, p.lo);
+          const CUtensorMap *map_a = second || at.a_lo ? &maps.a2 : &maps.a;
+          const CUtensorMap *map_b = at.b_lo ? &maps.b2 : &maps.b;
+          const int k0 = at.k * G::BK;
           if (is_a) {
             if (kAT && (p.mn3d & kA3d)) {
               tma_load_3d_pair(a_tile(stage), map_a, fb, 0, k0, m0 / G::BOX);
@@ -274,11 +278,11 @@ __global__ void __launch_bounds__(Cfg<LAYOUT>::THREADS, 1)
             }
           } else {
             if (!kBT && (p.mn3d & kB3d)) {
-              tma_load_3d_pair(b_tile(stage), &maps.b, fb, 0, k0, n0 / G::BOX);
+              tma_load_3d_pair(b_tile(stage), map_b, fb, 0, k0, n0 / G::BOX);
             } else {
 #pragma unroll
               for (int j = 0; j < G::B_BOXES; ++j)
-                tma_load_2d_pair(b_tile(stage) + j * G::B_BOX_BYTES, &maps.b, fb,
+                tma_load_2d_pair(b_tile(stage) + j * G::B_BOX_BYTES, map_b, fb,
                                  kBT ? k0 : n0 + j * G::BOX, kBT ? n0 : k0);
             }
           }
@@ -610,16 +614,19 @@ cudaError_t launch(const NewtonGemm &p, int *watchdog, cudaStream_t stream) {
     }
     return make_map(map, A, dt, 2, p.K, p.M, p.lda, G::BOX, G::BK, swz);
   };
-  bool ok = map_a(&maps.a, p.A);
-  if (p.A2 != nullptr) ok = ok && SYM && map_a(&maps.a2, p.A2);
-  if (G::kBT) {
-    ok = ok && make_map(&maps.b, p.B, dt, 2, p.N, p.K, p.ldb, G::BOX, G::HN, swz);
-  } else if (p.N % G::BOX == 0) {
-    a.mn3d |= kB3d;
-    ok = ok && make_map3(&maps.b, p.B, dt, 2, p.K, p.N, p.ldb, G::BOX, G::BK, G::HN / G::BOX, swz);
-  } else {
-    ok = ok && make_map(&maps.b, p.B, dt, 2, p.K, p.N, p.ldb, G::BOX, G::BK, swz);
-  }
+  auto map_b = [&](CUtensorMap *map, const void *B) {
+    if (G::kBT) return make_map(map, B, dt, 2, p.N, p.K, p.ldb, G::BOX, G::HN, swz);
+    if (p.N % G::BOX == 0) {
+      a.mn3d |= kB3d;
+      return make_map3(map, B, dt, 2, p.K, p.N, p.ldb, G::BOX, G::BK, G::HN / G::BOX, swz);
+    }
+    return make_map(map, B, dt, 2, p.K, p.N, p.ldb, G::BOX, G::BK, swz);
+  };
+  bool ok = map_a(&maps.a, p.A) && map_b(&maps.b, p.B);
+  if (p.A2 != nullptr) ok = ok && SYM && p.A_lo == nullptr && p.B_lo == nullptr && map_a(&maps.a2, p.A2);
+  if (p.A_lo != nullptr) ok = ok && map_a(&maps.a2, p.A_lo);
+  if (p.B_lo != nullptr) ok = ok && map_b(&maps.b2, p.B_lo);
+  a.lo = (p.B_lo != nullptr ? 1 : 0) | (p.A_lo != nullptr ? 2 : 0);
   if (!ok || p.K < 1 || (SYM && p.M != p.N)) return cudaErrorInvalidValue;
   a.M = p.M, a.N = p.N, a.K = p.K;
   a.products = p.A2 != nullptr ? 2 : 1;

@@ -67,7 +67,7 @@ enum : int {
 };
 
 struct Maps {
-  CUtensorMap a, a2, b;
+  CUtensorMap a, a2, b, b2;  // a2: of A2, or of A_lo; b2: of B_lo
   CUtensorMap o[2], in;  // 32 x 32 boxes
 };
 
@@ -97,6 +97,7 @@ __host__ __device__ __forceinline__ int upper_tiles(int M, int tiles_n) {
 struct Args {
   int M, N, K;
   int splits, products, stall, stages, area;
+  int lo;             // B_lo (1), A_lo (2)
   int o_tma, in_tma;  // without a K split: outputs may be written, in0 may be read by TMA
   float alpha, beta, gamma;
   const float *factor;
@@ -161,7 +162,8 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, TN>::THREADS, 2)
   auto b_tile = [&](int s) { return base + (uint32_t)(s * G::STAGE_BYTES + G::TILE_BYTES); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kblocks = (p.K + G::BK - 1) / G::BK, per = (kblocks + splits - 1) / splits;
+  const int kblocks1 = (p.K + G::BK - 1) / G::BK, kblocks = kblocks1 * terms_of(p.lo);
+  const int per = (kblocks + splits - 1) / splits;
   const int kb_begin = min(kblocks, part * per), blocks = min(kblocks, part * per + per) - kb_begin;
 
   if (threadIdx.x == 0) {
@@ -233,7 +235,6 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, TN>::THREADS, 2)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const CUtensorMap *map_a = o ? &maps.a2 : &maps.a;
       int issued = 0, s = 0;
       uint32_t phase = 1;  // a fresh barrier's phase before is complete
       bool ok = true;
@@ -243,7 +244,9 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, TN>::THREADS, 2)
           ok = false;
           break;
         }
-        const int k0 = (kb_begin + i) * G::BK;
+        const TermBlock at = term_block(kb_begin + i, kblocks1, p.lo);
+        const CUtensorMap *map_a = o || at.a_lo ? &maps.a2 : &maps.a, *map_b = at.b_lo ? &maps.b2 : &maps.b;
+        const int k0 = at.k * G::BK;
         const uint32_t fb = full_bar(s);
         if (kAT) {  // MN-major: 64 rows of the result x 64 k per box
           for (int j = 0; j < 2; ++j)
@@ -253,9 +256,9 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, TN>::THREADS, 2)
         }
         if (!kBT) {
           for (int j = 0; j < TN / G::BOX; ++j)
-            tma_load_2d(b_tile(s) + j * G::BOX_BYTES, &maps.b, fb, n0 + j * G::BOX, k0);
+            tma_load_2d(b_tile(s) + j * G::BOX_BYTES, map_b, fb, n0 + j * G::BOX, k0);
         } else {
-          tma_load_2d(b_tile(s), &maps.b, fb, k0, n0);
+          tma_load_2d(b_tile(s), map_b, fb, k0, n0);
         }
         mbar_arrive_expect_tx(fb, G::STAGE_BYTES);  // announced after the copies are issued
         ++issued;
@@ -611,10 +614,15 @@ cudaError_t launch(const NewtonGemm &p, int splits, int num_sms, int *watchdog, 
     return G::kAT ? make_map(map, A, dt, 2, p.K, p.M, p.lda, G::BOX, G::BK, swz)
                   : make_map(map, A, dt, 2, p.M, p.K, p.lda, G::BOX, G::T, swz);
   };
-  bool ok = map_a(&maps.a, p.A);
-  if (p.A2 != nullptr) ok = ok && SYM && map_a(&maps.a2, p.A2);
-  ok = ok && (G::kBT ? make_map(&maps.b, p.B, dt, 2, p.N, p.K, p.ldb, G::BOX, TN, swz)
-                     : make_map(&maps.b, p.B, dt, 2, p.K, p.N, p.ldb, G::BOX, G::BK, swz));
+  auto map_b = [&](CUtensorMap *map, const void *B) {
+    return G::kBT ? make_map(map, B, dt, 2, p.N, p.K, p.ldb, G::BOX, TN, swz)
+                  : make_map(map, B, dt, 2, p.K, p.N, p.ldb, G::BOX, G::BK, swz);
+  };
+  bool ok = map_a(&maps.a, p.A) && map_b(&maps.b, p.B);
+  if (p.A2 != nullptr) ok = ok && SYM && p.A_lo == nullptr && p.B_lo == nullptr && map_a(&maps.a2, p.A2);
+  if (p.A_lo != nullptr) ok = ok && map_a(&maps.a2, p.A_lo);
+  if (p.B_lo != nullptr) ok = ok && map_b(&maps.b2, p.B_lo);
+  a.lo = (p.B_lo != nullptr ? 1 : 0) | (p.A_lo != nullptr ? 2 : 0);
   // symmetric results are workspaces: rows of whole vectors
   const bool out_al = rows_aligned(p.out, p.ldo, sizeof(O)) && rows_aligned(p.out2, p.ldo, sizeof(O));
   if (!ok || p.K < 1 || (SYM && (p.M != p.N || !out_al || p.out_cols % 8 != 0)) ||

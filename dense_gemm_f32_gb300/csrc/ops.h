@@ -242,14 +242,16 @@ cudaError_t launch_int8_pair(const Int8Gemm &p, int nt, int *watchdog, cudaStrea
 // 16-byte boundaries.  symmetric: the result is (M = N), half of its tiles are
 // computed and written to both places; layouts 1 and 2, fp16 results.  With A2, a
 // second product A2 B goes to out2 in the same launch, without in0 and gamma
-// (symmetric ones only).  out and in0 are of `dtype`; out_cols: columns that may be
+// (symmetric ones only).  A_lo, B_lo (laid out like A, B; not with A2): what A and B leave
+// of operands of more than 11 bits; the product is A B + A B_lo + A_lo B then, in one
+// accumulator, without the terms that are null.  out and in0 are of `dtype`; out_cols: columns that may be
 // written, N or more (a workspace's padding).
 struct NewtonGemm {
   int layout = 1;
   bool symmetric = false;
   int dtype = 0;  // dgemm_dtype_t
   int M = 0, N = 0, K = 0;
-  const void *A = nullptr, *A2 = nullptr, *B = nullptr;
+  const void *A = nullptr, *A2 = nullptr, *B = nullptr, *A_lo = nullptr, *B_lo = nullptr;
   int64_t lda = 0, ldb = 0;
   float alpha = 1.f, beta = 0.f, gamma = 0.f;
   const float *factor = nullptr;

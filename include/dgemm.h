@@ -515,7 +515,8 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F,
  * coefficients: 3 * steps finite floats in HOST memory, a_k, b_k, c_k in turn,
  * read during the call; at most 64 in size.  steps: 1 to DGEMM_NEWTON_MAX_STEPS.  eps >=
  * 0 and finite.  Anything else: DGEMM_ERR_INVALID_VALUE.
- * The iteration runs in fp16 with fp32 sums, whatever the types.  Five steps of a = 3.4445,
+ * The iteration runs in fp16 with fp32 sums, whatever the types; an X in fp32 begins it as two
+ * fp16 terms.  Five steps of a = 3.4445,
  * -4.7750, 2.0315 are off by some 0.0015 of the update's norm for gradients with a few strong
  * directions over noise, 0.004 to 0.008 where the singular values fall as i^-2 to i^-4, and at
  * most 0.02, which a matrix of rank one comes near to (all products in bf16: 0.005 to 0.26).

@@ -34,7 +34,7 @@ def _off(x, **kw):
     return float((got - want).norm() / want.norm())
 
 
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
 @pytest.mark.parametrize("rows, cols", SIZES)
 @pytest.mark.parametrize("name", ns.NAMES)
 def test_within_the_documented_limit(name, rows, cols, dtype):
@@ -47,3 +47,29 @@ def test_within_the_documented_limit(name, rows, cols, dtype):
 def test_fewer_steps(name, rows, cols, steps):
     """Each step less enlarges what was rounded by a less."""
     assert _off(ns.make(name, rows, cols, torch.float16).cuda(), steps=steps) <= ns.LIMIT
+
+
+PLANS = [dict(PAIR=1), dict(PAIR=0, SPLITS=1, TN=64), dict(PAIR=0, SPLITS=1, TN=128), dict(PAIR=0, SPLITS=2),
+         dict(PAIR=0, SPLITS=8)]
+
+
+@pytest.mark.parametrize("plan", PLANS, ids=str)
+@pytest.mark.parametrize("rows, cols", [(40, 60), (60, 40), (130, 520), (520, 130), (257, 255), (513, 1030), (700, 515)])
+@pytest.mark.parametrize("name", ["rank one", "i^-2", "eight over a floor"])
+def test_both_terms_of_fp32_on_every_kernel_and_cut(name, rows, cols, plan, monkeypatch):
+    """Where either term of an fp32 matrix were lost, a matrix of rank one would be off by 0.15."""
+    for k, v in plan.items():
+        monkeypatch.setenv("DGEMM_NEWTON_" + k, str(v))
+    x = ns.make(name, rows, cols, torch.float32).cuda()
+    assert _off(x) <= ns.LIMIT
+    assert _off(x, steps=1) <= 2.0 ** -10  # one group: P of 2^-12, the result stored in fp32
+    wide = torch.full((rows, cols + 3), float("nan"), device="cuda")
+    wide[:, 1:cols + 1] = x
+    assert torch.equal(dg.orthogonalize(wide[:, 1:cols + 1]), dg.orthogonalize(x))
+
+
+def test_fp32_matrices_that_fp16_holds_are_those():
+    """Nothing is left of them for the second term: the result of the fp16 matrix, to the last bit."""
+    x = ns.make("i^-1", 300, 700, torch.float16).cuda()
+    out = [torch.empty(x.shape, device="cuda") for _ in range(2)]
+    assert torch.equal(dg.orthogonalize(x, out=out[0]), dg.orthogonalize(x.float(), out=out[1]))
