@@ -59,8 +59,11 @@ constexpr int kThreads = 512;
 constexpr int kAhead = 4;  // vectors of a thread in flight
 
 // Sums of squares in three scales, one of which neither overflows nor loses a
-// share that matters, whatever the elements' size.
-constexpr float kUp = 0x1p70f, kDown = 0x1p-70f;
+// share that matters, whatever the elements' size: the plain one from 2^-80 to 2^100 (2^38
+// elements of one size have squares of 2^-118 there, a normal number); below it (x 2^100)^2, which
+// are 2^-98 for the smallest subnormal and 2^120 in sum at most; above it (x 2^-90)^2, 2^76 for the
+// largest number and 2^-118 for 2^38 elements that reach 2^100 together.
+constexpr float kUp = 0x1p100f, kDown = 0x1p-90f;
 struct Squares {
   float mid = 0.f, big = 0.f, small = 0.f;
   __device__ __forceinline__ void add(float x) {
@@ -142,9 +145,9 @@ __global__ void __launch_bounds__(kThreads)
     // their range alone: sums in them took 3 us more.
     double norm;
     if (!(t[0] < 0x1p100f))
-      norm = sqrtf(t[1]) * 0x1p70;
-    else if (t[0] < 0x1p-60f)
-      norm = sqrtf(t[2]) * 0x1p-70;
+      norm = sqrtf(t[1]) * 0x1p90;
+    else if (t[0] < 0x1p-80f)
+      norm = sqrtf(t[2]) * 0x1p-100;
     else
       norm = sqrtf(t[0]);
     norm += (double)eps;

@@ -73,3 +73,19 @@ def test_fp32_matrices_that_fp16_holds_are_those():
     x = ns.make("i^-1", 300, 700, torch.float16).cuda()
     out = [torch.empty(x.shape, device="cuda") for _ in range(2)]
     assert torch.equal(dg.orthogonalize(x, out=out[0]), dg.orthogonalize(x.float(), out=out[1]))
+
+
+@pytest.mark.parametrize("dtype, least", [(torch.float32, -149), (torch.bfloat16, -133)], ids=str)
+@pytest.mark.parametrize("rows, cols", [(64, 100), (512, 600)])
+def test_the_ends_of_the_types(rows, cols, dtype, least):
+    """A power of two on X changes nothing where eps is 0, down to subnormal numbers and up to
+    the largest ones, whose squares' sum is 2^270."""
+    gen = torch.Generator().manual_seed(1)
+    x = torch.randint(-7, 8, (rows, cols), generator=gen).double().cuda()
+    out = [torch.empty((rows, cols), device="cuda") for _ in range(2)]
+    want = dg.orthogonalize(x.to(dtype), eps=0.0, out=out[0])
+    assert torch.isfinite(want).all()
+    for up in (least, least + 4, least + 20, -100, -60, -30, 30, 60, 100, 120, 125):
+        y = (x * 2.0 ** up).to(dtype)
+        assert torch.equal(y.double(), x * 2.0 ** up)
+        assert torch.equal(dg.orthogonalize(y, eps=0.0, out=out[1]), want), up
