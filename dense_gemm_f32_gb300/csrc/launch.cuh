@@ -3,12 +3,18 @@
 // Every kernel of the library is launched with the programmatic stream
 // serialization attribute: the GPU may start scheduling it while the kernel
 // before it on the stream is still finishing (each kernel signals this with
-// griddepcontrol.launch_dependents as soon as it starts).  The launched
+// griddepcontrol.launch_dependents as soon as it starts, but for those below).  The launched
 // kernel then runs its set-up (barrier initialisation, tensor-memory
 // allocation, descriptor prefetch) and executes griddepcontrol.wait, which
 // returns once the previous kernel has completed and its memory is visible,
 // before it touches global memory.  Back-to-back calls thus hide the launch
 // gap and the set-up of the next kernel.  DGEMM_PDL=0 launches plainly.
+//
+// The exceptions go together.  The 8-bit products (int8_small.cu, int8_pair.cu with
+// Int8Gemm::early, int8_row.cu with its `early`) read their weights, nothing else, before their wait.  That
+// is right only where the kernel ahead of them on the stream neither writes those weights nor
+// signals before its own wait has returned, so that whatever did write them is done: the kernels of
+// quant.cu and int8_row.cu, which no other may be put in the place of.
 #pragma once
 
 #include <cstdlib>

@@ -196,10 +196,12 @@ cudaError_t launch_quantize_columns(int dtype, int rows, int cols, const void *X
 // z[i][j] = t_scale[i] w_scale[j] sum_k T[i][k] W[j][k], T the integers in fp16 (M x
 // K, a multiple of 8 as leading dimension, written by the kernel just before on
 // the stream, one of the two above), W in 8 bits (N x K, rows on 16-byte
-// boundaries; early: they may be read before that kernel is done).  out = act(z + bias) + in0, of `dtype`; gated: out = act(z) z2 in
+// boundaries; early: they may be read before that kernel is done, as everything before it is
+// once it signals, which quant.cu's kernels do only after their own wait, and it writes no weights
+// itself).  out = act(z + bias) + in0, of `dtype`; gated: out = act(z) z2 in
 // fp32 (ldo a multiple of 8), z2 from W2 and w2_scale.
 struct Int8Gemm {
-  bool gated = false, early = true;
+  bool gated = false, early = false;
   int dtype = 0, act = 0;
   int M = 0, N = 0, K = 0;
   const void *T = nullptr, *W = nullptr, *W2 = nullptr;

@@ -584,6 +584,7 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F, const v
     p.dtype = dtype;
     p.M = M, p.N = D, p.K = F;
     p.T = tokens, p.ldt = line_pitch(F, 2), p.t_scale = scale;
+    p.early = true;  // copies of weights were made by the first tokens' launch
     p.W = wd, p.ldw = ld, p.w_scale = d_scale;
     p.in0 = R, p.ldi0 = ldr, p.out = Y, p.ldo = ldy;
     st = done(launch_int8(p, sms, stream), "down integer product launch");
