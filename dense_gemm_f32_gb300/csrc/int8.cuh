@@ -2,7 +2,8 @@
 //
 // The products run on the tensor cores in fp16: every 8-bit integer is an fp16
 // number, so are all products of two in the fp32 accumulator, and a sum is exact
-// while it stays within 2^24 (1040 products of the largest size; beyond that an
+// while it stays within 2^24 (1024 products of the largest size, -128 by -128; 1040 of integers
+// that are quantised here, which stop at 127; beyond that an
 // addition is rounded to 24 bits, as in every fp32 sum).  GB300's integer tensor rate
 // is a small part of its fp16 rate (an eighth or less), and two 4-bit halves in 8-bit floats would
 // take four products at twice the rate.  Weights are read from memory in 8 bits

@@ -444,7 +444,8 @@ int dgemm_gated_ffn_backward(int dtype, int activation, int op_w, int M, int D, 
  * scale: x_j is about q_j scale.  Weights are stored out x in (N x K), a row and
  * a scale for each output feature; tokens get theirs in the call.  Integers
  * are multiplied and summed in fp32, exactly while the partial sums stay
- * within 2^24 (any 1040 products do) and with fp32's rounding beyond.
+ * within 2^24 (any 1024 products of signed bytes do, 1040 where none is -128) and with fp32's
+ * rounding beyond; for one to four tokens in 32-bit integers where that is quicker, always exactly.
  * A row with NaN or an infinity gets that as its scale and zeros as integers;
  * results computed from it are NaN.
  */
