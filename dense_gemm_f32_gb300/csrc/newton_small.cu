@@ -53,7 +53,7 @@ struct Cfg {
 };
 
 constexpr int kMaxSplits = 8;
-constexpr int kInputsAhead = 4;  // vectors of in0 that a thread has in flight during the main loop
+constexpr int kInputsAhead = 4;  // vectors of in0 that a thread reads during the main loop: all of its share
 
 // Site codes of the bounded waits.
 enum : int {
@@ -486,17 +486,14 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, TN>::THREADS, 2)
         v[4 * h + 2] = alpha * x.z, v[4 * h + 3] = alpha * x.w;
       }
       if (has_in0) {
+        static_assert(G::T / 2 <= 16 * kInputsAhead, "a share of half a tile's rows or fewer is all ahead");
         float f[8];
-        if (r0 < 16 * kInputsAhead) {
 #pragma unroll
-          for (int k = 0; k < kInputsAhead; ++k)
-            if (r0 == 16 * k) {
+        for (int k = 0; k < kInputsAhead; ++k)
+          if (r0 == 16 * k) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) f[j] = ahead[k][j];
-            }
-        } else {
-          fetch(r, f);
-        }
+            for (int j = 0; j < 8; ++j) f[j] = ahead[k][j];
+          }
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += p.beta * f[j];
       }
