@@ -13,25 +13,37 @@
 
 namespace dg {
 
-Residency::Residency(int num_sms) {
-  for (int per_sm = 1; per_sm <= 2; ++per_sm)
-    for (int s = 1; s <= 8; ++s) tiles[per_sm][s] = small_resident({16, 1, s, per_sm}, num_sms);
-}
+namespace {
 
-const Residency *residency(int num_sms) {
-  static std::atomic<const Residency *> made[64] = {};
+// one(splits, per_sm): the tiles of a kernel.
+template <class F>
+const Residency *made_once(std::atomic<const Residency *> (&made)[64], F &&one) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   const Residency *r = made[dev].load(std::memory_order_acquire);
   if (r == nullptr) {
-    const Residency *mine = new (std::nothrow) Residency(num_sms);
+    Residency *mine = new (std::nothrow) Residency;
     if (mine == nullptr) return nullptr;
+    for (int per_sm = 1; per_sm <= 2; ++per_sm)
+      for (int s = 1; s <= 8; ++s) mine->tiles[per_sm][s] = one(s, per_sm);
     if (made[dev].compare_exchange_strong(r, mine, std::memory_order_acq_rel))
       r = mine;
     else
       delete mine;
   }
   return r;
+}
+
+}  // namespace
+
+const Residency *residency(int num_sms) {
+  static std::atomic<const Residency *> made[64] = {};
+  return made_once(made, [&](int s, int per_sm) { return small_resident({16, 1, s, per_sm}, num_sms); });
+}
+
+const Residency *int8_residency(int num_sms) {
+  static std::atomic<const Residency *> made[64] = {};
+  return made_once(made, [&](int s, int per_sm) { return int8_small_resident(s, per_sm, num_sms); });
 }
 
 namespace {

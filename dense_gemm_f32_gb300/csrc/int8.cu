@@ -96,7 +96,7 @@ bool int8_use_row(const Int8Gemm *p, int n, int num_sms) {
   const int force = knob("DGEMM_INT8_ROW", 0, 1);
   for (int i = 0; i < n; ++i)
     if (!int8_row_takes(p[i].M, p[i].K)) return false;
-  const Residency *res = residency(num_sms);
+  const Residency *res = int8_residency(num_sms);
   if (force == 0 || res == nullptr) return false;
   double row = 0, other = 0;
   for (int i = 0; i < n; ++i) {
@@ -113,7 +113,7 @@ bool int8_use_row(const Int8Gemm *p, int n, int num_sms) {
 cudaError_t launch_int8(const Int8Gemm &p, int num_sms, cudaStream_t stream) {
   int *wd = watchdog_address();
   if (wd == nullptr) return cudaErrorInvalidSymbol;
-  const Residency *res = residency(num_sms);
+  const Residency *res = int8_residency(num_sms);
   if (res == nullptr) return cudaErrorInvalidDevice;
   Int8Plan plan;
   int nt = 0;

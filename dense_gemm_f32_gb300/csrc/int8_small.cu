@@ -481,6 +481,37 @@ cudaError_t launch_small(const Int8Gemm &p, const Int8Plan &plan, int *watchdog,
 
 }  // namespace
 
+int64_t int8_small_resident(int splits, int per_sm, int num_sms) {
+  if (splits == 1) return (int64_t)per_sm * num_sms;
+  if (per_sm == 2) {
+    // The occupancy call counts one CTA of this kernel per SM whatever its shared memory (76 clusters
+    // of two at 104 KB a CTA as at 226), so: clusters of half the size with one each, or twice as many.
+    const bool even = splits % 2 == 0;
+    const int64_t one = int8_small_resident(even ? splits / 2 : splits, 1, num_sms);
+    return even ? one : 2 * one;
+  }
+  auto kern = int8_small_kernel<__half, false, true, true>;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)splits);
+  cfg.blockDim = dim3(Cfg::THREADS);
+  cfg.dynamicSmemBytes = Cfg::BUDGET1 + Cfg::TAIL_BYTES;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::BUDGET1 + Cfg::TAIL_BYTES) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();  // not sticky; an estimate will do
+    n = num_sms / splits;
+  }
+  return n;
+}
+
 cudaError_t launch_int8_small(const Int8Gemm &p, const Int8Plan &plan, int *watchdog,
                               cudaStream_t stream) {
   if (p.gated) return launch_small<__half, true>(p, plan, watchdog, stream);  // H is fp32

@@ -117,13 +117,13 @@ struct SmallPlan {
 // `splits` CTAs) the device holds at once.
 int small_stages(const SmallPlan &plan);
 int64_t small_resident(const SmallPlan &plan, int num_sms);
-// The same by CTAs per SM and K split; the current device's, made once (null: no device, no
-// memory).
+// Tiles of a kernel that the device holds at once, by CTAs per SM and K split; the current
+// device's, made once (null: no device, no memory): fused_small.cu's, int8_small.cu's.
 struct Residency {
   int64_t tiles[3][9];
-  explicit Residency(int num_sms);
 };
 const Residency *residency(int num_sms);
+const Residency *int8_residency(int num_sms);
 // `n` products in one launch (three at most for Epi::kLinear, one otherwise;
 // their plans agree in splits and per_sm).  0: bf16 linear, 1: fp16 linear, 2:
 // bf16 gated, 3: fp16 gated.
@@ -232,6 +232,7 @@ cudaError_t launch_int8_row(const Int8Gemm &p, const void *X, int64_t ldx, int x
 struct Int8Plan {
   int nt, splits, per_sm;
 };
+int64_t int8_small_resident(int splits, int per_sm, int num_sms);
 cudaError_t launch_int8_small(const Int8Gemm &p, const Int8Plan &plan, int *watchdog,
                               cudaStream_t stream);
 // int8_pair.cu, tiles of `nt` tokens (a multiple of 32 up to 192); K > 0.
