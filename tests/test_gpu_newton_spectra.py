@@ -89,3 +89,22 @@ def test_the_ends_of_the_types(rows, cols, dtype, least):
         y = (x * 2.0 ** up).to(dtype)
         assert torch.equal(y.double(), x * 2.0 ** up)
         assert torch.equal(dg.orthogonalize(y, eps=0.0, out=out[1]), want), up
+
+
+GENTLE = {"cubic": ((1.5, -0.5, 0.0), 6), "quintic": ((15 / 8, -10 / 8, 3 / 8), 6)}
+
+
+@pytest.mark.parametrize("plan", PLANS, ids=str)
+@pytest.mark.parametrize("c, steps", GENTLE.values(), ids=GENTLE.keys())
+@pytest.mark.parametrize("rows, cols", [(130, 520), (520, 130), (513, 1030), (1030, 1024)])
+@pytest.mark.parametrize("name", ["flat", "i^-1", "i^-3", "rank one", "two values, 1.7"])
+def test_longer_groups_of_gentle_steps(name, rows, cols, c, steps, plan, monkeypatch):
+    """Three and four steps among m x m matrices, the next Gram matrix and the product of the
+    polynomials in one launch: a growth of 2^4 as with two steps of the usual coefficients, and the
+    steps after the group enlarge what it rounds by a^3 = 6.6 at most, not 40.9, so by less than
+    the limit."""
+    for k, v in plan.items():
+        monkeypatch.setenv("DGEMM_NEWTON_" + k, str(v))
+    for dtype in (torch.float16, torch.float32):
+        x = ns.make(name, rows, cols, dtype).cuda()
+        assert _off(x, steps=steps, coefficients=c) <= ns.LIMIT
