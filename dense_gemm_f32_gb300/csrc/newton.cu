@@ -13,8 +13,8 @@
 // the iteration enlarges, sit in the rounding of the large ones), and storing the
 // result in bf16 by 0.0017.
 //  * X_0 is kept as X 2^(8 - e), 2^e the power of two next above |X| + eps: exact for
-//    16-bit X but for elements 2^-22 (fp16) or 2^-25 (bf16) of the norm and less.  The factor 2^e / (|X| + eps) that is
-//    missing goes into the first Gram matrix and the first product with X, in
+//    16-bit X but for elements of 2^-22 (fp16) or 2^-25 (bf16) of the norm and less.  The factor
+//    2^e / (|X| + eps) that is missing goes into the first Gram matrix and the first product with X, in
 //    fp32.  An fp32 X is kept in two fp16 terms until the first group ends, 22 bits of it: its Gram
 //    matrix is then H H^T + H L^T + L H^T and the product Q H + Q L, the terms blocks of K of one
 //    product.  (Rounded to 11 bits an fp32 matrix of rank one was off by 0.15 of the result's norm,
@@ -259,9 +259,9 @@ int knob(const char *name, int lo, int hi) {
 // GB300).  Small kernel: on 128 x 128 tiles 3.4 us of launch, first load and epilogue, and
 // 0.27 us for a CTA's stage of 64 k or its share where two run on an SM, 5 to 6.5 us for
 // joining the parts of a K split; on 128 x 64 tiles, half an epilogue on twice as many SMs,
-// 2.7 us and 0.255 for a stage, 0.165 its share.  (Five steps of 512 x 1408: 91 us on the
-// narrow tiles, 107 on the square ones; 1013 x 997: 116, 133; of 2048 x 2048, where the narrow
-// ones are two to an SM: 241, 215.)  Pair kernel: 8 us, and 0.28 us per 64 k of a wave of
+// 2.7 us and 0.255 for a stage, 0.165 its share.  (Five steps of 512 x 1408: 94 us on the
+// narrow tiles, 110 on the square ones; 997 x 1013: 111, 126; of 2048 x 2048, where the narrow
+// ones are two to an SM: 242, 213.)  Pair kernel: 8 us, and 0.28 us per 64 k of a wave of
 // 256 x 256 tiles.
 cudaError_t run(const NewtonGemm &p, int num_sms, int *wd, cudaStream_t stream) {
   const int f_pair = knob("DGEMM_NEWTON_PAIR", 0, 1), f_splits = knob("DGEMM_NEWTON_SPLITS", 1, 8);

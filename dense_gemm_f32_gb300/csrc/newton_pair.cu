@@ -15,8 +15,11 @@
 //    fp16, or for the last product to the type of the update.
 //  * A second product with the same B in one launch (the next Gram matrix's and
 //    the polynomials' products read the same polynomial).
-// Bound by the tensor pipe: 4096^3 symmetric takes 48 to 51 us (37 at cuBLAS's measured rate
-// for the 136 tiles, which are 1.8 waves of 76 pairs; tensor pipe 62 to 65% busy), with X 83 (71; 72%).
+//  * Operands of two terms (an fp32 X): the terms are further blocks of K of one sum.
+// Bound by waves and by the ends of each product, not by the tensor pipe: 4096^3 symmetric takes 48
+// to 51 us where its 136 tiles are 37 at cuBLAS's measured rate, as they are 1.8 waves of 76
+// pairs (89%) and nothing covers the first loads and the last epilogue, the next product needing all
+// of this one (tensor pipe 62 to 65% busy); with X, 256 tiles, 83 us (71; 72% busy).
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>

@@ -6,7 +6,9 @@
 // kinds of output: the integers, for a user; the integers in fp16, which hold
 // them exactly, for the products (int8_small.cu, int8_pair.cu multiply in fp16);
 // and columns instead of rows, transposed on the way, for weights stored in x
-// out.
+// out.  8192 x 4096 bf16 rows take 27 us (floor 15), 8192 x 14336 fp32 rows 110 (88): a
+// row's loads, maximum and stores follow one another.  Columns, which a program quantises once for each
+// weight, take 167 us for 4096 x 14336 bf16 (floor 26), read twice, an element per load.
 //
 // Weights on rows that TMA cannot read are copied by blocks of the same launch (in one of its
 // own a product of 1000 x 997 x 1013 took 14.1 us for 12.3, of 64 x 4095 x 14335 43.1 for 35.9).

@@ -522,7 +522,8 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F,
  * directions over noise, 0.004 to 0.008 where the singular values fall as i^-2 to i^-4, and at
  * most 0.02, which a matrix of rank one comes near to (all products in bf16: 0.005 to 0.26).
  * A rounding of 2^-12 in directions that X does not have is enlarged by the a of every
- * step after the first two, so more steps, or steeper ones, are off by more.  With eps = 0 a
+ * step after the first two, so more steps, or steeper ones, are off by more.  So is an X whose norm
+ * is far below eps (2^-10 of it): its elements leave fp16's range.  With eps = 0 a
  * matrix of zeros, and always one with NaN or an infinity, gives NaN.  Coefficients
  * under which the iteration diverges give infinities and NaN past 2^7 or so.
  * work: dgemm_orthogonalize_workspace(rows, cols) bytes on a 16-byte boundary.
