@@ -8,10 +8,10 @@
 //
 // Everything between X and the result is fp16 with fp32 accumulators: 11 bits, where
 // bf16 has 8, at the same rate, and with the scales below nothing that matters
-// leaves fp16's range.  Against 64 bits the result is off by 0.0008 to 0.003 of its
-// norm where one in bf16 is off by 0.01 to 0.05 (the small singular values, which
-// the iteration enlarges, sit in the rounding of the large ones), and storing the
-// result in bf16 by 0.0017.
+// leaves fp16's range.  Against 64 bits the result is off by 0.001 to 0.015 of its
+// norm where one in bf16 is off by 0.006 to 0.26 (the small singular values, which
+// the iteration enlarges, sit in the rounding of the large ones; by matrix in
+// tests/newton_spectra.py), and storing the result in bf16 by 0.0017.
 //  * X_0 is kept as X 2^(8 - e), 2^e the power of two next above |X| + eps: exact for
 //    16-bit X but for elements of 2^-22 (fp16) or 2^-25 (bf16) of the norm and less.  The factor
 //    2^e / (|X| + eps) that is missing goes into the first Gram matrix and the first product with X, in
