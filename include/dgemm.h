@@ -520,7 +520,8 @@ int dgemm_gated_ffn_int8(int dtype, int activation, int M, int D, int F,
  * fp16 terms.  Five steps of a = 3.4445,
  * -4.7750, 2.0315 are off by some 0.0015 of the update's norm for gradients with a few strong
  * directions over noise, 0.004 to 0.008 where the singular values fall as i^-2 to i^-4, and at
- * most 0.02, which a matrix of rank one comes near to (all products in bf16: 0.005 to 0.26).
+ * most 0.02, which a matrix of rank one comes near to (all products in bf16: 0.005 to 0.26); 0.07 where
+ * the smaller side is 2 to 7, too few for roundings to cancel.
  * A rounding of 2^-12 in directions that X does not have is enlarged by the a of every
  * step after the first two, so more steps, or steeper ones, are off by more.  So is an X whose norm
  * is far below eps (2^-10 of it): its elements leave fp16's range.  And so is an X with a side of millions:

@@ -108,3 +108,16 @@ def test_longer_groups_of_gentle_steps(name, rows, cols, c, steps, plan, monkeyp
     for dtype in (torch.float16, torch.float32):
         x = ns.make(name, rows, cols, dtype).cuda()
         assert _off(x, steps=steps, coefficients=c) <= ns.LIMIT
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("m", [2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("n", [1, 8, 100, 1400])
+def test_few_rows_or_columns(m, n, dtype):
+    """Products of two vectors with some noise, whose second singular value is small."""
+    gen = torch.Generator().manual_seed(m)
+    for noise in (0.03, 0.1, 0.3, 1.0):
+        for _ in range(6):
+            x = torch.randn((m, 1), generator=gen) * torch.randn((1, m + n), generator=gen)
+            x = (x + noise * torch.randn(x.shape, generator=gen)).to(dtype).cuda()
+            assert _off(x) <= ns.FEW and _off(x.t().contiguous()) <= ns.FEW
